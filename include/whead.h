@@ -43,6 +43,7 @@ extern "C" {
 #define WHEAD_ERR_TIMEOUT (-4)      /* a device-side wait gave up after its time limit */
 #define WHEAD_ERR_NO_COOP (-5)      /* the grid cannot be made co-resident (cooperative launch refused) */
 #define WHEAD_ERR_INTERNAL (-6)     /* a device-side consistency check failed */
+#define WHEAD_ERR_NO_PAGES (-7)     /* a KV cache's page pool, or a sequence's page table, is full (whead_kv.h) */
 
 typedef enum { WHEAD_MARKOV = 0, WHEAD_RECURRENT = 1 } whead_kind;
 

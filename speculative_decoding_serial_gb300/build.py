@@ -10,11 +10,13 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libwhead.so")
 # the host library and the walk kernel's instantiations (Markov / recurrent head x base logits read at each step /
-# copied a step ahead), compiled in parallel
+# copied a step ahead), the 4-bit KV cache's calls; compiled in parallel
 SOURCES = [os.path.join(CSRC, n) for n in ("whead_api.cu", "walk_resident.cu", "walk_resident_rec.cu",
-                                           "walk_async.cu", "walk_async_rec.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("walk_kernel.cuh", "walk_launch.cuh", "walk_launch.h")] + [
-    os.path.join(ROOT, "include", "whead.h")]
+                                           "walk_async.cu", "walk_async_rec.cu",
+                                           "kv_cache.cu", "kv_attend.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("walk_kernel.cuh", "walk_launch.cuh", "walk_launch.h",
+                                                      "kv_common.cuh", "kv_schedule.cuh")] + [
+    os.path.join(ROOT, "include", n) for n in ("whead.h", "whead_kv.h")]
 # measurement-only library used by the benchmark for the roofline's on-chip figures
 PROBE_LIB = os.path.join(BUILD, "libwhead_probe.so")
 PROBE_SRC = os.path.join(CSRC, "onchip_probe.cu")

@@ -1,0 +1,202 @@
+// kv_common.cuh — what the 4-bit paged KV cache's kernels share: the cache as kernels see it, the workspace's layout,
+// conversions of its number formats, and the attention's division of work over CTAs.
+#pragma once
+
+#include "../../include/whead_kv.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace whead_kv_impl {
+
+constexpr int kMaxCtas = 2048;        // most CTAs of an attend launch (partial results, counters)
+constexpr int kRegionPages = WHEAD_KV_MAX_BLOCK / 16 + 1;  // pages that a block's tokens can lie in
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Workspace: the control words, then per-slot arrays, then the attention's counters and partial results.
+struct Ctl {
+  int status;  // first device-side error
+  int abort;   // set by a planning kernel: the call's later kernels do nothing
+  int total;   // groups of an append
+  int pad;
+  unsigned ticket[4];
+};
+
+struct Cache {
+  uint8_t* pool;
+  int32_t* lens;
+  int32_t* refs;
+  int32_t* tables;
+  const float* k_scale;
+  const float* v_scale;
+  int page_size, page_shift, kv_heads, head_dim, max_seqs, max_pages, num_pages;
+  Ctl* ctl;
+  int32_t* seq_a;   // max_seqs + 1
+  int32_t* seq_b;   // max_seqs + 1
+  int32_t* region;  // max_seqs x 2 x kRegionPages: pages of a block before and after
+  int32_t* fresh;   // num_pages: free pages found
+  int32_t* rows;    // max_seqs x max_pages: tables after a fork
+  unsigned* counters;   // kMaxCtas
+  int32_t* starts;      // kMaxCtas x 4
+  float* partial;
+  int64_t partial_floats;
+};
+
+__host__ __device__ inline int64_t align256(int64_t x) { return (x + 255) & ~(int64_t)255; }
+
+// Floats of partial results: two for each CTA (a CTA's range of work begins inside one item and ends inside another).
+// The largest tiles: 128 rows by one CTA an SM (head_dim <= 128), or 32 rows by up to eight.
+inline int64_t partial_floats(int head_dim, int sms) {
+  const int64_t one = (int64_t)sms * 2 * 256 * (head_dim + 2);
+  return one;
+}
+
+// ---------------------------------------------------------------- number formats
+
+// the two e2m1 values of each byte of w as f16 pairs (low nibble in the low half)
+__device__ __forceinline__ void e2m1x8_to_half2(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+}
+
+// the four e4m3 values of w as two f16 pairs
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi) : "r"(w));
+}
+
+// byte of e2m1 codes: lo in the low nibble; nearest even, saturating
+__device__ __forceinline__ uint32_t e2m1x2_from_float(float lo, float hi) {
+  uint32_t r;
+  asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n mov.b32 %0, {b, 0, 0, 0};\n}\n" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+__device__ __forceinline__ float e4m3_to_float(uint8_t b) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t low2(uint32_t a) { return __byte_perm(a, a, 0x1010); }
+__device__ __forceinline__ uint32_t high2(uint32_t a) { return __byte_perm(a, a, 0x3232); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) {
+  if (dtype == WHEAD_KV_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  if (dtype == WHEAD_KV_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return static_cast<const float*>(p)[i];
+}
+
+// N consecutive elements (N = 2 or 4) from i on; `wide`: the address is a multiple of their size
+template <int N>
+__device__ __forceinline__ void load_elems(const void* p, int64_t i, int dtype, bool wide, float (&x)[N]) {
+  if (!wide) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) x[k] = load_elem(p, i + k, dtype);
+    return;
+  }
+  if (dtype == WHEAD_KV_F32) {
+    if constexpr (N == 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+    } else {
+      const float2 v = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p) + i));
+      x[0] = v.x; x[1] = v.y;
+    }
+    return;
+  }
+  uint32_t w[N / 2];
+  if constexpr (N == 4) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
+    w[0] = v.x; w[1] = v.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i));
+  }
+#pragma unroll
+  for (int k = 0; k < N / 2; ++k) {
+    if (dtype == WHEAD_KV_BF16) {
+      x[2 * k] = __uint_as_float(w[k] << 16);
+      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      x[2 * k] = f.x;
+      x[2 * k + 1] = f.y;
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int dtype) {
+  if (dtype == WHEAD_KV_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// ---------------------------------------------------------------- the cache
+
+__device__ __forceinline__ void set_status(const Cache& c, int code) { atomicCAS(&c.ctl->status, 0, code); }
+
+// Group `pos / 16` of head h in a slot's page; pages out of range read page 0 and are reported.
+template <int D>
+__device__ __forceinline__ uint8_t* group_ptr(const Cache& c, int page, int h, int pos) {
+  if ((unsigned)page >= (unsigned)c.num_pages) {
+    set_status(c, WHEAD_ERR_INTERNAL);
+    page = 0;
+  }
+  const int in_page = (pos & (c.page_size - 1)) >> 4;
+  return c.pool + (((int64_t)page * c.kv_heads + h) * (c.page_size >> 4) + in_page) * (18 * D);
+}
+
+// A slot's length, 0 (and an error) for what is not a slot.
+__device__ __forceinline__ int slot_len(const Cache& c, int slot) {
+  if ((unsigned)slot >= (unsigned)c.max_seqs) {
+    set_status(c, WHEAD_ERR_INVALID_ARG);
+    return 0;
+  }
+  const int len = c.lens[slot];
+  const int64_t most = (int64_t)c.max_pages * c.page_size;
+  if (len < 0 || len > most) {
+    set_status(c, WHEAD_ERR_INTERNAL);
+    return 0;
+  }
+  return len;
+}
+
+// ---------------------------------------------------------------- host
+
+struct HostCache {
+  Cache c;
+  cudaStream_t stream;
+  int sms;
+};
+
+// Checks a whead_kv and lays its workspace out; WHEAD_OK or an error.
+int host_cache(const whead_kv* kv, HostCache* out);
+int device_sms();
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline int launch_status() {
+  if (cudaGetLastError() != cudaSuccess) return WHEAD_ERR_CUDA;
+  return WHEAD_OK;
+}
+
+}  // namespace whead_kv_impl

@@ -1,0 +1,237 @@
+// kv_schedule.cuh — how an attention over the cache is divided over CTAs.
+//
+// The work is a list of items, one for each entry, tile of query rows and KV head. A row is a query token and one of the
+// query heads of a KV head (row = token * group + head in the group), so that all rows of a tile read the same keys. An
+// item is a run of units of UNIT keys, from the first that one of its rows sees to the last. All units, laid end to end,
+// are cut into as many equal ranges as there are CTAs: ragged lengths need no balancing, and a long sequence alone fills
+// the device. An item cut by a range's end leaves partial results (each row's running maximum, its sum and its output
+// before the division) in the workspace; the last CTA to finish one of its parts joins them, in the order of the keys, so
+// that results do not depend on which CTA comes last.
+#pragma once
+
+#include "kv_common.cuh"
+
+namespace whead_kv_impl {
+
+struct AttendArgs {
+  const void* q;
+  void* out;
+  float* lse;
+  const int32_t* indptr;
+  const int32_t* slots;
+  const unsigned long long* tree;
+  int64_t total, q_token_stride, q_head_stride;
+  int n, heads, group, row_tiles, dtype, causal, window, tree_words;
+  float scale;
+  bool wide_q;
+  int planned;  // the CTAs' starts are in the workspace
+};
+
+// One (entry, row tile): its rows and the units that they see.
+struct Tile {
+  int slot, len, tokens, first;  // first: row of q of the entry's first token
+  int row0, rows;                // the tile's first row, and its rows
+  int unit0, units;              // units of one KV head
+};
+
+template <int UNIT>
+__device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, int item, int tile_rows) {
+  Tile t;
+  const int i = item / a.row_tiles, m = item - i * a.row_tiles;
+  t.slot = a.slots ? a.slots[i] : i;
+  t.len = slot_len(c, t.slot);
+  if (t.len == 0) t.slot = 0;
+  if (a.indptr) {
+    const int lo = a.indptr[i], hi = a.indptr[i + 1];
+    const bool ok = lo >= 0 && hi >= lo && hi <= a.total;
+    if (!ok) set_status(c, WHEAD_ERR_INVALID_ARG);
+    t.first = ok ? lo : 0;
+    t.tokens = ok ? hi - lo : 0;
+  } else {
+    t.tokens = (int)(a.total / a.n);
+    t.first = t.tokens * i;
+  }
+  const int64_t all = (int64_t)t.tokens * a.group;
+  const int64_t row0 = (int64_t)m * tile_rows;
+  if (m == a.row_tiles - 1 && row0 + tile_rows < all) set_status(c, WHEAD_ERR_INVALID_ARG);  // more tokens than max_q
+  t.row0 = (int)row0;
+  t.rows = (int)(all - row0 < 0 ? 0 : all - row0 < tile_rows ? all - row0 : tile_rows);
+  t.unit0 = t.units = 0;
+  if (t.rows == 0) return t;
+  const int t0 = t.row0 / a.group, t1 = (t.row0 + t.rows - 1) / a.group;
+  int hi = t.len, lo = 0;
+  if (a.causal) hi = min(max(t.len - t.tokens + t1 + 1, 0), t.len);
+  if (a.window) lo = max(t.len - t.tokens + t0 - a.window + 1, 0);
+  t.unit0 = lo / UNIT;
+  t.units = max((hi + UNIT - 1) / UNIT - t.unit0, 1);  // at least one: somebody has to write the rows
+  return t;
+}
+
+// The keys that a row sees: lo <= j < hi, and the bits of its mask for j >= draft.
+struct RowView {
+  int lo, hi, draft;
+  const unsigned long long* bits;
+};
+
+__device__ __forceinline__ RowView row_view(const AttendArgs& a, const Tile& t, int row) {
+  RowView v{0, 0, 0x7FFFFFFF, nullptr};
+  if (row >= t.row0 + t.rows) return v;
+  const int tok = row / a.group;
+  const int pos = t.len - t.tokens + tok;
+  v.hi = a.causal ? min(pos + 1, t.len) : t.len;
+  if (a.window) v.lo = max(pos - a.window + 1, 0);
+  if (a.tree) {
+    v.draft = t.len - t.tokens;
+    v.bits = a.tree + (int64_t)(t.first + tok) * a.tree_words;
+  }
+  return v;
+}
+
+__device__ __forceinline__ bool sees(const RowView& v, int j) {
+  if (j < v.lo || j >= v.hi) return false;
+  if (j < v.draft) return true;
+  const int u = j - v.draft;
+  return (v.bits[u >> 6] >> (u & 63)) & 1;
+}
+
+// Where a CTA's range begins: the item, and the number of the item's first unit.
+struct Start {
+  int item;
+  int ctas;           // CTAs that have work: fewer than launched where there are fewer units
+  long long at;       // number of the item's first unit (of all its KV heads)
+  long long total;
+};
+
+__device__ __forceinline__ long long range_begin(const Start& s, int cta) { return s.total * cta / s.ctas; }
+// the CTA whose range holds unit x
+__device__ __forceinline__ int range_owner(const Start& s, long long x) { return (int)(((x + 1) * s.ctas - 1) / s.total); }
+
+// Sum of x over the threads before this one, and over all; `warps` words of shared memory.
+template <int THREADS>
+__device__ __forceinline__ long long scan64(long long x, long long* warps, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(~0u, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = v;
+  __syncthreads();
+  long long before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const long long y = warps[w];
+    if (w < warp) before += y;
+    all += y;
+  }
+  total = all;
+  return before + v - x;
+}
+
+struct SchedShared {
+  long long warps[32];
+  int item;
+  long long at;
+};
+
+// This CTA's start, from the lengths themselves (few items).
+template <int THREADS, int UNIT>
+__device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a, int tile_rows, SchedShared& s) {
+  const int items = a.n * a.row_tiles;
+  Start r;
+  r.total = 0;
+  long long mine = 0, before = 0;
+  for (int base = 0; base < items; base += THREADS) {
+    const int it = base + threadIdx.x;
+    mine = it < items ? (long long)make_tile<UNIT>(c, a, it, tile_rows).units * c.kv_heads : 0;
+    long long all;
+    before = r.total + scan64<THREADS>(mine, s.warps, all);
+    r.total += all;
+  }
+  r.ctas = (int)min((long long)gridDim.x, r.total);
+  r.item = 0;
+  r.at = 0;
+  if ((int)blockIdx.x >= r.ctas) return r;
+  const long long x = range_begin(r, blockIdx.x);
+  if (items <= THREADS) {
+    if (mine > 0 && before <= x && x < before + mine) {
+      s.item = threadIdx.x;
+      s.at = before;
+    }
+  } else {
+    long long sum = 0;
+    for (int base = 0; base < items && sum <= x; base += THREADS) {
+      const int it = base + threadIdx.x;
+      mine = it < items ? (long long)make_tile<UNIT>(c, a, it, tile_rows).units * c.kv_heads : 0;
+      long long all;
+      before = sum + scan64<THREADS>(mine, s.warps, all);
+      if (mine > 0 && before <= x && x < before + mine) {
+        s.item = it;
+        s.at = before;
+      }
+      sum += all;
+    }
+  }
+  __syncthreads();
+  r.item = s.item;
+  r.at = s.at;
+  return r;
+}
+
+// The same for all CTAs of a launch, by one CTA, into the workspace (many items).
+template <int UNIT>
+__global__ void __launch_bounds__(1024, 1) attend_plan(Cache c, AttendArgs a, int tile_rows, int ctas) {
+  __shared__ long long warps[32];
+  const int items = a.n * a.row_tiles;
+  long long total = 0;
+  for (int base = 0; base < items; base += 1024) {
+    const int it = base + threadIdx.x;
+    long long all;
+    scan64<1024>(it < items ? (long long)make_tile<UNIT>(c, a, it, tile_rows).units * c.kv_heads : 0, warps, all);
+    total += all;
+  }
+  Start r;
+  r.total = total;
+  r.ctas = (int)min((long long)ctas, total);
+  long long sum = 0;
+  for (int base = 0; base < items; base += 1024) {
+    const int it = base + threadIdx.x;
+    const long long mine = it < items ? (long long)make_tile<UNIT>(c, a, it, tile_rows).units * c.kv_heads : 0;
+    long long all;
+    const long long before = sum + scan64<1024>(mine, warps, all);
+    sum += all;
+    if (mine > 0) {
+      int k = range_owner(r, before);
+      if (range_begin(r, k) < before) ++k;
+      for (; k < r.ctas && range_begin(r, k) < before + mine; ++k) {
+        int32_t* to = c.starts + 4 * k;
+        to[0] = it;
+        *reinterpret_cast<long long*>(to + 2) = before;
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    c.ctl->pad = r.ctas;
+    *reinterpret_cast<long long*>(&c.ctl->ticket[2]) = total;
+  }
+}
+
+template <int THREADS, int UNIT>
+__device__ __forceinline__ Start get_start(const Cache& c, const AttendArgs& a, int tile_rows, SchedShared& s) {
+  if (!a.planned) return find_start<THREADS, UNIT>(c, a, tile_rows, s);
+  Start r;
+  r.ctas = c.ctl->pad;
+  r.total = *reinterpret_cast<const long long*>(&c.ctl->ticket[2]);
+  r.item = 0;
+  r.at = 0;
+  if ((int)blockIdx.x < r.ctas) {
+    const int32_t* from = c.starts + 4 * blockIdx.x;
+    r.item = from[0];
+    r.at = *reinterpret_cast<const long long*>(from + 2);
+  }
+  return r;
+}
+
+}  // namespace whead_kv_impl

@@ -337,6 +337,7 @@ const char* whead_strerror(int code) {
     case WHEAD_ERR_TIMEOUT: return "a device-side wait ran past its time limit";
     case WHEAD_ERR_NO_COOP: return "grid cannot be co-resident (cooperative launch refused)";
     case WHEAD_ERR_INTERNAL: return "device-side consistency check failed";
+    case WHEAD_ERR_NO_PAGES: return "a KV cache's page pool or page table is full";
     default: return "unknown error";
   }
 }
