@@ -19,11 +19,8 @@ namespace whead_kv_impl {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kUnit = kWarps * 16;  // keys of a unit: 16 a warp
-constexpr float kBias = 7.0f;       // m stands this far below the largest score at its setting: small p stay normal in f16
-constexpr float kSlack = 15.0f;     // and is set anew when a score passes it by more: p <= 2^15
+constexpr float kBias = 7.0f;                // m stands this far below the largest score at its setting: small p stay normal in f16
+constexpr float kSlack = 15.0f;              // and is set anew when a score passes it by more: p <= 2^15
 constexpr float kNoKey = -1e30f;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -38,78 +35,191 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return r;
 }
 
+// What one CTA needs for D channels and 8 NT rows. Every warp has a ring of its own, of one group (16 keys of one KV head) a
+// stage; red holds the warps' outputs while they are joined (rows 4 floats apart beyond D: a warp's stores then hit
+// every bank once).
 template <int D, int NT>
-struct Smem {
-  uint2 q[NT][D / 16][32];        // query rows as operands: [8-row tile][16 channels][lane]
-  float c[NT * 8];                // a row's factor from sums of products to scores in log2 units
-  float o[NT * 8][D + 8];         // outputs of the CTA's warps, added up
-  float m[kWarps][NT * 8];
-  float l[kWarps][NT * 8];
-  float row_m[NT * 8], row_l[NT * 8];
+struct Shape {
+  static constexpr int kRows = NT * 8;
+  static constexpr int kLoad = NT * D;  // a lane's output registers are a quarter of this
+  static constexpr int kCtas = kLoad <= 128 ? 2 : 1;
+  static constexpr int kWarps = kLoad == 256 ? 12 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kUnit = kWarps * 16;
+  static constexpr bool kQInRegs = kLoad <= 128;
+  static constexpr int kGroup = 18 * D;
+  static constexpr int kRed = kWarps * kRows * (D + 4) * 4;
+  static constexpr int kQ = kQInRegs ? 0 : NT * (D / 16) * 32 * 8;
+  static constexpr int kFixed = (2048 + 2 * kWarps * kRows * 4 + kRows * 4 + kQ + kRed + 127) / 128 * 128;
+  static constexpr int kRoom = (227 * 1024 / kCtas - 1024 * (kCtas - 1) - kFixed) / (kWarps * kGroup);
+  static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
+  static constexpr int kBytes = kFixed + kStages * kWarps * kGroup;
+  static_assert(kStages >= 2, "the rings need two stages");
+};
+
+struct Head {  // the fixed head of shared memory
+  unsigned long long full[12][8];
   SchedShared sched;
   int last;
 };
+static_assert(sizeof(Head) <= 2048, "");
+
+// A CTA's piece of one item: units u0 .. u1 - 1 of one (tile, KV head).
+struct Segment {
+  Tile tile;
+  int h, u0, u1;
+  long long head_at;
+};
+
+// A warp's way through a segment's groups, its ring and the pages' numbers: lane l holds those of the next 32 units.
+template <int D, int NT>
+struct Fetch {
+  const uint8_t* base;      // the pool at this KV head
+  const int32_t* table;
+  int next, end;            // units to fetch
+  int entries, entry0;
+  uint32_t slot;            // stage of the next group to fetch
+};
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) attend_rows(Cache c, AttendArgs a) {
-  constexpr int NB = D / 16, ROWS = NT * 8;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  Smem<D, NT>& s = *reinterpret_cast<Smem<D, NT>*>(smem_raw);
+__device__ __forceinline__ void fetch_one(const Cache& c, const Segment& sg, Fetch<D, NT>& f, uint32_t ring, uint32_t bars) {
+  using S = Shape<D, NT>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (f.next >= f.end) return;
+  const int key0 = (sg.tile.unit0 + f.next) * S::kUnit + warp * 16;
+  if (f.next >= f.entry0 + 32) {
+    f.entry0 = f.next;
+    const int64_t key = key0 + (int64_t)lane * S::kUnit;
+    f.entries = key < sg.tile.len ? f.table[key >> c.page_shift] : 0;
+    if ((unsigned)f.entries >= (unsigned)c.num_pages) {
+      set_status(c, WHEAD_ERR_INTERNAL);
+      f.entries = 0;
+    }
+  }
+  const int page = __shfl_sync(~0u, f.entries, f.next - f.entry0);
+  if (lane == 0) {
+    const int in_page = (key0 & (c.page_size - 1)) >> 4;
+    const uint8_t* src = f.base + ((int64_t)page * c.kv_heads * (c.page_size >> 4) + in_page) * S::kGroup;
+    mbar_expect(bars + f.slot * 8, S::kGroup);
+    bulk_load(ring + f.slot * S::kGroup, src, S::kGroup, bars + f.slot * 8);
+  }
+  f.slot = f.slot + 1 == S::kStages ? 0 : f.slot + 1;
+  ++f.next;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas)) attend_rows(Cache c, AttendArgs a) {
+  using S = Shape<D, NT>;
+  constexpr int NB = D / 16, ROWS = S::kRows, kWarps = S::kWarps, kConsumers = S::kThreads, kUnit = S::kUnit;
+  extern __shared__ __align__(128) uint8_t smem[];
+  Head& s = *reinterpret_cast<Head*>(smem);
+  float* s_m = reinterpret_cast<float*>(smem + 2048);       // [warp][row]
+  float* s_l = s_m + kWarps * ROWS;
+  float* s_c = s_l + kWarps * ROWS;                          // a row's factor from sums of products to scores in log2 units
+  uint2* s_q = reinterpret_cast<uint2*>(s_c + ROWS);         // query rows as operands: [8-row tile][16 channels][lane]
+  float* red = reinterpret_cast<float*>(smem + 2048 + 2 * kWarps * ROWS * 4 + ROWS * 4 + S::kQ);  // [warp][row][D + 4]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const Start start = get_start<kThreads, kUnit>(c, a, ROWS, s.sched);
+  const uint8_t* my_ring = smem + S::kFixed + warp * S::kStages * S::kGroup;
+  const uint32_t ring = smem_u32(my_ring), bars = smem_u32(&s.full[warp][0]);
+  if (lane == 0) {
+    for (int i = 0; i < S::kStages; ++i) mbar_init(bars + i * 8, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const Start start = get_start<S::kThreads, kUnit>(c, a, ROWS, s.sched);
   if ((int)blockIdx.x >= start.ctas) return;
   long long cur = range_begin(start, blockIdx.x);
   const long long begin = cur, end = range_begin(start, blockIdx.x + 1);
   int item = start.item;
   long long item_at = start.at;
-  while (cur < end) {
-    const Tile tile = make_tile<kUnit>(c, a, item, ROWS);
-    if (tile.units == 0) {
+  uint32_t stage = 0, phase = 0;
+  bool dead = false;
+  Segment sg;
+  Fetch<D, NT> fetch;
+  fetch.slot = 0;
+
+  // the segment that begins at unit `at`, and the first copies of this warp's groups
+  auto enter = [&](long long at) {
+    while (true) {
+      sg.tile = make_tile<kUnit>(c, a, item, ROWS);
+      if (sg.tile.units > 0) break;
       ++item;
-      continue;
     }
-    const int h = (int)((cur - item_at) / tile.units);
-    const long long head_at = item_at + (long long)h * tile.units;
-    const int u0 = (int)(cur - head_at);
-    const int u1 = (int)min((long long)tile.units, u0 + (end - cur));
-    __syncthreads();
-    // query rows
-    for (int nt = warp; nt < NT; nt += kWarps) {
-      const int row = tile.row0 + nt * 8 + g;
-      const bool live = nt * 8 + g < tile.rows;
-      const int64_t at = live ? (int64_t)(tile.first + row / a.group) * a.q_token_stride + (int64_t)(h * a.group + row % a.group) * a.q_head_stride : 0;
-      float big = 0.0f;
-      for (int b = 0; b < NB; ++b) {
-        float x[4] = {};
-        if (live) load_elems<4>(a.q, at + b * 16 + t * 4, a.dtype, a.wide_q, x);
-        big = fmaxf(big, fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+    sg.h = (int)((at - item_at) / sg.tile.units);
+    sg.head_at = item_at + (long long)sg.h * sg.tile.units;
+    sg.u0 = (int)(at - sg.head_at);
+    sg.u1 = (int)min((long long)sg.tile.units, sg.u0 + (end - at));
+    fetch.base = c.pool + (int64_t)sg.h * (c.page_size >> 4) * S::kGroup;
+    fetch.table = c.tables + (int64_t)sg.tile.slot * c.max_pages;
+    fetch.next = sg.u0;
+    // units whose group of this warp holds any key
+    fetch.end = min(sg.u1, max((sg.tile.len - warp * 16 + kUnit - 1) / kUnit - sg.tile.unit0, sg.u0));
+    if (dead) fetch.end = sg.u0;
+    fetch.entry0 = sg.u0 - 32;
+#pragma unroll 1
+    for (int i = 0; i < S::kStages; ++i) fetch_one(c, sg, fetch, ring, bars);
+  };
+  if (cur < end) enter(cur);
+
+  while (cur < end) {
+    const Tile tile = sg.tile;
+    const int h = sg.h, u0 = sg.u0, u1 = sg.u1;
+    int live_end = fetch.end;
+    const long long head_at = sg.head_at;
+    // query rows: from a power of two to f16, as operands
+    const float to_log2 = a.scale * c.k_scale[h] * kLog2e;
+    uint2 q[S::kQInRegs ? NT : 1][S::kQInRegs ? NB : 1];
+    float f[NT][2];
+    if (!S::kQInRegs) named_sync<kConsumers>(1);
+#pragma unroll
+    for (int i = 0; i < (S::kQInRegs ? NT : (NT + kWarps - 1) / kWarps); ++i) {
+      const int nt = S::kQInRegs ? i : i * kWarps + warp;
+      if (nt < NT) {
+        const int row = tile.row0 + nt * 8 + g;
+        const bool live = nt * 8 + g < tile.rows;
+        const int64_t at = live ? (int64_t)(tile.first + row / a.group) * a.q_token_stride + (int64_t)(h * a.group + row % a.group) * a.q_head_stride : 0;
+        float x[NB][4], big = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          x[b][0] = x[b][1] = x[b][2] = x[b][3] = 0.0f;
+          if (live) load_elems<4>(a.q, at + b * 16 + t * 4, a.dtype, a.wide_q, x[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) big = fmaxf(big, fmaxf(fmaxf(fabsf(x[b][0]), fabsf(x[b][1])), fmaxf(fabsf(x[b][2]), fabsf(x[b][3]))));
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+        // 2^e <= big < 2^(e + 1), in the range whose powers of two are normal both ways
+        const int e = min(max((int)((__float_as_uint(big) >> 23) & 255) - 127, -100), 100);
+        const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23), down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const __half2 lo = __floats2half2_rn(x[b][0] * up, x[b][1] * up), hi = __floats2half2_rn(x[b][2] * up, x[b][3] * up);
+          const uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          if constexpr (S::kQInRegs) q[i][b] = w;
+          else s_q[(nt * NB + b) * 32 + lane] = w;
+        }
+        if constexpr (S::kQInRegs) {
+          f[i][0] = __shfl_sync(~0u, down, t * 8) * to_log2;
+          f[i][1] = __shfl_sync(~0u, down, t * 8 + 4) * to_log2;
+        } else if (t == 0) {
+          s_c[nt * 8 + g] = down * to_log2;
+        }
       }
-      big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-      big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-      // 2^e <= big < 2^(e + 1), in the range whose powers of two are normal both ways
-      const int e = min(max((int)((__float_as_uint(big) >> 23) & 255) - 127, -100), 100);
-      const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23), down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
-      for (int b = 0; b < NB; ++b) {
-        float x[4] = {};
-        if (live) load_elems<4>(a.q, at + b * 16 + t * 4, a.dtype, a.wide_q, x);
-        const __half2 lo = __floats2half2_rn(x[0] * up, x[1] * up), hi = __floats2half2_rn(x[2] * up, x[3] * up);
-        s.q[nt][b][lane] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-      }
-      if (t == 0) s.c[nt * 8 + g] = down * (a.scale * c.k_scale[h] * kLog2e);
     }
-    __syncthreads();
+    if constexpr (!S::kQInRegs) {
+      named_sync<kConsumers>(1);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f[nt][0] = s_c[nt * 8 + 2 * t];
+        f[nt][1] = s_c[nt * 8 + 2 * t + 1];
+      }
+    }
     float o[NT][NB][4];
-    float m[NT][2], l[NT][2], f[NT][2];
-    RowView view[NT][2];
+    float m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[nt][e] = kNoKey;
-        l[nt][e] = 0.0f;
-        f[nt][e] = s.c[nt * 8 + 2 * t + e];
-        view[nt][e] = row_view(a, tile, tile.row0 + nt * 8 + 2 * t + e);
-      }
+      m[nt][0] = m[nt][1] = kNoKey;
+      l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -117,112 +227,145 @@ __global__ void __launch_bounds__(kThreads) attend_rows(Cache c, AttendArgs a) {
     }
     // keys that every row sees need no looking at masks
     const int t0 = tile.row0 / a.group, t1 = (tile.row0 + tile.rows - 1) / a.group, past = tile.len - tile.tokens;
-    const int free_hi = a.tree ? min(past, a.causal ? past + t0 + 1 : tile.len) : a.causal ? min(past + t0 + 1, tile.len) : tile.len;
+    const int free_hi = a.tree ? min(past, past + t0 + 1) : a.causal ? min(past + t0 + 1, tile.len) : tile.len;
     const int free_lo = a.window ? max(past + t1 - a.window + 1, 0) : 0;
-    const int32_t* table = c.tables + (int64_t)tile.slot * c.max_pages;
-    for (int u = u0; u < u1; ++u) {
+#pragma unroll 1
+    for (int u = u0; u < live_end; ++u) {
       const int key0 = (tile.unit0 + u) * kUnit + warp * 16;
-      if (key0 >= tile.len) break;
-      const uint8_t* gp = group_ptr<D>(c, table[key0 >> c.page_shift], h, key0);
-      uint32_t kw[NB], ks[NB / 2], vw[NB], vs[NB];
-#pragma unroll
-      for (int i = 0; i < NB / 4; ++i) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(gp + i * 512) + lane);
-        kw[4 * i] = x.x; kw[4 * i + 1] = x.y; kw[4 * i + 2] = x.z; kw[4 * i + 3] = x.w;
-        const uint4 y = __ldg(reinterpret_cast<const uint4*>(gp + 9 * D + i * 512) + lane);
-        vw[4 * i] = y.x; vw[4 * i + 1] = y.y; vw[4 * i + 2] = y.z; vw[4 * i + 3] = y.w;
-        const uint2 z = __ldg(reinterpret_cast<const uint2*>(gp + 8 * D + g * 2 * NB) + i);
-        ks[2 * i] = z.x; ks[2 * i + 1] = z.y;
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(gp + 17 * D + t * 4 * NB) + i);
-        vs[4 * i] = w.x; vs[4 * i + 1] = w.y; vs[4 * i + 2] = w.z; vs[4 * i + 3] = w.w;
+      // a copy that does not come is reported; nothing more is fetched, and what is under way is still waited for
+      if (!__all_sync(~0u, mbar_wait(bars + stage * 8, phase))) {
+        set_status(c, WHEAD_ERR_TIMEOUT);
+        dead = true;
+        fetch.end = live_end = fetch.next;
       }
-      float sc[NT][4];
+      {
+        const uint8_t* gp = my_ring + stage * S::kGroup;
+        float sc[NT][4];
+        {
+          float sb[NT][4];  // odd blocks: two chains of products instead of one
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) sc[nt][k] = 0.0f;
+            for (int k = 0; k < 4; ++k) sc[nt][k] = sb[nt][k] = 0.0f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint32_t x[4], s0, s1;
-        e2m1x8_to_half2(kw[b], x);
-        e4m3x4_to_half2(ks[b / 2], s0, s1);
-        const uint32_t sb = b & 1 ? s1 : s0, sg = low2(sb), sh = high2(sb);
-        x[0] = hmul2(x[0], sg);
-        x[1] = hmul2(x[1], sh);
-        x[2] = hmul2(x[2], sg);
-        x[3] = hmul2(x[3], sh);
+          for (int i = 0; i < NB / 4; ++i) {
+            const uint4 kw = *reinterpret_cast<const uint4*>(gp + i * 512 + lane * 16);
+            const uint2 ks = *reinterpret_cast<const uint2*>(gp + 8 * D + g * 2 * NB + i * 8);
+            uint32_t sg[4];
+            e4m3x4_to_half2(ks.x, sg[0], sg[1]);
+            e4m3x4_to_half2(ks.y, sg[2], sg[3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint2 q = s.q[nt][b][lane];
-          mma16816(sc[nt], x, q.x, q.y);
-        }
-      }
-      const bool masked = key0 < free_lo || key0 + 16 > free_hi;
-      bool raise = false;
+            for (int j = 0; j < 4; ++j) {
+              uint32_t x[4];
+              e2m1x8_to_half2(j == 0 ? kw.x : j == 1 ? kw.y : j == 2 ? kw.z : kw.w, x);
+              x[0] = hmul2_low(x[0], sg[j]);
+              x[1] = hmul2_high(x[1], sg[j]);
+              x[2] = hmul2_low(x[2], sg[j]);
+              x[3] = hmul2_high(x[3], sg[j]);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          sc[nt][k] *= f[nt][k & 1];
-          if (masked && !sees(view[nt][k & 1], key0 + g + (k >> 1) * 8)) sc[nt][k] = -INFINITY;
-          raise |= !(sc[nt][k] <= m[nt][k & 1] + kSlack);
-        }
-      }
-      if (__any_sync(~0u, raise)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float r[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = fmaxf(sc[nt][e], sc[nt][e + 2]);
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-            const float now = x > m[nt][e] + kSlack ? x - kBias : m[nt][e];
-            r[e] = ex2(m[nt][e] - now);
-            m[nt][e] = now;
-            l[nt][e] *= r[e];
+              for (int nt = 0; nt < NT; ++nt) {
+                uint2 w;
+                if constexpr (S::kQInRegs) w = q[nt][i * 4 + j];
+                else w = s_q[(nt * NB + i * 4 + j) * 32 + lane];
+                if (j & 1) mma16816(sb[nt], x, w.x, w.y);
+                else mma16816(sc[nt], x, w.x, w.y);
+              }
+            }
           }
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) o[nt][b][k] *= r[k & 1];
+            for (int k = 0; k < 4; ++k) sc[nt][k] = (sc[nt][k] + sb[nt][k]) * f[nt][k & 1];
+        }
+        if (key0 < free_lo || key0 + 16 > free_hi) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const RowView view = row_view(a, tile, tile.row0 + nt * 8 + 2 * t + e);
+              if (!sees(view, key0 + g)) sc[nt][e] = -INFINITY;
+              if (!sees(view, key0 + g + 8)) sc[nt][e + 2] = -INFINITY;
+            }
+        }
+        bool raise = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) raise |= !(fmaxf(sc[nt][e], sc[nt][e + 2]) <= m[nt][e] + kSlack);
+        if (__any_sync(~0u, raise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float r[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(sc[nt][e], sc[nt][e + 2]);
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+              const float now = x > m[nt][e] + kSlack ? x - kBias : m[nt][e];
+              r[e] = ex2(m[nt][e] - now);
+              m[nt][e] = now;
+              l[nt][e] *= r[e];
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[nt][b][k] *= r[k & 1];
+          }
+        }
+        uint32_t p[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            sc[nt][k] = ex2(sc[nt][k] - m[nt][k & 1]);
+            l[nt][k & 1] += sc[nt][k];
+          }
+          const __half2 p0 = __floats2half2_rn(sc[nt][0], sc[nt][1]), p1 = __floats2half2_rn(sc[nt][2], sc[nt][3]);
+          p[nt][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
+          p[nt][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
+        }
+        // what lies past the length may be anything: its scales become zero, so that 0 x NaN does not arise
+        uint32_t live = ~0u;
+        if (key0 + 16 > tile.len) {
+          live = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (key0 + 2 * t + (k & 1) + (k >> 1) * 8 < tile.len) live |= 0xFFu << (8 * k);
+        }
+#pragma unroll
+        for (int i = 0; i < NB / 4; ++i) {
+          const uint4 vw = *reinterpret_cast<const uint4*>(gp + 9 * D + i * 512 + lane * 16);
+          const uint4 vs = *reinterpret_cast<const uint4*>(gp + 17 * D + t * 4 * NB + i * 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x[4], s0, s1;
+            e2m1x8_to_half2(j == 0 ? vw.x : j == 1 ? vw.y : j == 2 ? vw.z : vw.w, x);
+            e4m3x4_to_half2((j == 0 ? vs.x : j == 1 ? vs.y : j == 2 ? vs.z : vs.w) & live, s0, s1);
+            x[0] = hmul2(x[0], s0);
+            x[1] = hmul2(x[1], s0);
+            x[2] = hmul2(x[2], s1);
+            x[3] = hmul2(x[3], s1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i * 4 + j], x, p[nt][0], p[nt][1]);
+          }
         }
       }
-      uint32_t p[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          sc[nt][k] = ex2(sc[nt][k] - m[nt][k & 1]);
-          l[nt][k & 1] += sc[nt][k];
-        }
-        const __half2 p0 = __floats2half2_rn(sc[nt][0], sc[nt][1]), p1 = __floats2half2_rn(sc[nt][2], sc[nt][3]);
-        p[nt][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
-        p[nt][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
-      }
-      // what lies past the length may be anything: its scales become zero, so that 0 x NaN does not arise
-      uint32_t live = ~0u;
-      if (key0 + 16 > tile.len) {
-        live = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (key0 + 2 * t + (k & 1) + (k >> 1) * 8 < tile.len) live |= 0xFFu << (8 * k);
-      }
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint32_t x[4], s0, s1;
-        e2m1x8_to_half2(vw[b], x);
-        e4m3x4_to_half2(vs[b] & live, s0, s1);
-        x[0] = hmul2(x[0], s0);
-        x[1] = hmul2(x[1], s0);
-        x[2] = hmul2(x[2], s1);
-        x[3] = hmul2(x[3], s1);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][b], x, p[nt][0], p[nt][1]);
+      __syncwarp();
+      fetch_one(c, sg, fetch, ring, bars);  // into the stage that has just been read
+      if (++stage == S::kStages) {
+        stage = 0;
+        phase ^= 1;
       }
     }
-    // the CTA's warps joined: one after the other they add their outputs, scaled to the common m
+    // the next segment's first copies come while this one is being joined
+    const long long next = head_at + u1;
+    if (u1 == tile.units && h == c.kv_heads - 1) {
+      item_at = next;
+      ++item;
+    }
+    if (next < end) enter(next);
+    // ---- the warps' parts joined
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -230,145 +373,174 @@ __global__ void __launch_bounds__(kThreads) attend_rows(Cache c, AttendArgs a) {
         l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], 4);
         l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], 8);
         l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], 16);
-        if (g == 0) {
-          s.m[warp][nt * 8 + 2 * t + e] = m[nt][e];
-          s.l[warp][nt * 8 + 2 * t + e] = l[nt][e];
+      }
+    named_sync<kConsumers>(1);  // red and s_m of the segment before have been read
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = nt * 8 + 2 * t + e;
+        if (row < tile.rows) {
+          if (g == 0) {
+            s_m[warp * ROWS + row] = m[nt][e];
+            s_l[warp * ROWS + row] = l[nt][e];
+          }
+          float* to = red + (warp * ROWS + row) * (D + 4) + 2 * g;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) *reinterpret_cast<float2*>(to + b * 16) = make_float2(o[nt][b][e], o[nt][b][e + 2]);
         }
       }
-    __syncthreads();
-    if (tid < ROWS) {
-      float mm = s.m[0][tid];
-      for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s.m[w][tid]);
-      float ll = 0.0f;
-      for (int w = 0; w < kWarps; ++w) ll += s.l[w][tid] * ex2(s.m[w][tid] - mm);
-      s.row_m[tid] = mm;
-      s.row_l[tid] = ll;
-    }
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) {
-      if (w == warp) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = nt * 8 + 2 * t + e;
-            const float r = ex2(m[nt][e] - s.row_m[row]);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              float2* to = reinterpret_cast<float2*>(&s.o[row][b * 16 + 2 * g]);
-              float2 v = make_float2(o[nt][b][e] * r, o[nt][b][e + 2] * r);
-              if (w) {
-                const float2 x = *to;
-                v.x += x.x;
-                v.y += x.y;
-              }
-              *to = v;
-            }
-          }
-      }
-      __syncthreads();
-    }
+    named_sync<kConsumers>(1);
     const long long head_end = head_at + tile.units;
     const bool whole = u0 == 0 && u1 == tile.units;
-    const int first_cta = whole ? 0 : range_owner(start, head_at), last_cta = whole ? 0 : range_owner(start, head_end - 1);
     constexpr int kPart = ROWS * (D + 2);
+    float* part = c.partial + (int64_t)(2 * blockIdx.x + (cur == begin ? 0 : 1)) * kPart;
+    const float gv = c.v_scale[h];
+    auto write_row = [&](int row, int col, float4 v, float mm, float ll) {
+      const int grow = tile.row0 + row;
+      const int64_t at = (int64_t)(tile.first + grow / a.group) * a.heads + h * a.group + grow % a.group;
+      const float r = ll != 0.0f ? gv / ll : 0.0f;
+      if (ll == 0.0f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + col) =
+          make_uint2(pack16(v.x * r, v.y * r, a.dtype), pack16(v.z * r, v.w * r, a.dtype));
+      if (a.lse && col == 0) a.lse[at] = ll == 0.0f ? -INFINITY : (mm + log2f(ll)) * kLn2;
+    };
+    for (int x = tid; x < tile.rows * (D / 4); x += kConsumers) {
+      const int row = x / (D / 4), col = x % (D / 4) * 4;
+      float mw[kWarps], mm = kNoKey, ll = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        mw[w] = s_m[w * ROWS + row];
+        mm = fmaxf(mm, mw[w]);
+      }
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float r = ex2(mw[w] - mm);
+        ll += s_l[w * ROWS + row] * r;
+        const float4 y = *reinterpret_cast<const float4*>(red + (w * ROWS + row) * (D + 4) + col);
+        v.x += y.x * r; v.y += y.y * r; v.z += y.z * r; v.w += y.w * r;
+      }
+      if (whole) {
+        write_row(row, col, v, mm, ll);
+      } else {
+        __stcg(reinterpret_cast<float4*>(part + 2 * ROWS + row * D + col), v);
+        if (col == 0) {
+          __stcg(part + row, mm);
+          __stcg(part + ROWS + row, ll);
+        }
+      }
+    }
     if (!whole) {
-      float* part = c.partial + (int64_t)(2 * blockIdx.x + (cur == begin ? 0 : 1)) * kPart;
-      for (int x = tid; x < tile.rows * (D / 4); x += kThreads) {
-        const int row = x / (D / 4), col = x % (D / 4) * 4;
-        __stcg(reinterpret_cast<float4*>(part + 2 * ROWS + row * D + col), *reinterpret_cast<const float4*>(&s.o[row][col]));
-      }
-      if (tid < tile.rows) {
-        __stcg(part + tid, s.row_m[tid]);
-        __stcg(part + ROWS + tid, s.row_l[tid]);
-      }
+      // ---- an item's parts joined, by the last CTA to get here
+      const int first_cta = range_owner(start, head_at), last_cta = range_owner(start, head_end - 1);
+      const int parts = last_cta - first_cta + 1;
       __threadfence();
-      __syncthreads();
+      named_sync<kConsumers>(1);
       if (tid == 0) {
-        const unsigned parts = last_cta - first_cta + 1;
         const unsigned done = atomicAdd(&c.counters[first_cta], 1u);
-        s.last = done + 1 == parts;
+        s.last = done + 1 == (unsigned)parts;
         if (s.last) c.counters[first_cta] = 0;
       }
-      __syncthreads();
-      __threadfence();
-    }
-    if (whole || s.last) {
-      const float gv = c.v_scale[h];
-      if (!whole) {
+      named_sync<kConsumers>(1);
+      if (s.last) {
+        __threadfence();
+        const int first_slot = 2 * first_cta + (range_begin(start, first_cta) == head_at ? 0 : 1);
+        auto part_at = [&](int k) { return c.partial + (int64_t)(k == 0 ? first_slot : 2 * (first_cta + k)) * kPart; };
+        // red as the parts' weights: [part][row], as many at a time as it holds
+        constexpr int kMost = kWarps * (D + 4) / 2;
+        constexpr int kPlaces = ROWS * (D / 4), kMine = (kPlaces + kConsumers - 1) / kConsumers;
+        // with fewer places than threads, several threads share a place's parts
+        constexpr int kShare = kPlaces >= kConsumers ? 1 : kConsumers / kPlaces;
+        static_assert(kShare == 1 || kShare * kPlaces == kConsumers, "");
+        float4 v[kMine];
+        float mm = kNoKey, ll = 0.0f;   // of row tid, if that is one
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = 0; k0 < parts; k0 += kMost) {
+          const int n = min(parts - k0, kMost);
+          float* wm = red;
+          float* wl = red + kMost * ROWS;
+          for (int x = tid; x < n * tile.rows; x += kConsumers) {
+            const int k = x / tile.rows, row = x % tile.rows;
+            const float* p = part_at(k0 + k);
+            wm[k * ROWS + row] = __ldcg(p + row);
+            wl[k * ROWS + row] = __ldcg(p + ROWS + row);
+          }
+          named_sync<kConsumers>(1);
+          if (tid < tile.rows) {
+            float now = mm;
+            for (int k = 0; k < n; ++k) now = fmaxf(now, wm[k * ROWS + tid]);
+            const float r = ex2(mm - now);
+            ll *= r;
+            for (int k = 0; k < n; ++k) {
+              const float w = ex2(wm[k * ROWS + tid] - now);
+              ll += wl[k * ROWS + tid] * w;
+              wm[k * ROWS + tid] = w;
+            }
+            mm = now;
+            s_c[tid] = r;
+          }
+          named_sync<kConsumers>(1);
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            const int x = tid / kShare + i * (kConsumers / kShare), row = x / (D / 4), col = x % (D / 4) * 4;
+            if (row < tile.rows) {
+              const float r = s_c[row];
+              v[i].x *= r; v[i].y *= r; v[i].z *= r; v[i].w *= r;
+#pragma unroll 8
+              for (int k = tid % kShare; k < n; k += kShare) {
+                const float w = wm[k * ROWS + row];
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(part_at(k0 + k) + 2 * ROWS + row * D + col));
+                v[i].x += y.x * w; v[i].y += y.y * w; v[i].z += y.z * w; v[i].w += y.w * w;
+              }
+            }
+          }
+          named_sync<kConsumers>(1);
+        }
         if (tid < tile.rows) {
-          float mm = kNoKey;
-          for (int k = first_cta; k <= last_cta; ++k) {
-            const bool in = k > first_cta || range_begin(start, k) == head_at;
-            mm = fmaxf(mm, __ldcg(c.partial + (int64_t)(2 * k + (in ? 0 : 1)) * kPart + tid));
-          }
-          float ll = 0.0f;
-          for (int k = first_cta; k <= last_cta; ++k) {
-            const bool in = k > first_cta || range_begin(start, k) == head_at;
-            const float* part = c.partial + (int64_t)(2 * k + (in ? 0 : 1)) * kPart;
-            ll += __ldcg(part + ROWS + tid) * ex2(__ldcg(part + tid) - mm);
-          }
-          s.row_m[tid] = mm;
-          s.row_l[tid] = ll;
+          s_m[tid] = mm;
+          s_l[tid] = ll;
         }
-        __syncthreads();
-      }
-      for (int x = tid; x < tile.rows * (D / 4); x += kThreads) {
-        const int row = x / (D / 4), col = x % (D / 4) * 4;
-        float4 v;
-        if (whole) {
-          v = *reinterpret_cast<const float4*>(&s.o[row][col]);
-        } else {
-          v = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float mm = s.row_m[row];
-          for (int k = first_cta; k <= last_cta; ++k) {
-            const bool in = k > first_cta || range_begin(start, k) == head_at;
-            const float* part = c.partial + (int64_t)(2 * k + (in ? 0 : 1)) * kPart;
-            const float r = ex2(__ldcg(part + row) - mm);
-            const float4 y = __ldcg(reinterpret_cast<const float4*>(part + 2 * ROWS + row * D + col));
-            v.x += y.x * r; v.y += y.y * r; v.z += y.z * r; v.w += y.w * r;
+        named_sync<kConsumers>(1);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int x = tid / kShare + i * (kConsumers / kShare), row = x / (D / 4), col = x % (D / 4) * 4;
+#pragma unroll
+          for (int o2 = 1; o2 < kShare; o2 <<= 1) {
+            v[i].x += __shfl_xor_sync(~0u, v[i].x, o2);
+            v[i].y += __shfl_xor_sync(~0u, v[i].y, o2);
+            v[i].z += __shfl_xor_sync(~0u, v[i].z, o2);
+            v[i].w += __shfl_xor_sync(~0u, v[i].w, o2);
           }
+          if (row < tile.rows && tid % kShare == 0) write_row(row, col, v[i], s_m[row], s_l[row]);
         }
-        const float ll = s.row_l[row];
-        const float r = ll != 0.0f ? gv / ll : 0.0f;
-        const int grow = tile.row0 + row;
-        const int64_t at = ((int64_t)(tile.first + grow / a.group) * a.heads + h * a.group + grow % a.group);
-        if (ll == 0.0f) v = make_float4(0.f, 0.f, 0.f, 0.f);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + col) =
-            make_uint2(pack16(v.x * r, v.y * r, a.dtype), pack16(v.z * r, v.w * r, a.dtype));
-        if (a.lse && col == 0) a.lse[at] = ll == 0.0f ? -INFINITY : (s.row_m[row] + log2f(ll)) * kLn2;
       }
     }
-    cur = head_at + u1;
-    if (u1 == tile.units && h == c.kv_heads - 1) {
-      item_at = cur;
-      ++item;
-    }
+    cur = next;
   }
 }
 
 template <int D, int NT>
 int launch_rows(const HostCache& h, AttendArgs a, int max_q) {
-  constexpr int ROWS = NT * 8;
-  constexpr int smem = sizeof(Smem<D, NT>);
-  static int per_sm = 0;
-  if (per_sm == 0) {
-    int n = 0;
-    if (cudaFuncSetAttribute(attend_rows<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attend_rows<D, NT>, kThreads, smem) != cudaSuccess || n < 1) {
+  using S = Shape<D, NT>;
+  constexpr int kUnit = S::kUnit;
+  static bool granted = false;
+  if (!granted) {
+    if (cudaFuncSetAttribute(attend_rows<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess) {
       (void)cudaGetLastError();
       return WHEAD_ERR_CUDA;
     }
-    per_sm = n;
+    granted = true;
   }
-  const int64_t tiles = ((int64_t)max_q * a.group + ROWS - 1) / ROWS;
+  const int64_t tiles = ((int64_t)max_q * a.group + S::kRows - 1) / S::kRows;
   if (tiles * a.n >= INT_MAX) return WHEAD_ERR_UNSUPPORTED;
   a.row_tiles = (int)tiles;
-  int64_t ctas = std::min<int64_t>((int64_t)h.sms * std::min(per_sm, 4), kMaxCtas);
-  ctas = std::min(ctas, h.c.partial_floats / (2 * ROWS * (D + 2)));
-  a.planned = tiles * a.n > 4 * kThreads;
-  if (a.planned) attend_plan<kUnit><<<1, 1024, 0, h.stream>>>(h.c, a, ROWS, (int)ctas);
-  attend_rows<D, NT><<<(unsigned)ctas, kThreads, smem, h.stream>>>(h.c, a);
+  int64_t ctas = std::min<int64_t>((int64_t)h.sms * S::kCtas, kMaxCtas);
+  ctas = std::min(ctas, h.c.partial_floats / (2 * S::kRows * (D + 2)));
+  a.planned = tiles * a.n > 4 * S::kThreads;
+  if (a.planned) attend_plan<kUnit><<<1, 1024, 0, h.stream>>>(h.c, a, S::kRows, (int)ctas);
+  attend_rows<D, NT><<<(unsigned)ctas, S::kThreads, S::kBytes, h.stream>>>(h.c, a);
   return launch_status();
 }
 
