@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 namespace whead_kv_impl {
 
@@ -27,6 +28,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
@@ -53,6 +60,7 @@ struct Shape {
   static constexpr int kFixed = (2048 + 2 * kWarps * kRows * 4 + kRows * 4 + kQ + kRed + 127) / 128 * 128;
   static constexpr int kRoom = (227 * 1024 / kCtas - 1024 * (kCtas - 1) - kFixed) / (kWarps * kGroup);
   static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
+  static constexpr int kTogether = kLoad <= 128 ? 2 : 1;  // groups worked on at once, for independent chains of products
   static constexpr int kBytes = kFixed + kStages * kWarps * kGroup;
   static_assert(kStages >= 2, "the rings need two stages");
 };
@@ -71,37 +79,36 @@ struct Segment {
   long long head_at;
 };
 
-// A warp's way through a segment's groups, its ring and the pages' numbers: lane l holds those of the next 32 units.
-template <int D, int NT>
+// A warp's way through a segment's groups and its ring. Lane 0 alone fetches; it has the next page's number one copy ahead.
 struct Fetch {
   const uint8_t* base;      // the pool at this KV head
   const int32_t* table;
   int next, end;            // units to fetch
-  int entries, entry0;
+  int key;                  // first key of the next group
+  int page;
   uint32_t slot;            // stage of the next group to fetch
 };
 
+__device__ __forceinline__ int page_of(const Cache& c, const int32_t* table, int key, int len) {
+  return key < len ? __ldg(table + (key >> c.page_shift)) : 0;
+}
+
 template <int D, int NT>
-__device__ __forceinline__ void fetch_one(const Cache& c, const Segment& sg, Fetch<D, NT>& f, uint32_t ring, uint32_t bars) {
+__device__ __forceinline__ void fetch_one(const Cache& c, int len, Fetch& f, uint32_t ring, uint32_t bars) {
   using S = Shape<D, NT>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (f.next >= f.end) return;
-  const int key0 = (sg.tile.unit0 + f.next) * S::kUnit + warp * 16;
-  if (f.next >= f.entry0 + 32) {
-    f.entry0 = f.next;
-    const int64_t key = key0 + (int64_t)lane * S::kUnit;
-    f.entries = key < sg.tile.len ? f.table[key >> c.page_shift] : 0;
-    if ((unsigned)f.entries >= (unsigned)c.num_pages) {
+  if ((threadIdx.x & 31) == 0) {
+    int page = f.page;
+    if ((unsigned)page >= (unsigned)c.num_pages) {
       set_status(c, WHEAD_ERR_INTERNAL);
-      f.entries = 0;
+      page = 0;
     }
-  }
-  const int page = __shfl_sync(~0u, f.entries, f.next - f.entry0);
-  if (lane == 0) {
-    const int in_page = (key0 & (c.page_size - 1)) >> 4;
-    const uint8_t* src = f.base + ((int64_t)page * c.kv_heads * (c.page_size >> 4) + in_page) * S::kGroup;
+    const int in_page = (f.key & (c.page_size - 1)) >> 4;
+    const uint8_t* src = f.base + (int64_t)page * (c.kv_heads * (c.page_size >> 4) * S::kGroup) + in_page * S::kGroup;
     mbar_expect(bars + f.slot * 8, S::kGroup);
     bulk_load(ring + f.slot * S::kGroup, src, S::kGroup, bars + f.slot * 8);
+    f.key = f.next + 1 < f.end ? f.key + S::kUnit : len;
+    f.page = page_of(c, f.table, f.key, len);
   }
   f.slot = f.slot + 1 == S::kStages ? 0 : f.slot + 1;
   ++f.next;
@@ -135,19 +142,26 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
   uint32_t stage = 0, phase = 0;
   bool dead = false;
   Segment sg;
-  Fetch<D, NT> fetch;
+  Fetch fetch;
   fetch.slot = 0;
 
-  // the segment that begins at unit `at`, and the first copies of this warp's groups
-  auto enter = [&](long long at) {
-    while (true) {
-      sg.tile = make_tile<kUnit>(c, a, item, ROWS);
-      if (sg.tile.units > 0) break;
-      ++item;
+  // the segment that begins at unit `at`, and the first copies of this warp's groups; `fresh`: not the next head of the same tile
+  auto enter = [&](long long at, bool fresh) {
+    if (fresh) {
+      while (true) {
+        sg.tile = make_tile<kUnit>(c, a, item, ROWS);
+        if (sg.tile.units > 0) break;
+        ++item;
+      }
+      const int past_item = (int)(at - item_at);
+      sg.h = past_item / sg.tile.units;
+      sg.u0 = past_item - sg.h * sg.tile.units;
+      sg.head_at = at - sg.u0;
+    } else {
+      ++sg.h;
+      sg.u0 = 0;
+      sg.head_at = at;
     }
-    sg.h = (int)((at - item_at) / sg.tile.units);
-    sg.head_at = item_at + (long long)sg.h * sg.tile.units;
-    sg.u0 = (int)(at - sg.head_at);
     sg.u1 = (int)min((long long)sg.tile.units, sg.u0 + (end - at));
     fetch.base = c.pool + (int64_t)sg.h * (c.page_size >> 4) * S::kGroup;
     fetch.table = c.tables + (int64_t)sg.tile.slot * c.max_pages;
@@ -155,11 +169,12 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
     // units whose group of this warp holds any key
     fetch.end = min(sg.u1, max((sg.tile.len - warp * 16 + kUnit - 1) / kUnit - sg.tile.unit0, sg.u0));
     if (dead) fetch.end = sg.u0;
-    fetch.entry0 = sg.u0 - 32;
+    fetch.key = (sg.tile.unit0 + sg.u0) * kUnit + warp * 16;
+    fetch.page = fetch.next < fetch.end ? page_of(c, fetch.table, fetch.key, sg.tile.len) : 0;
 #pragma unroll 1
-    for (int i = 0; i < S::kStages; ++i) fetch_one(c, sg, fetch, ring, bars);
+    for (int i = 0; i < S::kStages; ++i) fetch_one<D, NT>(c, sg.tile.len, fetch, ring, bars);
   };
-  if (cur < end) enter(cur);
+  if (cur < end) enter(cur, true);
 
   while (cur < end) {
     const Tile tile = sg.tile;
@@ -214,6 +229,12 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         f[nt][1] = s_c[nt * 8 + 2 * t + 1];
       }
     }
+    // a zero factor becomes one that leaves all scores at zero, so that a masked product can be one whose score is -inf
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (fabsf(f[nt][e]) < 1e-37f) f[nt][e] = 1e-37f;
     float o[NT][NB][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -229,142 +250,177 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
     const int t0 = tile.row0 / a.group, t1 = (tile.row0 + tile.rows - 1) / a.group, past = tile.len - tile.tokens;
     const int free_hi = a.tree ? min(past, past + t0 + 1) : a.causal ? min(past + t0 + 1, tile.len) : tile.len;
     const int free_lo = a.window ? max(past + t1 - a.window + 1, 0) : 0;
-#pragma unroll 1
-    for (int u = u0; u < live_end; ++u) {
-      const int key0 = (tile.unit0 + u) * kUnit + warp * 16;
+    // G groups at a time, in the next G stages: key0[] their first keys
+    auto work = [&](auto count, const uint8_t* const (&gp)[2], const int (&key0)[2]) {
+      constexpr int G = decltype(count)::value;
+      float sc[G][NT][4];
+#pragma unroll
+      for (int i = 0; i < NB / 4; ++i) {
+#pragma unroll
+        for (int w = 0; w < G; ++w) {
+          const uint4 kw = *reinterpret_cast<const uint4*>(gp[w] + i * 512 + lane * 16);
+          const uint2 ks = *reinterpret_cast<const uint2*>(gp[w] + 8 * D + g * 2 * NB + i * 8);
+          uint32_t sg4[4];
+          e4m3x4_to_half2(ks.x, sg4[0], sg4[1]);
+          e4m3x4_to_half2(ks.y, sg4[2], sg4[3]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x[4];
+            e2m1x8_to_half2(j == 0 ? kw.x : j == 1 ? kw.y : j == 2 ? kw.z : kw.w, x);
+            x[0] = hmul2_low(x[0], sg4[j]);
+            x[1] = hmul2_high(x[1], sg4[j]);
+            x[2] = hmul2_low(x[2], sg4[j]);
+            x[3] = hmul2_high(x[3], sg4[j]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              uint2 y;
+              if constexpr (S::kQInRegs) y = q[nt][i * 4 + j];
+              else y = s_q[(nt * NB + i * 4 + j) * 32 + lane];
+              if (i == 0 && j == 0) mma16816_first(sc[w][nt], x, y.x, y.y);
+              else mma16816(sc[w][nt], x, y.x, y.y);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < G; ++w) {
+        if (key0[w] < free_lo || key0[w] + 16 > free_hi) {
+          // what no row sees of the last group may be anything: its values' scales become zero, so that 0 x NaN does not arise
+          if (key0[w] + 16 > tile.len) {
+            uint8_t* vs = const_cast<uint8_t*>(gp[w]) + 17 * D;
+            for (int k = lane; k < 16; k += 32)
+              if (key0[w] + k >= tile.len)
+                for (int b = 0; b < NB; ++b) vs[(k & 7) / 2 * 4 * NB + b * 4 + (k >> 3) * 2 + (k & 1)] = 0;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
+            __syncwarp();
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const RowView view = row_view(a, tile, tile.row0 + nt * 8 + 2 * t + e);
+              // a masked product becomes the one whose score is -inf
+              if (!sees(view, key0[w] + g)) sc[w][nt][e] = -copysignf(INFINITY, f[nt][e]);
+              if (!sees(view, key0[w] + g + 8)) sc[w][nt][e + 2] = -copysignf(INFINITY, f[nt][e]);
+            }
+        }
+      }
+      float d[G][NT][4], top = -INFINITY;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int w = 0; w < G; ++w)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            d[w][nt][k] = fmaf(sc[w][nt][k], f[nt][k & 1], -m[nt][k & 1]);
+            top = fmaxf(top, d[w][nt][k]);
+          }
+      if (__any_sync(~0u, top > kSlack)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float r[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < G; ++w) x = fmaxf(x, fmaxf(sc[w][nt][e] * f[nt][e], sc[w][nt][e + 2] * f[nt][e]));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+            const float now = x > m[nt][e] + kSlack ? x - kBias : m[nt][e];
+            r[e] = ex2(m[nt][e] - now);
+            m[nt][e] = now;
+            l[nt][e] *= r[e];
+#pragma unroll
+            for (int w = 0; w < G; ++w) {
+              d[w][nt][e] = fmaf(sc[w][nt][e], f[nt][e], -now);
+              d[w][nt][e + 2] = fmaf(sc[w][nt][e + 2], f[nt][e], -now);
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[nt][b][k] *= r[k & 1];
+        }
+      }
+      uint32_t p[G][NT][2];
+#pragma unroll
+      for (int w = 0; w < G; ++w)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            d[w][nt][k] = ex2(d[w][nt][k]);
+            l[nt][k & 1] += d[w][nt][k];
+          }
+          const __half2 p0 = __floats2half2_rn(d[w][nt][0], d[w][nt][1]), p1 = __floats2half2_rn(d[w][nt][2], d[w][nt][3]);
+          p[w][nt][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
+          p[w][nt][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
+        }
+#pragma unroll
+      for (int w = 0; w < G; ++w)
+#pragma unroll
+        for (int i = 0; i < NB / 4; ++i) {
+          const uint4 vw = *reinterpret_cast<const uint4*>(gp[w] + 9 * D + i * 512 + lane * 16);
+          const uint4 vs = *reinterpret_cast<const uint4*>(gp[w] + 17 * D + t * 4 * NB + i * 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x[4], s0, s1;
+            e2m1x8_to_half2(j == 0 ? vw.x : j == 1 ? vw.y : j == 2 ? vw.z : vw.w, x);
+            e4m3x4_to_half2(j == 0 ? vs.x : j == 1 ? vs.y : j == 2 ? vs.z : vs.w, s0, s1);
+            x[0] = hmul2(x[0], s0);
+            x[1] = hmul2(x[1], s0);
+            x[2] = hmul2(x[2], s1);
+            x[3] = hmul2(x[3], s1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i * 4 + j], x, p[w][nt][0], p[w][nt][1]);
+          }
+        }
+      __syncwarp();
+    };
+    // the next stage's group, once its copy is there
+    auto arrived = [&](int u) -> const uint8_t* {
       // a copy that does not come is reported; nothing more is fetched, and what is under way is still waited for
       if (!__all_sync(~0u, mbar_wait(bars + stage * 8, phase))) {
         set_status(c, WHEAD_ERR_TIMEOUT);
         dead = true;
         fetch.end = live_end = fetch.next;
       }
-      {
-        const uint8_t* gp = my_ring + stage * S::kGroup;
-        float sc[NT][4];
-        {
-          float sb[NT][4];  // odd blocks: two chains of products instead of one
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) sc[nt][k] = sb[nt][k] = 0.0f;
-#pragma unroll
-          for (int i = 0; i < NB / 4; ++i) {
-            const uint4 kw = *reinterpret_cast<const uint4*>(gp + i * 512 + lane * 16);
-            const uint2 ks = *reinterpret_cast<const uint2*>(gp + 8 * D + g * 2 * NB + i * 8);
-            uint32_t sg[4];
-            e4m3x4_to_half2(ks.x, sg[0], sg[1]);
-            e4m3x4_to_half2(ks.y, sg[2], sg[3]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t x[4];
-              e2m1x8_to_half2(j == 0 ? kw.x : j == 1 ? kw.y : j == 2 ? kw.z : kw.w, x);
-              x[0] = hmul2_low(x[0], sg[j]);
-              x[1] = hmul2_high(x[1], sg[j]);
-              x[2] = hmul2_low(x[2], sg[j]);
-              x[3] = hmul2_high(x[3], sg[j]);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                uint2 w;
-                if constexpr (S::kQInRegs) w = q[nt][i * 4 + j];
-                else w = s_q[(nt * NB + i * 4 + j) * 32 + lane];
-                if (j & 1) mma16816(sb[nt], x, w.x, w.y);
-                else mma16816(sc[nt], x, w.x, w.y);
-              }
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) sc[nt][k] = (sc[nt][k] + sb[nt][k]) * f[nt][k & 1];
-        }
-        if (key0 < free_lo || key0 + 16 > free_hi) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const RowView view = row_view(a, tile, tile.row0 + nt * 8 + 2 * t + e);
-              if (!sees(view, key0 + g)) sc[nt][e] = -INFINITY;
-              if (!sees(view, key0 + g + 8)) sc[nt][e + 2] = -INFINITY;
-            }
-        }
-        bool raise = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) raise |= !(fmaxf(sc[nt][e], sc[nt][e + 2]) <= m[nt][e] + kSlack);
-        if (__any_sync(~0u, raise)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float r[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(sc[nt][e], sc[nt][e + 2]);
-              x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-              const float now = x > m[nt][e] + kSlack ? x - kBias : m[nt][e];
-              r[e] = ex2(m[nt][e] - now);
-              m[nt][e] = now;
-              l[nt][e] *= r[e];
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[nt][b][k] *= r[k & 1];
-          }
-        }
-        uint32_t p[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            sc[nt][k] = ex2(sc[nt][k] - m[nt][k & 1]);
-            l[nt][k & 1] += sc[nt][k];
-          }
-          const __half2 p0 = __floats2half2_rn(sc[nt][0], sc[nt][1]), p1 = __floats2half2_rn(sc[nt][2], sc[nt][3]);
-          p[nt][0] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
-          p[nt][1] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
-        }
-        // what lies past the length may be anything: its scales become zero, so that 0 x NaN does not arise
-        uint32_t live = ~0u;
-        if (key0 + 16 > tile.len) {
-          live = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (key0 + 2 * t + (k & 1) + (k >> 1) * 8 < tile.len) live |= 0xFFu << (8 * k);
-        }
-#pragma unroll
-        for (int i = 0; i < NB / 4; ++i) {
-          const uint4 vw = *reinterpret_cast<const uint4*>(gp + 9 * D + i * 512 + lane * 16);
-          const uint4 vs = *reinterpret_cast<const uint4*>(gp + 17 * D + t * 4 * NB + i * 16);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t x[4], s0, s1;
-            e2m1x8_to_half2(j == 0 ? vw.x : j == 1 ? vw.y : j == 2 ? vw.z : vw.w, x);
-            e4m3x4_to_half2((j == 0 ? vs.x : j == 1 ? vs.y : j == 2 ? vs.z : vs.w) & live, s0, s1);
-            x[0] = hmul2(x[0], s0);
-            x[1] = hmul2(x[1], s0);
-            x[2] = hmul2(x[2], s1);
-            x[3] = hmul2(x[3], s1);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i * 4 + j], x, p[nt][0], p[nt][1]);
-          }
-        }
-      }
-      __syncwarp();
-      fetch_one(c, sg, fetch, ring, bars);  // into the stage that has just been read
+      const uint8_t* gp = my_ring + stage * S::kGroup;
       if (++stage == S::kStages) {
         stage = 0;
         phase ^= 1;
       }
+      return gp;
+    };
+    int u = u0;
+#pragma unroll 1
+    for (; u + S::kTogether <= live_end; u += S::kTogether) {
+      const uint8_t* gp[2];
+      int key0[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        gp[w] = w < S::kTogether ? arrived(u + w) : nullptr;
+        key0[w] = (tile.unit0 + u + w) * kUnit + warp * 16;
+      }
+      work(std::integral_constant<int, S::kTogether>{}, gp, key0);
+#pragma unroll
+      for (int w = 0; w < S::kTogether; ++w) fetch_one<D, NT>(c, sg.tile.len, fetch, ring, bars);  // into the stages just read
+    }
+    if (S::kTogether == 2 && u < live_end) {
+      const uint8_t* const gp[2] = {arrived(u), nullptr};
+      const int key0[2] = {(tile.unit0 + u) * kUnit + warp * 16, 0};
+      work(std::integral_constant<int, 1>{}, gp, key0);
+      fetch_one<D, NT>(c, sg.tile.len, fetch, ring, bars);
     }
     // the next segment's first copies come while this one is being joined
     const long long next = head_at + u1;
-    if (u1 == tile.units && h == c.kv_heads - 1) {
+    const bool item_done = u1 == tile.units && h == c.kv_heads - 1;
+    if (item_done) {
       item_at = next;
       ++item;
     }
-    if (next < end) enter(next);
+    if (next < end) enter(next, item_done);
     // ---- the warps' parts joined
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
