@@ -42,35 +42,38 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return r;
 }
 
-// What one CTA needs for D channels and 8 NT rows. Every warp has a ring of its own, of one group (16 keys of one KV head) a
-// stage; red holds the warps' outputs while they are joined (rows 4 floats apart beyond D: a warp's stores then hit
-// every bank once).
+// What one CTA needs for D channels and 8 NT rows. Every warp has a ring of its own, with one or two groups (16 keys of one
+// KV head each) a stage; red holds two warps' outputs while they are joined (rows 4 floats apart beyond D: a warp's stores
+// then hit every bank once).
 template <int D, int NT>
 struct Shape {
   static constexpr int kRows = NT * 8;
+  static constexpr int kHead = 512;
   static constexpr int kLoad = NT * D;  // a lane's output registers are a quarter of this
-  static constexpr int kCtas = kLoad <= 128 ? 2 : 1;
-  static constexpr int kWarps = kLoad == 256 ? 12 : 8;
+  static constexpr int kWarps = 4;
+  static constexpr int kCtas = kLoad <= 128 ? 4 : kLoad == 256 ? 3 : 2;  // of an SM, by registers
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kUnit = kWarps * 16;
+  static constexpr int kGroups = D == 256 ? 1 : 2;  // of a stage
+  static constexpr int kKeys = kGroups * 16;
+  static constexpr int kUnit = kWarps * kKeys;
   static constexpr bool kQInRegs = kLoad <= 128;
-  static constexpr int kGroup = 18 * D;
-  static constexpr int kRed = kWarps * kRows * (D + 4) * 4;
+  static constexpr int kGroup = 18 * D, kStage = kGroups * kGroup;
+  static constexpr int kRed = 2 * kRows * (D + 4) * 4;
   static constexpr int kQ = kQInRegs ? 0 : NT * (D / 16) * 32 * 8;
-  static constexpr int kFixed = (2048 + 2 * kWarps * kRows * 4 + kRows * 4 + kQ + kRed + 127) / 128 * 128;
-  static constexpr int kRoom = (227 * 1024 / kCtas - 1024 * (kCtas - 1) - kFixed) / (kWarps * kGroup);
-  static constexpr int kStages = kRoom > 8 ? 8 : kRoom;
-  static constexpr int kTogether = kLoad <= 128 ? 2 : 1;  // groups worked on at once, for independent chains of products
-  static constexpr int kBytes = kFixed + kStages * kWarps * kGroup;
+  static constexpr int kFixed = (kHead + 2 * kWarps * kRows * 4 + kRows * 4 + kQ + kRed + 127) / 128 * 128;
+  static constexpr int kRoom = (228 * 1024 / kCtas - 1024 - kFixed) / (kWarps * kStage);
+  static constexpr int kStages = kRoom > 4 ? 4 : kRoom;
+  static constexpr bool kTogether = kLoad <= 128 && kGroups == 2;  // a stage's groups worked on at once, for independent chains of products
+  static constexpr int kBytes = kFixed + kStages * kWarps * kStage;
   static_assert(kStages >= 2, "the rings need two stages");
 };
 
 struct Head {  // the fixed head of shared memory
-  unsigned long long full[12][8];
   SchedShared sched;
+  unsigned long long full[4][4];
   int last;
 };
-static_assert(sizeof(Head) <= 2048, "");
+static_assert(sizeof(Head) <= 512, "");
 
 // A CTA's piece of one item: units u0 .. u1 - 1 of one (tile, KV head).
 struct Segment {
@@ -79,18 +82,22 @@ struct Segment {
   long long head_at;
 };
 
-// A warp's way through a segment's groups and its ring. Lane 0 alone fetches; it has the next page's number one copy ahead.
+// A warp's way through a segment's groups and its ring. Lane 0 alone fetches; it has the next pages' numbers one copy ahead.
 struct Fetch {
   const uint8_t* base;      // the pool at this KV head
   const int32_t* table;
   int next, end;            // units to fetch
-  int key;                  // first key of the next group
-  int page;
-  uint32_t slot;            // stage of the next group to fetch
+  int key;                  // first key of the next stage
+  int page, page1;          // its groups' pages (page1: where a page is one group)
+  uint32_t slot;            // the next stage
 };
 
 __device__ __forceinline__ int page_of(const Cache& c, const int32_t* table, int key, int len) {
-  return key < len ? __ldg(table + (key >> c.page_shift)) : 0;
+  if (key >= len) return 0;
+  const int page = __ldg(table + (key >> c.page_shift));
+  if ((unsigned)page < (unsigned)c.num_pages) return page;
+  set_status(c, WHEAD_ERR_INTERNAL);
+  return 0;
 }
 
 template <int D, int NT>
@@ -98,17 +105,20 @@ __device__ __forceinline__ void fetch_one(const Cache& c, int len, Fetch& f, uin
   using S = Shape<D, NT>;
   if (f.next >= f.end) return;
   if ((threadIdx.x & 31) == 0) {
-    int page = f.page;
-    if ((unsigned)page >= (unsigned)c.num_pages) {
-      set_status(c, WHEAD_ERR_INTERNAL);
-      page = 0;
+    const uint32_t bar = bars + f.slot * 8, dst = ring + f.slot * S::kStage;
+    const int64_t page_bytes = (int64_t)c.kv_heads * (c.page_size >> 4) * S::kGroup;
+    const uint8_t* src = f.base + f.page * page_bytes + ((f.key & (c.page_size - 1)) >> 4) * S::kGroup;
+    const uint32_t bytes = S::kGroups == 2 && f.key + 16 < len ? 2 * S::kGroup : S::kGroup;  // a second group that holds no key stays out
+    mbar_expect(bar, bytes);
+    if (c.page_size > 16) {
+      bulk_load(dst, src, bytes, bar);
+    } else {
+      bulk_load(dst, src, S::kGroup, bar);
+      if (bytes > S::kGroup) bulk_load(dst + S::kGroup, f.base + f.page1 * page_bytes, S::kGroup, bar);
     }
-    const int in_page = (f.key & (c.page_size - 1)) >> 4;
-    const uint8_t* src = f.base + (int64_t)page * (c.kv_heads * (c.page_size >> 4) * S::kGroup) + in_page * S::kGroup;
-    mbar_expect(bars + f.slot * 8, S::kGroup);
-    bulk_load(ring + f.slot * S::kGroup, src, S::kGroup, bars + f.slot * 8);
     f.key = f.next + 1 < f.end ? f.key + S::kUnit : len;
     f.page = page_of(c, f.table, f.key, len);
+    if (S::kGroups == 2 && c.page_size == 16) f.page1 = page_of(c, f.table, min(f.key, len - 16) + 16, len);
   }
   f.slot = f.slot + 1 == S::kStages ? 0 : f.slot + 1;
   ++f.next;
@@ -120,13 +130,13 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
   constexpr int NB = D / 16, ROWS = S::kRows, kWarps = S::kWarps, kConsumers = S::kThreads, kUnit = S::kUnit;
   extern __shared__ __align__(128) uint8_t smem[];
   Head& s = *reinterpret_cast<Head*>(smem);
-  float* s_m = reinterpret_cast<float*>(smem + 2048);       // [warp][row]
+  float* s_m = reinterpret_cast<float*>(smem + S::kHead);       // [warp][row]
   float* s_l = s_m + kWarps * ROWS;
   float* s_c = s_l + kWarps * ROWS;                          // a row's factor from sums of products to scores in log2 units
   uint2* s_q = reinterpret_cast<uint2*>(s_c + ROWS);         // query rows as operands: [8-row tile][16 channels][lane]
-  float* red = reinterpret_cast<float*>(smem + 2048 + 2 * kWarps * ROWS * 4 + ROWS * 4 + S::kQ);  // [warp][row][D + 4]
+  float* red = reinterpret_cast<float*>(smem + S::kHead + 2 * kWarps * ROWS * 4 + ROWS * 4 + S::kQ);  // [2][row][D + 4]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const uint8_t* my_ring = smem + S::kFixed + warp * S::kStages * S::kGroup;
+  const uint8_t* my_ring = smem + S::kFixed + warp * S::kStages * S::kStage;
   const uint32_t ring = smem_u32(my_ring), bars = smem_u32(&s.full[warp][0]);
   if (lane == 0) {
     for (int i = 0; i < S::kStages; ++i) mbar_init(bars + i * 8, 1);
@@ -166,11 +176,15 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
     fetch.base = c.pool + (int64_t)sg.h * (c.page_size >> 4) * S::kGroup;
     fetch.table = c.tables + (int64_t)sg.tile.slot * c.max_pages;
     fetch.next = sg.u0;
-    // units whose group of this warp holds any key
-    fetch.end = min(sg.u1, max((sg.tile.len - warp * 16 + kUnit - 1) / kUnit - sg.tile.unit0, sg.u0));
+    // units in which this warp has any key
+    fetch.end = min(sg.u1, max((sg.tile.len - warp * S::kKeys + kUnit - 1) / kUnit - sg.tile.unit0, sg.u0));
     if (dead) fetch.end = sg.u0;
-    fetch.key = (sg.tile.unit0 + sg.u0) * kUnit + warp * 16;
-    fetch.page = fetch.next < fetch.end ? page_of(c, fetch.table, fetch.key, sg.tile.len) : 0;
+    fetch.key = (sg.tile.unit0 + sg.u0) * kUnit + warp * S::kKeys;
+    fetch.page = fetch.page1 = 0;
+    if (fetch.next < fetch.end) {
+      fetch.page = page_of(c, fetch.table, fetch.key, sg.tile.len);
+      if (S::kGroups == 2 && c.page_size == 16) fetch.page1 = page_of(c, fetch.table, fetch.key + 16, sg.tile.len);
+    }
 #pragma unroll 1
     for (int i = 0; i < S::kStages; ++i) fetch_one<D, NT>(c, sg.tile.len, fetch, ring, bars);
   };
@@ -250,16 +264,16 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
     const int t0 = tile.row0 / a.group, t1 = (tile.row0 + tile.rows - 1) / a.group, past = tile.len - tile.tokens;
     const int free_hi = a.tree ? min(past, past + t0 + 1) : a.causal ? min(past + t0 + 1, tile.len) : tile.len;
     const int free_lo = a.window ? max(past + t1 - a.window + 1, 0) : 0;
-    // G groups at a time, in the next G stages: key0[] their first keys
-    auto work = [&](auto count, const uint8_t* const (&gp)[2], const int (&key0)[2]) {
+    // G neighbouring groups at a time, from key0 on
+    auto work = [&](auto count, const uint8_t* gp, int key0) {
       constexpr int G = decltype(count)::value;
       float sc[G][NT][4];
 #pragma unroll
       for (int i = 0; i < NB / 4; ++i) {
 #pragma unroll
         for (int w = 0; w < G; ++w) {
-          const uint4 kw = *reinterpret_cast<const uint4*>(gp[w] + i * 512 + lane * 16);
-          const uint2 ks = *reinterpret_cast<const uint2*>(gp[w] + 8 * D + g * 2 * NB + i * 8);
+          const uint4 kw = *reinterpret_cast<const uint4*>(gp + w * S::kGroup + i * 512 + lane * 16);
+          const uint2 ks = *reinterpret_cast<const uint2*>(gp + w * S::kGroup + 8 * D + g * 2 * NB + i * 8);
           uint32_t sg4[4];
           e4m3x4_to_half2(ks.x, sg4[0], sg4[1]);
           e4m3x4_to_half2(ks.y, sg4[2], sg4[3]);
@@ -284,12 +298,12 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
       }
 #pragma unroll
       for (int w = 0; w < G; ++w) {
-        if (key0[w] < free_lo || key0[w] + 16 > free_hi) {
+        if (key0 + w * 16 < free_lo || key0 + w * 16 + 16 > free_hi) {
           // what no row sees of the last group may be anything: its values' scales become zero, so that 0 x NaN does not arise
-          if (key0[w] + 16 > tile.len) {
-            uint8_t* vs = const_cast<uint8_t*>(gp[w]) + 17 * D;
+          if (key0 + w * 16 + 16 > tile.len) {
+            uint8_t* vs = const_cast<uint8_t*>(gp + w * S::kGroup) + 17 * D;
             for (int k = lane; k < 16; k += 32)
-              if (key0[w] + k >= tile.len)
+              if (key0 + w * 16 + k >= tile.len)
                 for (int b = 0; b < NB; ++b) vs[(k & 7) / 2 * 4 * NB + b * 4 + (k >> 3) * 2 + (k & 1)] = 0;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the stage's next copy
             __syncwarp();
@@ -300,8 +314,8 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
             for (int e = 0; e < 2; ++e) {
               const RowView view = row_view(a, tile, tile.row0 + nt * 8 + 2 * t + e);
               // a masked product becomes the one whose score is -inf
-              if (!sees(view, key0[w] + g)) sc[w][nt][e] = -copysignf(INFINITY, f[nt][e]);
-              if (!sees(view, key0[w] + g + 8)) sc[w][nt][e + 2] = -copysignf(INFINITY, f[nt][e]);
+              if (!sees(view, key0 + w * 16 + g)) sc[w][nt][e] = -copysignf(INFINITY, f[nt][e]);
+              if (!sees(view, key0 + w * 16 + g + 8)) sc[w][nt][e + 2] = -copysignf(INFINITY, f[nt][e]);
             }
         }
       }
@@ -361,8 +375,8 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
       for (int w = 0; w < G; ++w)
 #pragma unroll
         for (int i = 0; i < NB / 4; ++i) {
-          const uint4 vw = *reinterpret_cast<const uint4*>(gp[w] + 9 * D + i * 512 + lane * 16);
-          const uint4 vs = *reinterpret_cast<const uint4*>(gp[w] + 17 * D + t * 4 * NB + i * 16);
+          const uint4 vw = *reinterpret_cast<const uint4*>(gp + w * S::kGroup + 9 * D + i * 512 + lane * 16);
+          const uint4 vs = *reinterpret_cast<const uint4*>(gp + w * S::kGroup + 17 * D + t * 4 * NB + i * 16);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t x[4], s0, s1;
@@ -376,42 +390,29 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
             for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i * 4 + j], x, p[w][nt][0], p[w][nt][1]);
           }
         }
-      __syncwarp();
     };
-    // the next stage's group, once its copy is there
-    auto arrived = [&](int u) -> const uint8_t* {
+#pragma unroll 1
+    for (int u = u0; u < live_end; ++u) {
+      const int key0 = (tile.unit0 + u) * kUnit + warp * S::kKeys;
       // a copy that does not come is reported; nothing more is fetched, and what is under way is still waited for
       if (!__all_sync(~0u, mbar_wait(bars + stage * 8, phase))) {
         set_status(c, WHEAD_ERR_TIMEOUT);
         dead = true;
         fetch.end = live_end = fetch.next;
       }
-      const uint8_t* gp = my_ring + stage * S::kGroup;
+      const uint8_t* gp = my_ring + stage * S::kStage;
+      if (S::kTogether && key0 + 16 < tile.len) {
+        work(std::integral_constant<int, 2>{}, gp, key0);
+      } else {
+        work(std::integral_constant<int, 1>{}, gp, key0);
+        if (!S::kTogether && S::kGroups == 2 && key0 + 16 < tile.len) work(std::integral_constant<int, 1>{}, gp + S::kGroup, key0 + 16);
+      }
+      __syncwarp();
+      fetch_one<D, NT>(c, sg.tile.len, fetch, ring, bars);  // into the stage that has just been read
       if (++stage == S::kStages) {
         stage = 0;
         phase ^= 1;
       }
-      return gp;
-    };
-    int u = u0;
-#pragma unroll 1
-    for (; u + S::kTogether <= live_end; u += S::kTogether) {
-      const uint8_t* gp[2];
-      int key0[2];
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        gp[w] = w < S::kTogether ? arrived(u + w) : nullptr;
-        key0[w] = (tile.unit0 + u + w) * kUnit + warp * 16;
-      }
-      work(std::integral_constant<int, S::kTogether>{}, gp, key0);
-#pragma unroll
-      for (int w = 0; w < S::kTogether; ++w) fetch_one<D, NT>(c, sg.tile.len, fetch, ring, bars);  // into the stages just read
-    }
-    if (S::kTogether == 2 && u < live_end) {
-      const uint8_t* const gp[2] = {arrived(u), nullptr};
-      const int key0[2] = {(tile.unit0 + u) * kUnit + warp * 16, 0};
-      work(std::integral_constant<int, 1>{}, gp, key0);
-      fetch_one<D, NT>(c, sg.tile.len, fetch, ring, bars);
     }
     // the next segment's first copies come while this one is being joined
     const long long next = head_at + u1;
@@ -431,6 +432,8 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         l[nt][e] += __shfl_xor_sync(~0u, l[nt][e], 16);
       }
     named_sync<kConsumers>(1);  // red and s_m of the segment before have been read
+    const bool lower = warp < kWarps / 2;  // these add the others' outputs to their own
+    auto red_at = [&](int row) { return red + ((warp & 1) * ROWS + row) * (D + 4) + 2 * g; };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -441,11 +444,32 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
             s_m[warp * ROWS + row] = m[nt][e];
             s_l[warp * ROWS + row] = l[nt][e];
           }
-          float* to = red + (warp * ROWS + row) * (D + 4) + 2 * g;
+          if (!lower) {
 #pragma unroll
-          for (int b = 0; b < NB; ++b) *reinterpret_cast<float2*>(to + b * 16) = make_float2(o[nt][b][e], o[nt][b][e + 2]);
+            for (int b = 0; b < NB; ++b) *reinterpret_cast<float2*>(red_at(row) + b * 16) = make_float2(o[nt][b][e], o[nt][b][e + 2]);
+          }
         }
       }
+    named_sync<kConsumers>(1);
+    if (lower) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int row = nt * 8 + 2 * t + e;
+          if (row < tile.rows) {
+            const float other = s_m[(warp + 2) * ROWS + row];
+            const float mm = fmaxf(fmaxf(m[nt][e], other), fmaxf(s_m[(warp ^ 1) * ROWS + row], s_m[((warp ^ 1) + 2) * ROWS + row]));
+            const float r0 = ex2(m[nt][e] - mm), r1 = ex2(other - mm);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              float2* at = reinterpret_cast<float2*>(red_at(row) + b * 16);
+              const float2 y = *at;
+              *at = make_float2(o[nt][b][e] * r0 + y.x * r1, o[nt][b][e + 2] * r0 + y.y * r1);
+            }
+          }
+        }
+    }
     named_sync<kConsumers>(1);
     const long long head_end = head_at + tile.units;
     const bool whole = u0 == 0 && u1 == tile.units;
@@ -463,20 +487,14 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
     };
     for (int x = tid; x < tile.rows * (D / 4); x += kConsumers) {
       const int row = x / (D / 4), col = x % (D / 4) * 4;
-      float mw[kWarps], mm = kNoKey, ll = 0.0f;
+      float mm = kNoKey, ll = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        mw[w] = s_m[w * ROWS + row];
-        mm = fmaxf(mm, mw[w]);
-      }
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w * ROWS + row]);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float r = ex2(mw[w] - mm);
-        ll += s_l[w * ROWS + row] * r;
-        const float4 y = *reinterpret_cast<const float4*>(red + (w * ROWS + row) * (D + 4) + col);
-        v.x += y.x * r; v.y += y.y * r; v.z += y.z * r; v.w += y.w * r;
-      }
+      for (int w = 0; w < kWarps; ++w) ll += s_l[w * ROWS + row] * ex2(s_m[w * ROWS + row] - mm);
+      float4 v = *reinterpret_cast<const float4*>(red + row * (D + 4) + col);
+      const float4 y = *reinterpret_cast<const float4*>(red + (ROWS + row) * (D + 4) + col);
+      v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
       if (whole) {
         write_row(row, col, v, mm, ll);
       } else {
@@ -504,7 +522,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         const int first_slot = 2 * first_cta + (range_begin(start, first_cta) == head_at ? 0 : 1);
         auto part_at = [&](int k) { return c.partial + (int64_t)(k == 0 ? first_slot : 2 * (first_cta + k)) * kPart; };
         // red as the parts' weights: [part][row], as many at a time as it holds
-        constexpr int kMost = kWarps * (D + 4) / 2;
+        constexpr int kMost = D + 4;
         constexpr int kPlaces = ROWS * (D / 4), kMine = (kPlaces + kConsumers - 1) / kConsumers;
         // with fewer places than threads, several threads share a place's parts
         constexpr int kShare = kPlaces >= kConsumers ? 1 : kConsumers / kPlaces;
