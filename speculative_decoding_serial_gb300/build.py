@@ -13,7 +13,7 @@ LIB = os.path.join(BUILD, "libwhead.so")
 # copied a step ahead), the 4-bit KV cache's calls; compiled in parallel
 SOURCES = [os.path.join(CSRC, n) for n in ("whead_api.cu", "walk_resident.cu", "walk_resident_rec.cu",
                                            "walk_async.cu", "walk_async_rec.cu",
-                                           "kv_cache.cu", "kv_attend.cu")]
+                                           "kv_cache.cu", "kv_attend.cu", "kv_attend_tiles.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("walk_kernel.cuh", "walk_launch.cuh", "walk_launch.h",
                                                       "kv_common.cuh", "kv_schedule.cuh")] + [
     os.path.join(ROOT, "include", n) for n in ("whead.h", "whead_kv.h")]

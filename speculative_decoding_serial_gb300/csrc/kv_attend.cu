@@ -643,6 +643,7 @@ extern "C" int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* x
   AttendArgs a{x->q, x->out, x->lse, x->indptr, x->slots, reinterpret_cast<const unsigned long long*>(x->tree), x->total, x->q_token_stride,
                x->q_head_stride, x->n, x->heads, group, 1, x->dtype, x->causal, x->window, x->tree_words, x->scale, false, 0};
   a.wide_q = aligned(x->q, 8) && x->q_token_stride % 4 == 0 && x->q_head_stride % 4 == 0;
+  if (rows > 32 && kv->head_dim <= 128) return launch_tiles(h, a, x->max_q);
   const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   switch (kv->head_dim) {
     case 64: return nt == 1 ? launch_rows<64, 1>(h, a, x->max_q) : nt == 2 ? launch_rows<64, 2>(h, a, x->max_q) : launch_rows<64, 4>(h, a, x->max_q);

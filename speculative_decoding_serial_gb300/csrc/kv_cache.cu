@@ -9,7 +9,7 @@ namespace whead_kv_impl {
 namespace {
 
 struct Layout {
-  int64_t seq_a, seq_b, region, fresh, rows, counters, starts, partial, total;
+  int64_t seq_a, seq_b, region, fresh, rows, counters, starts, records, partial, total;
   int64_t floats;
 };
 
@@ -24,6 +24,7 @@ Layout layout(const whead_kv& k, int sms) {
   l.fresh = take(4LL * k.num_pages);
   l.rows = take(4LL * k.max_seqs * k.max_pages);
   l.starts = take(16LL * kMaxCtas);
+  l.records = take(16LL * kMaxCtas);
   l.floats = partial_floats(k.head_dim, sms);
   l.partial = take(4LL * l.floats);
   l.total = at;
@@ -92,6 +93,7 @@ int host_cache(const whead_kv* kv, HostCache* out) {
   c.rows = reinterpret_cast<int32_t*>(w + l.rows);
   c.counters = reinterpret_cast<unsigned*>(w + l.counters);
   c.starts = reinterpret_cast<int32_t*>(w + l.starts);
+  c.records = reinterpret_cast<int32_t*>(w + l.records);
   c.partial = reinterpret_cast<float*>(w + l.partial);
   c.partial_floats = l.floats;
   out->stream = static_cast<cudaStream_t>(kv->stream);

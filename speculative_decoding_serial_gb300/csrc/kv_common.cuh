@@ -43,6 +43,7 @@ struct Cache {
   int32_t* rows;    // max_seqs x max_pages: tables after a fork
   unsigned* counters;   // kMaxCtas
   int32_t* starts;      // kMaxCtas x 4
+  int32_t* records;     // kMaxCtas x 4: what a joining kernel has to do
   float* partial;
   int64_t partial_floats;
 };
@@ -147,6 +148,17 @@ __device__ __forceinline__ void load_elems(const void* p, int64_t i, int dtype, 
       x[2 * k + 1] = f.y;
     }
   }
+}
+
+// four consecutive elements of a 16-bit type from i on, as they are; `wide`: the address is a multiple of 8
+__device__ __forceinline__ uint2 load_four(const void* p, int64_t i, bool wide) {
+  const uint16_t* x = static_cast<const uint16_t*>(p) + i;
+  if (wide) return __ldg(reinterpret_cast<const uint2*>(x));
+  return make_uint2(x[0] | (uint32_t)x[1] << 16, x[2] | (uint32_t)x[3] << 16);
+}
+__device__ __forceinline__ float2 unpack16(uint32_t w, int dtype) {
+  if (dtype == WHEAD_KV_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, int dtype) {

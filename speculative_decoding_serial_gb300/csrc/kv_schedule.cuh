@@ -27,6 +27,9 @@ struct AttendArgs {
   int planned;  // the CTAs' starts are in the workspace
 };
 
+// Attention of more than a few rows a KV head (kv_attend_tiles.cu); head_dim 64 or 128.
+int launch_tiles(const struct HostCache& h, const AttendArgs& a, int max_q);
+
 // One (entry, row tile): its rows and the units that they see.
 struct Tile {
   int slot, len, tokens, first;  // first: row of q of the entry's first token
@@ -182,7 +185,7 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
 
 // The same for all CTAs of a launch, by one CTA, into the workspace (many items).
 template <int UNIT>
-__global__ void __launch_bounds__(1024, 1) attend_plan(Cache c, AttendArgs a, int tile_rows, int ctas) {
+static __global__ void __launch_bounds__(1024, 1) attend_plan(Cache c, AttendArgs a, int tile_rows, int ctas) {
   __shared__ long long warps[32];
   const int items = a.n * a.row_tiles;
   long long total = 0;
