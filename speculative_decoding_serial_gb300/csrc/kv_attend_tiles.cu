@@ -115,6 +115,73 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return r;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// The largest of a row's 128 scores, of those whose bits are set where MASKED (a code of its own: the bits cost more than the rest).
+template <bool MASKED>
+__device__ __forceinline__ float row_max(uint32_t st, const uint32_t (&seen)[4]) {
+  float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    uint32_t x[32], y[32];
+    tmem_load32(st + i * 32, x);
+    tmem_load32(st + i * 32 + 32, y);
+    tmem_wait_load(x);
+    tmem_wait_load(y);
+    if (MASKED) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        a0 = fmaxf(a0, (seen[i] >> k) & 1 ? __uint_as_float(x[k]) : -INFINITY);
+        a1 = fmaxf(a1, (seen[i + 1] >> k) & 1 ? __uint_as_float(y[k]) : -INFINITY);
+      }
+      __syncwarp();
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) {
+        a0 = max3(a0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+        a1 = max3(a1, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+      }
+    }
+  }
+  return fmaxf(a0, a1);
+}
+
+// Scores to p = 2^(score f - m), as f16 where the scores were; l: their sum.
+template <bool MASKED>
+__device__ __forceinline__ void row_exp(uint32_t st, const uint32_t (&seen)[4], float f, float m, float2& l) {
+  const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
+  float2 sum[2] = {l, make_float2(0.f, 0.f)};
+  uint32_t x[2][32];
+  tmem_load32(st, x[0]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t (&y)[32] = x[i & 1];
+    tmem_wait_load(y);
+    if (i < 3) tmem_load32(st + i * 32 + 32, x[(i + 1) & 1]);
+    uint32_t p[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      float2 d = fma2(make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), f2, m2);
+      d.x = ex2(d.x);
+      d.y = ex2(d.y);
+      if (MASKED) {
+        if (!((seen[i] >> (2 * k)) & 1)) d.x = 0.0f;
+        if (!((seen[i] >> (2 * k + 1)) & 1)) d.y = 0.0f;
+      }
+      sum[k & 1] = add2(sum[k & 1], d);
+      p[k] = pack16(d.x, d.y, WHEAD_KV_F16);
+    }
+    if (MASKED) __syncwarp();
+    tmem_store16(st + i * 16, p);  // over scores that have been read
+  }
+  l = add2(sum[0], sum[1]);
+  tmem_wait_store();
+}
+
 // The keys key .. key + 31 that a row sees, as bits.
 __device__ __forceinline__ uint32_t sees32(const AttendArgs& a, const RowView& v, int key) {
   uint32_t m = ~0u;
@@ -468,7 +535,6 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), (Shape<D, TILES>:
       const int free_lo = a.window ? max(past + w1 - a.window + 1, 0) : 0;
       float m = kNoKey;
       float2 l = make_float2(0.f, 0.f);
-      const float2 f2 = make_float2(f, f);
       for (int u = sg.u0; u < sg.u1; ++u, ++n) {
         const int key0 = (tile.unit0 + u) * kBlock;
         await(c, smem_u32(&s.s_full[t]), n & 1, dead);
@@ -481,36 +547,12 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), (Shape<D, TILES>:
         }
         const bool masked = key0 < free_lo || key0 + kBlock > free_hi;
         uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-        float top = -INFINITY;
         if (masked) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) seen[i] = sees32(a, view, key0 + 32 * i);
           __syncwarp();
         }
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          uint32_t x[32], y[32];
-          tmem_load32(st + i * 32, x);
-          tmem_load32(st + i * 32 + 32, y);
-          tmem_wait_load(x);
-          tmem_wait_load(y);
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              top = fmaxf(top, (seen[i] >> k) & 1 ? __uint_as_float(x[k]) : -INFINITY);
-              top = fmaxf(top, (seen[i + 1] >> k) & 1 ? __uint_as_float(y[k]) : -INFINITY);
-            }
-            __syncwarp();
-          } else {
-            float a0 = -INFINITY, a1 = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              a0 = fmaxf(a0, fmaxf(__uint_as_float(x[k]), __uint_as_float(x[k + 1])));
-              a1 = fmaxf(a1, fmaxf(__uint_as_float(y[k]), __uint_as_float(y[k + 1])));
-            }
-            top = fmaxf(top, fmaxf(a0, a1));
-          }
-        }
+        float top = masked ? row_max<true>(st, seen) : row_max<false>(st, seen);
         top = top == -INFINITY ? top : top * f;  // -inf: nothing seen, whatever f is
         const bool raise = top > m + kSlack;
         if (__any_sync(~0u, raise)) {
@@ -530,28 +572,8 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), (Shape<D, TILES>:
             }
           }
         }
-        const float2 m2 = make_float2(-m, -m);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t x[32], p[16];
-          tmem_load32(st + i * 32, x);
-          tmem_wait_load(x);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float2 d = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, m2);
-            d.x = ex2(d.x);
-            d.y = ex2(d.y);
-            if (masked) {
-              if (!((seen[i] >> (2 * k)) & 1)) d.x = 0.0f;
-              if (!((seen[i] >> (2 * k + 1)) & 1)) d.y = 0.0f;
-            }
-            l = add2(l, d);
-            p[k] = pack16(d.x, d.y, WHEAD_KV_F16);
-          }
-          __syncwarp();
-          tmem_store16(st + i * 16, p);  // over scores that have been read
-        }
-        tmem_wait_store();
+        if (masked) row_exp<true>(st, seen, f, m, l);
+        else row_exp<false>(st, seen, f, m, l);
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.p_full[t]));
