@@ -1,10 +1,12 @@
 // kv_attend_tiles.cu — attention over the 4-bit paged cache for many query rows: 128 rows a tile on the tensor cores' tcgen05
 // instructions, with scores and outputs in tensor memory.
 //
-// The mathematics is kv_attend.cu's. A block is 128 keys. Four warps turn its codes into f16 tiles in shared memory, which TILES
-// tiles of 128 rows then share; one thread issues the products S = Q K^T and O += P V; one warpgroup a tile reads S, a row a
-// thread, and puts P where S was. The order of the products is PV(tile 0, block j), QK(tile 0, block j + 1), PV(tile 1, ...):
-// one tile's softmax runs under the other's products. With one tile (at most 128 rows) two CTAs share an SM instead.
+// The mathematics is kv_attend.cu's. A block is 64 keys. Two teams of four warps turn the codes of alternate blocks into f16 tiles
+// in shared memory, which TILES tiles of 128 rows then share; one thread issues the products S = Q K^T and O += P V; four warps a
+// tile read S, a row a thread, and put P where S was. From P's store over PV, the next QK and back to the softmax is about 1.5 us,
+// most of it hand-overs, so scores are kept ahead: tensor memory holds four S (64 columns each) beside the outputs, two or four for
+// a tile. With blocks of 128 keys there is room for one a tile, and the softmax waits for every hand-over (2.8 us for 256 rows
+// and 128 keys, against MEASURED now).
 //
 // Shared memory holds operands in rows of 128 bytes (64 f16), 8 rows to an atom of 1024 bytes, 16-byte chunks swizzled by the row.
 // Channels 16 b + 8 s .. + 7 of a query row or key lie in chunk 4 s + b % 4 of the row, not 2 b + s: a warp's stores of a block's keys
@@ -19,7 +21,7 @@ namespace whead_kv_impl {
 
 namespace {
 
-constexpr int kBlock = 128;      // keys
+constexpr int kBlock = 64;       // keys
 constexpr float kBias = 7.0f;    // as in kv_attend.cu
 constexpr float kSlack = 15.0f;
 constexpr float kNoKey = -1e30f;
@@ -27,77 +29,65 @@ constexpr float kNoKey = -1e30f;
 template <int D, int TILES>
 struct Shape {
   static constexpr int kRows = 128 * TILES;
-  static constexpr int kBufs = TILES;                    // of key and value tiles
-  static constexpr int kCtas = TILES == 1 ? 2 : 1;       // of an SM
-  static constexpr int kSoft = 4 * TILES;                // softmax warps, then those that unpack, then the one that issues
-  static constexpr int kUnpack = 4, kMine = 8 / kUnpack; // groups of a block that each of them takes
+  static constexpr int kSBufs = 4 / TILES;               // score buffers of a tile
+  static constexpr int kBufs = 4;                        // key and value tiles
+  static constexpr int kSoft = 4 * TILES;                // softmax warps, then those that unpack, then one a tile that issues
+  static constexpr int kUnpack = 8;                      // a group of every other block to each
   static constexpr int kIssue = kSoft + kUnpack;
-  static constexpr int kThreads = (kIssue + 1) * 32;
+  static constexpr int kThreads = (kIssue + TILES) * 32;
   static constexpr int kGroup = 18 * D;
   static constexpr int kQ = 128 * D * 2, kK = kBlock * D * 2, kV = D * kBlock * 2;
-  static constexpr int kOffQ = 1024, kOffK = kOffQ + TILES * kQ, kOffV = kOffK + kBufs * kK;
+  static constexpr int kOffWalk = 640;                   // the warps' places
+  static constexpr int kOffF = 3072;                     // the rows' factors from products to scores
+  static constexpr int kOffQ = 4096, kOffK = kOffQ + TILES * kQ, kOffV = kOffK + kBufs * kK;
   static constexpr int kBytes = kOffV + kBufs * kV + 1024;  // + alignment
-  static constexpr int kCols = 256 * TILES;                 // of tensor memory: S of each tile, O of each tile
+  static constexpr int kCols = 512;                         // of tensor memory: two S, then O of each tile
 };
 
 struct Head {
   SchedShared sched;
-  unsigned long long k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2], q_full, drain;
+  unsigned long long k_full[4], k_free[4], v_full[4], v_free[4], s_full[4], p_full[4], pv_done[4], o_full[2], q_full[2], drain[2];
   uint32_t tmem;
 };
-static_assert(sizeof(Head) <= 1024, "");
 
 __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
   // rows of 128 bytes, atoms of 8 rows 1024 bytes apart, 128-byte swizzle
   return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1u << 16) | ((uint64_t)(1024u >> 4) << 32) | ((uint64_t)1u << 46) | ((uint64_t)2u << 61);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
-               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+// Issued by the lane whose `leader` is not zero. The rest of the warp runs along, so that addresses and descriptors stay in uniform
+// registers: under a branch for one lane, each product took a dozen moves and the issuing warp was the bottleneck.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t leader) {
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
-               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t leader) {
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"(leader) : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t leader) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
+               ::"r"(bar), "r"(leader) : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-#define KV_R32(x) "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), \
-  "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]), "=r"(x[18]), \
-  "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]), "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), \
-  "=r"(x[29]), "=r"(x[30]), "=r"(x[31])
-
-// 32 columns of this warp's lanes
-__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&x)[32]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-               "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];" : KV_R32(x) : "r"(addr));
+// 16 columns of this warp's lanes
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&x)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]),
+                 "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]) : "r"(addr));
 }
-__device__ __forceinline__ void tmem_wait_load(uint32_t (&x)[32]) {
-  // the registers are operands, so that no use of them moves before the wait
+__device__ __forceinline__ void tmem_wait_load(uint32_t (&x)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(x[0]), "+r"(x[1]), "+r"(x[2]), "+r"(x[3]), "+r"(x[4]), "+r"(x[5]), "+r"(x[6]), "+r"(x[7]), "+r"(x[8]), "+r"(x[9]),
-                 "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]), "+r"(x[16]), "+r"(x[17]), "+r"(x[18]),
-                 "+r"(x[19]), "+r"(x[20]), "+r"(x[21]), "+r"(x[22]), "+r"(x[23]), "+r"(x[24]), "+r"(x[25]), "+r"(x[26]), "+r"(x[27]),
-                 "+r"(x[28]), "+r"(x[29]) :: "memory");
-  asm volatile("" : "+r"(x[30]), "+r"(x[31]));
+                 "+r"(x[10]), "+r"(x[11]), "+r"(x[12]), "+r"(x[13]), "+r"(x[14]), "+r"(x[15]) :: "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&x)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                ::"r"(addr), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]),
                  "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]) : "memory");
-}
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&x)[32]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-               "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
-               ::"r"(addr), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]),
-                 "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]), "r"(x[16]), "r"(x[17]), "r"(x[18]), "r"(x[19]),
-                 "r"(x[20]), "r"(x[21]), "r"(x[22]), "r"(x[23]), "r"(x[24]), "r"(x[25]), "r"(x[26]), "r"(x[27]), "r"(x[28]), "r"(x[29]),
-                 "r"(x[30]), "r"(x[31]) : "memory");
 }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -121,65 +111,60 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// The largest of a row's 128 scores, of those whose bits are set where MASKED (a code of its own: the bits cost more than the rest).
+// The largest of a row's 64 scores, of those whose bits are set where MASKED (a code of its own: the bits cost more than the rest).
 template <bool MASKED>
-__device__ __forceinline__ float row_max(uint32_t st, const uint32_t (&seen)[4]) {
+__device__ __forceinline__ float row_max(uint32_t st, const uint32_t (&seen)[2]) {
   float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    uint32_t x[32], y[32];
-    tmem_load32(st + i * 32, x);
-    tmem_load32(st + i * 32 + 32, y);
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x[16];
+    tmem_load16(st + i * 16, x);
     tmem_wait_load(x);
-    tmem_wait_load(y);
     if (MASKED) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        a0 = fmaxf(a0, (seen[i] >> k) & 1 ? __uint_as_float(x[k]) : -INFINITY);
-        a1 = fmaxf(a1, (seen[i + 1] >> k) & 1 ? __uint_as_float(y[k]) : -INFINITY);
-      }
+      for (int k = 0; k < 16; ++k) a0 = fmaxf(a0, (seen[i / 2] >> (i % 2 * 16 + k)) & 1 ? __uint_as_float(x[k]) : -INFINITY);
       __syncwarp();
     } else {
 #pragma unroll
-      for (int k = 0; k < 32; k += 2) {
+      for (int k = 0; k < 16; k += 4) {
         a0 = max3(a0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-        a1 = max3(a1, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+        a1 = max3(a1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
       }
     }
   }
   return fmaxf(a0, a1);
 }
 
-// Scores to p = 2^(score f - m), as f16 where the scores were; l: their sum.
+// p = 2^(score f - m) of a row's scores, as f16 pairs, their sum, and the largest exponent: one pass, on the guess that m still does.
 template <bool MASKED>
-__device__ __forceinline__ void row_exp(uint32_t st, const uint32_t (&seen)[4], float f, float m, float2& l) {
+__device__ __forceinline__ float row_exp(uint32_t st, const uint32_t (&seen)[2], float f, float m, float2& sum, uint32_t (&p)[2][16]) {
   const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
-  float2 sum[2] = {l, make_float2(0.f, 0.f)};
-  uint32_t x[2][32];
-  tmem_load32(st, x[0]);
+  float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+  float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t (&y)[32] = x[i & 1];
-    tmem_wait_load(y);
-    if (i < 3) tmem_load32(st + i * 32 + 32, x[(i + 1) & 1]);
-    uint32_t p[16];
+  for (int i = 0; i < 4; ++i) {  // 16 columns at a time: registers are short, and what spills misses the small L1
+    uint32_t x[16];
+    tmem_load16(st + i * 16, x);
+    tmem_wait_load(x);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      float2 d = fma2(make_float2(__uint_as_float(y[2 * k]), __uint_as_float(y[2 * k + 1])), f2, m2);
+    for (int k = 0; k < 8; ++k) {
+      float2 d = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, m2);
+      if (MASKED) {
+        d.x = (seen[i / 2] >> (i % 2 * 16 + 2 * k)) & 1 ? d.x : -INFINITY;
+        d.y = (seen[i / 2] >> (i % 2 * 16 + 2 * k + 1)) & 1 ? d.y : -INFINITY;
+      }
+      if (k & 1) t1 = max3(t1, d.x, d.y);
+      else t0 = max3(t0, d.x, d.y);
       d.x = ex2(d.x);
       d.y = ex2(d.y);
-      if (MASKED) {
-        if (!((seen[i] >> (2 * k)) & 1)) d.x = 0.0f;
-        if (!((seen[i] >> (2 * k + 1)) & 1)) d.y = 0.0f;
-      }
-      sum[k & 1] = add2(sum[k & 1], d);
-      p[k] = pack16(d.x, d.y, WHEAD_KV_F16);
+      if (k & 1) s1 = add2(s1, d);
+      else s0 = add2(s0, d);
+      p[i / 2][i % 2 * 8 + k] = pack16(d.x, d.y, WHEAD_KV_F16);
     }
     if (MASKED) __syncwarp();
-    tmem_store16(st + i * 16, p);  // over scores that have been read
   }
-  l = add2(sum[0], sum[1]);
-  tmem_wait_store();
+  sum = add2(s0, s1);
+  return fmaxf(t0, t1);
 }
 
 // The keys key .. key + 31 that a row sees, as bits.
@@ -209,36 +194,51 @@ struct Segment {
   long long head_at;
 };
 
-// A CTA's way through its range; every role walks it for itself.
-template <int D, int TILES>
+// A CTA's way through its range. Every warp walks it for itself and keeps its place in shared memory, not in registers: those are
+// short here, and what spills is read back from L2 (shared memory takes nearly all of L1).
 struct Walk {
   long long cur, end, item_at;
-  int item, n;  // n: blocks before this segment
-  __device__ __forceinline__ bool next(const Cache& c, const AttendArgs& a, Segment& s) {
-    if (cur >= end) return false;
-    while (true) {
-      s.tile = make_tile<kBlock>(c, a, item, Shape<D, TILES>::kRows);
-      if (s.tile.units > 0) break;
-      ++item;
-    }
-    s.item = item;
-    const int past = (int)(cur - item_at);
-    s.h = past / s.tile.units;
-    s.u0 = past - s.h * s.tile.units;
-    s.head_at = cur - s.u0;
-    s.u1 = (int)min((long long)s.tile.units, s.u0 + (end - cur));
-    cur = s.head_at + s.u1;
-    if (s.u1 == s.tile.units && s.h == c.kv_heads - 1) {
-      item_at = cur;
-      ++item;
-    }
-    return true;
-  }
+  int next_item;
+  Segment sg;
+  int free_lo, free_hi;  // keys that all rows of a softmax warp's tile see
 };
 
-// A wait that has run out is reported once; the role then goes on without waiting, on whatever is there, to its end.
+// The next segment, by a whole warp; false at the end.
+template <int ROWS>
+__device__ __forceinline__ bool next_segment(const Cache& c, const AttendArgs& a, Walk& w) {
+  const long long cur = w.cur, end = w.end;
+  if (cur >= end) return false;
+  int item = w.next_item;
+  Segment s;
+  while (true) {
+    s.tile = make_tile<kBlock>(c, a, item, ROWS);
+    if (s.tile.units > 0) break;
+    ++item;
+  }
+  s.item = item;
+  const long long item_at = w.item_at;
+  const int past = (int)(cur - item_at);
+  s.h = past / s.tile.units;
+  s.u0 = past - s.h * s.tile.units;
+  s.head_at = cur - s.u0;
+  s.u1 = (int)min((long long)s.tile.units, s.u0 + (end - cur));
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    w.sg = s;
+    w.cur = s.head_at + s.u1;
+    const bool done = s.u1 == s.tile.units && s.h == c.kv_heads - 1;
+    w.next_item = done ? item + 1 : item;
+    if (done) w.item_at = s.head_at + s.u1;
+  }
+  __syncwarp();
+  return true;
+}
+
+static_assert(sizeof(Head) <= 640 && 640 + 18 * sizeof(Walk) <= 3072, "");
+
+// A whole warp's wait. One that has run out is reported once; the warp then goes on without waiting, on whatever is there, to its end.
 __device__ __forceinline__ void await(const Cache& c, uint32_t bar, uint32_t parity, bool& dead) {
-  if (!dead && !mbar_wait(bar, parity)) {
+  if (!dead && !__all_sync(~0u, mbar_wait(bar, parity))) {
     set_status(c, WHEAD_ERR_TIMEOUT);
     dead = true;
   }
@@ -256,25 +256,28 @@ struct RawV {
 };
 
 template <int D, int TILES>
-__global__ void __launch_bounds__((Shape<D, TILES>::kThreads), (Shape<D, TILES>::kCtas)) attend_tiles(Cache c, AttendArgs a) {
+__global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(const __grid_constant__ Cache c, const __grid_constant__ AttendArgs a) {
   using S = Shape<D, TILES>;
   constexpr int NB = D / 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   Head& s = *reinterpret_cast<Head*>(smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s.k_full[i]), S::kUnpack);
-      mbar_init(smem_u32(&s.k_free[i]), 1);
-      mbar_init(smem_u32(&s.v_full[i]), S::kUnpack);
-      mbar_init(smem_u32(&s.v_free[i]), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&s.k_full[i]), 4);
+      mbar_init(smem_u32(&s.k_free[i]), TILES);
+      mbar_init(smem_u32(&s.v_full[i]), 4);
+      mbar_init(smem_u32(&s.v_free[i]), TILES);
       mbar_init(smem_u32(&s.s_full[i]), 1);
       mbar_init(smem_u32(&s.p_full[i]), 4);
-      mbar_init(smem_u32(&s.o_full[i]), 1);
+      mbar_init(smem_u32(&s.pv_done[i]), 1);
     }
-    mbar_init(smem_u32(&s.q_full), S::kSoft);
-    mbar_init(smem_u32(&s.drain), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.o_full[i]), 1);
+      mbar_init(smem_u32(&s.q_full[i]), 4);
+      mbar_init(smem_u32(&s.drain[i]), 1);
+    }
     fence_mbar_init();
   }
   const Start start = get_start<S::kThreads, kBlock>(c, a, S::kRows, s.sched);
@@ -289,215 +292,200 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), (Shape<D, TILES>:
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = s.tmem;
-  Walk<D, TILES> walk{range_begin(start, blockIdx.x), range_begin(start, blockIdx.x + 1), start.at, start.item, 0};
-  const long long begin = walk.cur;
-  Segment sg;
+  const uint32_t tmem = __shfl_sync(~0u, s.tmem, 0);
+  const long long begin = range_begin(start, blockIdx.x);
+  Walk& walk = reinterpret_cast<Walk*>(smem + S::kOffWalk)[warp];
+  if (lane == 0) {
+    walk.cur = begin;
+    walk.end = range_begin(start, blockIdx.x + 1);
+    walk.item_at = start.at;
+    walk.next_item = start.item;
+  }
+  __syncwarp();
+  const Segment& sg = walk.sg;
   bool dead = false;
 
-  if (warp == S::kIssue) {
-    // ---- the thread that issues the products
-    if (lane == 0) {
-      constexpr uint32_t kQK = (1u << 4) | ((kBlock / 8u) << 17) | ((128u / 16u) << 24);  // fp32 from f16 x f16, both along k
-      constexpr uint32_t kPV = (1u << 4) | ((D / 8u) << 17) | ((128u / 16u) << 24);
-      const uint32_t q0 = smem_u32(smem + S::kOffQ), k0 = smem_u32(smem + S::kOffK), v0 = smem_u32(smem + S::kOffV);
-      auto scores = [&](int t, int buf) {
+  if (warp >= S::kIssue) {
+    // ---- a tile's products
+    constexpr uint32_t kQK = (1u << 4) | ((kBlock / 8u) << 17) | ((128u / 16u) << 24);  // fp32 from f16 x f16, both along k
+    constexpr uint32_t kPV = (1u << 4) | ((D / 8u) << 17) | ((128u / 16u) << 24);
+    const int t = warp - S::kIssue;
+    const uint32_t leader = lane == 0;
+    const uint64_t dq = tile_desc(smem_u32(smem + S::kOffQ) + t * S::kQ), dk = tile_desc(smem_u32(smem + S::kOffK)), dv = tile_desc(smem_u32(smem + S::kOffV));
+    const uint32_t s_col = tmem + t * S::kSBufs * kBlock, o_col = tmem + 256 + t * 128;
+    auto scores = [&](int n) {
+      const int buf = n % S::kBufs, sb = n % S::kSBufs;
+      await(c, smem_u32(&s.k_full[buf]), n / S::kBufs & 1, dead);
+      if (dead) return;
+      fence_after();
+      const uint64_t db = dk + (uint64_t)(buf * (S::kK >> 4));
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + t * 128, tile_desc(q0 + t * S::kQ + k / 4 * (128 * 128) + k % 4 * 32), tile_desc(k0 + buf * S::kK + k / 4 * (kBlock * 128) + k % 4 * 32),
-                 kQK, k > 0);
-      };
-      auto outputs = [&](int t, int buf, bool add) {
-#pragma unroll
-        for (int k = 0; k < kBlock / 16; ++k)
-          mma_ts(tmem + TILES * 128 + t * 128, tmem + t * 128 + k * 8, tile_desc(v0 + buf * S::kV + k / 4 * (D * 128) + k % 4 * 32), kPV, add || k > 0);
-      };
-      int n = 0, seg = 0;
-      while (walk.next(c, a, sg)) {
-        const int blocks = sg.u1 - sg.u0;
-        await(c, smem_u32(&s.q_full), seg & 1, dead);
-        await(c, smem_u32(&s.k_full[n % S::kBufs]), n / S::kBufs & 1, dead);
+      for (int k = 0; k < D / 16; ++k)
+        mma_ss(s_col + sb * kBlock, dq + (k / 4 * (128 * 128) + k % 4 * 32) / 16, db + (k / 4 * (kBlock * 128) + k % 4 * 32) / 16, kQK, k > 0, leader);
+      commit(smem_u32(&s.s_full[t * S::kSBufs + sb]), leader);
+      commit(smem_u32(&s.k_free[buf]), leader);
+    };
+    int n = 0, seg = 0;
+    while (!dead && next_segment<S::kRows>(c, a, walk)) {
+      const int first = n, last = n + sg.u1 - sg.u0;  // blocks first .. last - 1; scores are kSBufs ahead of outputs
+      await(c, smem_u32(&s.q_full[t]), seg & 1, dead);
+      fence_after();
+      for (int i = n; i < min(n + S::kSBufs, last) && !dead; ++i) scores(i);
+      for (; n < last && !dead; ++n) {
+        const int buf = n % S::kBufs, sb = n % S::kSBufs;
+        await(c, smem_u32(&s.v_full[buf]), n / S::kBufs & 1, dead);
+        await(c, smem_u32(&s.p_full[t * S::kSBufs + sb]), n / S::kSBufs & 1, dead);
         if (dead) break;
         fence_after();
-        for (int t = 0; t < TILES; ++t) {
-          scores(t, n % S::kBufs);
-          commit(smem_u32(&s.s_full[t]));
-        }
-        commit(smem_u32(&s.k_free[n % S::kBufs]));
-        for (int j = 0; j < blocks && !dead; ++j, ++n) {
-          const bool more = j + 1 < blocks;
-          const int buf = n % S::kBufs, next = (n + 1) % S::kBufs;
-          await(c, smem_u32(&s.v_full[buf]), n / S::kBufs & 1, dead);
-          for (int t = 0; t < TILES; ++t) {
-            await(c, smem_u32(&s.p_full[t]), n & 1, dead);
-            if (dead) break;
-            fence_after();
-            outputs(t, buf, j > 0);
-            if (t == TILES - 1) commit(smem_u32(&s.v_free[buf]));
-            if (more) {
-              if (t == 0) await(c, smem_u32(&s.k_full[next]), (n + 1) / S::kBufs & 1, dead);
-              if (dead) break;
-              fence_after();
-              scores(t, next);
-              commit(smem_u32(&s.s_full[t]));
-              if (t == TILES - 1) commit(smem_u32(&s.k_free[next]));
-            } else {
-              commit(smem_u32(&s.o_full[t]));
-            }
-          }
-        }
-        if (dead) break;
-        ++seg;
+        const uint64_t db = dv + (uint64_t)(buf * (S::kV >> 4));
+#pragma unroll
+        for (int k = 0; k < kBlock / 16; ++k)
+          mma_ts(o_col, s_col + sb * kBlock + k * 8, db + k * 2, kPV, n > first || k > 0, leader);
+        commit(smem_u32(&s.pv_done[t * S::kSBufs + sb]), leader);
+        commit(smem_u32(&s.v_free[buf]), leader);
+        if (n + S::kSBufs < last) scores(n + S::kSBufs);
+        if (n == last - 1) commit(smem_u32(&s.o_full[t]), leader);
       }
-      // nothing may be under way when the CTA gives its tensor memory back
-      commit(smem_u32(&s.drain));
-      mbar_wait(smem_u32(&s.drain), 0);
+      ++seg;
     }
+    // nothing may be under way when the CTA gives its tensor memory back
+    __syncwarp();
+    commit(smem_u32(&s.drain[t]), leader);
+    mbar_wait(smem_u32(&s.drain[t]), 0);
     __syncwarp();
   } else if (warp >= S::kSoft) {
-    // ---- codes to f16 tiles: groups w, w + kUnpack, .. of each block
-    const int w = warp - S::kSoft, g = lane >> 2, t = lane & 3;
+    // ---- codes to f16 tiles: group w of every other block, by the block's number in the CTA's range
+    const int w = (warp - S::kSoft) & 3, team = (warp - S::kSoft) >> 2, g = lane >> 2, t = lane & 3;
     const int64_t page_bytes = (int64_t)c.kv_heads * (c.page_size >> 4) * S::kGroup;
     int n = 0;
-    while (walk.next(c, a, sg)) {
+    while (next_segment<S::kRows>(c, a, walk)) {
       const int32_t* table = c.tables + (int64_t)sg.tile.slot * c.max_pages;
       const uint8_t* base = c.pool + (int64_t)sg.h * (c.page_size >> 4) * S::kGroup;
       const int len = sg.tile.len, stop = min((sg.tile.unit0 + sg.u1) * kBlock, len);
-      // codes come one block ahead of the tiles, the numbers of their pages two
-      RawK<D> rk[S::kMine];
-      RawV<D> rv[S::kMine];
-      int page[S::kMine];
+      // codes come one of the team's blocks ahead of the tiles, the numbers of their pages two
+      RawK<D> rk;
+      RawV<D> rv;
+      int page;
       auto look = [&](int u) {
-#pragma unroll
-        for (int i = 0; i < S::kMine; ++i) {
-          const int key = u * kBlock + (w + S::kUnpack * i) * 16;
-          page[i] = key < stop ? __ldg(table + (key >> c.page_shift)) : 0;
-        }
+        const int key = u * kBlock + w * 16;
+        page = key < stop ? __ldg(table + (key >> c.page_shift)) : 0;
       };
-      auto group_at = [&](int i, int key) -> const uint8_t* {
-        if ((unsigned)page[i] >= (unsigned)c.num_pages) {
+      auto group_at = [&](int key) -> const uint8_t* {
+        if ((unsigned)page >= (unsigned)c.num_pages) {
           set_status(c, WHEAD_ERR_INTERNAL);
-          page[i] = 0;
+          page = 0;
         }
-        return base + page[i] * page_bytes + ((key & (c.page_size - 1)) >> 4) * S::kGroup;
+        return base + page * page_bytes + ((key & (c.page_size - 1)) >> 4) * S::kGroup;
       };
       auto fetch_k = [&](int u) {
+        const int key = u * kBlock + w * 16;
+        if (key >= stop) return;
+        const uint8_t* gp = group_at(key);
 #pragma unroll
-        for (int i = 0; i < S::kMine; ++i) {
-          const int key = u * kBlock + (w + S::kUnpack * i) * 16;
-          if (key >= stop) continue;
-          const uint8_t* gp = group_at(i, key);
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            rk[i].code[j] = __ldg(reinterpret_cast<const uint4*>(gp + j * 512) + lane);
-            rk[i].scale[j] = __ldg(reinterpret_cast<const uint2*>(gp + 8 * D + g * 2 * NB) + j);
-          }
+        for (int j = 0; j < D / 64; ++j) {
+          rk.code[j] = __ldg(reinterpret_cast<const uint4*>(gp + j * 512) + lane);
+          rk.scale[j] = __ldg(reinterpret_cast<const uint2*>(gp + 8 * D + g * 2 * NB) + j);
         }
       };
       auto fetch_v = [&](int u) {
+        const int key = u * kBlock + w * 16;
+        if (key >= stop) return;
+        const uint8_t* gp = group_at(key);
 #pragma unroll
-        for (int i = 0; i < S::kMine; ++i) {
-          const int key = u * kBlock + (w + S::kUnpack * i) * 16;
-          if (key >= stop) continue;
-          const uint8_t* gp = group_at(i, key);
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            rv[i].code[j] = __ldg(reinterpret_cast<const uint4*>(gp + 9 * D + j * 512) + lane);
-            rv[i].scale[j] = __ldg(reinterpret_cast<const uint4*>(gp + 17 * D + t * 4 * NB) + j);
-          }
+        for (int j = 0; j < D / 64; ++j) {
+          rv.code[j] = __ldg(reinterpret_cast<const uint4*>(gp + 9 * D + j * 512) + lane);
+          rv.scale[j] = __ldg(reinterpret_cast<const uint4*>(gp + 17 * D + t * 4 * NB) + j);
         }
       };
-      const int first = sg.tile.unit0 + sg.u0;
-      look(first);
-      fetch_k(first);
-      fetch_v(first);
-      look(first + 1);
-      for (int u = first; u < sg.tile.unit0 + sg.u1; ++u, ++n) {
-        const int buf = n % S::kBufs;
-        const uint32_t used = (n / S::kBufs - 1) & 1;
-        if (n >= S::kBufs) await(c, smem_u32(&s.k_free[buf]), used, dead);
+      const int blocks = sg.u1 - sg.u0, skip = (n ^ team) & 1;  // the team's first block of the segment: 0 or 1
+      int u = sg.tile.unit0 + sg.u0 + skip;
+      const int end = sg.tile.unit0 + sg.u1;
+      look(u);
+      fetch_k(u);
+      fetch_v(u);
+      look(u + 2);
+      for (int k = n + skip; u < end; u += 2, k += 2) {
+        const int buf = k % S::kBufs, key0 = u * kBlock + w * 16;
+        const uint32_t used = (k / S::kBufs - 1) & 1;
+        if (k >= S::kBufs) await(c, smem_u32(&s.k_free[buf]), used, dead);
+        if (key0 < len) {
+          uint8_t* to = smem + S::kOffK + buf * S::kK + w * 2048 + g * 128 + (t & 1) * 8;
 #pragma unroll
-        for (int i = 0; i < S::kMine; ++i) {
-          const int gi = w + S::kUnpack * i;
-          if (u * kBlock + gi * 16 < len) {
-            uint8_t* to = smem + S::kOffK + buf * S::kK + gi * 2048 + g * 128 + (t & 1) * 8;
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-              const uint4 kw = rk[i].code[b / 4];
-              uint32_t x[4], s0, s1;
-              e2m1x8_to_half2(b % 4 == 0 ? kw.x : b % 4 == 1 ? kw.y : b % 4 == 2 ? kw.z : kw.w, x);
-              e4m3x4_to_half2(b % 4 < 2 ? rk[i].scale[b / 4].x : rk[i].scale[b / 4].y, s0, s1);
-              const uint32_t sc = b & 1 ? s1 : s0;
-              uint8_t* at = to + b / 4 * (kBlock * 128) + ((((t >> 1) * 4 + b % 4) ^ g) << 4);
-              *reinterpret_cast<uint2*>(at) = make_uint2(hmul2_low(x[0], sc), hmul2_low(x[2], sc));
-              *reinterpret_cast<uint2*>(at + 1024) = make_uint2(hmul2_high(x[1], sc), hmul2_high(x[3], sc));
-            }
+          for (int b = 0; b < NB; ++b) {
+            const uint4 kw = rk.code[b / 4];
+            uint32_t x[4], s0, s1;
+            e2m1x8_to_half2(b % 4 == 0 ? kw.x : b % 4 == 1 ? kw.y : b % 4 == 2 ? kw.z : kw.w, x);
+            e4m3x4_to_half2(b % 4 < 2 ? rk.scale[b / 4].x : rk.scale[b / 4].y, s0, s1);
+            const uint32_t sc = b & 1 ? s1 : s0;
+            uint8_t* at = to + b / 4 * (kBlock * 128) + ((((t >> 1) * 4 + b % 4) ^ g) << 4);
+            *reinterpret_cast<uint2*>(at) = make_uint2(hmul2_low(x[0], sc), hmul2_low(x[2], sc));
+            *reinterpret_cast<uint2*>(at + 1024) = make_uint2(hmul2_high(x[1], sc), hmul2_high(x[3], sc));
           }
         }
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.k_full[buf]));
-        fetch_k(u + 1);
-        if (n >= S::kBufs) await(c, smem_u32(&s.v_free[buf]), used, dead);
+        fetch_k(u + 2);
+        if (k >= S::kBufs) await(c, smem_u32(&s.v_free[buf]), used, dead);
+        // what lies past the length may be anything: it becomes zero, so that 0 x NaN does not arise
+        uint32_t live = ~0u;
+        if (key0 + 16 > len) {
+          live = 0;
 #pragma unroll
-        for (int i = 0; i < S::kMine; ++i) {
-          const int gi = w + S::kUnpack * i, key0 = u * kBlock + gi * 16;
-          // what lies past the length may be anything: it becomes zero, so that 0 x NaN does not arise
-          uint32_t live = 0;
+          for (int i = 0; i < 4; ++i)
+            if (key0 + 2 * t + (i & 1) + (i >> 1) * 8 < len) live |= 0xFFu << (8 * i);
+          __syncwarp();
+        }
+        uint8_t* to = smem + S::kOffV + buf * S::kV + g * 128 + t * 4;
+        const int c0 = ((w * 2) ^ g) << 4, c1 = ((w * 2 + 1) ^ g) << 4;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (key0 + 2 * t + (k & 1) + (k >> 1) * 8 < len) live |= 0xFFu << (8 * k);
-          uint8_t* to = smem + S::kOffV + buf * S::kV + gi / 4 * (D * 128) + g * 128 + t * 4;
-          const int c0 = (gi % 4 * 2 ^ g) << 4, c1 = ((gi % 4 * 2 + 1) ^ g) << 4;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const uint4 vw = rv[i].code[b / 4], vs = rv[i].scale[b / 4];
-            uint32_t x[4], s0, s1;
-            e2m1x8_to_half2(b % 4 == 0 ? vw.x : b % 4 == 1 ? vw.y : b % 4 == 2 ? vw.z : vw.w, x);
-            e4m3x4_to_half2((b % 4 == 0 ? vs.x : b % 4 == 1 ? vs.y : b % 4 == 2 ? vs.z : vs.w) & live, s0, s1);
-            uint8_t* at = to + b * 2048;
-            *reinterpret_cast<uint32_t*>(at + c0) = hmul2(x[0], s0);
-            *reinterpret_cast<uint32_t*>(at + 1024 + c0) = hmul2(x[1], s0);
-            *reinterpret_cast<uint32_t*>(at + c1) = hmul2(x[2], s1);
-            *reinterpret_cast<uint32_t*>(at + 1024 + c1) = hmul2(x[3], s1);
-          }
+        for (int b = 0; b < NB; ++b) {
+          const uint4 vw = rv.code[b / 4], vs = rv.scale[b / 4];
+          uint32_t x[4], s0, s1;
+          e2m1x8_to_half2(b % 4 == 0 ? vw.x : b % 4 == 1 ? vw.y : b % 4 == 2 ? vw.z : vw.w, x);
+          e4m3x4_to_half2((b % 4 == 0 ? vs.x : b % 4 == 1 ? vs.y : b % 4 == 2 ? vs.z : vs.w) & live, s0, s1);
+          uint8_t* at = to + b * 2048;
+          *reinterpret_cast<uint32_t*>(at + c0) = hmul2(x[0], s0);
+          *reinterpret_cast<uint32_t*>(at + 1024 + c0) = hmul2(x[1], s0);
+          *reinterpret_cast<uint32_t*>(at + c1) = hmul2(x[2], s1);
+          *reinterpret_cast<uint32_t*>(at + 1024 + c1) = hmul2(x[3], s1);
         }
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.v_full[buf]));
-        fetch_v(u + 1);
-        look(u + 2);
+        fetch_v(u + 2);
+        look(u + 4);
       }
+      n += blocks;
     }
   } else {
     // ---- softmax: a thread a row
-    const int t = warp >> 2, sub = t * 128, r = sub + (warp & 3) * 32 + lane;  // row of the CTA's tile
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;                         // this warp's lanes of tensor memory (lane 32 w at bit 16)
-    const uint32_t st = tmem + t * 128 + lanes, ot = tmem + TILES * 128 + t * 128 + lanes;
+    const int t = warp >> 2, quarter = warp & 3, sub = t * 128;
+    const int r = sub + quarter * 32 + lane;           // row of the CTA's tile
+    const uint32_t lanes = (uint32_t)quarter << 21;    // this warp's lanes of tensor memory (lane 32 w at bit 16)
+    const uint32_t ot = tmem + 256 + t * 128 + lanes;
+    float* factors = reinterpret_cast<float*>(smem + S::kOffF) + sub + quarter * 32;
     int n = 0, seg = 0;
-    while (walk.next(c, a, sg)) {
-      const Tile tile = sg.tile;
-      const int row = tile.row0 + r;
-      const bool live = r < tile.rows;
-      const int tok = row / a.group, head = sg.h * a.group + row % a.group;
-      const bool idle = (warp & 3) * 32 + sub >= tile.rows;  // no row of this warp is one: its part of P may be anything
+    while (next_segment<S::kRows>(c, a, walk)) {
+      const Tile& tile = sg.tile;
+      const bool idle = quarter * 32 + sub >= tile.rows;  // no row of this warp is one: its part of P may be anything
       float f;
       {
         // the warp's query rows, from a power of two to f16; a row is kPer lanes with 8 channels each, kAtOnce rows a load. The
         // sign of the scale goes into the rows, so that f is positive and scores need it only after their maximum is known.
-        constexpr int kPer = D / 8, kAtOnce = 32 / kPer, kTurns = 32 / kAtOnce;
+        constexpr int kPer = D / 8, kAtOnce = 32 / kPer, kTurns = 16 / kAtOnce;  // 16 rows at a time
         const float to_log2 = a.scale * c.k_scale[sg.h] * kLog2e;
-        const long long at = live ? (long long)(tile.first + tok) * a.q_token_stride + (long long)head * a.q_head_stride : -1;
+        const int row = tile.row0 + r;
+        const long long at = r < tile.rows ? (long long)(tile.first + row / a.group) * a.q_token_stride + (long long)(sg.h * a.group + row % a.group) * a.q_head_stride : -1;
         const int sub_lane = lane % kPer, sub_row = lane / kPer;
         const int b = sub_lane / 2, chunk = (sub_lane & 1) * 4 + b % 4;
-        uint8_t* to = smem + S::kOffQ + t * S::kQ + (warp & 3) * 32 * 128 + b / 4 * (128 * 128);
-        f = 0.0f;
+        uint8_t* to = smem + S::kOffQ + t * S::kQ + quarter * 32 * 128 + b / 4 * (128 * 128);
 #pragma unroll 1
-        for (int i0 = 0; i0 < kTurns; i0 += 8) {
-          uint4 x[8];
+        for (int half = 0; half < 2; ++half) {
+          uint4 x[kTurns];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const long long from = __shfl_sync(~0u, at, (i0 + i) * kAtOnce + sub_row);
+          for (int i = 0; i < kTurns; ++i) {
+            const long long from = __shfl_sync(~0u, at, half * 16 + i * kAtOnce + sub_row);
             x[i] = make_uint4(0u, 0u, 0u, 0u);
             if (from >= 0) {
               const uint2 lo = load_four(a.q, from + sub_lane * 8, a.wide_q), hi = load_four(a.q, from + sub_lane * 8 + 4, a.wide_q);
@@ -505,7 +493,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), (Shape<D, TILES>:
             }
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < kTurns; ++i) {
             const float2 y[4] = {unpack16(x[i].x, a.dtype), unpack16(x[i].y, a.dtype), unpack16(x[i].z, a.dtype), unpack16(x[i].w, a.dtype)};
             float big = 0.0f;
 #pragma unroll
@@ -518,70 +506,91 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), (Shape<D, TILES>:
             uint32_t z[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) z[k] = pack16(y[k].x * up, y[k].y * up, WHEAD_KV_F16);
-            const int mine = (i0 + i) * kAtOnce + sub_row;
+            const int mine = half * 16 + i * kAtOnce + sub_row;
             *reinterpret_cast<uint4*>(to + mine * 128 + ((chunk ^ (mine & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
-            const float of = __shfl_sync(~0u, down, (lane % kAtOnce) * kPer);
-            if (lane / kAtOnce == i0 + i) f = of * fabsf(to_log2);
+            if (sub_lane == 0) factors[mine] = down * fabsf(to_log2);
           }
         }
         fence_async();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.q_full));
+        if (lane == 0) mbar_arrive(smem_u32(&s.q_full[t]));
+        f = factors[lane];
       }
-      const RowView view = row_view(a, tile, row);
-      const int w0 = (tile.row0 + sub) / a.group, w1 = (tile.row0 + max(min(sub + 128, tile.rows), sub + 1) - 1) / a.group, past = tile.len - tile.tokens;
-      const int free_hi = a.tree ? min(past, past + w0 + 1) : a.causal ? min(past + w0 + 1, tile.len) : tile.len;
-      const int free_lo = a.window ? max(past + w1 - a.window + 1, 0) : 0;
+      {
+        const int w0 = (tile.row0 + sub) / a.group, w1 = (tile.row0 + max(min(sub + 128, tile.rows), sub + 1) - 1) / a.group, past = tile.len - tile.tokens;
+        const int hi = a.tree ? min(past, past + w0 + 1) : a.causal ? min(past + w0 + 1, tile.len) : tile.len;
+        const int lo = a.window ? max(past + w1 - a.window + 1, 0) : 0;
+        if (lane == 0) {
+          walk.free_hi = hi;
+          walk.free_lo = lo;
+        }
+        __syncwarp();
+      }
       float m = kNoKey;
       float2 l = make_float2(0.f, 0.f);
       for (int u = sg.u0; u < sg.u1; ++u, ++n) {
         const int key0 = (tile.unit0 + u) * kBlock;
-        await(c, smem_u32(&s.s_full[t]), n & 1, dead);
-        dead = __any_sync(~0u, dead);
+        // both barriers belong to the score buffer: with one of each a tile, two blocks' scores could be turned into P
+        // before the issuing thread has looked for the first, and it would miss that phase
+        const int sb = t * S::kSBufs + n % S::kSBufs;
+        await(c, smem_u32(&s.s_full[sb]), n / S::kSBufs & 1, dead);
         fence_after();
         if (idle) {
           fence_before();
-          if (lane == 0) mbar_arrive(smem_u32(&s.p_full[t]));
+          if (lane == 0) mbar_arrive(smem_u32(&s.p_full[sb]));
           continue;
         }
-        const bool masked = key0 < free_lo || key0 + kBlock > free_hi;
-        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+        const uint32_t st = tmem + sb * kBlock + lanes;
+        const bool masked = key0 < walk.free_lo || key0 + kBlock > walk.free_hi;
+        uint32_t seen[2] = {~0u, ~0u};
         if (masked) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) seen[i] = sees32(a, view, key0 + 32 * i);
+          const RowView view = row_view(a, tile, tile.row0 + r);
+          seen[0] = sees32(a, view, key0);
+          seen[1] = sees32(a, view, key0 + 32);
           __syncwarp();
         }
-        float top = masked ? row_max<true>(st, seen) : row_max<false>(st, seen);
-        top = top == -INFINITY ? top : top * f;  // -inf: nothing seen, whatever f is
-        const bool raise = top > m + kSlack;
-        if (__any_sync(~0u, raise)) {
-          const float now = raise ? top - kBias : m, rr = ex2(m - now);
-          m = now;
+        if (__any_sync(~0u, m == kNoKey)) {  // a row's first keys: its reference is their maximum
+          const float top = masked ? row_max<true>(st, seen) : row_max<false>(st, seen);
+          if (m == kNoKey && top != -INFINITY) m = top * f - kBias;
+        }
+        uint32_t p[2][16];
+        float2 sum;
+        const float top = masked ? row_exp<true>(st, seen, f, m, sum, p) : row_exp<false>(st, seen, f, m, sum, p);
+        if (__any_sync(~0u, top > kSlack)) {  // some p came out too large: the reference goes up, what there is comes down, once more
+          const float up = top > kSlack ? top - kBias : 0.0f, rr = ex2(-up);
+          m += up;
           l.x *= rr;
           l.y *= rr;
-          if (u > sg.u0) {  // the products before this block's are done: its scores were issued after them
+          if (u > sg.u0) {
+            await(c, smem_u32(&s.pv_done[t * S::kSBufs + (n - 1) % S::kSBufs]), (n - 1) / S::kSBufs & 1, dead);
+            fence_after();
 #pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) {
-              uint32_t x[32];
-              tmem_load32(ot + i * 32, x);
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t x[16];
+              tmem_load16(ot + i * 16, x);
               tmem_wait_load(x);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * rr);
-              tmem_store32(ot + i * 32, x);
+              for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * rr);
+              tmem_store16(ot + i * 16, x);
             }
           }
+          masked ? row_exp<true>(st, seen, f, m, sum, p) : row_exp<false>(st, seen, f, m, sum, p);
         }
-        if (masked) row_exp<true>(st, seen, f, m, l);
-        else row_exp<false>(st, seen, f, m, l);
+        l = add2(l, sum);
+        tmem_store16(st, p[0]);  // over the scores
+        tmem_store16(st + 16, p[1]);
+        tmem_wait_store();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.p_full[t]));
+        if (lane == 0) mbar_arrive(smem_u32(&s.p_full[sb]));
       }
       await(c, smem_u32(&s.o_full[t]), seg & 1, dead);
-      dead = __any_sync(~0u, dead);
       ++seg;
       fence_after();
+      const int row = tile.row0 + r;
+      const bool live = r < tile.rows;
+      const int tok = row / a.group, head = sg.h * a.group + row % a.group;
       const bool whole = sg.u0 == 0 && sg.u1 == tile.units;
       const float ll = l.x + l.y;
       constexpr int kPart = S::kRows * (D + 2);
@@ -589,31 +598,30 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), (Shape<D, TILES>:
       const float gv = c.v_scale[sg.h];
       float* part = c.partial + (int64_t)(2 * blockIdx.x + (sg.head_at + sg.u0 == begin ? 0 : 1)) * kPart;
       const float scale = whole ? (ll != 0.0f ? gv / ll : 0.0f) : 1.0f;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t x[32];
-        tmem_load32(ot + i * 32, x);
+#pragma unroll 1
+      for (int i = 0; i < D / 16; ++i) {
+        uint32_t x[16];
+        tmem_load16(ot + i * 16, x);
         tmem_wait_load(x);
-#pragma unroll
-        for (int b = 0; b < 2 && live; ++b) {  // 16 channels: column i and column 8 + i are channels 2i and 2i + 1
+        if (live) {  // 16 channels: columns k and 8 + k are channels 2k and 2k + 1
           float y[16];
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            y[2 * k] = __uint_as_float(x[b * 16 + k]) * scale;
-            y[2 * k + 1] = __uint_as_float(x[b * 16 + 8 + k]) * scale;
+            y[2 * k] = __uint_as_float(x[k]) * scale;
+            y[2 * k + 1] = __uint_as_float(x[8 + k]) * scale;
           }
           if (whole) {
             if (ll == 0.0f) {
 #pragma unroll
               for (int k = 0; k < 16; ++k) y[k] = 0.0f;
             }
-            uint16_t* to = static_cast<uint16_t*>(a.out) + out_row * D + i * 32 + b * 16;
+            uint16_t* to = static_cast<uint16_t*>(a.out) + out_row * D + i * 16;
 #pragma unroll
             for (int k = 0; k < 16; k += 8)
               *reinterpret_cast<uint4*>(to + k) = make_uint4(pack16(y[k], y[k + 1], a.dtype), pack16(y[k + 2], y[k + 3], a.dtype),
                                                              pack16(y[k + 4], y[k + 5], a.dtype), pack16(y[k + 6], y[k + 7], a.dtype));
           } else {
-            float* to = part + 2 * S::kRows + r * D + i * 32 + b * 16;
+            float* to = part + 2 * S::kRows + r * D + i * 16;
 #pragma unroll
             for (int k = 0; k < 16; k += 4) __stcg(reinterpret_cast<float4*>(to + k), make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]));
           }
@@ -698,7 +706,7 @@ int launch(const HostCache& h, AttendArgs a, int max_q) {
   const int64_t tiles = ((int64_t)max_q * a.group + S::kRows - 1) / S::kRows;
   if (tiles * a.n >= INT_MAX) return WHEAD_ERR_UNSUPPORTED;
   a.row_tiles = (int)tiles;
-  int64_t ctas = std::min<int64_t>((int64_t)h.sms * S::kCtas, kMaxCtas);
+  int64_t ctas = std::min<int64_t>((int64_t)h.sms, kMaxCtas);
   ctas = std::min(ctas, h.c.partial_floats / (2 * S::kRows * (D + 2)));
   a.planned = tiles * a.n > 2 * S::kThreads;
   if (a.planned) attend_plan<kBlock><<<1, 1024, 0, h.stream>>>(h.c, a, S::kRows, (int)ctas);
