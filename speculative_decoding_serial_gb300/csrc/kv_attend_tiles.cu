@@ -1,12 +1,12 @@
 // kv_attend_tiles.cu — attention over the 4-bit paged cache for many query rows: 128 rows a tile on the tensor cores' tcgen05
 // instructions, with scores and outputs in tensor memory.
 //
-// The mathematics is kv_attend.cu's. A block is 64 keys. Two teams of four warps turn the codes of alternate blocks into f16 tiles
-// in shared memory, which TILES tiles of 128 rows then share; one thread issues the products S = Q K^T and O += P V; four warps a
-// tile read S, a row a thread, and put P where S was. From P's store over PV, the next QK and back to the softmax is about 1.5 us,
-// most of it hand-overs, so scores are kept ahead: tensor memory holds four S (64 columns each) beside the outputs, two or four for
-// a tile. With blocks of 128 keys there is room for one a tile, and the softmax waits for every hand-over (2.8 us for 256 rows
-// and 128 keys, against MEASURED now).
+// The mathematics is kv_attend.cu's. A block is 128 keys. Eight warps turn its codes into f16 tiles in shared memory, which TILES
+// tiles of 128 rows then share; a warp a tile issues the products S = Q K^T and O += P V; four warps a tile read S, a row a thread,
+// and put P where S was. Tensor memory holds two S (128 columns each) beside the outputs: with two tiles one tile's softmax runs under
+// the other's products, with one tile (at most 128 rows) the next block's scores are there when a block's softmax ends. An issuing
+// warp needs some 1,100 cycles a block beside the products themselves (waits on barriers that are ready, commits): blocks of 64 keys,
+// which leave room for twice as many S, cost 2,200 cycles each and are slower.
 //
 // Shared memory holds operands in rows of 128 bytes (64 f16), 8 rows to an atom of 1024 bytes, 16-byte chunks swizzled by the row.
 // Channels 16 b + 8 s .. + 7 of a query row or key lie in chunk 4 s + b % 4 of the row, not 2 b + s: a warp's stores of a block's keys
@@ -21,7 +21,7 @@ namespace whead_kv_impl {
 
 namespace {
 
-constexpr int kBlock = 64;       // keys
+constexpr int kBlock = 128;      // keys
 constexpr float kBias = 7.0f;    // as in kv_attend.cu
 constexpr float kSlack = 15.0f;
 constexpr float kNoKey = -1e30f;
@@ -29,10 +29,10 @@ constexpr float kNoKey = -1e30f;
 template <int D, int TILES>
 struct Shape {
   static constexpr int kRows = 128 * TILES;
-  static constexpr int kSBufs = 4 / TILES;               // score buffers of a tile
-  static constexpr int kBufs = 4;                        // key and value tiles
+  static constexpr int kSBufs = 2 / TILES;               // score buffers of a tile
+  static constexpr int kBufs = 2;                        // key and value tiles
   static constexpr int kSoft = 4 * TILES;                // softmax warps, then those that unpack, then one a tile that issues
-  static constexpr int kUnpack = 8;                      // a group of every other block to each
+  static constexpr int kUnpack = 8;                      // a group of each block to each
   static constexpr int kIssue = kSoft + kUnpack;
   static constexpr int kThreads = (kIssue + TILES) * 32;
   static constexpr int kGroup = 18 * D;
@@ -46,7 +46,7 @@ struct Shape {
 
 struct Head {
   SchedShared sched;
-  unsigned long long k_full[4], k_free[4], v_full[4], v_free[4], s_full[4], p_full[4], pv_done[4], o_full[2], q_full[2], drain[2];
+  unsigned long long k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[4], pv_done[4], o_full[2], q_full[2], drain[2];
   uint32_t tmem;
 };
 
@@ -73,7 +73,7 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// 16 columns of this warp's lanes
+// 16 columns of this warp's lanes; the registers are operands of the wait, so that no use of them moves before it
 __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&x)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]),
@@ -238,9 +238,11 @@ static_assert(sizeof(Head) <= 640 && 640 + 18 * sizeof(Walk) <= 3072, "");
 
 // A whole warp's wait. One that has run out is reported once; the warp then goes on without waiting, on whatever is there, to its end.
 __device__ __forceinline__ void await(const Cache& c, uint32_t bar, uint32_t parity, bool& dead) {
-  if (!dead && !__all_sync(~0u, mbar_wait(bar, parity))) {
-    set_status(c, WHEAD_ERR_TIMEOUT);
-    dead = true;
+  while (!dead && !__all_sync(~0u, mbar_try(bar, parity))) {
+    if (!__all_sync(~0u, mbar_wait(bar, parity))) {
+      set_status(c, WHEAD_ERR_TIMEOUT);
+      dead = true;
+    }
   }
 }
 
@@ -264,16 +266,16 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
   Head& s = *reinterpret_cast<Head*>(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(~0u, tid >> 5, 0);
   if (tid == 0) {
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&s.k_full[i]), 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s.k_full[i]), S::kUnpack);
       mbar_init(smem_u32(&s.k_free[i]), TILES);
-      mbar_init(smem_u32(&s.v_full[i]), 4);
+      mbar_init(smem_u32(&s.v_full[i]), S::kUnpack);
       mbar_init(smem_u32(&s.v_free[i]), TILES);
       mbar_init(smem_u32(&s.s_full[i]), 1);
-      mbar_init(smem_u32(&s.p_full[i]), 4);
-      mbar_init(smem_u32(&s.pv_done[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(smem_u32(&s.p_full[2 * i + h]), 4);
+        mbar_init(smem_u32(&s.pv_done[2 * i + h]), 1);
+      }
       mbar_init(smem_u32(&s.o_full[i]), 1);
       mbar_init(smem_u32(&s.q_full[i]), 4);
       mbar_init(smem_u32(&s.drain[i]), 1);
@@ -316,7 +318,6 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
     auto scores = [&](int n) {
       const int buf = n % S::kBufs, sb = n % S::kSBufs;
       await(c, smem_u32(&s.k_full[buf]), n / S::kBufs & 1, dead);
-      if (dead) return;
       fence_after();
       const uint64_t db = dk + (uint64_t)(buf * (S::kK >> 4));
 #pragma unroll
@@ -326,26 +327,31 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       commit(smem_u32(&s.k_free[buf]), leader);
     };
     int n = 0, seg = 0;
-    while (!dead && next_segment<S::kRows>(c, a, walk)) {
-      const int first = n, last = n + sg.u1 - sg.u0;  // blocks first .. last - 1; scores are kSBufs ahead of outputs
+    while (next_segment<S::kRows>(c, a, walk)) {
+      // blocks first .. last - 1; scores are kSBufs ahead of outputs
+      const int first = n, last = n + __shfl_sync(~0u, sg.u1 - sg.u0, 0);
       await(c, smem_u32(&s.q_full[t]), seg & 1, dead);
       fence_after();
-      for (int i = n; i < min(n + S::kSBufs, last) && !dead; ++i) scores(i);
-      for (; n < last && !dead; ++n) {
-        const int buf = n % S::kBufs, sb = n % S::kSBufs;
+#pragma unroll 1
+      for (int i = first; i < min(first + S::kSBufs, last); ++i) scores(i);
+#pragma unroll 1
+      for (; n < last; ++n) {
+        const int buf = n % S::kBufs, sb = n % S::kSBufs, half0 = (t * S::kSBufs + sb) * 2;
         await(c, smem_u32(&s.v_full[buf]), n / S::kBufs & 1, dead);
-        await(c, smem_u32(&s.p_full[t * S::kSBufs + sb]), n / S::kSBufs & 1, dead);
-        if (dead) break;
-        fence_after();
         const uint64_t db = dv + (uint64_t)(buf * (S::kV >> 4));
 #pragma unroll
-        for (int k = 0; k < kBlock / 16; ++k)
-          mma_ts(o_col, s_col + sb * kBlock + k * 8, db + k * 2, kPV, n > first || k > 0, leader);
-        commit(smem_u32(&s.pv_done[t * S::kSBufs + sb]), leader);
+        for (int h = 0; h < 2; ++h) {
+          await(c, smem_u32(&s.p_full[half0 + h]), n / S::kSBufs & 1, dead);
+          fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts(o_col, s_col + sb * kBlock + h * 64 + k * 8, db + (h * (D * 128) + k * 32) / 16, kPV, n > first || h + k > 0, leader);
+          commit(smem_u32(&s.pv_done[half0 + h]), leader);
+        }
         commit(smem_u32(&s.v_free[buf]), leader);
         if (n + S::kSBufs < last) scores(n + S::kSBufs);
-        if (n == last - 1) commit(smem_u32(&s.o_full[t]), leader);
       }
+      commit(smem_u32(&s.o_full[t]), leader);
       ++seg;
     }
     // nothing may be under way when the CTA gives its tensor memory back
@@ -354,15 +360,15 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
     mbar_wait(smem_u32(&s.drain[t]), 0);
     __syncwarp();
   } else if (warp >= S::kSoft) {
-    // ---- codes to f16 tiles: group w of every other block, by the block's number in the CTA's range
-    const int w = (warp - S::kSoft) & 3, team = (warp - S::kSoft) >> 2, g = lane >> 2, t = lane & 3;
+    // ---- codes to f16 tiles: group w of each block
+    const int w = warp - S::kSoft, g = lane >> 2, t = lane & 3;
     const int64_t page_bytes = (int64_t)c.kv_heads * (c.page_size >> 4) * S::kGroup;
     int n = 0;
     while (next_segment<S::kRows>(c, a, walk)) {
       const int32_t* table = c.tables + (int64_t)sg.tile.slot * c.max_pages;
       const uint8_t* base = c.pool + (int64_t)sg.h * (c.page_size >> 4) * S::kGroup;
       const int len = sg.tile.len, stop = min((sg.tile.unit0 + sg.u1) * kBlock, len);
-      // codes come one of the team's blocks ahead of the tiles, the numbers of their pages two
+      // codes come one block ahead of the tiles, the numbers of their pages two
       RawK<D> rk;
       RawV<D> rv;
       int page;
@@ -397,17 +403,16 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
           rv.scale[j] = __ldg(reinterpret_cast<const uint4*>(gp + 17 * D + t * 4 * NB) + j);
         }
       };
-      const int blocks = sg.u1 - sg.u0, skip = (n ^ team) & 1;  // the team's first block of the segment: 0 or 1
-      int u = sg.tile.unit0 + sg.u0 + skip;
       const int end = sg.tile.unit0 + sg.u1;
+      int u = sg.tile.unit0 + sg.u0;
       look(u);
       fetch_k(u);
       fetch_v(u);
-      look(u + 2);
-      for (int k = n + skip; u < end; u += 2, k += 2) {
-        const int buf = k % S::kBufs, key0 = u * kBlock + w * 16;
-        const uint32_t used = (k / S::kBufs - 1) & 1;
-        if (k >= S::kBufs) await(c, smem_u32(&s.k_free[buf]), used, dead);
+      look(u + 1);
+      for (; u < end; ++u, ++n) {
+        const int buf = n % S::kBufs, key0 = u * kBlock + w * 16;
+        const uint32_t used = (n / S::kBufs - 1) & 1;
+        if (n >= S::kBufs) await(c, smem_u32(&s.k_free[buf]), used, dead);
         if (key0 < len) {
           uint8_t* to = smem + S::kOffK + buf * S::kK + w * 2048 + g * 128 + (t & 1) * 8;
 #pragma unroll
@@ -425,8 +430,8 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.k_full[buf]));
-        fetch_k(u + 2);
-        if (k >= S::kBufs) await(c, smem_u32(&s.v_free[buf]), used, dead);
+        fetch_k(u + 1);
+        if (n >= S::kBufs) await(c, smem_u32(&s.v_free[buf]), used, dead);
         // what lies past the length may be anything: it becomes zero, so that 0 x NaN does not arise
         uint32_t live = ~0u;
         if (key0 + 16 > len) {
@@ -436,8 +441,8 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
             if (key0 + 2 * t + (i & 1) + (i >> 1) * 8 < len) live |= 0xFFu << (8 * i);
           __syncwarp();
         }
-        uint8_t* to = smem + S::kOffV + buf * S::kV + g * 128 + t * 4;
-        const int c0 = ((w * 2) ^ g) << 4, c1 = ((w * 2 + 1) ^ g) << 4;
+        uint8_t* to = smem + S::kOffV + buf * S::kV + w / 4 * (D * 128) + g * 128 + t * 4;
+        const int c0 = ((w % 4 * 2) ^ g) << 4, c1 = ((w % 4 * 2 + 1) ^ g) << 4;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           const uint4 vw = rv.code[b / 4], vs = rv.scale[b / 4];
@@ -453,10 +458,9 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
         fence_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.v_full[buf]));
-        fetch_v(u + 2);
-        look(u + 4);
+        fetch_v(u + 1);
+        look(u + 2);
       }
-      n += blocks;
     }
   } else {
     // ---- softmax: a thread a row
@@ -531,59 +535,65 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       float2 l = make_float2(0.f, 0.f);
       for (int u = sg.u0; u < sg.u1; ++u, ++n) {
         const int key0 = (tile.unit0 + u) * kBlock;
-        // both barriers belong to the score buffer: with one of each a tile, two blocks' scores could be turned into P
-        // before the issuing thread has looked for the first, and it would miss that phase
+        // these barriers belong to the score buffer: with one of each a tile, two blocks' scores could be turned into P
+        // before the issuing warp has looked for the first, and it would miss that phase
         const int sb = t * S::kSBufs + n % S::kSBufs;
         await(c, smem_u32(&s.s_full[sb]), n / S::kSBufs & 1, dead);
         fence_after();
-        if (idle) {
-          fence_before();
-          if (lane == 0) mbar_arrive(smem_u32(&s.p_full[sb]));
-          continue;
-        }
-        const uint32_t st = tmem + sb * kBlock + lanes;
-        const bool masked = key0 < walk.free_lo || key0 + kBlock > walk.free_hi;
-        uint32_t seen[2] = {~0u, ~0u};
-        if (masked) {
-          const RowView view = row_view(a, tile, tile.row0 + r);
-          seen[0] = sees32(a, view, key0);
-          seen[1] = sees32(a, view, key0 + 32);
-          __syncwarp();
-        }
-        if (__any_sync(~0u, m == kNoKey)) {  // a row's first keys: its reference is their maximum
-          const float top = masked ? row_max<true>(st, seen) : row_max<false>(st, seen);
-          if (m == kNoKey && top != -INFINITY) m = top * f - kBias;
-        }
-        uint32_t p[2][16];
-        float2 sum;
-        const float top = masked ? row_exp<true>(st, seen, f, m, sum, p) : row_exp<false>(st, seen, f, m, sum, p);
-        if (__any_sync(~0u, top > kSlack)) {  // some p came out too large: the reference goes up, what there is comes down, once more
-          const float up = top > kSlack ? top - kBias : 0.0f, rr = ex2(-up);
-          m += up;
-          l.x *= rr;
-          l.y *= rr;
-          if (u > sg.u0) {
-            await(c, smem_u32(&s.pv_done[t * S::kSBufs + (n - 1) % S::kSBufs]), (n - 1) / S::kSBufs & 1, dead);
-            fence_after();
+        // half a block at a time, each with its own P over its own scores: the first half's products run under the second's softmax
 #pragma unroll 1
-            for (int i = 0; i < D / 16; ++i) {
-              uint32_t x[16];
-              tmem_load16(ot + i * 16, x);
-              tmem_wait_load(x);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * rr);
-              tmem_store16(ot + i * 16, x);
-            }
+        for (int h = 0; h < 2; ++h) {
+          if (idle) {
+            fence_before();
+            if (lane == 0) mbar_arrive(smem_u32(&s.p_full[2 * sb + h]));
+            continue;
           }
-          masked ? row_exp<true>(st, seen, f, m, sum, p) : row_exp<false>(st, seen, f, m, sum, p);
+          const uint32_t st = tmem + sb * kBlock + h * 64 + lanes;
+          const int key = key0 + h * 64;
+          const bool masked = key < walk.free_lo || key + 64 > walk.free_hi;
+          uint32_t seen[2] = {~0u, ~0u};
+          if (masked) {
+            const RowView view = row_view(a, tile, tile.row0 + r);
+            seen[0] = sees32(a, view, key);
+            seen[1] = sees32(a, view, key + 32);
+            __syncwarp();
+          }
+          if (__any_sync(~0u, m == kNoKey)) {  // a row's first keys: its reference is their maximum
+            const float top = masked ? row_max<true>(st, seen) : row_max<false>(st, seen);
+            if (m == kNoKey && top != -INFINITY) m = top * f - kBias;
+          }
+          uint32_t p[2][16];
+          float2 sum;
+          const float top = masked ? row_exp<true>(st, seen, f, m, sum, p) : row_exp<false>(st, seen, f, m, sum, p);
+          if (__any_sync(~0u, top > kSlack)) {  // some p came out too large: the reference goes up, what there is comes down, once more
+            const float up = top > kSlack ? top - kBias : 0.0f, rr = ex2(-up);
+            m += up;
+            l.x *= rr;
+            l.y *= rr;
+            if (u > sg.u0 || h > 0) {  // after the products of the half before
+              const int nb = h ? n : n - 1;
+              await(c, smem_u32(&s.pv_done[(t * S::kSBufs + nb % S::kSBufs) * 2 + (h ^ 1)]), nb / S::kSBufs & 1, dead);
+              fence_after();
+#pragma unroll 1
+              for (int i = 0; i < D / 16; ++i) {
+                uint32_t x[16];
+                tmem_load16(ot + i * 16, x);
+                tmem_wait_load(x);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * rr);
+                tmem_store16(ot + i * 16, x);
+              }
+            }
+            masked ? row_exp<true>(st, seen, f, m, sum, p) : row_exp<false>(st, seen, f, m, sum, p);
+          }
+          l = add2(l, sum);
+          tmem_store16(st, p[0]);  // over the scores
+          tmem_store16(st + 16, p[1]);
+          tmem_wait_store();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s.p_full[2 * sb + h]));
         }
-        l = add2(l, sum);
-        tmem_store16(st, p[0]);  // over the scores
-        tmem_store16(st + 16, p[1]);
-        tmem_wait_store();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s.p_full[sb]));
       }
       await(c, smem_u32(&s.o_full[t]), seg & 1, dead);
       ++seg;
