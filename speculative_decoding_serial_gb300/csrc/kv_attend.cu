@@ -158,10 +158,14 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
   // the segment that begins at unit `at`, and the first copies of this warp's groups; `fresh`: not the next head of the same tile
   auto enter = [&](long long at, bool fresh) {
     if (fresh) {
-      while (true) {
-        sg.tile = make_tile<kUnit>(c, a, item, ROWS);
-        if (sg.tile.units > 0) break;
-        ++item;
+      if (item == s.sched.item && s.sched.has_tile) {
+        sg.tile = s.sched.tile;
+      } else {
+        while (true) {
+          sg.tile = make_tile<kUnit>(c, a, item, ROWS);
+          if (sg.tile.units > 0) break;
+          ++item;
+        }
       }
       const int past_item = (int)(at - item_at);
       sg.h = past_item / sg.tile.units;
@@ -206,7 +210,8 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
       if (nt < NT) {
         const int row = tile.row0 + nt * 8 + g;
         const bool live = nt * 8 + g < tile.rows;
-        const int64_t at = live ? (int64_t)(tile.first + row / a.group) * a.q_token_stride + (int64_t)(h * a.group + row % a.group) * a.q_head_stride : 0;
+        const int tok = row_token(a, row);
+        const int64_t at = live ? (int64_t)(tile.first + tok) * a.q_token_stride + (int64_t)(h * a.group + row - tok * a.group) * a.q_head_stride : 0;
         float x[NB][4], big = 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         for (int k = 0; k < 4; ++k) o[nt][b][k] = 0.0f;
     }
     // keys that every row sees need no looking at masks
-    const int t0 = tile.row0 / a.group, t1 = (tile.row0 + tile.rows - 1) / a.group, past = tile.len - tile.tokens;
+    const int t0 = row_token(a, tile.row0), t1 = row_token(a, tile.row0 + tile.rows - 1), past = tile.len - tile.tokens;
     const int free_hi = a.tree ? min(past, past + t0 + 1) : a.causal ? min(past + t0 + 1, tile.len) : tile.len;
     const int free_lo = a.window ? max(past + t1 - a.window + 1, 0) : 0;
     // G neighbouring groups at a time, from key0 on
@@ -478,7 +483,8 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
     const float gv = c.v_scale[h];
     auto write_row = [&](int row, int col, float4 v, float mm, float ll) {
       const int grow = tile.row0 + row;
-      const int64_t at = (int64_t)(tile.first + grow / a.group) * a.heads + h * a.group + grow % a.group;
+      const int tok = row_token(a, grow);
+      const int64_t at = (int64_t)(tile.first + tok) * a.heads + h * a.group + grow - tok * a.group;
       const float r = ll != 0.0f ? gv / ll : 0.0f;
       if (ll == 0.0f) v = make_float4(0.f, 0.f, 0.f, 0.f);
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + col) =
@@ -640,8 +646,27 @@ extern "C" int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* x
   const int group = x->heads / kv->kv_heads;
   const int64_t rows = (int64_t)x->max_q * group;
   if (rows >= INT_MAX / 2) return WHEAD_ERR_UNSUPPORTED;
-  AttendArgs a{x->q, x->out, x->lse, x->indptr, x->slots, reinterpret_cast<const unsigned long long*>(x->tree), x->total, x->q_token_stride,
-               x->q_head_stride, x->n, x->heads, group, 1, x->dtype, x->causal, x->window, x->tree_words, x->scale, false, 0};
+  AttendArgs a{};
+  a.q = x->q;
+  a.out = x->out;
+  a.lse = x->lse;
+  a.indptr = x->indptr;
+  a.slots = x->slots;
+  a.tree = reinterpret_cast<const unsigned long long*>(x->tree);
+  a.total = x->total;
+  a.q_token_stride = x->q_token_stride;
+  a.q_head_stride = x->q_head_stride;
+  a.n = x->n;
+  a.each = (int)(x->total / x->n);
+  a.heads = x->heads;
+  set_group(&a, group);
+  a.row_tiles = 1;
+  a.dtype = x->dtype;
+  a.causal = x->causal;
+  a.window = x->window;
+  a.tree_words = x->tree_words;
+  a.scale = x->scale;
+  a.wide_q16 = aligned(x->q, 16) && x->q_token_stride % 8 == 0 && x->q_head_stride % 8 == 0;
   a.wide_q = aligned(x->q, 8) && x->q_token_stride % 4 == 0 && x->q_head_stride % 4 == 0;
   if (rows > 32 && kv->head_dim <= 128) return launch_tiles(h, a, x->max_q);
   const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;

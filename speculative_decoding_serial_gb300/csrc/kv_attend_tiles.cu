@@ -16,6 +16,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 namespace whead_kv_impl {
 
@@ -31,10 +32,10 @@ struct Shape {
   static constexpr int kRows = 128 * TILES;
   static constexpr int kSBufs = 2 / TILES;               // score buffers of a tile
   static constexpr int kBufs = 2;                        // key and value tiles
-  static constexpr int kSoft = 4 * TILES;                // softmax warps, then those that unpack, then one a tile that issues
+  static constexpr int kSoft = 4 * TILES;                // softmax warps, then those that unpack, then two that issue: one a tile, or with one tile one for QK and one for PV
   static constexpr int kUnpack = 8;                      // a group of each block to each
   static constexpr int kIssue = kSoft + kUnpack;
-  static constexpr int kThreads = (kIssue + TILES) * 32;
+  static constexpr int kThreads = (kIssue + 2) * 32;
   static constexpr int kGroup = 18 * D;
   static constexpr int kQ = 128 * D * 2, kK = kBlock * D * 2, kV = D * kBlock * 2;
   static constexpr int kOffWalk = 640;                   // the warps' places
@@ -141,11 +142,13 @@ __device__ __forceinline__ float row_exp(uint32_t st, const uint32_t (&seen)[2],
   const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
   float2 s0 = make_float2(0.f, 0.f), s1 = s0;
   float t0 = -INFINITY, t1 = -INFINITY;
+  uint32_t ahead[2][16];
+  tmem_load16(st, ahead[0]);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {  // 16 columns at a time: registers are short, and what spills misses the small L1
-    uint32_t x[16];
-    tmem_load16(st + i * 16, x);
+    uint32_t (&x)[16] = ahead[i & 1];
     tmem_wait_load(x);
+    if (i < 3) tmem_load16(st + i * 16 + 16, ahead[(i + 1) & 1]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       float2 d = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, m2);
@@ -200,20 +203,23 @@ struct Walk {
   long long cur, end, item_at;
   int next_item;
   Segment sg;
-  int free_lo, free_hi;  // keys that all rows of a softmax warp's tile see
 };
 
 // The next segment, by a whole warp; false at the end.
 template <int ROWS>
-__device__ __forceinline__ bool next_segment(const Cache& c, const AttendArgs& a, Walk& w) {
+__device__ __forceinline__ bool next_segment(const Cache& c, const AttendArgs& a, Walk& w, const SchedShared& sched) {
   const long long cur = w.cur, end = w.end;
   if (cur >= end) return false;
   int item = w.next_item;
   Segment s;
-  while (true) {
-    s.tile = make_tile<kBlock>(c, a, item, ROWS);
-    if (s.tile.units > 0) break;
-    ++item;
+  if (item == sched.item && sched.has_tile) {
+    s.tile = sched.tile;
+  } else {
+    while (true) {
+      s.tile = make_tile<kBlock>(c, a, item, ROWS);
+      if (s.tile.units > 0) break;
+      ++item;
+    }
   }
   s.item = item;
   const long long item_at = w.item_at;
@@ -311,7 +317,8 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
     // ---- a tile's products
     constexpr uint32_t kQK = (1u << 4) | ((kBlock / 8u) << 17) | ((128u / 16u) << 24);  // fp32 from f16 x f16, both along k
     constexpr uint32_t kPV = (1u << 4) | ((D / 8u) << 17) | ((128u / 16u) << 24);
-    const int t = warp - S::kIssue;
+    const int t = TILES == 1 ? 0 : warp - S::kIssue;
+    const bool does_qk = TILES == 2 || warp == S::kIssue, does_pv = TILES == 2 || warp != S::kIssue;
     const uint32_t leader = lane == 0;
     const uint64_t dq = tile_desc(smem_u32(smem + S::kOffQ) + t * S::kQ), dk = tile_desc(smem_u32(smem + S::kOffK)), dv = tile_desc(smem_u32(smem + S::kOffV));
     const uint32_t s_col = tmem + t * S::kSBufs * kBlock, o_col = tmem + 256 + t * 128;
@@ -327,13 +334,24 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       commit(smem_u32(&s.k_free[buf]), leader);
     };
     int n = 0, seg = 0;
-    while (next_segment<S::kRows>(c, a, walk)) {
+    while (next_segment<S::kRows>(c, a, walk, s.sched)) {
       // blocks first .. last - 1; scores are kSBufs ahead of outputs
       const int first = n, last = n + __shfl_sync(~0u, sg.u1 - sg.u0, 0);
-      await(c, smem_u32(&s.q_full[t]), seg & 1, dead);
-      fence_after();
+      if (does_qk) {
+        await(c, smem_u32(&s.q_full[t]), seg & 1, dead);
+        fence_after();
 #pragma unroll 1
-      for (int i = first; i < min(first + S::kSBufs, last); ++i) scores(i);
+        for (int i = first; i < (does_pv ? min(first + S::kSBufs, last) : last); ++i) {
+          // alone, this warp does not follow the products that read what was in the score buffer: it waits for them
+          if (!does_pv && i >= S::kSBufs) await(c, smem_u32(&s.pv_done[i % S::kSBufs * 2 + 1]), (i - S::kSBufs) / S::kSBufs & 1, dead);
+          scores(i);
+        }
+      }
+      if (!does_pv) {
+        n = last;
+        ++seg;
+        continue;
+      }
 #pragma unroll 1
       for (; n < last; ++n) {
         const int buf = n % S::kBufs, sb = n % S::kSBufs, half0 = (t * S::kSBufs + sb) * 2;
@@ -349,22 +367,23 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
           commit(smem_u32(&s.pv_done[half0 + h]), leader);
         }
         commit(smem_u32(&s.v_free[buf]), leader);
-        if (n + S::kSBufs < last) scores(n + S::kSBufs);
+        if (does_qk && n + S::kSBufs < last) scores(n + S::kSBufs);
       }
       commit(smem_u32(&s.o_full[t]), leader);
       ++seg;
     }
     // nothing may be under way when the CTA gives its tensor memory back
     __syncwarp();
-    commit(smem_u32(&s.drain[t]), leader);
-    mbar_wait(smem_u32(&s.drain[t]), 0);
+    const uint32_t drain = smem_u32(&s.drain[warp - S::kIssue]);
+    commit(drain, leader);
+    mbar_wait(drain, 0);
     __syncwarp();
   } else if (warp >= S::kSoft) {
     // ---- codes to f16 tiles: group w of each block
     const int w = warp - S::kSoft, g = lane >> 2, t = lane & 3;
     const int64_t page_bytes = (int64_t)c.kv_heads * (c.page_size >> 4) * S::kGroup;
     int n = 0;
-    while (next_segment<S::kRows>(c, a, walk)) {
+    while (next_segment<S::kRows>(c, a, walk, s.sched)) {
       const int32_t* table = c.tables + (int64_t)sg.tile.slot * c.max_pages;
       const uint8_t* base = c.pool + (int64_t)sg.h * (c.page_size >> 4) * S::kGroup;
       const int len = sg.tile.len, stop = min((sg.tile.unit0 + sg.u1) * kBlock, len);
@@ -470,67 +489,83 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
     const uint32_t ot = tmem + 256 + t * 128 + lanes;
     float* factors = reinterpret_cast<float*>(smem + S::kOffF) + sub + quarter * 32;
     int n = 0, seg = 0;
-    while (next_segment<S::kRows>(c, a, walk)) {
+    while (next_segment<S::kRows>(c, a, walk, s.sched)) {
       const Tile& tile = sg.tile;
       const bool idle = quarter * 32 + sub >= tile.rows;  // no row of this warp is one: its part of P may be anything
       float f;
       {
-        // the warp's query rows, from a power of two to f16; a row is kPer lanes with 8 channels each, kAtOnce rows a load. The
-        // sign of the scale goes into the rows, so that f is positive and scores need it only after their maximum is known.
-        constexpr int kPer = D / 8, kAtOnce = 32 / kPer, kTurns = 16 / kAtOnce;  // 16 rows at a time
+        // the warp's query rows: a row is kPer lanes with 8 channels each, kAtOnce rows a turn. They come as they are to where they will
+        // stand and are then turned, in place, from a power of two to f16. The sign of the scale goes into the rows, so that f is positive
+        // and scores need it only after their maximum is known.
+        constexpr int kPer = D / 8, kAtOnce = 32 / kPer, kTurns = 32 / kAtOnce;
         const float to_log2 = a.scale * c.k_scale[sg.h] * kLog2e;
-        const int row = tile.row0 + r;
-        const long long at = r < tile.rows ? (long long)(tile.first + row / a.group) * a.q_token_stride + (long long)(sg.h * a.group + row % a.group) * a.q_head_stride : -1;
+        const int row = tile.row0 + r, tok = row_token(a, row);
+        const long long at = r < tile.rows ? (long long)(tile.first + tok) * a.q_token_stride + (long long)(sg.h * a.group + row - tok * a.group) * a.q_head_stride : -1;
         const int sub_lane = lane % kPer, sub_row = lane / kPer;
         const int b = sub_lane / 2, chunk = (sub_lane & 1) * 4 + b % 4;
         uint8_t* to = smem + S::kOffQ + t * S::kQ + quarter * 32 * 128 + b / 4 * (128 * 128);
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint4 x[kTurns];
-#pragma unroll
-          for (int i = 0; i < kTurns; ++i) {
-            const long long from = __shfl_sync(~0u, at, half * 16 + i * kAtOnce + sub_row);
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 4
+        for (int i = 0; i < kTurns; ++i) {
+          const int mine = i * kAtOnce + sub_row;
+          const long long from = __shfl_sync(~0u, at, mine);
+          uint8_t* place = to + mine * 128 + ((chunk ^ (mine & 7)) << 4);
+          const uint16_t* src = static_cast<const uint16_t*>(a.q) + (from < 0 ? 0 : from + sub_lane * 8);
+          if (a.wide_q16) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place)), "l"(src), "r"(from < 0 ? 0 : 16) : "memory");
+          } else {
+            uint2 lo = make_uint2(0u, 0u), hi = lo;
             if (from >= 0) {
-              const uint2 lo = load_four(a.q, from + sub_lane * 8, a.wide_q), hi = load_four(a.q, from + sub_lane * 8 + 4, a.wide_q);
-              x[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+              lo = load_four(src, 0, a.wide_q);
+              hi = load_four(src, 4, a.wide_q);
             }
-          }
-#pragma unroll
-          for (int i = 0; i < kTurns; ++i) {
-            const float2 y[4] = {unpack16(x[i].x, a.dtype), unpack16(x[i].y, a.dtype), unpack16(x[i].z, a.dtype), unpack16(x[i].w, a.dtype)};
-            float big = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(y[k].x), fabsf(y[k].y)));
-#pragma unroll
-            for (int o = 1; o < kPer; o <<= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, o));
-            // 2^e <= big < 2^(e + 1), in the range whose powers of two are normal both ways
-            const int e = min(max((int)((__float_as_uint(big) >> 23) & 255) - 127, -100), 100);
-            const float up = copysignf(__uint_as_float((uint32_t)(127 + 13 - e) << 23), to_log2), down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
-            uint32_t z[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) z[k] = pack16(y[k].x * up, y[k].y * up, WHEAD_KV_F16);
-            const int mine = half * 16 + i * kAtOnce + sub_row;
-            *reinterpret_cast<uint4*>(to + mine * 128 + ((chunk ^ (mine & 7)) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
-            if (sub_lane == 0) factors[mine] = down * fabsf(to_log2);
+            *reinterpret_cast<uint4*>(place) = make_uint4(lo.x, lo.y, hi.x, hi.y);
           }
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        auto turn = [&](auto bf16) {
+          constexpr int kType = decltype(bf16)::value ? WHEAD_KV_BF16 : WHEAD_KV_F16;
+#pragma unroll 4
+          for (int i = 0; i < kTurns; ++i) {
+            const int mine = i * kAtOnce + sub_row;
+            uint4* place = reinterpret_cast<uint4*>(to + mine * 128 + ((chunk ^ (mine & 7)) << 4));
+            const uint4 x = *place;
+            // the largest magnitude, by its bits: they are ordered like the values
+            uint32_t big = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+#pragma unroll
+            for (int o = 1; o < kPer; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(~0u, big, o));
+            big = max(big & 0xFFFFu, big >> 16);
+            // 2^e <= largest < 2^(e + 1) (an f16 below 2^-14 counts as one just there), in the range whose powers of two are normal both ways
+            const int e = min(max(kType == WHEAD_KV_BF16 ? (int)(big >> 7) - 127 : max((int)(big >> 10), 1) - 15, -100), 100);
+            const float up = copysignf(__uint_as_float((uint32_t)(127 + 13 - e) << 23), to_log2), down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t z[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 y = unpack16(w[k], kType);
+              z[k] = pack16(y.x * up, y.y * up, WHEAD_KV_F16);
+            }
+            *place = make_uint4(z[0], z[1], z[2], z[3]);
+            if (sub_lane == 0) factors[mine] = down * fabsf(to_log2);
+          }
+        };
+        if (a.dtype == WHEAD_KV_BF16) turn(std::true_type{});
+        else turn(std::false_type{});
         fence_async();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.q_full[t]));
         f = factors[lane];
       }
+      int free_lo, free_hi;  // keys that all rows of the tile see
       {
-        const int w0 = (tile.row0 + sub) / a.group, w1 = (tile.row0 + max(min(sub + 128, tile.rows), sub + 1) - 1) / a.group, past = tile.len - tile.tokens;
+        const int w0 = row_token(a, tile.row0 + sub), w1 = row_token(a, tile.row0 + max(min(sub + 128, tile.rows), sub + 1) - 1), past = tile.len - tile.tokens;
         const int hi = a.tree ? min(past, past + w0 + 1) : a.causal ? min(past + w0 + 1, tile.len) : tile.len;
         const int lo = a.window ? max(past + w1 - a.window + 1, 0) : 0;
-        if (lane == 0) {
-          walk.free_hi = hi;
-          walk.free_lo = lo;
-        }
-        __syncwarp();
+        free_hi = hi;
+        free_lo = lo;
       }
+      bool fresh = true;  // some row of the warp has no reference yet
       float m = kNoKey;
       float2 l = make_float2(0.f, 0.f);
       for (int u = sg.u0; u < sg.u1; ++u, ++n) {
@@ -550,7 +585,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
           }
           const uint32_t st = tmem + sb * kBlock + h * 64 + lanes;
           const int key = key0 + h * 64;
-          const bool masked = key < walk.free_lo || key + 64 > walk.free_hi;
+          const bool masked = key < free_lo || key + 64 > free_hi;
           uint32_t seen[2] = {~0u, ~0u};
           if (masked) {
             const RowView view = row_view(a, tile, tile.row0 + r);
@@ -558,9 +593,10 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
             seen[1] = sees32(a, view, key + 32);
             __syncwarp();
           }
-          if (__any_sync(~0u, m == kNoKey)) {  // a row's first keys: its reference is their maximum
+          if (fresh) {  // a row's first keys: its reference is their maximum
             const float top = masked ? row_max<true>(st, seen) : row_max<false>(st, seen);
             if (m == kNoKey && top != -INFINITY) m = top * f - kBias;
+            fresh = __any_sync(~0u, m == kNoKey);
           }
           uint32_t p[2][16];
           float2 sum;
@@ -600,7 +636,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       fence_after();
       const int row = tile.row0 + r;
       const bool live = r < tile.rows;
-      const int tok = row / a.group, head = sg.h * a.group + row % a.group;
+      const int tok = row_token(a, row), head = sg.h * a.group + row - tok * a.group;
       const bool whole = sg.u0 == 0 && sg.u1 == tile.units;
       const float ll = l.x + l.y;
       constexpr int kPart = S::kRows * (D + 2);
@@ -693,7 +729,8 @@ __global__ void __launch_bounds__(128) join_parts(Cache c, AttendArgs a) {
       v.x = v.x * r0 + y.x * r1; v.y = v.y * r0 + y.y * r1; v.z = v.z * r0 + y.z * r1; v.w = v.w * r0 + y.w * r1;
     }
     const int grow = tile.row0 + row;
-    const int64_t at = (int64_t)(tile.first + grow / a.group) * a.heads + record.y * a.group + grow % a.group;
+    const int tok = row_token(a, grow);
+    const int64_t at = (int64_t)(tile.first + tok) * a.heads + record.y * a.group + grow - tok * a.group;
     const float q = l != 0.0f ? gv / l : 0.0f;
     if (l == 0.0f) v = make_float4(0.f, 0.f, 0.f, 0.f);
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + col) =

@@ -21,9 +21,10 @@ struct AttendArgs {
   const int32_t* slots;
   const unsigned long long* tree;
   int64_t total, q_token_stride, q_head_stride;
-  int n, heads, group, row_tiles, dtype, causal, window, tree_words;
+  int n, each, heads, group, group_shift, row_tiles, dtype, causal, window, tree_words;
+  uint32_t group_mul;  // row / group = (row * group_mul >> 32 + row) >> group_shift, for rows below 2^31
   float scale;
-  bool wide_q;
+  bool wide_q, wide_q16;  // query rows can be read 8, 16 bytes at a time
   int planned;  // the CTAs' starts are in the workspace
 };
 
@@ -37,10 +38,25 @@ struct Tile {
   int unit0, units;              // units of one KV head
 };
 
+// The token of a row: division by the group, by multiplication with its reciprocal rounded up to 33 bits (Granlund and Montgomery, "Division
+// by invariant integers using multiplication", 1994, figure 4.1). A division takes some 150 cycles of latency, and there are several
+// before a CTA can load anything.
+__device__ __forceinline__ int row_token(const AttendArgs& a, int row) {
+  const uint32_t t = __umulhi(a.group_mul, (uint32_t)row);
+  return (int)((t + (((uint32_t)row - t) >> (a.group_shift ? 1 : 0))) >> (a.group_shift ? a.group_shift - 1 : 0));
+}
+inline void set_group(AttendArgs* a, int group) {
+  int l = 0;
+  while ((1LL << l) < group) ++l;
+  a->group = group;
+  a->group_shift = l;
+  a->group_mul = (uint32_t)(((1ULL << 32) * ((1ULL << l) - (uint64_t)group)) / (uint64_t)group + 1);
+}
+
 template <int UNIT>
 __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, int item, int tile_rows) {
   Tile t;
-  const int i = item / a.row_tiles, m = item - i * a.row_tiles;
+  const int i = a.row_tiles == 1 ? item : item / a.row_tiles, m = item - i * a.row_tiles;
   t.slot = a.slots ? a.slots[i] : i;
   t.len = slot_len(c, t.slot);
   if (t.len == 0) t.slot = 0;
@@ -51,7 +67,7 @@ __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, i
     t.first = ok ? lo : 0;
     t.tokens = ok ? hi - lo : 0;
   } else {
-    t.tokens = (int)(a.total / a.n);
+    t.tokens = a.each;
     t.first = t.tokens * i;
   }
   const int64_t all = (int64_t)t.tokens * a.group;
@@ -61,7 +77,7 @@ __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, i
   t.rows = (int)(all - row0 < 0 ? 0 : all - row0 < tile_rows ? all - row0 : tile_rows);
   t.unit0 = t.units = 0;
   if (t.rows == 0) return t;
-  const int t0 = t.row0 / a.group, t1 = (t.row0 + t.rows - 1) / a.group;
+  const int t0 = row_token(a, t.row0), t1 = row_token(a, t.row0 + t.rows - 1);
   int hi = t.len, lo = 0;
   if (a.causal) hi = min(max(t.len - t.tokens + t1 + 1, 0), t.len);
   if (a.window) lo = max(t.len - t.tokens + t0 - a.window + 1, 0);
@@ -79,7 +95,7 @@ struct RowView {
 __device__ __forceinline__ RowView row_view(const AttendArgs& a, const Tile& t, int row) {
   RowView v{0, 0, 0x7FFFFFFF, nullptr};
   if (row >= t.row0 + t.rows) return v;
-  const int tok = row / a.group;
+  const int tok = row_token(a, row);
   const int pos = t.len - t.tokens + tok;
   v.hi = a.causal ? min(pos + 1, t.len) : t.len;
   if (a.window) v.lo = max(pos - a.window + 1, 0);
@@ -135,8 +151,10 @@ __device__ __forceinline__ long long scan64(long long x, long long* warps, long 
 
 struct SchedShared {
   long long warps[32];
-  int item;
   long long at;
+  int item;
+  int has_tile;  // tile is the item's
+  Tile tile;
 };
 
 // This CTA's start, from the lengths themselves (few items).
@@ -146,9 +164,11 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
   Start r;
   r.total = 0;
   long long mine = 0, before = 0;
+  Tile tile{};
   for (int base = 0; base < items; base += THREADS) {
     const int it = base + threadIdx.x;
-    mine = it < items ? (long long)make_tile<UNIT>(c, a, it, tile_rows).units * c.kv_heads : 0;
+    if (it < items) tile = make_tile<UNIT>(c, a, it, tile_rows);
+    mine = it < items ? (long long)tile.units * c.kv_heads : 0;
     long long all;
     before = r.total + scan64<THREADS>(mine, s.warps, all);
     r.total += all;
@@ -162,8 +182,11 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
     if (mine > 0 && before <= x && x < before + mine) {
       s.item = threadIdx.x;
       s.at = before;
+      s.tile = tile;
+      s.has_tile = 1;
     }
   } else {
+    if (threadIdx.x == 0) s.has_tile = 0;
     long long sum = 0;
     for (int base = 0; base < items && sum <= x; base += THREADS) {
       const int it = base + threadIdx.x;
@@ -224,6 +247,8 @@ static __global__ void __launch_bounds__(1024, 1) attend_plan(Cache c, AttendArg
 template <int THREADS, int UNIT>
 __device__ __forceinline__ Start get_start(const Cache& c, const AttendArgs& a, int tile_rows, SchedShared& s) {
   if (!a.planned) return find_start<THREADS, UNIT>(c, a, tile_rows, s);
+  if (threadIdx.x == 0) s.has_tile = 0;
+  __syncthreads();
   Start r;
   r.ctas = c.ctl->pad;
   r.total = *reinterpret_cast<const long long*>(&c.ctl->ticket[2]);
