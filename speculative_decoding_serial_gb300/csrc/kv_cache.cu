@@ -102,6 +102,31 @@ int host_cache(const whead_kv* kv, HostCache* out) {
 
 namespace {
 
+// ---------------------------------------------------------------- launches
+
+// Every kernel here may be placed while the one before it in the stream still runs, and waits for it before anything else: that
+// hides about a microsecond of each launch, which counts where a call is two or three small kernels.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  if (cudaLaunchKernelEx(&config, kernel, P(args)...) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return WHEAD_ERR_CUDA;
+  }
+  return WHEAD_OK;
+}
+
 // ---------------------------------------------------------------- planning: one CTA of kPlan threads
 
 constexpr int kPlan = 1024;
@@ -208,6 +233,7 @@ __device__ __forceinline__ void append_entry(const Cache& c, const AppendArgs& a
 
 // Lengths, pages and tables for an append; seq_a: each entry's length before, seq_b: sums of the groups it touches.
 __global__ void __launch_bounds__(kPlan, 1) append_plan(Cache c, AppendArgs a) {
+  after_previous();
   __shared__ PlanShared s;
   if (threadIdx.x == 0) s.bad = 0;
   __syncthreads();
@@ -238,7 +264,7 @@ __global__ void __launch_bounds__(kPlan, 1) append_plan(Cache c, AppendArgs a) {
     block_scan(pages, s, total);
     need += total;
   }
-  if (threadIdx.x == 0) c.seq_b[a.n] = groups;
+  if (threadIdx.x == 0) c.ctl->total = groups;
   __syncthreads();
   int bad = s.bad;
   if (!bad && need > 0 && find_free(c, need, s) < need) bad = WHEAD_ERR_NO_PAGES;
@@ -302,17 +328,20 @@ __device__ __forceinline__ float scaled(float x, float inv) {
   return y == y ? y : 0.0f;
 }
 
-// One warp quantizes the new tokens of one group of one head. A group's owner is the only writer of its words, so the
-// codes of two tokens that share a byte do not race; what an owner does not write of a word it reads first.
+// A warp quantizes 64 channels of the keys, or of the values, of the new tokens of one group of one head; a CTA has all of the
+// group's. Its loads are all under way before the first is used (one loop over the blocks took 27 us for a single token: its stores kept
+// the next block's loads back). A group's owner is the only writer of its words, so the codes of two tokens that share a byte
+// do not race; what an owner does not write of a word it reads first. Bound by the inputs' bytes for prompts, by latency for
+// single tokens.
 template <int D>
-__global__ void __launch_bounds__(128) append_write(Cache c, AppendArgs a) {
+__global__ void __launch_bounds__(D) append_write(const __grid_constant__ Cache c, const __grid_constant__ AppendArgs a) {
   constexpr int NB = D / 16;
+  after_previous();
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int h = blockIdx.y, chunk = part >> 1;  // 64 channels; even parts: keys
   if (c.ctl->abort) return;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y;
-  const float gk = c.k_scale[h], gv = c.v_scale[h];
-  const int total = c.seq_b[a.n];
-  for (int x = blockIdx.x * 4 + (threadIdx.x >> 5); x < total; x += gridDim.x * 4) {
+  const int total = c.ctl->total;
+  for (int x = blockIdx.x; x < total; x += gridDim.x) {
     const int i = find_entry(c.seq_b, a.n, x);
     int slot, count;
     int64_t first;
@@ -321,86 +350,95 @@ __global__ void __launch_bounds__(128) append_write(Cache c, AppendArgs a) {
     const int pos0 = ((len >> 4) + (x - c.seq_b[i])) << 4;  // position of the group's first token
     const int lo = max(len - pos0, 0), hi = min(len + count - pos0, 16);  // new tokens of the group: lo .. hi - 1
     const bool whole = lo == 0 && hi == 16;
-    uint8_t* gp = group_ptr<D>(c, c.tables[(int64_t)slot * c.max_pages + (pos0 >> c.page_shift)], h, pos0);
     const int64_t row0 = first + pos0 - len;  // row of k, v of the group's first token
-    // keys: this lane's tokens g and g + 8, four channels of each block
-    {
-      uint32_t* codes = reinterpret_cast<uint32_t*>(gp);
-      uint8_t* scales = gp + 8 * D;
+    const int page = c.tables[(int64_t)slot * c.max_pages + (pos0 >> c.page_shift)];
+    if ((part & 1) == 0) {
+      // this lane's tokens g and g + 8, four channels of each block
       const bool in0 = g >= lo && g < hi, in1 = g + 8 >= lo && g + 8 < hi;
-#pragma unroll 4
-      for (int b = 0; b < NB; ++b) {
-        float x0[4] = {}, x1[4] = {};
-        const int64_t ch = (int64_t)h * a.kh + b * 16 + t * 4;
-        if (in0) load_elems<4>(a.k, (row0 + g) * a.kt + ch, a.dtype, a.wide_k, x0);
-        if (in1) load_elems<4>(a.k, (row0 + g + 8) * a.kt + ch, a.dtype, a.wide_k, x1);
-        float m0 = fmaxf(fmaxf(fabsf(x0[0]), fabsf(x0[1])), fmaxf(fabsf(x0[2]), fabsf(x0[3])));
-        float m1 = fmaxf(fmaxf(fabsf(x1[0]), fabsf(x1[1])), fmaxf(fabsf(x1[2]), fabsf(x1[3])));
-        m0 = fmaxf(m0, __shfl_xor_sync(~0u, m0, 1));
-        m1 = fmaxf(m1, __shfl_xor_sync(~0u, m1, 1));
-        m0 = fmaxf(m0, __shfl_xor_sync(~0u, m0, 2));
-        m1 = fmaxf(m1, __shfl_xor_sync(~0u, m1, 2));
-        float i0, i1;
-        const uint32_t s0 = block_scale(m0, gk, i0), s1 = block_scale(m1, gk, i1);
-        uint32_t w = e2m1x2_from_float(scaled(x0[0], i0), scaled(x0[1], i0)) |
-                     e2m1x2_from_float(scaled(x1[0], i1), scaled(x1[1], i1)) << 8 |
-                     e2m1x2_from_float(scaled(x0[2], i0), scaled(x0[3], i0)) << 16 |
-                     e2m1x2_from_float(scaled(x1[2], i1), scaled(x1[3], i1)) << 24;
-        uint32_t* at = codes + (b / 4) * 128 + lane * 4 + (b % 4);
-        if (!whole) {
-          const uint32_t mine = (in0 ? 0x00FF00FFu : 0u) | (in1 ? 0xFF00FF00u : 0u);
-          w = (w & mine) | (*at & ~mine);
-        }
-        *at = w;
-        if (t == 0) {
-          if (in0) scales[g * 2 * NB + b * 2] = (uint8_t)s0;
-          if (in1) scales[g * 2 * NB + b * 2 + 1] = (uint8_t)s1;
-        }
+      const int64_t ch = (int64_t)h * a.kh + chunk * 64 + t * 4;
+      float v[4][2][4] = {};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        if (in0) load_elems<4>(a.k, (row0 + g) * a.kt + ch + b * 16, a.dtype, a.wide_k, v[b][0]);
+        if (in1) load_elems<4>(a.k, (row0 + g + 8) * a.kt + ch + b * 16, a.dtype, a.wide_k, v[b][1]);
       }
-    }
-    // values: this lane's tokens 2t, 2t + 1, 2t + 8, 2t + 9, two channels of each block
-    {
-      uint32_t* codes = reinterpret_cast<uint32_t*>(gp + 9 * D);
-      uint8_t* scales = gp + 17 * D;
+      uint8_t* gp = group_ptr<D>(c, page, h, pos0);
+      uint4* codes = reinterpret_cast<uint4*>(gp + chunk * 512) + lane;
+      uint2* scales = reinterpret_cast<uint2*>(gp + 8 * D + g * 2 * NB + chunk * 8);  // [block][token g, g + 8]
+      uint4 old = make_uint4(0, 0, 0, 0);
+      uint2 old_s = make_uint2(0, 0);
+      if (!whole) {
+        old = *codes;
+        old_s = *scales;
+      }
+      const float gk = c.k_scale[h];
+      uint32_t w[4], s[2] = {};
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        float inv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float m = fmaxf(fmaxf(fabsf(v[b][e][0]), fabsf(v[b][e][1])), fmaxf(fabsf(v[b][e][2]), fabsf(v[b][e][3])));
+          m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+          s[b / 2] |= block_scale(m, gk, inv[e]) << ((b % 2 * 2 + e) * 8);
+        }
+        w[b] = e2m1x2_from_float(scaled(v[b][0][0], inv[0]), scaled(v[b][0][1], inv[0])) |
+               e2m1x2_from_float(scaled(v[b][1][0], inv[1]), scaled(v[b][1][1], inv[1])) << 8 |
+               e2m1x2_from_float(scaled(v[b][0][2], inv[0]), scaled(v[b][0][3], inv[0])) << 16 |
+               e2m1x2_from_float(scaled(v[b][1][2], inv[1]), scaled(v[b][1][3], inv[1])) << 24;
+      }
+      const uint32_t mine = (in0 ? 0x00FF00FFu : 0u) | (in1 ? 0xFF00FF00u : 0u);
+      *codes = make_uint4((w[0] & mine) | (old.x & ~mine), (w[1] & mine) | (old.y & ~mine), (w[2] & mine) | (old.z & ~mine), (w[3] & mine) | (old.w & ~mine));
+      if (t == 0) *scales = make_uint2((s[0] & mine) | (old_s.x & ~mine), (s[1] & mine) | (old_s.y & ~mine));
+    } else {
+      // this lane's tokens 2t, 2t + 1, 2t + 8, 2t + 9, two channels of each block
       bool in[4];
-      uint32_t mine = 0;
+      uint32_t mine = 0, mine_s = 0;
+      float v[4][4][2] = {};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = 2 * t + (k & 1) + (k >> 1) * 8;
         in[k] = r >= lo && r < hi;
-        if (in[k]) mine |= 0x0F0Fu << ((k & 1) * 4 + (k >> 1) * 16);
-      }
-#pragma unroll 2
-      for (int b = 0; b < NB; ++b) {
-        float x[4][2] = {};
-        uint32_t w = 0;
-        float inv[4];
-        uint32_t s[4];
+        if (in[k]) {
+          mine |= 0x0F0Fu << ((k & 1) * 4 + (k >> 1) * 16);
+          mine_s |= 0xFFu << ((k >> 1) * 16 + (k & 1) * 8);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (in[k])
-            load_elems<2>(a.v, (row0 + 2 * t + (k & 1) + (k >> 1) * 8) * a.vt + (int64_t)h * a.vh + b * 16 + g * 2, a.dtype, a.wide_v, x[k]);
+          for (int b = 0; b < 4; ++b) load_elems<2>(a.v, (row0 + r) * a.vt + (int64_t)h * a.vh + chunk * 64 + b * 16 + g * 2, a.dtype, a.wide_v, v[b][k]);
+        }
+      }
+      uint8_t* gp = group_ptr<D>(c, page, h, pos0);
+      uint4* codes = reinterpret_cast<uint4*>(gp + 9 * D + chunk * 512) + lane;
+      uint4* scales = reinterpret_cast<uint4*>(gp + 17 * D + t * 4 * NB + chunk * 16);  // [block][token 2t, 2t + 1, 2t + 8, 2t + 9]
+      uint4 old = make_uint4(0, 0, 0, 0), old_s = old;
+      if (!whole) {
+        old = *codes;
+        old_s = *scales;
+      }
+      const float gv = c.v_scale[h];
+      uint32_t w[4], s[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        float inv[4];
+        s[b] = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float m = fmaxf(fabsf(x[k][0]), fabsf(x[k][1]));
+          float m = fmaxf(fabsf(v[b][k][0]), fabsf(v[b][k][1]));
           m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
           m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
           m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
-          s[k] = block_scale(m, gv, inv[k]);
+          s[b] |= block_scale(m, gv, inv[k]) << ((k >> 1) * 16 + (k & 1) * 8);
         }
+        w[b] = 0;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          w |= e2m1x2_from_float(scaled(x[0][e], inv[0]), scaled(x[1][e], inv[1])) << (e * 8) |
-               e2m1x2_from_float(scaled(x[2][e], inv[2]), scaled(x[3][e], inv[3])) << (e * 8 + 16);
-        uint32_t* at = codes + (b / 4) * 128 + lane * 4 + (b % 4);
-        if (!whole) w = (w & mine) | (*at & ~mine);
-        *at = w;
-        if (g == 0) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (in[k]) scales[t * 4 * NB + b * 4 + (k >> 1) * 2 + (k & 1)] = (uint8_t)s[k];
-        }
+          w[b] |= e2m1x2_from_float(scaled(v[b][0][e], inv[0]), scaled(v[b][1][e], inv[1])) << (e * 8) |
+                  e2m1x2_from_float(scaled(v[b][2][e], inv[2]), scaled(v[b][3][e], inv[3])) << (e * 8 + 16);
       }
+      *codes = make_uint4((w[0] & mine) | (old.x & ~mine), (w[1] & mine) | (old.y & ~mine), (w[2] & mine) | (old.z & ~mine), (w[3] & mine) | (old.w & ~mine));
+      if (g == 0)
+        *scales = make_uint4((s[0] & mine_s) | (old_s.x & ~mine_s), (s[1] & mine_s) | (old_s.y & ~mine_s), (s[2] & mine_s) | (old_s.z & ~mine_s),
+                             (s[3] & mine_s) | (old_s.w & ~mine_s));
     }
   }
 }
@@ -428,16 +466,16 @@ __device__ __forceinline__ void store2(void* p, int64_t i, int dtype, float x, f
     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + i) = pack16(x, y, dtype);
 }
 
-// One warp takes one group of one head apart and writes those of its tokens that are asked for.
+// A warp takes 64 channels of the keys, or of the values, of one group of one head apart and writes those of its tokens that are asked
+// for; a CTA has all of a group. Bound by the bytes that it writes.
 template <int D>
-__global__ void __launch_bounds__(128) read_kernel(Cache c, ReadArgs a) {
+__global__ void __launch_bounds__(D) read_kernel(const __grid_constant__ Cache c, const __grid_constant__ ReadArgs a) {
   constexpr int NB = D / 16;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int h = blockIdx.y;
+  after_previous();
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int h = blockIdx.y, chunk = part >> 1;
   const int per = (a.count + 30) / 16;  // groups that `count` tokens can touch, whatever the first one's place
-  const int64_t x = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (x >= (int64_t)a.n * per) return;
-  const int i = (int)(x / per);
+  const int i = (int)(blockIdx.x / (unsigned)per);
   const int slot = entry_slot(a.slots, i);
   int len = slot_len(c, slot);
   int start = a.start[i];
@@ -446,39 +484,56 @@ __global__ void __launch_bounds__(128) read_kernel(Cache c, ReadArgs a) {
     start = 0;
     len = 0;
   }
-  const int64_t pos0 = ((int64_t)(start >> 4) + x % per) << 4;
+  const int64_t pos0 = ((int64_t)(start >> 4) + (blockIdx.x - (unsigned)i * per)) << 4;
   const int64_t end = (int64_t)start + a.count;
   if (pos0 >= end) return;
   const bool held = pos0 < len;
   const uint8_t* gp = held ? group_ptr<D>(c, c.tables[(int64_t)slot * c.max_pages + (pos0 >> c.page_shift)], h, (int)pos0) : nullptr;
   const int64_t out0 = ((int64_t)i * a.count + (pos0 - start)) * c.kv_heads + h;  // row of the group's first token
-  const float gk = c.k_scale[h], gv = c.v_scale[h];
-#pragma unroll 2
-  for (int b = 0; b < NB; ++b) {
-    uint32_t hk[4], hv[4];
-    const int word = (b / 4) * 128 + lane * 4 + (b % 4);
-    e2m1x8_to_half2(held ? reinterpret_cast<const uint32_t*>(gp)[word] : 0u, hk);
-    e2m1x8_to_half2(held ? reinterpret_cast<const uint32_t*>(gp + 9 * D)[word] : 0u, hv);
+  if ((part & 1) == 0) {
+    uint4 code = make_uint4(0, 0, 0, 0);
+    uint2 scale = make_uint2(0, 0);
+    if (held) {
+      code = *(reinterpret_cast<const uint4*>(gp + chunk * 512) + lane);
+      scale = *reinterpret_cast<const uint2*>(gp + 8 * D + g * 2 * NB + chunk * 8);
+    }
+    const float gk = c.k_scale[h];
 #pragma unroll
     for (int hi = 0; hi < 2; ++hi) {
       const int64_t pos = pos0 + g + hi * 8;
-      if (pos >= start && pos < end) {
-        const bool live = pos < len;
-        const float s = live ? __fmul_rn(e4m3_to_float(gp[8 * D + g * 2 * NB + b * 2 + hi]), gk) : 0.0f;
-        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&hk[hi])), q = __half22float2(*reinterpret_cast<const __half2*>(&hk[hi + 2]));
+      if (pos < start || pos >= end) continue;
+      const bool live = pos < len;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t x[4];
+        e2m1x8_to_half2(b == 0 ? code.x : b == 1 ? code.y : b == 2 ? code.z : code.w, x);
+        const float s = __fmul_rn(e4m3_to_float((uint8_t)((b < 2 ? scale.x : scale.y) >> ((b % 2 * 2 + hi) * 8))), gk);
+        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&x[hi])), q = __half22float2(*reinterpret_cast<const __half2*>(&x[hi + 2]));
         const float y[4] = {live ? p.x * s : 0.0f, live ? p.y * s : 0.0f, live ? q.x * s : 0.0f, live ? q.y * s : 0.0f};
-        store4(a.k, (out0 + (int64_t)(g + hi * 8) * c.kv_heads) * D + b * 16 + t * 4, a.dtype, y);
+        store4(a.k, (out0 + (int64_t)(g + hi * 8) * c.kv_heads) * D + chunk * 64 + b * 16 + t * 4, a.dtype, y);
       }
     }
+  } else {
+    uint4 code = make_uint4(0, 0, 0, 0), scale = code;
+    if (held) {
+      code = *(reinterpret_cast<const uint4*>(gp + 9 * D + chunk * 512) + lane);
+      scale = *reinterpret_cast<const uint4*>(gp + 17 * D + t * 4 * NB + chunk * 16);
+    }
+    const float gv = c.v_scale[h];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int r = 2 * t + (k & 1) + (k >> 1) * 8;
       const int64_t pos = pos0 + r;
-      if (pos >= start && pos < end) {
-        const bool live = pos < len;
-        const float s = live ? __fmul_rn(e4m3_to_float(gp[17 * D + t * 4 * NB + b * 4 + (k >> 1) * 2 + (k & 1)]), gv) : 0.0f;
-        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&hv[(k >> 1) * 2])), q = __half22float2(*reinterpret_cast<const __half2*>(&hv[(k >> 1) * 2 + 1]));
-        store2(a.v, (out0 + (int64_t)r * c.kv_heads) * D + b * 16 + g * 2, a.dtype, live ? ((k & 1) ? p.y : p.x) * s : 0.0f,
+      if (pos < start || pos >= end) continue;
+      const bool live = pos < len;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t x[4];
+        e2m1x8_to_half2(b == 0 ? code.x : b == 1 ? code.y : b == 2 ? code.z : code.w, x);
+        const uint32_t sw = b == 0 ? scale.x : b == 1 ? scale.y : b == 2 ? scale.z : scale.w;
+        const float s = __fmul_rn(e4m3_to_float((uint8_t)(sw >> ((k >> 1) * 16 + (k & 1) * 8))), gv);
+        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&x[(k >> 1) * 2])), q = __half22float2(*reinterpret_cast<const __half2*>(&x[(k >> 1) * 2 + 1]));
+        store2(a.v, (out0 + (int64_t)r * c.kv_heads) * D + chunk * 64 + b * 16 + g * 2, a.dtype, live ? ((k & 1) ? p.y : p.x) * s : 0.0f,
                live ? ((k & 1) ? q.y : q.x) * s : 0.0f);
       }
     }
@@ -535,6 +590,7 @@ __device__ __forceinline__ CompactEntry compact_entry(const Cache& c, const Comp
 
 // Tables, lengths and references after a compact; region: the pages that each entry's block lay in and those that it lies in.
 __global__ void __launch_bounds__(kPlan, 1) compact_plan(Cache c, CompactArgs a) {
+  after_previous();
   __shared__ PlanShared s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) s.bad = 0;
@@ -614,6 +670,7 @@ __global__ void __launch_bounds__(kPlan, 1) compact_plan(Cache c, CompactArgs a)
 // first one is written, so a group may be source and target.
 template <int D>
 __global__ void __launch_bounds__(128) compact_move(Cache c, CompactArgs a) {
+  after_previous();
   constexpr int NB = D / 16, kGroup = 18 * D;
   extern __shared__ __align__(16) uint8_t smem[];
   if (c.ctl->abort) return;
@@ -685,6 +742,7 @@ __global__ void __launch_bounds__(128) compact_move(Cache c, CompactArgs a) {
 
 // Which slots get a copy of a partial last page, and the page: seq_a[i] = that page or -1.
 __global__ void __launch_bounds__(kPlan, 1) fork_plan(Cache c, const int32_t* parents) {
+  after_previous();
   __shared__ PlanShared s;
   if (threadIdx.x == 0) s.bad = 0;
   __syncthreads();
@@ -721,6 +779,7 @@ __global__ void __launch_bounds__(kPlan, 1) fork_plan(Cache c, const int32_t* pa
 // The slots' new rows and lengths (into the workspace: other slots may still read the old ones), the partial pages' copies.
 // gridDim.y CTAs share a slot's copy; the first of them does its row.
 __global__ void __launch_bounds__(256) fork_copy(Cache c, const int32_t* parents) {
+  after_previous();
   if (c.ctl->abort) return;
   const int i = blockIdx.x;
   const int p = parents[i];
@@ -747,6 +806,7 @@ __global__ void __launch_bounds__(256) fork_copy(Cache c, const int32_t* parents
 }
 
 __global__ void __launch_bounds__(256) fork_apply(Cache c, const int32_t* parents) {
+  after_previous();
   if (c.ctl->abort) return;
   const int i = blockIdx.x;
   const int p = parents[i];
@@ -782,8 +842,7 @@ int launch_move(const HostCache& h, const CompactArgs& a) {
     }
     granted = true;
   }
-  compact_move<D><<<dim3(a.n, h.c.kv_heads), 128, smem, h.stream>>>(h.c, a);
-  return WHEAD_OK;
+  return launch_after(compact_move<D>, dim3(a.n, h.c.kv_heads), 128, smem, h.stream, h.c, a);
 }
 }  // namespace
 
@@ -829,14 +888,13 @@ int whead_kv_append(const whead_kv* kv, const void* k, const void* v, int32_t dt
   AppendArgs a{k, v, dtype, k_token_stride, k_head_stride, v_token_stride, v_head_stride, indptr, slots, n, total, false, false};
   a.wide_k = aligned(k, 4 * e) && k_token_stride % 4 == 0 && k_head_stride % 4 == 0;
   a.wide_v = aligned(v, 2 * e) && v_token_stride % 2 == 0 && v_head_stride % 2 == 0;
-  append_plan<<<1, kPlan, 0, h.stream>>>(h.c, a);
-  const int64_t groups = total / 16 + 2 * (int64_t)n;  // most that the tokens can touch
-  const int gx = (int)std::min<int64_t>((std::min(groups, total) + 3) / 4, 16384);
-  const dim3 grid(gx, kv->kv_heads);
-  if (kv->head_dim == 64) append_write<64><<<grid, 128, 0, h.stream>>>(h.c, a);
-  else if (kv->head_dim == 128) append_write<128><<<grid, 128, 0, h.stream>>>(h.c, a);
-  else append_write<256><<<grid, 128, 0, h.stream>>>(h.c, a);
-  return launch_status();
+  int st = launch_after(append_plan, dim3(1), kPlan, 0, h.stream, h.c, a);
+  if (st != WHEAD_OK) return st;
+  const int64_t groups = std::min(total / 16 + 2 * (int64_t)n, total);  // most that the tokens can touch
+  const dim3 grid((unsigned)std::min<int64_t>(groups, 65535 * 4), kv->kv_heads);
+  return kv->head_dim == 64    ? launch_after(append_write<64>, grid, 64, 0, h.stream, h.c, a)
+         : kv->head_dim == 128 ? launch_after(append_write<128>, grid, 128, 0, h.stream, h.c, a)
+                               : launch_after(append_write<256>, grid, 256, 0, h.stream, h.c, a);
 }
 
 int whead_kv_read(const whead_kv* kv, const int32_t* start, const int32_t* slots, int32_t n, int32_t count, int32_t dtype,
@@ -847,14 +905,13 @@ int whead_kv_read(const whead_kv* kv, const int32_t* start, const int32_t* slots
   if (!start || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)) return WHEAD_ERR_INVALID_ARG;
   const int rc = host_cache(kv, &h);
   if (rc != WHEAD_OK) return rc;
-  const int64_t warps = (int64_t)n * ((count + 30LL) / 16);
-  if (count > INT_MAX - 64 || (warps + 3) / 4 >= INT_MAX) return WHEAD_ERR_UNSUPPORTED;
+  const int64_t groups = (int64_t)n * ((count + 30LL) / 16);
+  if (count > INT_MAX - 64 || groups >= INT_MAX) return WHEAD_ERR_UNSUPPORTED;
   const ReadArgs a{start, slots, n, count, dtype, k_out, v_out};
-  const dim3 grid((unsigned)((warps + 3) / 4), kv->kv_heads);
-  if (kv->head_dim == 64) read_kernel<64><<<grid, 128, 0, h.stream>>>(h.c, a);
-  else if (kv->head_dim == 128) read_kernel<128><<<grid, 128, 0, h.stream>>>(h.c, a);
-  else read_kernel<256><<<grid, 128, 0, h.stream>>>(h.c, a);
-  return launch_status();
+  const dim3 grid((unsigned)groups, kv->kv_heads);
+  return kv->head_dim == 64    ? launch_after(read_kernel<64>, grid, 64, 0, h.stream, h.c, a)
+         : kv->head_dim == 128 ? launch_after(read_kernel<128>, grid, 128, 0, h.stream, h.c, a)
+                               : launch_after(read_kernel<256>, grid, 256, 0, h.stream, h.c, a);
 }
 
 int whead_kv_compact(const whead_kv* kv, const int32_t* start, const int32_t* keep, const int32_t* count, const int32_t* slots,
@@ -866,9 +923,9 @@ int whead_kv_compact(const whead_kv* kv, const int32_t* start, const int32_t* ke
   int rc = host_cache(kv, &h);
   if (rc != WHEAD_OK) return rc;
   const CompactArgs a{start, keep, count, slots, n, keep_width};
-  compact_plan<<<1, kPlan, 0, h.stream>>>(h.c, a);
-  rc = kv->head_dim == 64 ? launch_move<64>(h, a) : kv->head_dim == 128 ? launch_move<128>(h, a) : launch_move<256>(h, a);
-  return rc != WHEAD_OK ? rc : launch_status();
+  rc = launch_after(compact_plan, dim3(1), kPlan, 0, h.stream, h.c, a);
+  if (rc != WHEAD_OK) return rc;
+  return kv->head_dim == 64 ? launch_move<64>(h, a) : kv->head_dim == 128 ? launch_move<128>(h, a) : launch_move<256>(h, a);
 }
 
 int whead_kv_fork(const whead_kv* kv, const int32_t* parents) {
@@ -876,11 +933,12 @@ int whead_kv_fork(const whead_kv* kv, const int32_t* parents) {
   HostCache h;
   const int rc = host_cache(kv, &h);
   if (rc != WHEAD_OK) return rc;
-  fork_plan<<<1, kPlan, 0, h.stream>>>(h.c, parents);
+  int st = launch_after(fork_plan, dim3(1), kPlan, 0, h.stream, h.c, parents);
+  if (st != WHEAD_OK) return st;
   const int64_t bytes = (int64_t)kv->kv_heads * (kv->page_size / 16) * 18 * kv->head_dim;
-  fork_copy<<<dim3(kv->max_seqs, (unsigned)std::min<int64_t>(8, (bytes + 16383) / 16384)), 256, 0, h.stream>>>(h.c, parents);
-  fork_apply<<<kv->max_seqs, 256, 0, h.stream>>>(h.c, parents);
-  return launch_status();
+  st = launch_after(fork_copy, dim3(kv->max_seqs, (unsigned)std::min<int64_t>(8, (bytes + 16383) / 16384)), 256, 0, h.stream, h.c, parents);
+  if (st != WHEAD_OK) return st;
+  return launch_after(fork_apply, dim3(kv->max_seqs), 256, 0, h.stream, h.c, parents);
 }
 
 int whead_kv_status(const whead_kv* kv) {

@@ -153,18 +153,19 @@ class KvCache:
         assert self.device.index is not None
         self._index = self.device.index
         self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._int32 = torch.int32
 
-    def _call(self, name, *args):
+    def _call(self, call, *args):
         self._p.stream = self._raw_stream(self._index)
-        rc = getattr(self._lib, name)(self._ref, *args)
+        rc = call(self._ref, *args)
         if rc:
-            raise _wh.WheadError(rc, name)
+            raise _wh.WheadError(rc, call.__name__)
 
     def _ints(self, x, shape, what):
         """The pointer of an int32 tensor of this shape on the cache's device, or None."""
         if x is None:
             return None
-        if x.dtype != self._torch.int32 or tuple(x.shape) != shape or not x.is_contiguous() or x.device != self.device:
+        if x.dtype is not self._int32 or x.shape != shape or not x.is_contiguous() or x.get_device() != self._index:
             raise ValueError(f"{what}: a contiguous int32 tensor of shape {shape} on {self.device} is wanted")
         return x.data_ptr()
 
@@ -179,15 +180,16 @@ class KvCache:
         """Appends tokens: k, v (total, kv_heads, head_dim) in bfloat16, float16 or float32, channels contiguous. Entry i's
         are rows indptr[i] .. indptr[i + 1] - 1 (None: an equal share each) and go to slot slots[i] (None: slot i)."""
         n, ip, sl = self._entries(indptr, slots)
-        if k.shape != v.shape or k.dim() != 3 or k.shape[1] != self.kv_heads or k.shape[2] != self.head_dim:
+        shape = k.shape
+        if shape != v.shape or len(shape) != 3 or shape[1] != self.kv_heads or shape[2] != self.head_dim:
             raise ValueError(f"k and v: shape (total, {self.kv_heads}, {self.head_dim}) is wanted")
-        if k.dtype != v.dtype or k.device != self.device or v.device != self.device:
+        if k.dtype is not v.dtype or k.get_device() != self._index or v.get_device() != self._index:
             raise ValueError("k and v: one type, on the cache's device")
         ks, vs = k.stride(), v.stride()
         if ks[2] != 1 or vs[2] != 1:
             raise ValueError("k and v: channels have to be contiguous")
-        self._call("whead_kv_append", k.data_ptr(), v.data_ptr(), _code(k.dtype, "k and v"), ks[0], ks[1], vs[0], vs[1], ip, sl,
-                   n, k.shape[0])
+        self._call(self._lib.whead_kv_append, k.data_ptr(), v.data_ptr(), _code(k.dtype, "k and v"), ks[0], ks[1], vs[0], vs[1], ip, sl,
+                   n, shape[0])
 
     def read(self, start, count, slots=None, *, dtype=None):
         """The held values of `count` tokens from positions start (int32, one an entry): k, v of (n, count, kv_heads,
@@ -198,9 +200,10 @@ class KvCache:
             raise ValueError(f"start: {n} values are wanted")
         dtype = torch.bfloat16 if dtype is None else dtype
         code, count = _code(dtype, "read"), int(count)
-        k = torch.empty((n, count, self.kv_heads, self.head_dim), dtype=dtype, device=self.device)
-        v = torch.empty_like(k)
-        self._call("whead_kv_read", self._ints(start, (n,), "start"), sl, n, count, code, k.data_ptr(), v.data_ptr())
+        shape = (n, count, self.kv_heads, self.head_dim)
+        k = torch.empty(shape, dtype=dtype, device=self.device)
+        v = torch.empty(shape, dtype=dtype, device=self.device)
+        self._call(self._lib.whead_kv_read, self._ints(start, (n,), "start"), sl, n, count, code, k.data_ptr(), v.data_ptr())
         return k, v
 
     def attend(self, q, indptr=None, slots=None, *, scale=None, causal=True, window=0, tree=None, max_q=None, out=None,
@@ -215,7 +218,7 @@ class KvCache:
         out (as q, contiguous) and lse (total, heads) float32 may be given."""
         torch = self._torch
         n, ip, sl = self._entries(indptr, slots)
-        if q.dim() != 3 or q.shape[2] != self.head_dim or q.stride(2) != 1 or q.device != self.device:
+        if q.dim() != 3 or q.shape[2] != self.head_dim or q.stride(2) != 1 or q.get_device() != self._index:
             raise ValueError(f"q: shape (total, heads, {self.head_dim}) with contiguous channels on the cache's device is wanted")
         total, heads = q.shape[0], q.shape[1]
         code = _code(q.dtype, "attend", f32=False)
@@ -238,7 +241,7 @@ class KvCache:
         a = KvAttendArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr(), ip, sl, None if tree is None else tree.data_ptr(), total,
                          q.stride(0), q.stride(1), n, heads, int(max_q), code, int(bool(causal)), int(window), words,
                          1.0 / math.sqrt(self.head_dim) if scale is None else float(scale))
-        self._call("whead_kv_attend", ctypes.addressof(a))
+        self._call(self._lib.whead_kv_attend, ctypes.addressof(a))
         return out, lse
 
     def compact(self, start, keep=None, count=None, slots=None):
@@ -253,12 +256,12 @@ class KvCache:
             if keep.dim() != 2 or keep.shape[1] > MAX_BLOCK:
                 raise ValueError(f"keep: (n, width) with width <= {MAX_BLOCK} is wanted")
             width = keep.shape[1]
-        self._call("whead_kv_compact", self._ints(start, (n,), "start"), self._ints(keep, (n, width), "keep"),
+        self._call(self._lib.whead_kv_compact, self._ints(start, (n,), "start"), self._ints(keep, (n, width), "keep"),
                    self._ints(count, (n,), "count"), sl, n, width)
 
     def fork(self, parents):
         """Slot i takes over what slot parents[i] (int32, max_seqs) held: i leaves it alone, -1 empties it."""
-        self._call("whead_kv_fork", self._ints(parents, (self.max_seqs,), "parents"))
+        self._call(self._lib.whead_kv_fork, self._ints(parents, (self.max_seqs,), "parents"))
 
     def free(self, slots):
         """Empties the given slots (int32)."""
