@@ -231,7 +231,27 @@ __device__ __forceinline__ void append_entry(const Cache& c, const AppendArgs& a
   count = (unsigned)slot >= (unsigned)c.max_seqs || first < 0 || end < first || end > a.total ? -1 : (int)(end - first);
 }
 
-// Lengths, pages and tables for an append; seq_a: each entry's length before, seq_b: sums of the groups it touches.
+// One group that an append writes, as the writing kernel needs it: one load away, instead of a search and four dependent loads in every
+// CTA (33,000 tokens: 109 us then, MEASURED now).
+struct __align__(16) AppendGroup {
+  int page;    // of the pool
+  int place;   // of the group in the page, the first new token in bits 8.., the one past the last in bits 16..
+  int64_t row; // of k, v: the group's first token
+};
+
+// The last of n ascending sums that is at most x.
+__device__ __forceinline__ int find_sum(const int32_t* sums, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (sums[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Lengths, pages and tables for an append, and the groups it writes; seq_a: each entry's length before, seq_b: sums of the groups it
+// touches.
 __global__ void __launch_bounds__(kPlan, 1) append_plan(Cache c, AppendArgs a) {
   after_previous();
   __shared__ PlanShared s;
@@ -282,37 +302,39 @@ __global__ void __launch_bounds__(kPlan, 1) append_plan(Cache c, AppendArgs a) {
       pages = pages_of(c, len + count) - had;
       c.lens[slot] = len + count;
     }
-    int total;
-    const int at = taken + block_scan(pages, s, total);
-    taken += total;
-    // the entries' pages, a warp for each entry at a time
-    const int lane = threadIdx.x & 31;
-    for (int l = 0; l < 32; ++l) {
-      const int p = __shfl_sync(~0u, pages, l);
-      if (p == 0) continue;
-      const int sl = __shfl_sync(~0u, slot, l), h = __shfl_sync(~0u, had, l), f = __shfl_sync(~0u, at, l);
-      for (int j = lane; j < p; j += 32) {
-        const int page = c.fresh[f + j];
-        c.tables[(int64_t)sl * c.max_pages + h + j] = page;
-        c.refs[page] = 1;
+    if (need > 0) {
+      int total;
+      const int at = taken + block_scan(pages, s, total);
+      taken += total;
+      // the entries' pages, a warp for each entry at a time
+      const int lane = threadIdx.x & 31;
+      for (unsigned left = __ballot_sync(~0u, pages > 0); left; left &= left - 1) {
+        const int l = __ffs(left) - 1;
+        const int p = __shfl_sync(~0u, pages, l), sl = __shfl_sync(~0u, slot, l), h = __shfl_sync(~0u, had, l), f = __shfl_sync(~0u, at, l);
+#pragma unroll 4
+        for (int j = lane; j < p; j += 32) {
+          const int page = c.fresh[f + j];
+          c.tables[(int64_t)sl * c.max_pages + h + j] = page;
+          c.refs[page] = 1;
+        }
       }
     }
   }
-}
-
-// Which entry of `sums` (n + 1 ascending sums) holds x, by a whole warp.
-__device__ __forceinline__ int find_entry(const int32_t* sums, int n, int x) {
-  const int lane = threadIdx.x & 31;
-  int entry = 0;
-  for (int base = 0; base < n; base += 32) {
-    const int i = base + lane;
-    const unsigned m = __ballot_sync(~0u, i < n && sums[i] <= x);
-    if (m == 0) break;
-    entry = base + 31 - __clz(m);
-    if (m != ~0u) break;
+  __syncthreads();
+  AppendGroup* to = reinterpret_cast<AppendGroup*>(c.partial);
+  for (int x = threadIdx.x; x < groups; x += kPlan) {
+    const int i = find_sum(c.seq_b, a.n, x);  // entries without groups share their sum with the next one: the last of them holds x
+    int slot, count;
+    int64_t first;
+    append_entry(c, a, i, slot, first, count);
+    const int len = c.seq_a[i];
+    const int pos0 = ((len >> 4) + (x - c.seq_b[i])) << 4;
+    AppendGroup g;
+    g.page = c.tables[(int64_t)slot * c.max_pages + (pos0 >> c.page_shift)];
+    g.place = ((pos0 & (c.page_size - 1)) >> 4) | max(len - pos0, 0) << 8 | min(len + count - pos0, 16) << 16;
+    g.row = first + pos0 - len;
+    to[x] = g;
   }
-  // entries without groups share their sum with the next one: the last of them holds x
-  return entry;
 }
 
 // One block of 16 channels' scale byte and the factor 1 / (s g) that its codes are formed with.
@@ -328,12 +350,30 @@ __device__ __forceinline__ float scaled(float x, float inv) {
   return y == y ? y : 0.0f;
 }
 
+// Largest of N values over the lanes that differ in the bits BIT, BIT / 2, .. (log2(N / 2) of them); each lane ends with two of the
+// N: those of its number in these bits, the first of them in x[0].
+template <int N, int BIT>
+__device__ __forceinline__ void max_scatter(float (&x)[N]) {
+  if constexpr (N > 2) {
+    const bool up = (threadIdx.x & BIT) != 0;
+    float half[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float send = up ? x[i] : x[N / 2 + i];
+      half[i] = fmaxf(up ? x[N / 2 + i] : x[i], __shfl_xor_sync(~0u, send, BIT));
+    }
+    max_scatter<N / 2, BIT / 2>(half);
+    x[0] = half[0];
+    x[1] = half[1];
+  }
+}
+
 // A warp quantizes 64 channels of the keys, or of the values, of the new tokens of one group of one head; a CTA has all of the
 // group's. Its loads are all under way before the first is used (one loop over the blocks took 27 us for a single token: its stores kept
 // the next block's loads back). A group's owner is the only writer of its words, so the codes of two tokens that share a byte
 // do not race; what an owner does not write of a word it reads first. Bound by the inputs' bytes for prompts, by latency for
 // single tokens.
-template <int D>
+template <int D, int DTYPE>
 __global__ void __launch_bounds__(D) append_write(const __grid_constant__ Cache c, const __grid_constant__ AppendArgs a) {
   constexpr int NB = D / 16;
   after_previous();
@@ -342,103 +382,102 @@ __global__ void __launch_bounds__(D) append_write(const __grid_constant__ Cache 
   if (c.ctl->abort) return;
   const int total = c.ctl->total;
   for (int x = blockIdx.x; x < total; x += gridDim.x) {
-    const int i = find_entry(c.seq_b, a.n, x);
-    int slot, count;
-    int64_t first;
-    append_entry(c, a, i, slot, first, count);
-    const int len = c.seq_a[i];
-    const int pos0 = ((len >> 4) + (x - c.seq_b[i])) << 4;  // position of the group's first token
-    const int lo = max(len - pos0, 0), hi = min(len + count - pos0, 16);  // new tokens of the group: lo .. hi - 1
+    const int4 what = __ldcg(reinterpret_cast<const int4*>(c.partial) + x);  // an AppendGroup
+    const int lo = what.y >> 8 & 0xFF, hi = what.y >> 16;                    // new tokens of the group: lo .. hi - 1
     const bool whole = lo == 0 && hi == 16;
-    const int64_t row0 = first + pos0 - len;  // row of k, v of the group's first token
-    const int page = c.tables[(int64_t)slot * c.max_pages + (pos0 >> c.page_shift)];
+    const int64_t row0 = (int64_t)((uint64_t)(uint32_t)what.z | (uint64_t)(uint32_t)what.w << 32);  // row of k, v of the group's first token
     if ((part & 1) == 0) {
       // this lane's tokens g and g + 8, four channels of each block
       const bool in0 = g >= lo && g < hi, in1 = g + 8 >= lo && g + 8 < hi;
       const int64_t ch = (int64_t)h * a.kh + chunk * 64 + t * 4;
-      float v[4][2][4] = {};
+      RawElems<DTYPE, 4> raw[4][2] = {};
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        if (in0) load_elems<4>(a.k, (row0 + g) * a.kt + ch + b * 16, a.dtype, a.wide_k, v[b][0]);
-        if (in1) load_elems<4>(a.k, (row0 + g + 8) * a.kt + ch + b * 16, a.dtype, a.wide_k, v[b][1]);
+        if (in0) load_raw(a.k, (row0 + g) * a.kt + ch + b * 16, a.wide_k, raw[b][0]);
+        if (in1) load_raw(a.k, (row0 + g + 8) * a.kt + ch + b * 16, a.wide_k, raw[b][1]);
       }
-      uint8_t* gp = group_ptr<D>(c, page, h, pos0);
+      uint8_t* gp = group_ptr<D>(c, what.x, h, (what.y & 0xFF) << 4);
       uint4* codes = reinterpret_cast<uint4*>(gp + chunk * 512) + lane;
-      uint2* scales = reinterpret_cast<uint2*>(gp + 8 * D + g * 2 * NB + chunk * 8);  // [block][token g, g + 8]
+      uint16_t* scales = reinterpret_cast<uint16_t*>(gp + 8 * D + g * 2 * NB + chunk * 8) + t;  // of block t: tokens g, g + 8
       uint4 old = make_uint4(0, 0, 0, 0);
-      uint2 old_s = make_uint2(0, 0);
-      if (!whole) {
-        old = *codes;
-        old_s = *scales;
-      }
+      if (!whole) old = *codes;
       const float gk = c.k_scale[h];
-      uint32_t w[4], s[2] = {};
+      // the four lanes of a token share its blocks' scales: lane t works out block t's, for tokens g and g + 8
+      float v[4][2][4], top[8], inv[2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        raw_values(raw[i / 2][i % 2], v[i / 2][i % 2]);
+        const float (&x)[4] = v[i / 2][i % 2];
+        top[i] = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+      }
+      max_scatter<8, 2>(top);
+      const uint32_t s0 = block_scale(top[0], gk, inv[0]), s1 = block_scale(top[1], gk, inv[1]);
+      uint32_t w[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        float inv[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float m = fmaxf(fmaxf(fabsf(v[b][e][0]), fabsf(v[b][e][1])), fmaxf(fabsf(v[b][e][2]), fabsf(v[b][e][3])));
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-          s[b / 2] |= block_scale(m, gk, inv[e]) << ((b % 2 * 2 + e) * 8);
-        }
-        w[b] = e2m1x2_from_float(scaled(v[b][0][0], inv[0]), scaled(v[b][0][1], inv[0])) |
-               e2m1x2_from_float(scaled(v[b][1][0], inv[1]), scaled(v[b][1][1], inv[1])) << 8 |
-               e2m1x2_from_float(scaled(v[b][0][2], inv[0]), scaled(v[b][0][3], inv[0])) << 16 |
-               e2m1x2_from_float(scaled(v[b][1][2], inv[1]), scaled(v[b][1][3], inv[1])) << 24;
+        const float i0 = __shfl_sync(~0u, inv[0], g * 4 + b), i1 = __shfl_sync(~0u, inv[1], g * 4 + b);
+        w[b] = e2m1x2_from_float(scaled(v[b][0][0], i0), scaled(v[b][0][1], i0)) |
+               e2m1x2_from_float(scaled(v[b][1][0], i1), scaled(v[b][1][1], i1)) << 8 |
+               e2m1x2_from_float(scaled(v[b][0][2], i0), scaled(v[b][0][3], i0)) << 16 |
+               e2m1x2_from_float(scaled(v[b][1][2], i1), scaled(v[b][1][3], i1)) << 24;
       }
       const uint32_t mine = (in0 ? 0x00FF00FFu : 0u) | (in1 ? 0xFF00FF00u : 0u);
       *codes = make_uint4((w[0] & mine) | (old.x & ~mine), (w[1] & mine) | (old.y & ~mine), (w[2] & mine) | (old.z & ~mine), (w[3] & mine) | (old.w & ~mine));
-      if (t == 0) *scales = make_uint2((s[0] & mine) | (old_s.x & ~mine), (s[1] & mine) | (old_s.y & ~mine));
+      if (whole) {
+        *scales = (uint16_t)(s0 | s1 << 8);
+      } else {
+        if (in0) reinterpret_cast<uint8_t*>(scales)[0] = (uint8_t)s0;
+        if (in1) reinterpret_cast<uint8_t*>(scales)[1] = (uint8_t)s1;
+      }
     } else {
       // this lane's tokens 2t, 2t + 1, 2t + 8, 2t + 9, two channels of each block
       bool in[4];
-      uint32_t mine = 0, mine_s = 0;
-      float v[4][4][2] = {};
+      uint32_t mine = 0;
+      RawElems<DTYPE, 2> raw[4][4] = {};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = 2 * t + (k & 1) + (k >> 1) * 8;
         in[k] = r >= lo && r < hi;
         if (in[k]) {
           mine |= 0x0F0Fu << ((k & 1) * 4 + (k >> 1) * 16);
-          mine_s |= 0xFFu << ((k >> 1) * 16 + (k & 1) * 8);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) load_elems<2>(a.v, (row0 + r) * a.vt + (int64_t)h * a.vh + chunk * 64 + b * 16 + g * 2, a.dtype, a.wide_v, v[b][k]);
+          for (int b = 0; b < 4; ++b) load_raw(a.v, (row0 + r) * a.vt + (int64_t)h * a.vh + chunk * 64 + b * 16 + g * 2, a.wide_v, raw[b][k]);
         }
       }
-      uint8_t* gp = group_ptr<D>(c, page, h, pos0);
+      uint8_t* gp = group_ptr<D>(c, what.x, h, (what.y & 0xFF) << 4);
       uint4* codes = reinterpret_cast<uint4*>(gp + 9 * D + chunk * 512) + lane;
-      uint4* scales = reinterpret_cast<uint4*>(gp + 17 * D + t * 4 * NB + chunk * 16);  // [block][token 2t, 2t + 1, 2t + 8, 2t + 9]
-      uint4 old = make_uint4(0, 0, 0, 0), old_s = old;
-      if (!whole) {
-        old = *codes;
-        old_s = *scales;
-      }
+      uint16_t* scales = reinterpret_cast<uint16_t*>(gp + 17 * D + t * 4 * NB + chunk * 16) + g;  // bytes 2g, 2g + 1 of [block][token]
+      uint4 old = make_uint4(0, 0, 0, 0);
+      if (!whole) old = *codes;
       const float gv = c.v_scale[h];
-      uint32_t w[4], s[4];
+      // the eight lanes of a token pair share its 16 scales: lane g works out two, block g / 2's for tokens 2t + 8 (g % 2) and the one after
+      float v[4][4][2], top[16], inv[2];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) raw_values(raw[i / 4][i % 4], v[i / 4][i % 4]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top[i] = fmaxf(fabsf(v[i / 4][i % 4][0]), fabsf(v[i / 4][i % 4][1]));
+      max_scatter<16, 16>(top);
+      const uint32_t s0 = block_scale(top[0], gv, inv[0]), s1 = block_scale(top[1], gv, inv[1]);
+      uint32_t w[4];
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        float inv[4];
-        s[b] = 0;
+        float i4[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float m = fmaxf(fabsf(v[b][k][0]), fabsf(v[b][k][1]));
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
-          m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
-          s[b] |= block_scale(m, gv, inv[k]) << ((k >> 1) * 16 + (k & 1) * 8);
-        }
+        for (int k = 0; k < 4; ++k) i4[k] = __shfl_sync(~0u, inv[k & 1], (b * 2 + (k >> 1)) * 4 + t);
         w[b] = 0;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          w[b] |= e2m1x2_from_float(scaled(v[b][0][e], inv[0]), scaled(v[b][1][e], inv[1])) << (e * 8) |
-                  e2m1x2_from_float(scaled(v[b][2][e], inv[2]), scaled(v[b][3][e], inv[3])) << (e * 8 + 16);
+          w[b] |= e2m1x2_from_float(scaled(v[b][0][e], i4[0]), scaled(v[b][1][e], i4[1])) << (e * 8) |
+                  e2m1x2_from_float(scaled(v[b][2][e], i4[2]), scaled(v[b][3][e], i4[3])) << (e * 8 + 16);
       }
       *codes = make_uint4((w[0] & mine) | (old.x & ~mine), (w[1] & mine) | (old.y & ~mine), (w[2] & mine) | (old.z & ~mine), (w[3] & mine) | (old.w & ~mine));
-      if (g == 0)
-        *scales = make_uint4((s[0] & mine_s) | (old_s.x & ~mine_s), (s[1] & mine_s) | (old_s.y & ~mine_s), (s[2] & mine_s) | (old_s.z & ~mine_s),
-                             (s[3] & mine_s) | (old_s.w & ~mine_s));
+      if (whole) {
+        *scales = (uint16_t)(s0 | s1 << 8);
+      } else {
+        const bool high = (g & 1) != 0;
+        if (high ? in[2] : in[0]) reinterpret_cast<uint8_t*>(scales)[0] = (uint8_t)s0;
+        if (high ? in[3] : in[1]) reinterpret_cast<uint8_t*>(scales)[1] = (uint8_t)s1;
+      }
     }
   }
 }
@@ -832,6 +871,13 @@ using namespace whead_kv_impl;
 
 namespace {
 template <int D>
+int launch_write(const HostCache& h, const AppendArgs& a, dim3 grid) {
+  return a.dtype == WHEAD_KV_BF16  ? launch_after(append_write<D, WHEAD_KV_BF16>, grid, D, 0, h.stream, h.c, a)
+         : a.dtype == WHEAD_KV_F16 ? launch_after(append_write<D, WHEAD_KV_F16>, grid, D, 0, h.stream, h.c, a)
+                                   : launch_after(append_write<D, WHEAD_KV_F32>, grid, D, 0, h.stream, h.c, a);
+}
+
+template <int D>
 int launch_move(const HostCache& h, const CompactArgs& a) {
   const int smem = kMoveTokens * 4 + kMoveGroups * 18 * D;
   static bool granted = false;
@@ -888,13 +934,12 @@ int whead_kv_append(const whead_kv* kv, const void* k, const void* v, int32_t dt
   AppendArgs a{k, v, dtype, k_token_stride, k_head_stride, v_token_stride, v_head_stride, indptr, slots, n, total, false, false};
   a.wide_k = aligned(k, 4 * e) && k_token_stride % 4 == 0 && k_head_stride % 4 == 0;
   a.wide_v = aligned(v, 2 * e) && v_token_stride % 2 == 0 && v_head_stride % 2 == 0;
-  int st = launch_after(append_plan, dim3(1), kPlan, 0, h.stream, h.c, a);
-  if (st != WHEAD_OK) return st;
   const int64_t groups = std::min(total / 16 + 2 * (int64_t)n, total);  // most that the tokens can touch
+  if (groups > h.c.partial_floats / 4) return WHEAD_ERR_UNSUPPORTED;    // more than the workspace can list: some 40 million tokens
+  const int st = launch_after(append_plan, dim3(1), kPlan, 0, h.stream, h.c, a);
+  if (st != WHEAD_OK) return st;
   const dim3 grid((unsigned)std::min<int64_t>(groups, 65535 * 4), kv->kv_heads);
-  return kv->head_dim == 64    ? launch_after(append_write<64>, grid, 64, 0, h.stream, h.c, a)
-         : kv->head_dim == 128 ? launch_after(append_write<128>, grid, 128, 0, h.stream, h.c, a)
-                               : launch_after(append_write<256>, grid, 256, 0, h.stream, h.c, a);
+  return kv->head_dim == 64 ? launch_write<64>(h, a, grid) : kv->head_dim == 128 ? launch_write<128>(h, a, grid) : launch_write<256>(h, a, grid);
 }
 
 int whead_kv_read(const whead_kv* kv, const int32_t* start, const int32_t* slots, int32_t n, int32_t count, int32_t dtype,

@@ -150,6 +150,44 @@ __device__ __forceinline__ void load_elems(const void* p, int64_t i, int dtype, 
   }
 }
 
+// The same in two steps, so that many loads can be under way before the first is looked at: N elements as they are, and their values.
+template <int DTYPE, int N>
+struct RawElems {
+  uint32_t w[DTYPE == WHEAD_KV_F32 ? N : N / 2];
+};
+template <int DTYPE, int N>
+__device__ __forceinline__ void load_raw(const void* p, int64_t i, bool wide, RawElems<DTYPE, N>& r) {
+  constexpr int W = DTYPE == WHEAD_KV_F32 ? N : N / 2;
+  const char* at = static_cast<const char*>(p) + i * (DTYPE == WHEAD_KV_F32 ? 4 : 2);
+  if (wide) {
+    if constexpr (W == 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
+      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else if constexpr (W == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+      r.w[0] = v.x; r.w[1] = v.y;
+    } else {
+      r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+    }
+  } else if constexpr (DTYPE == WHEAD_KV_F32) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) r.w[k] = __ldg(reinterpret_cast<const uint32_t*>(at) + k);
+  } else {
+    const unsigned short* x = reinterpret_cast<const unsigned short*>(at);
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) r.w[k] = __ldg(x + 2 * k) | (uint32_t)__ldg(x + 2 * k + 1) << 16;
+  }
+}
+template <int DTYPE, int N>
+__device__ __forceinline__ void raw_values(const RawElems<DTYPE, N>& r, float (&x)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if constexpr (DTYPE == WHEAD_KV_F32) x[k] = __uint_as_float(r.w[k]);
+    else if constexpr (DTYPE == WHEAD_KV_BF16) x[k] = __uint_as_float(k & 1 ? r.w[k / 2] & 0xFFFF0000u : r.w[k / 2] << 16);
+    else x[k] = __half2float(__ushort_as_half((unsigned short)(r.w[k / 2] >> (k & 1) * 16)));
+  }
+}
+
 // four consecutive elements of a 16-bit type from i on, as they are; `wide`: the address is a multiple of 8
 __device__ __forceinline__ uint2 load_four(const void* p, int64_t i, bool wide) {
   const uint16_t* x = static_cast<const uint16_t*>(p) + i;
