@@ -619,6 +619,7 @@ int launch_rows(const HostCache& h, AttendArgs a, int max_q) {
   int64_t ctas = std::min<int64_t>((int64_t)h.sms * S::kCtas, kMaxCtas);
   ctas = std::min(ctas, h.c.partial_floats / (2 * S::kRows * (D + 2)));
   a.planned = tiles * a.n > 4 * S::kThreads;
+  a.small = tiles * a.n * h.c.kv_heads * ((int64_t)h.c.max_pages * h.c.page_size / kUnit + 2) < INT_MAX;
   if (a.planned) attend_plan<kUnit><<<1, 1024, 0, h.stream>>>(h.c, a, S::kRows, (int)ctas);
   attend_rows<D, NT><<<(unsigned)ctas, S::kThreads, S::kBytes, h.stream>>>(h.c, a);
   return launch_status();

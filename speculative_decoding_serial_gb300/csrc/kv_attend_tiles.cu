@@ -759,6 +759,7 @@ int launch(const HostCache& h, AttendArgs a, int max_q) {
   int64_t ctas = std::min<int64_t>((int64_t)h.sms, kMaxCtas);
   ctas = std::min(ctas, h.c.partial_floats / (2 * S::kRows * (D + 2)));
   a.planned = tiles * a.n > 2 * S::kThreads;
+  a.small = tiles * a.n * h.c.kv_heads * ((int64_t)h.c.max_pages * h.c.page_size / kBlock + 2) < INT_MAX;
   if (a.planned) attend_plan<kBlock><<<1, 1024, 0, h.stream>>>(h.c, a, S::kRows, (int)ctas);
   attend_tiles<D, TILES><<<(unsigned)ctas, S::kThreads, S::kBytes, h.stream>>>(h.c, a);
   // the joining kernel's blocks may be placed while the last CTAs still work; they wait for the grid before they read

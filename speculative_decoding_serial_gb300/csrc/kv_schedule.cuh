@@ -26,6 +26,7 @@ struct AttendArgs {
   float scale;
   bool wide_q, wide_q16;  // query rows can be read 8, 16 bytes at a time
   int planned;  // the CTAs' starts are in the workspace
+  int small;    // all units are less than 2^31
 };
 
 // Attention of more than a few rows a KV head (kv_attend_tiles.cu); head_dim 64 or 128.
@@ -162,6 +163,35 @@ template <int THREADS, int UNIT>
 __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a, int tile_rows, SchedShared& s) {
   const int items = a.n * a.row_tiles;
   Start r;
+  if (items <= 32 && a.small) {
+    // every warp finds the start for itself, a lane an item: no barrier before the CTA's first loads, and 32-bit sums
+    const int lane = threadIdx.x & 31;
+    Tile tile{};
+    if (lane < items) tile = make_tile<UNIT>(c, a, lane, tile_rows);
+    const int mine = tile.units * c.kv_heads;
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(~0u, sum, o);
+      if (lane >= o) sum += y;
+    }
+    r.total = __shfl_sync(~0u, sum, 31);
+    r.ctas = (int)min((long long)gridDim.x, r.total);
+    r.item = 0;
+    r.at = 0;
+    if ((int)blockIdx.x >= r.ctas) return r;
+    const int x = (int)range_begin(r, blockIdx.x);
+    const int owner = __ffs(__ballot_sync(~0u, x < sum)) - 1;  // sums ascend, and an item without units adds none
+    r.item = owner;
+    r.at = __shfl_sync(~0u, sum - mine, owner);
+    if (threadIdx.x == owner) {
+      s.item = owner;
+      s.tile = tile;
+      s.has_tile = 1;
+    }
+    __syncthreads();
+    return r;
+  }
   r.total = 0;
   long long mine = 0, before = 0;
   Tile tile{};
