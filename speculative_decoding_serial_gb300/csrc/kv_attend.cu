@@ -212,23 +212,24 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         const bool live = nt * 8 + g < tile.rows;
         const int tok = row_token(a, row);
         const int64_t at = live ? (int64_t)(tile.first + tok) * a.q_token_stride + (int64_t)(h * a.group + row - tok * a.group) * a.q_head_stride : 0;
-        float x[NB][4], big = 0.0f;
+        // all of the row's loads before any of its values is looked at
+        uint2 raw[NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          x[b][0] = x[b][1] = x[b][2] = x[b][3] = 0.0f;
-          if (live) load_elems<4>(a.q, at + b * 16 + t * 4, a.dtype, a.wide_q, x[b]);
-        }
+        for (int b = 0; b < NB; ++b) raw[b] = live ? load_four(a.q, at + b * 16 + t * 4, a.wide_q) : make_uint2(0u, 0u);
+        // the largest magnitude, by its bits: they are ordered like the values
+        uint32_t top = 0;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) big = fmaxf(big, fmaxf(fmaxf(fabsf(x[b][0]), fabsf(x[b][1])), fmaxf(fabsf(x[b][2]), fabsf(x[b][3]))));
-        big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-        // 2^e <= big < 2^(e + 1), in the range whose powers of two are normal both ways
-        const int e = min(max((int)((__float_as_uint(big) >> 23) & 255) - 127, -100), 100);
+        for (int b = 0; b < NB; ++b) top = __vmaxu2(top, __vmaxu2(raw[b].x & 0x7FFF7FFFu, raw[b].y & 0x7FFF7FFFu));
+        top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 2));
+        top = max(top & 0xFFFFu, top >> 16);
+        // 2^e <= largest < 2^(e + 1) (an f16 below 2^-14 counts as one just there), in the range whose powers of two are normal both ways
+        const int e = min(max(a.dtype == WHEAD_KV_BF16 ? (int)(top >> 7) - 127 : max((int)(top >> 10), 1) - 15, -100), 100);
         const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23), down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const __half2 lo = __floats2half2_rn(x[b][0] * up, x[b][1] * up), hi = __floats2half2_rn(x[b][2] * up, x[b][3] * up);
-          const uint2 w = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          const float2 lo = unpack16(raw[b].x, a.dtype), hi = unpack16(raw[b].y, a.dtype);
+          const uint2 w = make_uint2(pack16(lo.x * up, lo.y * up, WHEAD_KV_F16), pack16(hi.x * up, hi.y * up, WHEAD_KV_F16));
           if constexpr (S::kQInRegs) q[i][b] = w;
           else s_q[(nt * NB + b) * 32 + lane] = w;
         }
@@ -515,85 +516,49 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
       // ---- an item's parts joined, by the last CTA to get here
       const int first_cta = range_owner(start, head_at), last_cta = range_owner(start, head_end - 1);
       const int parts = last_cta - first_cta + 1;
-      __threadfence();
       named_sync<kConsumers>(1);
-      if (tid == 0) {
-        const unsigned done = atomicAdd(&c.counters[first_cta], 1u);
+      if (tid == 0) {  // its fence covers what the others wrote before the barrier
+        unsigned done;
+        asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(done) : "l"(c.counters + first_cta) : "memory");
         s.last = done + 1 == (unsigned)parts;
         if (s.last) c.counters[first_cta] = 0;
       }
       named_sync<kConsumers>(1);
       if (s.last) {
-        __threadfence();
         const int first_slot = 2 * first_cta + (range_begin(start, first_cta) == head_at ? 0 : 1);
         auto part_at = [&](int k) { return c.partial + (int64_t)(k == 0 ? first_slot : 2 * (first_cta + k)) * kPart; };
-        // red as the parts' weights: [part][row], as many at a time as it holds
-        constexpr int kMost = D + 4;
-        constexpr int kPlaces = ROWS * (D / 4), kMine = (kPlaces + kConsumers - 1) / kConsumers;
-        // with fewer places than threads, several threads share a place's parts
-        constexpr int kShare = kPlaces >= kConsumers ? 1 : kConsumers / kPlaces;
-        static_assert(kShare == 1 || kShare * kPlaces == kConsumers, "");
-        float4 v[kMine];
-        float mm = kNoKey, ll = 0.0f;   // of row tid, if that is one
+#pragma unroll 1
+        for (int x = tid; x < tile.rows * (D / 4); x += kConsumers) {
+          const int row = x / (D / 4), col = x % (D / 4) * 4;
+          float mm = kNoKey, ll = 0.0f;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int k0 = 0; k0 < parts; k0 += 8) {  // eight parts' loads under way at once
+            float pm[8], pl[8];
+            float4 y[8];
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = 0; k0 < parts; k0 += kMost) {
-          const int n = min(parts - k0, kMost);
-          float* wm = red;
-          float* wl = red + kMost * ROWS;
-          for (int x = tid; x < n * tile.rows; x += kConsumers) {
-            const int k = x / tile.rows, row = x % tile.rows;
-            const float* p = part_at(k0 + k);
-            wm[k * ROWS + row] = __ldcg(p + row);
-            wl[k * ROWS + row] = __ldcg(p + ROWS + row);
-          }
-          named_sync<kConsumers>(1);
-          if (tid < tile.rows) {
+            for (int k = 0; k < 8; ++k) {
+              const float* p = part_at(min(k0 + k, parts - 1));
+              pm[k] = __ldcg(p + row);
+              pl[k] = __ldcg(p + ROWS + row);
+              y[k] = __ldcg(reinterpret_cast<const float4*>(p + 2 * ROWS + row * D + col));
+            }
             float now = mm;
-            for (int k = 0; k < n; ++k) now = fmaxf(now, wm[k * ROWS + tid]);
-            const float r = ex2(mm - now);
-            ll *= r;
-            for (int k = 0; k < n; ++k) {
-              const float w = ex2(wm[k * ROWS + tid] - now);
-              ll += wl[k * ROWS + tid] * w;
-              wm[k * ROWS + tid] = w;
-            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) now = fmaxf(now, pm[k]);
+            const float r0 = ex2(mm - now);
             mm = now;
-            s_c[tid] = r;
-          }
-          named_sync<kConsumers>(1);
+            ll *= r0;
+            v.x *= r0; v.y *= r0; v.z *= r0; v.w *= r0;
 #pragma unroll
-          for (int i = 0; i < kMine; ++i) {
-            const int x = tid / kShare + i * (kConsumers / kShare), row = x / (D / 4), col = x % (D / 4) * 4;
-            if (row < tile.rows) {
-              const float r = s_c[row];
-              v[i].x *= r; v[i].y *= r; v[i].z *= r; v[i].w *= r;
-#pragma unroll 8
-              for (int k = tid % kShare; k < n; k += kShare) {
-                const float w = wm[k * ROWS + row];
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(part_at(k0 + k) + 2 * ROWS + row * D + col));
-                v[i].x += y.x * w; v[i].y += y.y * w; v[i].z += y.z * w; v[i].w += y.w * w;
-              }
+            for (int k = 0; k < 8; ++k) {
+              if (k0 + k >= parts) break;
+              const float r1 = ex2(pm[k] - mm);
+              ll += pl[k] * r1;
+              v.x += y[k].x * r1; v.y += y[k].y * r1; v.z += y[k].z * r1; v.w += y[k].w * r1;
             }
           }
-          named_sync<kConsumers>(1);
-        }
-        if (tid < tile.rows) {
-          s_m[tid] = mm;
-          s_l[tid] = ll;
-        }
-        named_sync<kConsumers>(1);
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int x = tid / kShare + i * (kConsumers / kShare), row = x / (D / 4), col = x % (D / 4) * 4;
-#pragma unroll
-          for (int o2 = 1; o2 < kShare; o2 <<= 1) {
-            v[i].x += __shfl_xor_sync(~0u, v[i].x, o2);
-            v[i].y += __shfl_xor_sync(~0u, v[i].y, o2);
-            v[i].z += __shfl_xor_sync(~0u, v[i].z, o2);
-            v[i].w += __shfl_xor_sync(~0u, v[i].w, o2);
-          }
-          if (row < tile.rows && tid % kShare == 0) write_row(row, col, v[i], s_m[row], s_l[row]);
+          write_row(row, col, v, mm, ll);
         }
       }
     }
