@@ -39,15 +39,14 @@ struct Shape {
   static constexpr int kGroup = 18 * D;
   static constexpr int kQ = 128 * D * 2, kK = kBlock * D * 2, kV = D * kBlock * 2;
   static constexpr int kOffWalk = 640;                   // the warps' places
-  static constexpr int kOffF = 3072;                     // the rows' factors from products to scores
-  static constexpr int kOffQ = 4096, kOffK = kOffQ + TILES * kQ, kOffV = kOffK + kBufs * kK;
+  static constexpr int kOffQ = 3072, kOffK = kOffQ + TILES * kQ, kOffV = kOffK + kBufs * kK;
   static constexpr int kBytes = kOffV + kBufs * kV + 1024;  // + alignment
   static constexpr int kCols = 512;                         // of tensor memory: two S, then O of each tile
 };
 
 struct Head {
   SchedShared sched;
-  unsigned long long k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[4], pv_done[4], o_full[2], q_full[2], drain[2], q_raw[8];
+  unsigned long long k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[4], pv_done[4], o_full[2], q_full[2], drain[2];
   uint32_t tmem;
 };
 
@@ -285,7 +284,6 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       mbar_init(smem_u32(&s.o_full[i]), 1);
       mbar_init(smem_u32(&s.q_full[i]), 4);
       mbar_init(smem_u32(&s.drain[i]), 1);
-      for (int w = 0; w < 4; ++w) mbar_init(smem_u32(&s.q_raw[4 * i + w]), 1);
     }
     fence_mbar_init();
   }
@@ -488,77 +486,66 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
     const int r = sub + quarter * 32 + lane;           // row of the CTA's tile
     const uint32_t lanes = (uint32_t)quarter << 21;    // this warp's lanes of tensor memory (lane 32 w at bit 16)
     const uint32_t ot = tmem + 256 + t * 128 + lanes;
-    float* factors = reinterpret_cast<float*>(smem + S::kOffF) + sub + quarter * 32;
     int n = 0, seg = 0;
     while (next_segment<S::kRows>(c, a, walk, s.sched)) {
       const Tile& tile = sg.tile;
       const bool idle = quarter * 32 + sub >= tile.rows;  // no row of this warp is one: its part of P may be anything
       float f;
       {
-        // The warp's query rows, 64 channels of a row to 128 bytes of shared memory, first as they are (each lane fetches its row), then in
-        // place to f16, from a power of two: a row is kPer lanes with 8 channels each, kAtOnce rows at once. The sign of the scale goes
-        // into the rows, so that f is positive and scores need it only after their maximum is known.
-        constexpr int kPer = D / 8, kAtOnce = 32 / kPer;
-        const int row = tile.row0 + r, tok = row_token(a, row);
-        const bool here = r < tile.rows;
-        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (here ? (long long)(tile.first + tok) * a.q_token_stride + (long long)(sg.h * a.group + row - tok * a.group) * a.q_head_stride : 0);
-        uint8_t* mine = smem + S::kOffQ + t * S::kQ + quarter * 32 * 128;
-        const uint32_t raw = smem_u32(&s.q_raw[warp]);
-        if (a.wide_q16) {
-          if (lane == 0) mbar_expect(raw, (uint32_t)max(min(tile.rows - sub - quarter * 32, 32), 0) * (D * 2));
-          __syncwarp();
-          if (here) {
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) bulk_load(smem_u32(mine + lane * 128 + i * (128 * 128)), src + i * 64, 128, raw);
-          }
-        } else if (here) {
-#pragma unroll 1
-          for (int i = 0; i < D / 4; ++i)
-            *reinterpret_cast<uint2*>(mine + lane * 128 + i / 16 * (128 * 128) + i % 16 * 8) = load_four(src, i * 4, a.wide_q);
-        }
+        // The thread's query row, from a power of two to f16. All of its loads are under way before it looks at one. (Rows fetched by bulk
+        // or asynchronous copies took 4,500 cycles to ask for: those are issued lane by lane.) The sign of the scale goes into the
+        // row, so that f is positive and scores need it only after their maximum is known.
         const float to_log2 = a.scale * c.k_scale[sg.h] * kLog2e;
-        if (a.wide_q16) await(c, raw, seg & 1, dead);
-        else __syncwarp();
-        const int sub_lane = lane % kPer, b = sub_lane / 2;
-        const int from = sub_lane % 8 * 16, chunk = (sub_lane & 1) * 4 + b % 4;
-        mine += b / 4 * (128 * 128);
-        auto turn = [&](auto bf16) {
-          constexpr int kType = decltype(bf16)::value ? WHEAD_KV_BF16 : WHEAD_KV_F16, kBatch = 4;
-#pragma unroll 1
-          for (int i0 = lane / kPer; i0 < 32; i0 += kBatch * kAtOnce) {
-            uint4 x[kBatch];
+        const int row = tile.row0 + r, tok = row_token(a, row);
+        uint4 x[D / 8];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) x[i] = *reinterpret_cast<const uint4*>(mine + (i0 + i * kAtOnce) * 128 + from);
-            __syncwarp();
+        for (int i = 0; i < D / 8; ++i) x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < tile.rows) {
+          const uint16_t* src = static_cast<const uint16_t*>(a.q) + (long long)(tile.first + tok) * a.q_token_stride + (long long)(sg.h * a.group + row - tok * a.group) * a.q_head_stride;
+          if (a.wide_q16) {
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const int at = i0 + i * kAtOnce;
-              uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-              // the largest magnitude, by its bits: they are ordered like the values
-              uint32_t big = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+            for (int i = 0; i < D / 8; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+          } else {
 #pragma unroll
-              for (int o = 1; o < kPer; o <<= 1) big = __vmaxu2(big, __shfl_xor_sync(~0u, big, o));
-              big = max(big & 0xFFFFu, big >> 16);
-              // 2^e <= largest < 2^(e + 1) (an f16 below 2^-14 counts as one just there), in the range whose powers of two are normal both ways
-              const int e = min(max(kType == WHEAD_KV_BF16 ? (int)(big >> 7) - 127 : max((int)(big >> 10), 1) - 15, -100), 100);
-              const float up = copysignf(__uint_as_float((uint32_t)(127 + 13 - e) << 23), to_log2);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 y = unpack16(w[k], kType);
-                w[k] = pack16(y.x * up, y.y * up, WHEAD_KV_F16);
-              }
-              *reinterpret_cast<uint4*>(mine + at * 128 + ((chunk ^ (at & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-              if (sub_lane == 0) factors[at] = __uint_as_float((uint32_t)(127 - 13 + e) << 23) * fabsf(to_log2);
+            for (int i = 0; i < D / 8; ++i) {
+              const uint2 lo = load_four(src, i * 8, a.wide_q), hi = load_four(src, i * 8 + 4, a.wide_q);
+              x[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
             }
           }
+        }
+        // the largest magnitude, by its bits: they are ordered like the values
+        uint32_t big = 0, also = 0;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          big = __vmaxu2(big, __vmaxu2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu));
+          also = __vmaxu2(also, __vmaxu2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
+        }
+        big = __vmaxu2(big, also);
+        big = max(big & 0xFFFFu, big >> 16);
+        // 2^e <= largest < 2^(e + 1) (an f16 below 2^-14 counts as one just there), in the range whose powers of two are normal both ways
+        const int e = min(max(a.dtype == WHEAD_KV_BF16 ? (int)(big >> 7) - 127 : max((int)(big >> 10), 1) - 15, -100), 100);
+        const float up = copysignf(__uint_as_float((uint32_t)(127 + 13 - e) << 23), to_log2);
+        f = __uint_as_float((uint32_t)(127 - 13 + e) << 23) * fabsf(to_log2);
+        uint8_t* to = smem + S::kOffQ + t * S::kQ + (quarter * 32 + lane) * 128;
+        auto put = [&](auto bf16) {
+          constexpr int kType = decltype(bf16)::value ? WHEAD_KV_BF16 : WHEAD_KV_F16;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {  // 8 channels: block i / 2, half i % 2
+            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 y = unpack16(w[k], kType);
+              w[k] = pack16(y.x * up, y.y * up, WHEAD_KV_F16);
+            }
+            *reinterpret_cast<uint4*>(to + i / 8 * (128 * 128) + (((i % 2 * 4 + i / 2 % 4) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         };
-        if (a.dtype == WHEAD_KV_BF16) turn(std::true_type{});
-        else turn(std::false_type{});
+        if (a.dtype == WHEAD_KV_BF16) put(std::true_type{});
+        else put(std::false_type{});
         fence_async();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s.q_full[t]));
-        f = factors[lane];
       }
       int free_lo, free_hi;  // keys that all rows of the tile see
       {
