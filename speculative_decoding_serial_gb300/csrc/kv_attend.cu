@@ -75,13 +75,6 @@ struct Head {  // the fixed head of shared memory
 };
 static_assert(sizeof(Head) <= 512, "");
 
-// A CTA's piece of one item: units u0 .. u1 - 1 of one (tile, KV head).
-struct Segment {
-  Tile tile;
-  int h, u0, u1;
-  long long head_at;
-};
-
 // A warp's way through a segment's groups and its ring. Lane 0 alone fetches; it has the next pages' numbers one copy ahead.
 struct Fetch {
   const uint8_t* base;      // the pool at this KV head
@@ -146,7 +139,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
   const Start start = get_start<S::kThreads, kUnit>(c, a, ROWS, s.sched);
   if ((int)blockIdx.x >= start.ctas) return;
   long long cur = range_begin(start, blockIdx.x);
-  const long long begin = cur, end = range_begin(start, blockIdx.x + 1);
+  const long long end = range_begin(start, blockIdx.x + 1);
   int item = start.item;
   long long item_at = start.at;
   uint32_t stage = 0, phase = 0;
@@ -156,6 +149,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
   fetch.slot = 0;
 
   // the segment that begins at unit `at`, and the first copies of this warp's groups; `fresh`: not the next head of the same tile
+  long long next = cur;
   auto enter = [&](long long at, bool fresh) {
     if (fresh) {
       if (item == s.sched.item && s.sched.has_tile) {
@@ -167,16 +161,14 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
           ++item;
         }
       }
-      const int past_item = (int)(at - item_at);
-      sg.h = past_item / sg.tile.units;
-      sg.u0 = past_item - sg.h * sg.tile.units;
-      sg.head_at = at - sg.u0;
+      const int past_item = (int)(at - item_at), each = sg.tile.units + kLead;
+      sg.h = past_item / each;
+      sg.head_at = item_at + (long long)sg.h * each;
     } else {
       ++sg.h;
-      sg.u0 = 0;
       sg.head_at = at;
     }
-    sg.u1 = (int)min((long long)sg.tile.units, sg.u0 + (end - at));
+    next = cut_segment(sg, at, end);
     fetch.base = c.pool + (int64_t)sg.h * (c.page_size >> 4) * S::kGroup;
     fetch.table = c.tables + (int64_t)sg.tile.slot * c.max_pages;
     fetch.next = sg.u0;
@@ -194,11 +186,11 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
   };
   if (cur < end) enter(cur, true);
 
-  while (cur < end) {
-    const Tile tile = sg.tile;
-    const int h = sg.h, u0 = sg.u0, u1 = sg.u1;
+  while (cur < end && sg.u1 > sg.u0) {  // a range may end inside a lead
+    const Segment now = sg;
+    const Tile& tile = now.tile;
+    const int h = now.h, u0 = now.u0, u1 = now.u1;
     int live_end = fetch.end;
-    const long long head_at = sg.head_at;
     // query rows: from a power of two to f16, as operands
     const float to_log2 = a.scale * c.k_scale[h] * kLog2e;
     uint2 q[S::kQInRegs ? NT : 1][S::kQInRegs ? NB : 1];
@@ -421,13 +413,13 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
       }
     }
     // the next segment's first copies come while this one is being joined
-    const long long next = head_at + u1;
+    const long long after = next;
     const bool item_done = u1 == tile.units && h == c.kv_heads - 1;
     if (item_done) {
-      item_at = next;
+      item_at = after;
       ++item;
     }
-    if (next < end) enter(next, item_done);
+    if (after < end) enter(after, item_done);
     // ---- the warps' parts joined
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -477,10 +469,9 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         }
     }
     named_sync<kConsumers>(1);
-    const long long head_end = head_at + tile.units;
     const bool whole = u0 == 0 && u1 == tile.units;
     constexpr int kPart = ROWS * (D + 2);
-    float* part = c.partial + (int64_t)(2 * blockIdx.x + (cur == begin ? 0 : 1)) * kPart;
+    float* part = c.partial + (int64_t)part_slot(start, now, blockIdx.x) * kPart;
     const float gv = c.v_scale[h];
     auto write_row = [&](int row, int col, float4 v, float mm, float ll) {
       const int grow = tile.row0 + row;
@@ -514,7 +505,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
     }
     if (!whole) {
       // ---- an item's parts joined, by the last CTA to get here
-      const int first_cta = range_owner(start, head_at), last_cta = range_owner(start, head_end - 1);
+      const int first_cta = first_owner(start, now), last_cta = last_owner(start, now);
       const int parts = last_cta - first_cta + 1;
       named_sync<kConsumers>(1);
       if (tid == 0) {  // its fence covers what the others wrote before the barrier
@@ -525,7 +516,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
       }
       named_sync<kConsumers>(1);
       if (s.last) {
-        const int first_slot = 2 * first_cta + (range_begin(start, first_cta) == head_at ? 0 : 1);
+        const int first_slot = part_slot(start, now, first_cta);
         auto part_at = [&](int k) { return c.partial + (int64_t)(k == 0 ? first_slot : 2 * (first_cta + k)) * kPart; };
 #pragma unroll 1
         for (int x = tid; x < tile.rows * (D / 4); x += kConsumers) {
@@ -562,7 +553,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         }
       }
     }
-    cur = next;
+    cur = after;
   }
 }
 
@@ -584,7 +575,7 @@ int launch_rows(const HostCache& h, AttendArgs a, int max_q) {
   int64_t ctas = std::min<int64_t>((int64_t)h.sms * S::kCtas, kMaxCtas);
   ctas = std::min(ctas, h.c.partial_floats / (2 * S::kRows * (D + 2)));
   a.planned = tiles * a.n > 4 * S::kThreads;
-  a.small = tiles * a.n * h.c.kv_heads * ((int64_t)h.c.max_pages * h.c.page_size / kUnit + 2) < INT_MAX;
+  a.small = tiles * a.n * h.c.kv_heads * ((int64_t)h.c.max_pages * h.c.page_size / kUnit + 2 + kLead) < INT_MAX;
   if (a.planned) attend_plan<kUnit><<<1, 1024, 0, h.stream>>>(h.c, a, S::kRows, (int)ctas);
   attend_rows<D, NT><<<(unsigned)ctas, S::kThreads, S::kBytes, h.stream>>>(h.c, a);
   return launch_status();

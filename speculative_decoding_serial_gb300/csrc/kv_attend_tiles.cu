@@ -190,12 +190,6 @@ __device__ __forceinline__ uint32_t sees32(const AttendArgs& a, const RowView& v
   return m;
 }
 
-struct Segment {
-  Tile tile;
-  int item, h, u0, u1;
-  long long head_at;
-};
-
 // A CTA's way through its range. Every warp walks it for itself and keeps its place in shared memory, not in registers: those are
 // short here, and what spills is read back from L2 (shared memory takes nearly all of L1).
 struct Walk {
@@ -222,18 +216,18 @@ __device__ __forceinline__ bool next_segment(const Cache& c, const AttendArgs& a
   }
   s.item = item;
   const long long item_at = w.item_at;
-  const int past = (int)(cur - item_at);
-  s.h = past / s.tile.units;
-  s.u0 = past - s.h * s.tile.units;
-  s.head_at = cur - s.u0;
-  s.u1 = (int)min((long long)s.tile.units, s.u0 + (end - cur));
+  const int past = (int)(cur - item_at), each = s.tile.units + kLead;
+  s.h = past / each;
+  s.head_at = item_at + (long long)s.h * each;
+  const long long next = cut_segment(s, cur, end);
+  if (s.u1 == s.u0) return false;  // a range may end inside a lead
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
     w.sg = s;
-    w.cur = s.head_at + s.u1;
+    w.cur = next;
     const bool done = s.u1 == s.tile.units && s.h == c.kv_heads - 1;
     w.next_item = done ? item + 1 : item;
-    if (done) w.item_at = s.head_at + s.u1;
+    if (done) w.item_at = next;
   }
   __syncwarp();
   return true;
@@ -300,12 +294,13 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
   __syncthreads();
   fence_after();
   const uint32_t tmem = __shfl_sync(~0u, s.tmem, 0);
-  const long long begin = range_begin(start, blockIdx.x);
   Walk& walk = reinterpret_cast<Walk*>(smem + S::kOffWalk)[warp];
   if (lane == 0) {
-    walk.cur = begin;
+    walk.cur = range_begin(start, blockIdx.x);
     walk.end = range_begin(start, blockIdx.x + 1);
     walk.item_at = start.at;
+    walk.sg.u0 = walk.sg.u1 = 0;
+    walk.sg.tile.units = 0;
     walk.next_item = start.item;
   }
   __syncwarp();
@@ -632,7 +627,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       constexpr int kPart = S::kRows * (D + 2);
       const int64_t out_row = (int64_t)(tile.first + tok) * a.heads + head;
       const float gv = c.v_scale[sg.h];
-      float* part = c.partial + (int64_t)(2 * blockIdx.x + (sg.head_at + sg.u0 == begin ? 0 : 1)) * kPart;
+      float* part = c.partial + (int64_t)part_slot(start, sg, blockIdx.x) * kPart;
       const float scale = whole ? (ll != 0.0f ? gv / ll : 0.0f) : 1.0f;
 #pragma unroll 1
       for (int i = 0; i < D / 16; ++i) {
@@ -676,9 +671,8 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
     // what the joining kernel has to do for the item that begins in this CTA's range and ends outside it
     if (tid == 0) {
       int4 record = make_int4(0, 0, 0, 0);
-      if (sg.u0 == 0 && sg.u1 < sg.tile.units)
-        record = make_int4(sg.item, sg.h, range_owner(start, sg.head_at + sg.tile.units - 1) - (int)blockIdx.x + 1,
-                           2 * blockIdx.x + (sg.head_at == begin ? 0 : 1));
+      if (sg.u0 == 0 && sg.u1 > 0 && sg.u1 < sg.tile.units)
+        record = make_int4(sg.item, sg.h, last_owner(start, sg) - (int)blockIdx.x + 1, part_slot(start, sg, blockIdx.x));
       *reinterpret_cast<int4*>(c.records + 4 * blockIdx.x) = record;
     }
   }
@@ -746,7 +740,7 @@ int launch(const HostCache& h, AttendArgs a, int max_q) {
   int64_t ctas = std::min<int64_t>((int64_t)h.sms, kMaxCtas);
   ctas = std::min(ctas, h.c.partial_floats / (2 * S::kRows * (D + 2)));
   a.planned = tiles * a.n > 2 * S::kThreads;
-  a.small = tiles * a.n * h.c.kv_heads * ((int64_t)h.c.max_pages * h.c.page_size / kBlock + 2) < INT_MAX;
+  a.small = tiles * a.n * h.c.kv_heads * ((int64_t)h.c.max_pages * h.c.page_size / kBlock + 2 + kLead) < INT_MAX;
   if (a.planned) attend_plan<kBlock><<<1, 1024, 0, h.stream>>>(h.c, a, S::kRows, (int)ctas);
   attend_tiles<D, TILES><<<(unsigned)ctas, S::kThreads, S::kBytes, h.stream>>>(h.c, a);
   // the joining kernel's blocks may be placed while the last CTAs still work; they wait for the grid before they read

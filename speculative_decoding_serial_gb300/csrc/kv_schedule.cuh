@@ -4,7 +4,9 @@
 // query heads of a KV head (row = token * group + head in the group), so that all rows of a tile read the same keys. An
 // item is a run of units of UNIT keys, from the first that one of its rows sees to the last. All units, laid end to end,
 // are cut into as many equal ranges as there are CTAs: ragged lengths need no balancing, and a long sequence alone fills
-// the device. An item cut by a range's end leaves partial results (each row's running maximum, its sum and its output
+// the device. Each item counts kLead units more than it has, ahead of its own: a CTA that goes on to another item spends some 9,000
+// cycles on the joins, the query rows and the first copies, a unit 2,800 to 3,400 (16 sequences of 300 to 8,200 keys: with equal units
+// the CTAs with two items ended at 26 us, those with one at 16). An item cut by a range's end leaves partial results (each row's running maximum, its sum and its output
 // before the division) in the workspace; the last CTA to finish one of its parts joins them, in the order of the keys, so
 // that results do not depend on which CTA comes last.
 #pragma once
@@ -12,6 +14,8 @@
 #include "kv_common.cuh"
 
 namespace whead_kv_impl {
+
+constexpr int kLead = 3;
 
 struct AttendArgs {
   const void* q;
@@ -87,6 +91,9 @@ __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, i
   return t;
 }
 
+// What a tile counts for in the division of the work: all KV heads' units, and their leads.
+__device__ __forceinline__ long long tile_cost(const Cache& c, const Tile& t) { return t.units ? (long long)(t.units + kLead) * c.kv_heads : 0; }
+
 // The keys that a row sees: lo <= j < hi, and the bits of its mask for j >= draft.
 struct RowView {
   int lo, hi, draft;
@@ -114,7 +121,7 @@ __device__ __forceinline__ bool sees(const RowView& v, int j) {
   return (v.bits[u >> 6] >> (u & 63)) & 1;
 }
 
-// Where a CTA's range begins: the item, and the number of the item's first unit.
+// Where a CTA's range begins: the item, and the number of the item's first unit (of its lead).
 struct Start {
   int item;
   int ctas;           // CTAs that have work: fewer than launched where there are fewer units
@@ -125,6 +132,26 @@ struct Start {
 __device__ __forceinline__ long long range_begin(const Start& s, int cta) { return s.total * cta / s.ctas; }
 // the CTA whose range holds unit x
 __device__ __forceinline__ int range_owner(const Start& s, long long x) { return (int)(((x + 1) * s.ctas - 1) / s.total); }
+
+// A CTA's piece of one (tile, KV head): its units u0 .. u1 - 1, none where the range ends inside the lead. head_at: number of the lead's
+// first unit.
+struct Segment {
+  Tile tile;
+  int item, h, u0, u1;
+  long long head_at;
+};
+// The piece of head h, whose lead begins at head_at, that a range from `at` to `end` holds; the range's rest begins where it ends.
+__device__ __forceinline__ long long cut_segment(Segment& s, long long at, long long end) {
+  const int from = (int)(at - s.head_at), to = (int)min((long long)(s.tile.units + kLead), end - s.head_at);
+  s.u0 = max(from - kLead, 0);
+  s.u1 = max(to - kLead, s.u0);
+  return s.head_at + to;
+}
+// The CTAs that hold a head's units, and where the first of them keeps its partial result: in its first place if nothing of its
+// range comes before this head.
+__device__ __forceinline__ int first_owner(const Start& s, const Segment& g) { return range_owner(s, g.head_at + kLead); }
+__device__ __forceinline__ int last_owner(const Start& s, const Segment& g) { return range_owner(s, g.head_at + kLead + g.tile.units - 1); }
+__device__ __forceinline__ int part_slot(const Start& s, const Segment& g, int cta) { return 2 * cta + (range_begin(s, cta) >= g.head_at ? 0 : 1); }
 
 // Sum of x over the threads before this one, and over all; `warps` words of shared memory.
 template <int THREADS>
@@ -168,7 +195,7 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
     const int lane = threadIdx.x & 31;
     Tile tile{};
     if (lane < items) tile = make_tile<UNIT>(c, a, lane, tile_rows);
-    const int mine = tile.units * c.kv_heads;
+    const int mine = (int)tile_cost(c, tile);
     int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -198,7 +225,7 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
   for (int base = 0; base < items; base += THREADS) {
     const int it = base + threadIdx.x;
     if (it < items) tile = make_tile<UNIT>(c, a, it, tile_rows);
-    mine = it < items ? (long long)tile.units * c.kv_heads : 0;
+    mine = it < items ? tile_cost(c, tile) : 0;
     long long all;
     before = r.total + scan64<THREADS>(mine, s.warps, all);
     r.total += all;
@@ -220,7 +247,7 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
     long long sum = 0;
     for (int base = 0; base < items && sum <= x; base += THREADS) {
       const int it = base + threadIdx.x;
-      mine = it < items ? (long long)make_tile<UNIT>(c, a, it, tile_rows).units * c.kv_heads : 0;
+      mine = it < items ? tile_cost(c, make_tile<UNIT>(c, a, it, tile_rows)) : 0;
       long long all;
       before = sum + scan64<THREADS>(mine, s.warps, all);
       if (mine > 0 && before <= x && x < before + mine) {
@@ -245,7 +272,7 @@ static __global__ void __launch_bounds__(1024, 1) attend_plan(Cache c, AttendArg
   for (int base = 0; base < items; base += 1024) {
     const int it = base + threadIdx.x;
     long long all;
-    scan64<1024>(it < items ? (long long)make_tile<UNIT>(c, a, it, tile_rows).units * c.kv_heads : 0, warps, all);
+    scan64<1024>(it < items ? tile_cost(c, make_tile<UNIT>(c, a, it, tile_rows)) : 0, warps, all);
     total += all;
   }
   Start r;
@@ -254,7 +281,7 @@ static __global__ void __launch_bounds__(1024, 1) attend_plan(Cache c, AttendArg
   long long sum = 0;
   for (int base = 0; base < items; base += 1024) {
     const int it = base + threadIdx.x;
-    const long long mine = it < items ? (long long)make_tile<UNIT>(c, a, it, tile_rows).units * c.kv_heads : 0;
+    const long long mine = it < items ? tile_cost(c, make_tile<UNIT>(c, a, it, tile_rows)) : 0;
     long long all;
     const long long before = sum + scan64<1024>(mine, warps, all);
     sum += all;
