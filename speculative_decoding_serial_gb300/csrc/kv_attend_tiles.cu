@@ -32,10 +32,10 @@ struct Shape {
   static constexpr int kRows = 128 * TILES;
   static constexpr int kSBufs = 2 / TILES;               // score buffers of a tile
   static constexpr int kBufs = 2;                        // key and value tiles
-  static constexpr int kSoft = 4 * TILES;                // softmax warps, then those that unpack, then two that issue: one a tile, or with one tile one for QK and one for PV
+  static constexpr int kSoft = 4 * TILES;                // softmax warps, then those that unpack, then two a tile that issue: QK, PV
   static constexpr int kUnpack = 8;                      // a group of each block to each
   static constexpr int kIssue = kSoft + kUnpack;
-  static constexpr int kThreads = (kIssue + 2) * 32;
+  static constexpr int kThreads = (kIssue + 2 * TILES) * 32;
   static constexpr int kGroup = 18 * D;
   static constexpr int kQ = 128 * D * 2, kK = kBlock * D * 2, kV = D * kBlock * 2;
   static constexpr int kOffWalk = 640;                   // the warps' places
@@ -46,7 +46,7 @@ struct Shape {
 
 struct Head {
   SchedShared sched;
-  unsigned long long k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[4], pv_done[4], o_full[2], q_full[2], drain[2];
+  unsigned long long k_full[2], k_free[2], v_full[2], v_free[2], s_full[4], p_full[4], pv_done[4], o_full[2], q_full[2], drain[4];
   uint32_t tmem;
 };
 
@@ -233,7 +233,7 @@ __device__ __forceinline__ bool next_segment(const Cache& c, const AttendArgs& a
   return true;
 }
 
-static_assert(sizeof(Head) <= 640 && 640 + 18 * sizeof(Walk) <= 3072, "");
+static_assert(sizeof(Head) <= 640 && 640 + 20 * sizeof(Walk) <= 3072, "");
 
 // A whole warp's wait. One that has run out is reported once; the warp then goes on without waiting, on whatever is there, to its end.
 __device__ __forceinline__ void await(const Cache& c, uint32_t bar, uint32_t parity, bool& dead) {
@@ -270,14 +270,15 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       mbar_init(smem_u32(&s.k_free[i]), TILES);
       mbar_init(smem_u32(&s.v_full[i]), S::kUnpack);
       mbar_init(smem_u32(&s.v_free[i]), TILES);
-      mbar_init(smem_u32(&s.s_full[i]), 1);
       for (int h = 0; h < 2; ++h) {
+        mbar_init(smem_u32(&s.s_full[2 * i + h]), 1);
         mbar_init(smem_u32(&s.p_full[2 * i + h]), 4);
         mbar_init(smem_u32(&s.pv_done[2 * i + h]), 1);
       }
       mbar_init(smem_u32(&s.o_full[i]), 1);
       mbar_init(smem_u32(&s.q_full[i]), 4);
-      mbar_init(smem_u32(&s.drain[i]), 1);
+      mbar_init(smem_u32(&s.drain[2 * i]), 1);
+      mbar_init(smem_u32(&s.drain[2 * i + 1]), 1);
     }
     fence_mbar_init();
   }
@@ -308,63 +309,62 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
   bool dead = false;
 
   if (warp >= S::kIssue) {
-    // ---- a tile's products
-    constexpr uint32_t kQK = (1u << 4) | ((kBlock / 8u) << 17) | ((128u / 16u) << 24);  // fp32 from f16 x f16, both along k
+    // ---- a tile's products: QK by one warp, PV by another (each spends as long on its barriers and commits as on the products). With
+    // two tiles there is one score buffer a tile: QK goes by half blocks, each as soon as the P there before has been taken, under the
+    // other half's softmax. With one tile, whose next scores have a buffer of their own, whole blocks cost less: a product of 64 keys takes
+    // 60 cycles, one of 128 keys 64 (two tiles, prompt chunk: 299 us by halves, 344 by blocks; one tile, 8 x 17 tokens: 34.8, 32.7).
+    constexpr int kKeys = kBlock / TILES, kPieces = kBlock / kKeys;  // of a QK product
+    constexpr uint32_t kQK = (1u << 4) | ((kKeys / 8u) << 17) | ((128u / 16u) << 24);  // fp32 from f16 x f16, both along k
     constexpr uint32_t kPV = (1u << 4) | ((D / 8u) << 17) | ((128u / 16u) << 24);
-    const int t = TILES == 1 ? 0 : warp - S::kIssue;
-    const bool does_qk = TILES == 2 || warp == S::kIssue, does_pv = TILES == 2 || warp != S::kIssue;
+    const int t = (warp - S::kIssue) % TILES;
     const uint32_t leader = lane == 0;
     const uint64_t dq = tile_desc(smem_u32(smem + S::kOffQ) + t * S::kQ), dk = tile_desc(smem_u32(smem + S::kOffK)), dv = tile_desc(smem_u32(smem + S::kOffV));
     const uint32_t s_col = tmem + t * S::kSBufs * kBlock, o_col = tmem + 256 + t * 128;
-    auto scores = [&](int n) {
-      const int buf = n % S::kBufs, sb = n % S::kSBufs;
-      await(c, smem_u32(&s.k_full[buf]), n / S::kBufs & 1, dead);
-      fence_after();
-      const uint64_t db = dk + (uint64_t)(buf * (S::kK >> 4));
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_ss(s_col + sb * kBlock, dq + (k / 4 * (128 * 128) + k % 4 * 32) / 16, db + (k / 4 * (kBlock * 128) + k % 4 * 32) / 16, kQK, k > 0, leader);
-      commit(smem_u32(&s.s_full[t * S::kSBufs + sb]), leader);
-      commit(smem_u32(&s.k_free[buf]), leader);
-    };
     int n = 0, seg = 0;
-    while (next_segment<S::kRows>(c, a, walk, s.sched)) {
-      // blocks first .. last - 1; scores are kSBufs ahead of outputs
-      const int first = n, last = n + __shfl_sync(~0u, sg.u1 - sg.u0, 0);
-      if (does_qk) {
+    if (warp < S::kIssue + TILES) {
+      while (next_segment<S::kRows>(c, a, walk, s.sched)) {
+        const int last = n + __shfl_sync(~0u, sg.u1 - sg.u0, 0);
         await(c, smem_u32(&s.q_full[t]), seg & 1, dead);
-        fence_after();
 #pragma unroll 1
-        for (int i = first; i < (does_pv ? min(first + S::kSBufs, last) : last); ++i) {
-          // alone, this warp does not follow the products that read what was in the score buffer: it waits for them
-          if (!does_pv && i >= S::kSBufs) await(c, smem_u32(&s.pv_done[i % S::kSBufs * 2 + 1]), (i - S::kSBufs) / S::kSBufs & 1, dead);
-          scores(i);
+        for (; n < last; ++n) {
+          const int buf = n % S::kBufs, sb = n % S::kSBufs, half0 = (t * S::kSBufs + sb) * 2;
+          await(c, smem_u32(&s.k_full[buf]), n / S::kBufs & 1, dead);
+          const uint64_t db = dk + (uint64_t)(buf * (S::kK >> 4));
+#pragma unroll
+          for (int h = 0; h < kPieces; ++h) {
+            if (n >= S::kSBufs) await(c, smem_u32(&s.pv_done[half0 + 2 / kPieces * (h + 1) - 1]), (n / S::kSBufs - 1) & 1, dead);
+            fence_after();
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_ss(s_col + sb * kBlock + h * 64, dq + (k / 4 * (128 * 128) + k % 4 * 32) / 16, db + (h * 64 * 128 + k / 4 * (kBlock * 128) + k % 4 * 32) / 16, kQK, k > 0, leader);
+            commit(smem_u32(&s.s_full[half0 + h]), leader);
+            if (kPieces == 1) commit(smem_u32(&s.s_full[half0 + 1]), leader);
+          }
+          commit(smem_u32(&s.k_free[buf]), leader);
         }
-      }
-      if (!does_pv) {
-        n = last;
         ++seg;
-        continue;
       }
+    } else {
+      while (next_segment<S::kRows>(c, a, walk, s.sched)) {
+        const int first = n, last = n + __shfl_sync(~0u, sg.u1 - sg.u0, 0);
 #pragma unroll 1
-      for (; n < last; ++n) {
-        const int buf = n % S::kBufs, sb = n % S::kSBufs, half0 = (t * S::kSBufs + sb) * 2;
-        await(c, smem_u32(&s.v_full[buf]), n / S::kBufs & 1, dead);
-        const uint64_t db = dv + (uint64_t)(buf * (S::kV >> 4));
+        for (; n < last; ++n) {
+          const int buf = n % S::kBufs, sb = n % S::kSBufs, half0 = (t * S::kSBufs + sb) * 2;
+          await(c, smem_u32(&s.v_full[buf]), n / S::kBufs & 1, dead);
+          const uint64_t db = dv + (uint64_t)(buf * (S::kV >> 4));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          await(c, smem_u32(&s.p_full[half0 + h]), n / S::kSBufs & 1, dead);
-          fence_after();
+          for (int h = 0; h < 2; ++h) {
+            await(c, smem_u32(&s.p_full[half0 + h]), n / S::kSBufs & 1, dead);
+            fence_after();
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_ts(o_col, s_col + sb * kBlock + h * 64 + k * 8, db + (h * (D * 128) + k * 32) / 16, kPV, n > first || h + k > 0, leader);
-          commit(smem_u32(&s.pv_done[half0 + h]), leader);
+            for (int k = 0; k < 4; ++k)
+              mma_ts(o_col, s_col + sb * kBlock + h * 64 + k * 8, db + (h * (D * 128) + k * 32) / 16, kPV, n > first || h + k > 0, leader);
+            commit(smem_u32(&s.pv_done[half0 + h]), leader);
+          }
+          commit(smem_u32(&s.v_free[buf]), leader);
         }
-        commit(smem_u32(&s.v_free[buf]), leader);
-        if (does_qk && n + S::kSBufs < last) scores(n + S::kSBufs);
+        commit(smem_u32(&s.o_full[t]), leader);
       }
-      commit(smem_u32(&s.o_full[t]), leader);
-      ++seg;
     }
     // nothing may be under way when the CTA gives its tensor memory back
     __syncwarp();
@@ -555,14 +555,14 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       float2 l = make_float2(0.f, 0.f);
       for (int u = sg.u0; u < sg.u1; ++u, ++n) {
         const int key0 = (tile.unit0 + u) * kBlock;
-        // these barriers belong to the score buffer: with one of each a tile, two blocks' scores could be turned into P
-        // before the issuing warp has looked for the first, and it would miss that phase
+        // these barriers belong to the half of the score buffer: with one of each a tile, two blocks' scores could be turned into
+        // P before the issuing warp has looked for the first, and it would miss that phase
         const int sb = t * S::kSBufs + n % S::kSBufs;
-        await(c, smem_u32(&s.s_full[sb]), n / S::kSBufs & 1, dead);
-        fence_after();
         // half a block at a time, each with its own P over its own scores: the first half's products run under the second's softmax
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
+          await(c, smem_u32(&s.s_full[2 * sb + h]), n / S::kSBufs & 1, dead);
+          fence_after();
           if (idle) {
             fence_before();
             if (lane == 0) mbar_arrive(smem_u32(&s.p_full[2 * sb + h]));
