@@ -596,7 +596,7 @@ extern "C" int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* x
   if (x->tree && (x->tree_words < 1 || (int64_t)x->tree_words * 64 < x->max_q || !aligned(x->tree, 8))) return WHEAD_ERR_INVALID_ARG;
   HostCache h;
   if (x->n == 0 || x->total == 0) return x->total > 0 ? WHEAD_ERR_INVALID_ARG : host_cache(kv, &h);
-  if (!x->q || !x->out || !aligned(x->q, 2) || !aligned(x->out, 16) || !aligned(x->lse, 4) || x->max_q < 1) return WHEAD_ERR_INVALID_ARG;
+  if (!x->q || !x->out || !aligned(x->q, 2) || !aligned(x->out, 16) || !aligned(x->lse, 4) || !aligned(x->indptr, 4) || !aligned(x->slots, 4) || x->max_q < 1) return WHEAD_ERR_INVALID_ARG;
   if (!x->indptr && (x->total % x->n || x->total / x->n > x->max_q)) return WHEAD_ERR_INVALID_ARG;
   const int rc = host_cache(kv, &h);
   if (rc != WHEAD_OK) return rc;

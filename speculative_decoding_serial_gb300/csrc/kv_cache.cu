@@ -947,7 +947,7 @@ int whead_kv_read(const whead_kv* kv, const int32_t* start, const int32_t* slots
   if (!kv || n < 0 || n > kv->max_seqs || count < 0 || dtype < WHEAD_KV_BF16 || dtype > WHEAD_KV_F32) return WHEAD_ERR_INVALID_ARG;
   HostCache h;
   if (n == 0 || count == 0) return host_cache(kv, &h);
-  if (!start || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16)) return WHEAD_ERR_INVALID_ARG;
+  if (!start || !k_out || !v_out || !aligned(start, 4) || !aligned(slots, 4) || !aligned(k_out, 16) || !aligned(v_out, 16)) return WHEAD_ERR_INVALID_ARG;
   const int rc = host_cache(kv, &h);
   if (rc != WHEAD_OK) return rc;
   const int64_t groups = (int64_t)n * ((count + 30LL) / 16);
@@ -965,6 +965,7 @@ int whead_kv_compact(const whead_kv* kv, const int32_t* start, const int32_t* ke
   HostCache h;
   if (n == 0) return host_cache(kv, &h);
   if (!start || (keep != nullptr) != (count != nullptr) || (!keep && keep_width > 0)) return WHEAD_ERR_INVALID_ARG;
+  if (!aligned(start, 4) || !aligned(keep, 4) || !aligned(count, 4) || !aligned(slots, 4)) return WHEAD_ERR_INVALID_ARG;
   int rc = host_cache(kv, &h);
   if (rc != WHEAD_OK) return rc;
   const CompactArgs a{start, keep, count, slots, n, keep_width};

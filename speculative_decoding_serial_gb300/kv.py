@@ -154,6 +154,7 @@ class KvCache:
         self._index = self.device.index
         self._raw_stream = torch._C._cuda_getCurrentRawStream
         self._int32 = torch.int32
+        self._scale = 1.0 / math.sqrt(head_dim)
 
     def _call(self, call, *args):
         self._p.stream = self._raw_stream(self._index)
@@ -218,29 +219,30 @@ class KvCache:
         out (as q, contiguous) and lse (total, heads) float32 may be given."""
         torch = self._torch
         n, ip, sl = self._entries(indptr, slots)
-        if q.dim() != 3 or q.shape[2] != self.head_dim or q.stride(2) != 1 or q.get_device() != self._index:
+        shape, strides = q.shape, q.stride()
+        if len(shape) != 3 or shape[2] != self.head_dim or strides[2] != 1 or q.get_device() != self._index:
             raise ValueError(f"q: shape (total, heads, {self.head_dim}) with contiguous channels on the cache's device is wanted")
-        total, heads = q.shape[0], q.shape[1]
-        code = _code(q.dtype, "attend", f32=False)
+        total, heads = shape[0], shape[1]
+        dtype = q.dtype
+        code = _code(dtype, "attend", f32=False)
         if out is None:
-            out = torch.empty((total, heads, self.head_dim), dtype=q.dtype, device=self.device)
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != self.device:
+            out = torch.empty(shape, dtype=dtype, device=self.device)
+        elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or out.get_device() != self._index:
             raise ValueError("out: a contiguous tensor like q is wanted")
         if lse is None:
             lse = torch.empty((total, heads), dtype=torch.float32, device=self.device)
-        elif lse.shape != (total, heads) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != self.device:
+        elif lse.shape != (total, heads) or lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.get_device() != self._index:
             raise ValueError("lse: a contiguous float32 tensor (total, heads) is wanted")
-        words = 0
+        words, bits = 0, None
         if tree is not None:
-            if tree.dtype != torch.int64 or tree.dim() not in (1, 2) or tree.shape[0] != total or not tree.is_contiguous() \
-                    or tree.device != self.device:
+            if tree.dtype is not torch.int64 or tree.dim() not in (1, 2) or tree.shape[0] != total or not tree.is_contiguous() \
+                    or tree.get_device() != self._index:
                 raise ValueError("tree: a contiguous int64 tensor (total,) or (total, words) is wanted")
-            words = 1 if tree.dim() == 1 else tree.shape[1]
+            words, bits = 1 if tree.dim() == 1 else tree.shape[1], tree.data_ptr()
         if max_q is None:
             max_q = total if indptr is not None else total // max(n, 1)
-        a = KvAttendArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr(), ip, sl, None if tree is None else tree.data_ptr(), total,
-                         q.stride(0), q.stride(1), n, heads, int(max_q), code, int(bool(causal)), int(window), words,
-                         1.0 / math.sqrt(self.head_dim) if scale is None else float(scale))
+        a = KvAttendArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr(), ip, sl, bits, total, strides[0], strides[1], n, heads, max_q, code,
+                         bool(causal), window, words, self._scale if scale is None else scale)
         self._call(self._lib.whead_kv_attend, ctypes.addressof(a))
         return out, lse
 
