@@ -4,6 +4,13 @@
 // s_j = scale log2(e) q.k_j, l = sum_j p_j, lse = ln 2 (m + log2 l). m is any reference near the largest s; here it is a running
 // one that is raised only when a score passes it by 2^kSlack, so that most tiles rescale nothing.
 //
+// This file: few rows of a KV head, on mma.sync. S^T = K Q^T and O^T = V^T P^T have the keys and the channels on the 16-row side and
+// the query rows on the side of 8, so that one token's 4 rows waste half a tile and not three quarters; the groups of the cache lie in
+// the operands' lane order. Bound by the cache's bytes where there are enough: 32 sequences on 2,000 to 32,768 keys, one token, 654 MB in
+// 119 us, 5.5 TB/s, 82 % of the measured copy rate; what is missing is the spread of the CTAs' ends (93 to 119 us: the memory's
+// share of an SM differs) and the unpacking, some 70 % of the issue slots. 16 on 300 to 8,200 keys (78 MB, 24 us, 3.3 TB/s) and
+// below: a CTA's start, 4 us, and the joining of the parts.
+//
 // Arithmetic. A held value without its head's fp32 factor is e2m1 x e4m3: 6 significant bits, at most 2688 and a multiple of
 // 2^-10, so f16 holds it exactly, and the factor goes into the scores' scale (keys) and the output (values). A query
 // row is scaled by a power of two to a largest value in [2^13, 2^14): bf16 and f16 rows then are f16 without rounding,
@@ -22,7 +29,6 @@ namespace {
 
 constexpr float kBias = 7.0f;                // m stands this far below the largest score at its setting: small p stay normal in f16
 constexpr float kSlack = 15.0f;              // and is set anew when a score passes it by more: p <= 2^15
-constexpr float kNoKey = -1e30f;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -118,7 +124,8 @@ __device__ __forceinline__ void fetch_one(const Cache& c, int len, Fetch& f, uin
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas)) attend_rows(Cache c, AttendArgs a) {
+__global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas)) attend_rows(const __grid_constant__ Cache c, const __grid_constant__ AttendArgs a) {
+  after_previous();
   using S = Shape<D, NT>;
   constexpr int NB = D / 16, ROWS = S::kRows, kWarps = S::kWarps, kConsumers = S::kThreads, kUnit = S::kUnit;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -137,6 +144,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
   }
   __syncwarp();
   const Start start = get_start<S::kThreads, kUnit>(c, a, ROWS, s.sched);
+  if (a.apart && tid == 0) put_record(c, 0, 0, 0, 0);
   if ((int)blockIdx.x >= start.ctas) return;
   long long cur = range_begin(start, blockIdx.x);
   const long long end = range_begin(start, blockIdx.x + 1);
@@ -503,7 +511,9 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         }
       }
     }
-    if (!whole) {
+    if (!whole && a.apart) {
+      if (tid == 0 && u0 == 0) put_record(c, item, h, last_owner(start, now) - (int)blockIdx.x + 1, part_slot(start, now, blockIdx.x));
+    } else if (!whole) {
       // ---- an item's parts joined, by the last CTA to get here
       const int first_cta = first_owner(start, now), last_cta = last_owner(start, now);
       const int parts = last_cta - first_cta + 1;
@@ -576,9 +586,17 @@ int launch_rows(const HostCache& h, AttendArgs a, int max_q) {
   ctas = std::min(ctas, h.c.partial_floats / (2 * S::kRows * (D + 2)));
   a.planned = tiles * a.n > 4 * S::kThreads;
   a.small = tiles * a.n * h.c.kv_heads * ((int64_t)h.c.max_pages * h.c.page_size / kUnit + 2 + kLead) < INT_MAX;
-  if (a.planned) attend_plan<kUnit><<<1, 1024, 0, h.stream>>>(h.c, a, S::kRows, (int)ctas);
-  attend_rows<D, NT><<<(unsigned)ctas, S::kThreads, S::kBytes, h.stream>>>(h.c, a);
-  return launch_status();
+  if (a.planned) {
+    const int rc = launch_after(attend_plan<kUnit>, dim3(1), 1024, 0, h.stream, h.c, a, S::kRows, (int)ctas);
+    if (rc != WHEAD_OK) return rc;
+  }
+  // The last CTA joins an item alone: up to 4 rows that is soon done (16 sequences of 4,096 keys 23 us, by a kernel of its own 28), for
+  // more it is the longest part of the call (one sequence, 32 rows: 71 us, 22 by a kernel of its own; 16 sequences 50 and 44). Between 4
+  // and 8 rows it depends on the parts of an item (1 sequence 24 and 17 us, 8 sequences 20 and 18, 16 sequences 25 and 26).
+  const int64_t rows = (int64_t)max_q * a.group;
+  a.apart = rows > 8 || (rows > 4 && tiles * a.n * h.c.kv_heads * 8 <= ctas);
+  const int rc = launch_after(attend_rows<D, NT>, dim3((unsigned)ctas), S::kThreads, S::kBytes, h.stream, h.c, a);
+  return rc == WHEAD_OK && a.apart ? launch_join<D, S::kRows, kUnit>(h, a, (int)ctas, max_q) : rc;
 }
 
 }  // namespace
@@ -625,6 +643,10 @@ extern "C" int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* x
   a.scale = x->scale;
   a.wide_q16 = aligned(x->q, 16) && x->q_token_stride % 8 == 0 && x->q_head_stride % 8 == 0;
   a.wide_q = aligned(x->q, 8) && x->q_token_stride % 4 == 0 && x->q_head_stride % 4 == 0;
+  // Up to 32 rows the keys' bytes and their unpacking are the work, and the rows ride along in one pass; above, every 32 rows would
+  // unpack the keys again, and the tiles' products cost the same for 36 rows as for 128. 64 sequences on 8,192 keys, 8 KV heads, by rows
+  // and tiles: 32 rows 268 and 399 us, 36 rows 510 and 403; 16 on 4,096: 44 and 61, 80 and 54.
+  // Fewer rows have kernels of fewer registers: 4 rows by the kernel for 32 take 254 us, by their own 113.
   if (rows > 32 && kv->head_dim <= 128) return launch_tiles(h, a, x->max_q);
   const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
   switch (kv->head_dim) {

@@ -2,11 +2,20 @@
 // instructions, with scores and outputs in tensor memory.
 //
 // The mathematics is kv_attend.cu's. A block is 128 keys. Eight warps turn its codes into f16 tiles in shared memory, which TILES
-// tiles of 128 rows then share; a warp a tile issues the products S = Q K^T and O += P V; four warps a tile read S, a row a thread,
-// and put P where S was. Tensor memory holds two S (128 columns each) beside the outputs: with two tiles one tile's softmax runs under
-// the other's products, with one tile (at most 128 rows) the next block's scores are there when a block's softmax ends. An issuing
-// warp needs some 1,100 cycles a block beside the products themselves (waits on barriers that are ready, commits): blocks of 64 keys,
-// which leave room for twice as many S, cost 2,200 cycles each and are slower.
+// tiles of 128 rows then share; two warps a tile issue the products, one S = Q K^T, one O += P V (one warp for both: its waits for
+// the softmax held the next block's scores back); four warps a tile read S, a
+// row a thread, and put P where S was. Tensor memory holds two S (128 columns each) beside the outputs. With one tile (at most 128
+// rows) the next block's scores are there when a block's softmax ends. With two, a tile's S is one buffer: its next scores are
+// issued by halves of 64 keys, each as soon as the product with P has read that half, and the softmax starts on the first (this and the two issuing
+// warps: 2 prompts of 2,048 tokens 344 -> 300 us).
+//
+// What bounds it: for prompts the softmax, one thread a row. At 128 keys a row and block its 128 exponentials, as many
+// multiply-adds, maxima, additions and half as many packings are some 600 issue slots of a warp; eight such warps and the eight that
+// unpack share four schedulers. 2 x 2048 tokens on 4,100 and 6,200 keys, 32 query heads on 8: 297 us, 1.03 PFLOP/s, 54 % of the
+// measured rate of large matrix products. Two threads a row (half the chain, but a trade of maxima and sums through shared memory
+// for every block) and blocks of 64 keys (twice the barriers) were slower. For a few tokens a sequence (8 x 17, 31 MB: 33 us) what a
+// CTA does once (tensor memory, query rows, the first blocks, its part for the joining) and the chain through one block: copy,
+// unpack, QK, softmax, PV.
 //
 // Shared memory holds operands in rows of 128 bytes (64 f16), 8 rows to an atom of 1024 bytes, 16-byte chunks swizzled by the row.
 // Channels 16 b + 8 s .. + 7 of a query row or key lie in chunk 4 s + b % 4 of the row, not 2 b + s: a warp's stores of a block's keys
@@ -25,7 +34,6 @@ namespace {
 constexpr int kBlock = 128;      // keys
 constexpr float kBias = 7.0f;    // as in kv_attend.cu
 constexpr float kSlack = 15.0f;
-constexpr float kNoKey = -1e30f;
 
 template <int D, int TILES>
 struct Shape {
@@ -258,6 +266,7 @@ struct RawV {
 
 template <int D, int TILES>
 __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(const __grid_constant__ Cache c, const __grid_constant__ AttendArgs a) {
+  after_previous();
   using S = Shape<D, TILES>;
   constexpr int NB = D / 16;
   extern __shared__ uint8_t smem_raw[];
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
   }
   const Start start = get_start<S::kThreads, kBlock>(c, a, S::kRows, s.sched);
   if ((int)blockIdx.x >= start.ctas) {
-    if (tid == 0) *reinterpret_cast<int4*>(c.records + 4 * blockIdx.x) = make_int4(0, 0, 0, 0);
+    if (tid == 0) put_record(c, 0, 0, 0, 0);
     return;
   }
   if (warp == S::kIssue) {
@@ -670,10 +679,8 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
     }
     // what the joining kernel has to do for the item that begins in this CTA's range and ends outside it
     if (tid == 0) {
-      int4 record = make_int4(0, 0, 0, 0);
-      if (sg.u0 == 0 && sg.u1 > 0 && sg.u1 < sg.tile.units)
-        record = make_int4(sg.item, sg.h, last_owner(start, sg) - (int)blockIdx.x + 1, part_slot(start, sg, blockIdx.x));
-      *reinterpret_cast<int4*>(c.records + 4 * blockIdx.x) = record;
+      const bool cut = sg.u0 == 0 && sg.u1 > 0 && sg.u1 < sg.tile.units;
+      put_record(c, sg.item, sg.h, cut ? last_owner(start, sg) - (int)blockIdx.x + 1 : 0, cut ? part_slot(start, sg, blockIdx.x) : 0);
     }
   }
   // tensor memory goes back when every role is through with it
@@ -681,46 +688,6 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
   __syncthreads();
   fence_after();
   if (warp == S::kIssue) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(S::kCols) : "memory");
-}
-
-// Joins the parts of the items that are cut: block (k, z) rows 16 z .. of the item that begins in CTA k's range. A kernel of its own
-// spreads this over the device: by the last CTA of each item it took 20 us of 84 (68 rows, 5 parts), here it takes 4.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(128) join_parts(Cache c, AttendArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 record = __ldcg(reinterpret_cast<const int4*>(c.records) + blockIdx.x);
-  const int parts = record.z;
-  if (parts == 0) return;
-  constexpr int kPart = ROWS * (D + 2), kLanes = D / 4, kAt = 128 / kLanes, kSlice = 16;
-  const Tile tile = make_tile<kBlock>(c, a, record.x, ROWS);
-  const float gv = c.v_scale[record.y];
-  auto part_at = [&](int k) { return c.partial + (int64_t)(k == 0 ? record.w : 2 * ((int)blockIdx.x + k)) * kPart; };
-  const int col = threadIdx.x % kLanes * 4;
-#pragma unroll 1
-  for (int i = 0; i < kSlice; i += kAt) {
-    const int row = blockIdx.y * kSlice + i + threadIdx.x / kLanes;
-    if (row >= tile.rows) return;
-    float m = kNoKey, l = 0.0f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float* p = part_at(k);
-      const float pm = __ldcg(p + row), pl = __ldcg(p + ROWS + row);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(p + 2 * ROWS + row * D + col));
-      const float now = fmaxf(m, pm), r0 = ex2(m - now), r1 = ex2(pm - now);
-      m = now;
-      l = l * r0 + pl * r1;
-      v.x = v.x * r0 + y.x * r1; v.y = v.y * r0 + y.y * r1; v.z = v.z * r0 + y.z * r1; v.w = v.w * r0 + y.w * r1;
-    }
-    const int grow = tile.row0 + row;
-    const int tok = row_token(a, grow);
-    const int64_t at = (int64_t)(tile.first + tok) * a.heads + record.y * a.group + grow - tok * a.group;
-    const float q = l != 0.0f ? gv / l : 0.0f;
-    if (l == 0.0f) v = make_float4(0.f, 0.f, 0.f, 0.f);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + col) =
-        make_uint2(pack16(v.x * q, v.y * q, a.dtype), pack16(v.z * q, v.w * q, a.dtype));
-    if (a.lse && col == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-  }
 }
 
 template <int D, int TILES>
@@ -741,28 +708,18 @@ int launch(const HostCache& h, AttendArgs a, int max_q) {
   ctas = std::min(ctas, h.c.partial_floats / (2 * S::kRows * (D + 2)));
   a.planned = tiles * a.n > 2 * S::kThreads;
   a.small = tiles * a.n * h.c.kv_heads * ((int64_t)h.c.max_pages * h.c.page_size / kBlock + 2 + kLead) < INT_MAX;
-  if (a.planned) attend_plan<kBlock><<<1, 1024, 0, h.stream>>>(h.c, a, S::kRows, (int)ctas);
-  attend_tiles<D, TILES><<<(unsigned)ctas, S::kThreads, S::kBytes, h.stream>>>(h.c, a);
-  // the joining kernel's blocks may be placed while the last CTAs still work; they wait for the grid before they read
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t config{};
-  config.gridDim = dim3((unsigned)ctas, (unsigned)std::min<int64_t>(S::kRows / 16, ((int64_t)max_q * a.group + 15) / 16));
-  config.blockDim = dim3(128);
-  config.stream = h.stream;
-  config.attrs = &early;
-  config.numAttrs = 1;
-  if (cudaLaunchKernelEx(&config, join_parts<D, S::kRows>, h.c, a) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return WHEAD_ERR_CUDA;
-  }
-  return launch_status();
+  int rc = WHEAD_OK;
+  if (a.planned) rc = launch_after(attend_plan<kBlock>, dim3(1), 1024, 0, h.stream, h.c, a, S::kRows, (int)ctas);
+  if (rc == WHEAD_OK) rc = launch_after(attend_tiles<D, TILES>, dim3((unsigned)ctas), S::kThreads, S::kBytes, h.stream, h.c, a);
+  if (rc != WHEAD_OK) return rc;
+  return launch_join<D, S::kRows, kBlock>(h, a, (int)ctas, max_q);
 }
 
 }  // namespace
 
 int launch_tiles(const HostCache& h, const AttendArgs& a, int max_q) {
+  // Two tiles share the unpacked keys where there are rows for both (64 sequences on 8,192 keys, 256 rows: 468 us, one tile a CTA 811); one
+  // has its scores a block ahead (128 rows: 419 us, in a CTA for two 424; 16 on 4,096 keys 36 rows 62 and 67).
   const int64_t rows = (int64_t)max_q * a.group;
   if (h.c.head_dim == 64) return rows <= 128 ? launch<64, 1>(h, a, max_q) : launch<64, 2>(h, a, max_q);
   return rows <= 128 ? launch<128, 1>(h, a, max_q) : launch<128, 2>(h, a, max_q);

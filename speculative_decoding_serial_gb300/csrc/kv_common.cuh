@@ -17,6 +17,7 @@ constexpr int kMaxCtas = 2048;        // most CTAs of an attend launch (partial 
 constexpr int kRegionPages = WHEAD_KV_MAX_BLOCK / 16 + 1;  // pages that a block's tokens can lie in
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoKey = -1e30f;  // a running maximum before the first key
 
 // Workspace: the control words, then per-slot arrays, then the attention's counters and partial results.
 struct Ctl {
@@ -50,12 +51,9 @@ struct Cache {
 
 __host__ __device__ inline int64_t align256(int64_t x) { return (x + 255) & ~(int64_t)255; }
 
-// Floats of partial results: two for each CTA (a CTA's range of work begins inside one item and ends inside another).
-// The largest tiles: 128 rows by one CTA an SM (head_dim <= 128), or 32 rows by up to eight.
-inline int64_t partial_floats(int head_dim, int sms) {
-  const int64_t one = (int64_t)sms * 2 * 256 * (head_dim + 2);
-  return one;
-}
+// Floats of partial results: two for each CTA (a CTA's range of work begins inside one item and ends inside another). The most
+// rows an SM has under way: 256, by one CTA of two tiles; the kernel for few rows has up to four CTAs of 32.
+inline int64_t partial_floats(int head_dim, int sms) { return (int64_t)sms * 2 * 256 * (head_dim + 2); }
 
 // ---------------------------------------------------------------- number formats
 
@@ -106,51 +104,8 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-__device__ __forceinline__ float load_elem(const void* p, int64_t i, int dtype) {
-  if (dtype == WHEAD_KV_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  if (dtype == WHEAD_KV_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return static_cast<const float*>(p)[i];
-}
-
-// N consecutive elements (N = 2 or 4) from i on; `wide`: the address is a multiple of their size
-template <int N>
-__device__ __forceinline__ void load_elems(const void* p, int64_t i, int dtype, bool wide, float (&x)[N]) {
-  if (!wide) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) x[k] = load_elem(p, i + k, dtype);
-    return;
-  }
-  if (dtype == WHEAD_KV_F32) {
-    if constexpr (N == 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-      const float2 v = __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p) + i));
-      x[0] = v.x; x[1] = v.y;
-    }
-    return;
-  }
-  uint32_t w[N / 2];
-  if constexpr (N == 4) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
-    w[0] = v.x; w[1] = v.y;
-  } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i));
-  }
-#pragma unroll
-  for (int k = 0; k < N / 2; ++k) {
-    if (dtype == WHEAD_KV_BF16) {
-      x[2 * k] = __uint_as_float(w[k] << 16);
-      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-      x[2 * k] = f.x;
-      x[2 * k + 1] = f.y;
-    }
-  }
-}
-
-// The same in two steps, so that many loads can be under way before the first is looked at: N elements as they are, and their values.
+// N consecutive elements from i on, in two steps, so that many loads can be under way before the first is looked at: the elements as
+// they are, and their values. `wide`: the address is a multiple of their size.
 template <int DTYPE, int N>
 struct RawElems {
   uint32_t w[DTYPE == WHEAD_KV_F32 ? N : N / 2];
@@ -298,8 +253,35 @@ int host_cache(const whead_kv* kv, HostCache* out);
 int device_sms();
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-inline int launch_status() {
-  if (cudaGetLastError() != cudaSuccess) return WHEAD_ERR_CUDA;
+
+// ---------------------------------------------------------------- launches
+
+// Every kernel of the cache may be placed while the one before it in the stream still runs. It lets the next one be placed as soon
+// as all of its own CTAs are, and waits for the one before it to end before it looks at anything: that hides most of the time
+// between two kernels, which counts where a call is two or three small ones (a fork, three kernels, and the reading of what it
+// wrote: 16.7 us where a kernel waits but does not let the next one go early, 15.7 so). A chain stays in order: a kernel that has
+// ended has waited for all before it.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  if (cudaLaunchKernelEx(&config, kernel, P(args)...) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return WHEAD_ERR_CUDA;
+  }
   return WHEAD_OK;
 }
 

@@ -5,10 +5,11 @@
 // item is a run of units of UNIT keys, from the first that one of its rows sees to the last. All units, laid end to end,
 // are cut into as many equal ranges as there are CTAs: ragged lengths need no balancing, and a long sequence alone fills
 // the device. Each item counts kLead units more than it has, ahead of its own: a CTA that goes on to another item spends some 9,000
-// cycles on the joins, the query rows and the first copies, a unit 2,800 to 3,400 (16 sequences of 300 to 8,200 keys: with equal units
-// the CTAs with two items ended at 26 us, those with one at 16). An item cut by a range's end leaves partial results (each row's running maximum, its sum and its output
-// before the division) in the workspace; the last CTA to finish one of its parts joins them, in the order of the keys, so
-// that results do not depend on which CTA comes last.
+// cycles on the joins, the query rows and the first copies, a unit 2,800 to 3,400 (16 sequences of 300 to 8,200 keys: with equal
+// units the CTAs with two items ended at 26 us, those with one at 16). An item cut by a range's end leaves partial results (each
+// row's running maximum, its sum and its output before the division) in the workspace. Few rows: the last CTA to finish one
+// of an item's parts joins them; many rows: a second kernel does. Either way in the order of the keys, so that results do not
+// depend on which CTA comes last.
 #pragma once
 
 #include "kv_common.cuh"
@@ -30,6 +31,7 @@ struct AttendArgs {
   float scale;
   bool wide_q, wide_q16;  // query rows can be read 8, 16 bytes at a time
   int planned;  // the CTAs' starts are in the workspace
+  int apart;    // a kernel of its own joins the parts (few rows; always so for many)
   int small;    // all units are less than 2^31
 };
 
@@ -265,7 +267,8 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
 
 // The same for all CTAs of a launch, by one CTA, into the workspace (many items).
 template <int UNIT>
-static __global__ void __launch_bounds__(1024, 1) attend_plan(Cache c, AttendArgs a, int tile_rows, int ctas) {
+static __global__ void __launch_bounds__(1024, 1) attend_plan(const __grid_constant__ Cache c, const __grid_constant__ AttendArgs a, int tile_rows, int ctas) {
+  after_previous();
   __shared__ long long warps[32];
   const int items = a.n * a.row_tiles;
   long long total = 0;
@@ -317,6 +320,79 @@ __device__ __forceinline__ Start get_start(const Cache& c, const AttendArgs& a, 
     r.at = *reinterpret_cast<const long long*>(from + 2);
   }
   return r;
+}
+
+// What a joining kernel has to do for the item that begins in this CTA's range and ends outside it: c.records + 4 CTA holds item, KV
+// head, parts (none: 0) and the first part's place. Written by one thread, zeros first.
+__device__ __forceinline__ void put_record(const Cache& c, int item, int h, int parts, int slot) {
+  *reinterpret_cast<int4*>(c.records + 4 * blockIdx.x) = make_int4(item, h, parts, slot);
+}
+
+// Joins the parts of the items that are cut: block (k, z) the z-th `slice` rows of the item that begins in CTA k's range. Bound by
+// latency, so four parts' loads are under way at once. A kernel of its own spreads this over the device: by the last CTA of each
+// item it took 20 us of 84 (8 sequences, 68 rows, 5 parts), and 55 of 71 for one sequence (32 rows, 32 parts).
+template <int D, int ROWS, int UNIT>
+__global__ void __launch_bounds__(128) join_parts(const __grid_constant__ Cache c, const __grid_constant__ AttendArgs a, int slice) {
+  after_previous();
+  const int4 record = __ldcg(reinterpret_cast<const int4*>(c.records) + blockIdx.x);
+  const int parts = record.z;
+  if (parts == 0) return;
+  constexpr int kPart = ROWS * (D + 2), kLanes = D / 4, kAt = 128 / kLanes;
+  const Tile tile = make_tile<UNIT>(c, a, record.x, ROWS);
+  const float gv = c.v_scale[record.y];
+  auto part_at = [&](int k) { return c.partial + (int64_t)(k == 0 ? record.w : 2 * ((int)blockIdx.x + k)) * kPart; };
+  const int col = threadIdx.x % kLanes * 4;
+#pragma unroll 1
+  for (int i = 0; i < slice; i += kAt) {
+    const int row = blockIdx.y * slice + i + threadIdx.x / kLanes;
+    if (row >= tile.rows) return;
+    float m = kNoKey, l = 0.0f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int k0 = 0; k0 < parts; k0 += 4) {
+      float pm[4], pl[4];
+      float4 y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float* p = part_at(min(k0 + k, parts - 1));
+        pm[k] = __ldcg(p + row);
+        pl[k] = __ldcg(p + ROWS + row);
+        y[k] = __ldcg(reinterpret_cast<const float4*>(p + 2 * ROWS + row * D + col));
+      }
+      float now = m;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) now = fmaxf(now, pm[k]);
+      const float r0 = ex2(m - now);
+      m = now;
+      l *= r0;
+      v.x *= r0; v.y *= r0; v.z *= r0; v.w *= r0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k0 + k >= parts) break;
+        const float r1 = ex2(pm[k] - m);
+        l += pl[k] * r1;
+        v.x += y[k].x * r1; v.y += y[k].y * r1; v.z += y[k].z * r1; v.w += y[k].w * r1;
+      }
+    }
+    const int grow = tile.row0 + row;
+    const int tok = row_token(a, grow);
+    const int64_t at = (int64_t)(tile.first + tok) * a.heads + record.y * a.group + grow - tok * a.group;
+    const float q = l != 0.0f ? gv / l : 0.0f;
+    if (l == 0.0f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * D + col) =
+        make_uint2(pack16(v.x * q, v.y * q, a.dtype), pack16(v.z * q, v.w * q, a.dtype));
+    if (a.lse && col == 0) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
+// A block takes as many rows as its threads hold, and no second pass (one sequence of 4,096 keys, 256 rows: 35 us, with 16 rows a block
+// 45). Where entries have several tiles there are blocks enough, most with nothing to join, and fewer are better (2 x 2048 tokens 299
+// us, with 4 rows a block 300; one of 2048 on 512 keys 29 and 32).
+template <int D, int ROWS, int UNIT>
+int launch_join(const HostCache& h, const AttendArgs& a, int ctas, int max_q) {
+  const int64_t most = (int64_t)max_q * a.group, rows = most < ROWS ? most : ROWS;
+  const int slice = most > 256 ? 16 : 512 / D;
+  return launch_after(join_parts<D, ROWS, UNIT>, dim3((unsigned)ctas, (unsigned)((rows + slice - 1) / slice)), 128, 0, h.stream, h.c, a, slice);
 }
 
 }  // namespace whead_kv_impl
