@@ -269,7 +269,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
     // keys that every row sees need no looking at masks
     const int t0 = row_token(a, tile.row0), t1 = row_token(a, tile.row0 + tile.rows - 1), past = tile.len - tile.tokens;
     const int free_hi = a.tree ? min(past, past + t0 + 1) : a.causal ? min(past + t0 + 1, tile.len) : tile.len;
-    const int free_lo = a.window ? max(past + t1 - a.window + 1, 0) : 0;
+    const int free_lo = a.window ? window_begin(a, past + t1) : 0;
     // G neighbouring groups at a time, from key0 on
     auto work = [&](auto count, const uint8_t* gp, int key0) {
       constexpr int G = decltype(count)::value;

@@ -555,7 +555,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       {
         const int w0 = row_token(a, tile.row0 + sub), w1 = row_token(a, tile.row0 + max(min(sub + 128, tile.rows), sub + 1) - 1), past = tile.len - tile.tokens;
         const int hi = a.tree ? min(past, past + w0 + 1) : a.causal ? min(past + w0 + 1, tile.len) : tile.len;
-        const int lo = a.window ? max(past + w1 - a.window + 1, 0) : 0;
+        const int lo = a.window ? window_begin(a, past + w1) : 0;
         free_hi = hi;
         free_lo = lo;
       }

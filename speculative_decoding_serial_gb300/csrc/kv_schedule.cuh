@@ -60,6 +60,10 @@ inline void set_group(AttendArgs* a, int group) {
   a->group_mul = (uint32_t)(((1ULL << 32) * ((1ULL << l) - (uint64_t)group)) / (uint64_t)group + 1);
 }
 
+// The first key in the window of a token at this position. A position may be negative (more query tokens than keys) and a window as long
+// as an int holds, so that their difference is formed only where it is not.
+__device__ __forceinline__ int window_begin(const AttendArgs& a, int pos) { return pos >= a.window ? pos - a.window + 1 : 0; }
+
 template <int UNIT>
 __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, int item, int tile_rows) {
   Tile t;
@@ -87,7 +91,7 @@ __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, i
   const int t0 = row_token(a, t.row0), t1 = row_token(a, t.row0 + t.rows - 1);
   int hi = t.len, lo = 0;
   if (a.causal) hi = min(max(t.len - t.tokens + t1 + 1, 0), t.len);
-  if (a.window) lo = max(t.len - t.tokens + t0 - a.window + 1, 0);
+  if (a.window) lo = window_begin(a, t.len - t.tokens + t0);
   t.unit0 = lo / UNIT;
   t.units = max((hi + UNIT - 1) / UNIT - t.unit0, 1);  // at least one: somebody has to write the rows
   return t;
@@ -108,7 +112,7 @@ __device__ __forceinline__ RowView row_view(const AttendArgs& a, const Tile& t, 
   const int tok = row_token(a, row);
   const int pos = t.len - t.tokens + tok;
   v.hi = a.causal ? min(pos + 1, t.len) : t.len;
-  if (a.window) v.lo = max(pos - a.window + 1, 0);
+  if (a.window) v.lo = window_begin(a, pos);
   if (a.tree) {
     v.draft = t.len - t.tokens;
     v.bits = a.tree + (int64_t)(t.first + tok) * a.tree_words;

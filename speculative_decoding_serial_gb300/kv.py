@@ -20,6 +20,7 @@ from . import whead as _wh
 
 BF16, F16, F32 = 0, 1, 2
 MAX_BLOCK = 256
+INT_MAX = 2 ** 31 - 1
 
 # Every symbol include/whead_kv.h declares.
 EXPORTS = ("whead_kv_page_bytes", "whead_kv_workspace_bytes", "whead_kv_append", "whead_kv_read", "whead_kv_attend",
@@ -201,6 +202,8 @@ class KvCache:
             raise ValueError(f"start: {n} values are wanted")
         dtype = torch.bfloat16 if dtype is None else dtype
         code, count = _code(dtype, "read"), int(count)
+        if not 0 <= count <= INT_MAX:
+            raise ValueError("read: 0 <= count < 2^31 is wanted")
         shape = (n, count, self.kv_heads, self.head_dim)
         k = torch.empty(shape, dtype=dtype, device=self.device)
         v = torch.empty(shape, dtype=dtype, device=self.device)
@@ -241,6 +244,8 @@ class KvCache:
             words, bits = 1 if tree.dim() == 1 else tree.shape[1], tree.data_ptr()
         if max_q is None:
             max_q = total if indptr is not None else total // max(n, 1)
+        if window > INT_MAX or max_q > INT_MAX:
+            raise ValueError("window and max_q have to be below 2^31")
         a = KvAttendArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr(), ip, sl, bits, total, strides[0], strides[1], n, heads, max_q, code,
                          bool(causal), window, words, self._scale if scale is None else scale)
         self._call(self._lib.whead_kv_attend, ctypes.addressof(a))

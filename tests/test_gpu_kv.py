@@ -263,6 +263,21 @@ def test_attend_ragged_queries_any_slots_and_strides(torch, kv, d, group, counts
     check(torch, c, kvs, q, out, lse, counts, slots=slots)
 
 
+@pytest.mark.parametrize("t", [3, 40])
+def test_attend_longest_window(torch, kv, t):
+    """A window as long as an int holds limits nothing, also where an entry has more query tokens than keys."""
+    lens, h, d = [2, 0, 100], 2, 64
+    c = make(kv, torch, 3, 128, h, d, 16)
+    kvs = fill(torch, c, lens, 11)
+    q = randn(torch, (3 * t, h * 2, d), torch.bfloat16, 12)
+    out, lse = c.attend(q, window=2 ** 31 - 1)
+    assert c.status() == 0
+    check(torch, c, kvs, q, out, lse, [t] * 3)
+    for bad in (2 ** 31, 2 ** 32 + 5, -1):
+        with pytest.raises((ValueError, RuntimeError)):
+            c.attend(q, window=bad)
+
+
 def test_attend_many_entries(torch, kv):
     """More (entry, row tile) pairs than a CTA scans for itself, for both ways of dividing the rows."""
     n, h, d = 600, 1, 64
