@@ -571,14 +571,8 @@ template <int D, int NT>
 int launch_rows(const HostCache& h, AttendArgs a, int max_q) {
   using S = Shape<D, NT>;
   constexpr int kUnit = S::kUnit;
-  static bool granted = false;
-  if (!granted) {
-    if (cudaFuncSetAttribute(attend_rows<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return WHEAD_ERR_CUDA;
-    }
-    granted = true;
-  }
+  static std::atomic<bool> granted[kMaxDevices];
+  if (!grant_smem(attend_rows<D, NT>, S::kBytes, h, granted)) return WHEAD_ERR_CUDA;
   const int64_t tiles = ((int64_t)max_q * a.group + S::kRows - 1) / S::kRows;
   if (tiles * a.n >= INT_MAX) return WHEAD_ERR_UNSUPPORTED;
   a.row_tiles = (int)tiles;

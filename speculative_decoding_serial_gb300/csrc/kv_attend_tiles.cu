@@ -693,14 +693,8 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
 template <int D, int TILES>
 int launch(const HostCache& h, AttendArgs a, int max_q) {
   using S = Shape<D, TILES>;
-  static bool granted = false;
-  if (!granted) {
-    if (cudaFuncSetAttribute(attend_tiles<D, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return WHEAD_ERR_CUDA;
-    }
-    granted = true;
-  }
+  static std::atomic<bool> granted[kMaxDevices];
+  if (!grant_smem(attend_tiles<D, TILES>, S::kBytes, h, granted)) return WHEAD_ERR_CUDA;
   const int64_t tiles = ((int64_t)max_q * a.group + S::kRows - 1) / S::kRows;
   if (tiles * a.n >= INT_MAX) return WHEAD_ERR_UNSUPPORTED;
   a.row_tiles = (int)tiles;

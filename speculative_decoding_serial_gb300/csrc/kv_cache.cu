@@ -42,16 +42,17 @@ int check_shape(const whead_kv& k) {
 
 }  // namespace
 
-int device_sms() {
-  static int cached[64] = {};
+int device_sms(int* device) {
+  static std::atomic<int> cached[kMaxDevices];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  if (cached[dev] == 0) {
-    int n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  *device = dev;
+  int n = cached[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    cached[dev] = n;
+    cached[dev].store(n, std::memory_order_relaxed);
   }
-  return cached[dev];
+  return n;
 }
 
 int host_cache(const whead_kv* kv, HostCache* out) {
@@ -63,7 +64,7 @@ int host_cache(const whead_kv* kv, HostCache* out) {
   if (!aligned(kv->pool, 16) || !aligned(kv->workspace, 256) || !aligned(kv->lens, 4) || !aligned(kv->refs, 4) ||
       !aligned(kv->tables, 4) || !aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4))
     return WHEAD_ERR_INVALID_ARG;
-  out->sms = device_sms();
+  out->sms = device_sms(&out->device);
   if (out->sms < 1) {
     (void)cudaGetLastError();
     return WHEAD_ERR_CUDA;
@@ -861,14 +862,8 @@ int launch_write(const HostCache& h, const AppendArgs& a, dim3 grid) {
 template <int D>
 int launch_move(const HostCache& h, const CompactArgs& a) {
   const int smem = kMoveTokens * 4 + kMoveGroups * 18 * D;
-  static bool granted = false;
-  if (!granted) {
-    if (cudaFuncSetAttribute(compact_move<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return WHEAD_ERR_CUDA;
-    }
-    granted = true;
-  }
+  static std::atomic<bool> granted[kMaxDevices];
+  if (!grant_smem(compact_move<D>, smem, h, granted)) return WHEAD_ERR_CUDA;
   return launch_after(compact_move<D>, dim3(a.n, h.c.kv_heads), 128, smem, h.stream, h.c, a);
 }
 }  // namespace
@@ -889,7 +884,8 @@ int64_t whead_kv_workspace_bytes(const whead_kv* kv) {
   if (!kv) return WHEAD_ERR_INVALID_ARG;
   const int rc = check_shape(*kv);
   if (rc != WHEAD_OK) return rc;
-  const int sms = device_sms();
+  int device;
+  const int sms = device_sms(&device);
   if (sms < 1) {
     (void)cudaGetLastError();
     return WHEAD_ERR_CUDA;

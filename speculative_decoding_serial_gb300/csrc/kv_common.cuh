@@ -9,6 +9,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 namespace whead_kv_impl {
@@ -245,12 +246,12 @@ __device__ __forceinline__ int slot_len(const Cache& c, int slot) {
 struct HostCache {
   Cache c;
   cudaStream_t stream;
-  int sms;
+  int device, sms;
 };
 
 // Checks a whead_kv and lays its workspace out; WHEAD_OK or an error.
 int host_cache(const whead_kv* kv, HostCache* out);
-int device_sms();
+int device_sms(int* device);  // SMs of the current device, 0 on an error
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -264,6 +265,19 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Lets a kernel have more than 48 KB of shared memory, once on each device; `granted`: a static of the kernel's own.
+constexpr int kMaxDevices = 64;
+template <typename K>
+bool grant_smem(K* kernel, int bytes, const HostCache& h, std::atomic<bool> (&granted)[kMaxDevices]) {
+  if (granted[h.device].load(std::memory_order_relaxed)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return false;
+  }
+  granted[h.device].store(true, std::memory_order_relaxed);
+  return true;
 }
 
 template <typename... P, typename... A>

@@ -154,12 +154,17 @@ class KvCache:
         assert self.device.index is not None
         self._index = self.device.index
         self._raw_stream = torch._C._cuda_getCurrentRawStream
+        self._device = torch._C._cuda_getDevice
         self._int32 = torch.int32
         self._scale = 1.0 / math.sqrt(head_dim)
 
     def _call(self, call, *args):
         self._p.stream = self._raw_stream(self._index)
-        rc = call(self._ref, *args)
+        if self._device() == self._index:
+            rc = call(self._ref, *args)
+        else:
+            with self._torch.cuda.device(self._index):
+                rc = call(self._ref, *args)
         if rc:
             raise _wh.WheadError(rc, call.__name__)
 
@@ -277,7 +282,8 @@ class KvCache:
     def status(self, check=False) -> int:
         """Waits for the current stream and returns the first device-side error since the last call (0: none)."""
         self._p.stream = self._raw_stream(self._index)
-        code = int(self._lib.whead_kv_status(self._ref))
+        with self._torch.cuda.device(self._index):
+            code = int(self._lib.whead_kv_status(self._ref))
         if check and code:
             raise _wh.WheadError(code, "whead_kv_status")
         return code
