@@ -13,7 +13,7 @@
 // multiply-adds, maxima, additions and half as many packings are some 600 issue slots of a warp; eight such warps and the eight that
 // unpack share four schedulers. 2 x 2048 tokens on 4,100 and 6,200 keys, 32 query heads on 8: 297 us, 1.03 PFLOP/s, 54 % of the
 // measured rate of large matrix products. Two threads a row (half the chain, but a trade of maxima and sums through shared memory
-// for every block) and blocks of 64 keys (twice the barriers) were slower. For a few tokens a sequence (8 x 17, 31 MB: 33 us) what a
+// for every block) and blocks of 64 keys (twice the barriers) were slower. For a few tokens a sequence (8 x 17, 31 MB: 30 us) what a
 // CTA does once (tensor memory, query rows, the first blocks, its part for the joining) and the chain through one block: copy,
 // unpack, QK, softmax, PV.
 //
