@@ -49,7 +49,7 @@ typedef struct {
   int32_t kv_heads;      /* 1..1024 */
   int32_t head_dim;      /* 64, 128 or 256 */
   int32_t max_seqs;      /* slots: 1..4096 */
-  int32_t max_pages;     /* most pages of a slot; max_pages * page_size < 2^31 */
+  int32_t max_pages;     /* most pages of a slot; max_pages * page_size <= 2^31 - 1024 */
   int32_t num_pages;     /* pages of the pool */
   void* pool;            /* 16-byte aligned */
   int32_t* lens;

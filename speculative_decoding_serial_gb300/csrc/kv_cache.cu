@@ -36,7 +36,8 @@ int check_shape(const whead_kv& k) {
   if (k.head_dim != 64 && k.head_dim != 128 && k.head_dim != 256) return WHEAD_ERR_UNSUPPORTED;
   if (k.kv_heads < 1 || k.max_seqs < 1 || k.max_pages < 1 || k.num_pages < 1) return WHEAD_ERR_INVALID_ARG;
   if (k.kv_heads > 1024 || k.max_seqs > 4096) return WHEAD_ERR_UNSUPPORTED;
-  if ((int64_t)k.max_pages * k.page_size >= INT_MAX || (int64_t)k.max_seqs * k.max_pages >= INT_MAX) return WHEAD_ERR_UNSUPPORTED;
+  // positions are ints, and the attention forms those of up to three blocks of 128 keys past a slot's end
+  if ((int64_t)k.max_pages * k.page_size > INT_MAX - 1023 || (int64_t)k.max_seqs * k.max_pages >= INT_MAX) return WHEAD_ERR_UNSUPPORTED;
   return WHEAD_OK;
 }
 

@@ -71,6 +71,15 @@ def test_a_bad_cache_is_refused_by_every_call(L, kw, code):
             assert L.whead_kv_attend(p, ctypes.addressof(a)) == code
 
 
+@pytest.mark.parametrize("page", [16, 64, 128])
+def test_longest_slot(L, page):
+    """Positions are ints: the keys of a block that begins before a slot's end, and of the two after it, have to stay below 2^31."""
+    most = (2 ** 31 - 1024) // page
+    for extra, refused in ((0, False), (1, True), (1024 // page - 1, True)):
+        p = params(page_size=page, max_seqs=1, max_pages=most + extra)
+        assert (L.whead_kv_workspace_bytes(ctypes.addressof(p)) == wh.ERR_UNSUPPORTED) == refused
+
+
 def attend_args(**kw):
     a = kv.KvAttendArgs(q=FAKE, out=FAKE, lse=FAKE, total=8, q_token_stride=4096, q_head_stride=128, n=2, heads=32, max_q=4, dtype=0,
                         causal=1, scale=0.1)
