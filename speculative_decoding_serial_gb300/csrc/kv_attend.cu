@@ -574,7 +574,6 @@ int launch_rows(const HostCache& h, AttendArgs a, int max_q) {
   static std::atomic<bool> granted[kMaxDevices];
   if (!grant_smem(attend_rows<D, NT>, S::kBytes, h, granted)) return WHEAD_ERR_CUDA;
   const int64_t tiles = ((int64_t)max_q * a.group + S::kRows - 1) / S::kRows;
-  if (tiles * a.n >= INT_MAX) return WHEAD_ERR_UNSUPPORTED;
   a.row_tiles = (int)tiles;
   int64_t ctas = std::min<int64_t>((int64_t)h.sms * S::kCtas, kMaxCtas);
   ctas = std::min(ctas, h.c.partial_floats / (2 * S::kRows * (D + 2)));
@@ -610,11 +609,13 @@ extern "C" int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* x
   if (x->n == 0 || x->total == 0) return x->total > 0 ? WHEAD_ERR_INVALID_ARG : host_cache(kv, &h);
   if (!x->q || !x->out || !aligned(x->q, 2) || !aligned(x->out, 16) || !aligned(x->lse, 4) || !aligned(x->indptr, 4) || !aligned(x->slots, 4) || x->max_q < 1) return WHEAD_ERR_INVALID_ARG;
   if (!x->indptr && (x->total % x->n || x->total / x->n > x->max_q)) return WHEAD_ERR_INVALID_ARG;
+  const int group = x->heads / kv->kv_heads;
+  const int max_q = (int)std::min<int64_t>(x->max_q, x->total);
+  const int64_t rows = (int64_t)max_q * group;
+  const int tile = tile_rows(kv->head_dim, rows);
+  if (rows >= INT_MAX / 2 || (rows + tile - 1) / tile * x->n > kMaxItems) return WHEAD_ERR_UNSUPPORTED;
   const int rc = host_cache(kv, &h);
   if (rc != WHEAD_OK) return rc;
-  const int group = x->heads / kv->kv_heads;
-  const int64_t rows = (int64_t)x->max_q * group;
-  if (rows >= INT_MAX / 2) return WHEAD_ERR_UNSUPPORTED;
   AttendArgs a{};
   a.q = x->q;
   a.out = x->out;
@@ -641,11 +642,10 @@ extern "C" int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* x
   // unpack the keys again, and the tiles' products cost the same for 36 rows as for 128. 64 sequences on 8,192 keys, 8 KV heads, by rows
   // and tiles: 32 rows 268 and 399 us, 36 rows 510 and 403; 16 on 4,096: 44 and 61, 80 and 54.
   // Fewer rows have kernels of fewer registers: 4 rows by the kernel for 32 take 254 us, by their own 113.
-  if (rows > 32 && kv->head_dim <= 128) return launch_tiles(h, a, x->max_q);
-  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+  if (tile > 32) return launch_tiles(h, a, max_q);
   switch (kv->head_dim) {
-    case 64: return nt == 1 ? launch_rows<64, 1>(h, a, x->max_q) : nt == 2 ? launch_rows<64, 2>(h, a, x->max_q) : launch_rows<64, 4>(h, a, x->max_q);
-    case 128: return nt == 1 ? launch_rows<128, 1>(h, a, x->max_q) : nt == 2 ? launch_rows<128, 2>(h, a, x->max_q) : launch_rows<128, 4>(h, a, x->max_q);
-    default: return nt == 1 ? launch_rows<256, 1>(h, a, x->max_q) : launch_rows<256, 2>(h, a, x->max_q);
+    case 64: return tile == 8 ? launch_rows<64, 1>(h, a, max_q) : tile == 16 ? launch_rows<64, 2>(h, a, max_q) : launch_rows<64, 4>(h, a, max_q);
+    case 128: return tile == 8 ? launch_rows<128, 1>(h, a, max_q) : tile == 16 ? launch_rows<128, 2>(h, a, max_q) : launch_rows<128, 4>(h, a, max_q);
+    default: return tile == 8 ? launch_rows<256, 1>(h, a, max_q) : launch_rows<256, 2>(h, a, max_q);
   }
 }

@@ -696,7 +696,6 @@ int launch(const HostCache& h, AttendArgs a, int max_q) {
   static std::atomic<bool> granted[kMaxDevices];
   if (!grant_smem(attend_tiles<D, TILES>, S::kBytes, h, granted)) return WHEAD_ERR_CUDA;
   const int64_t tiles = ((int64_t)max_q * a.group + S::kRows - 1) / S::kRows;
-  if (tiles * a.n >= INT_MAX) return WHEAD_ERR_UNSUPPORTED;
   a.row_tiles = (int)tiles;
   int64_t ctas = std::min<int64_t>((int64_t)h.sms, kMaxCtas);
   ctas = std::min(ctas, h.c.partial_floats / (2 * S::kRows * (D + 2)));
@@ -714,9 +713,9 @@ int launch(const HostCache& h, AttendArgs a, int max_q) {
 int launch_tiles(const HostCache& h, const AttendArgs& a, int max_q) {
   // Two tiles share the unpacked keys where there are rows for both (64 sequences on 8,192 keys, 256 rows: 468 us, one tile a CTA 811); one
   // has its scores a block ahead (128 rows: 419 us, in a CTA for two 424; 16 on 4,096 keys 36 rows 62 and 67).
-  const int64_t rows = (int64_t)max_q * a.group;
-  if (h.c.head_dim == 64) return rows <= 128 ? launch<64, 1>(h, a, max_q) : launch<64, 2>(h, a, max_q);
-  return rows <= 128 ? launch<128, 1>(h, a, max_q) : launch<128, 2>(h, a, max_q);
+  const bool one = tile_rows(h.c.head_dim, (int64_t)max_q * a.group) == 128;
+  if (h.c.head_dim == 64) return one ? launch<64, 1>(h, a, max_q) : launch<64, 2>(h, a, max_q);
+  return one ? launch<128, 1>(h, a, max_q) : launch<128, 2>(h, a, max_q);
 }
 
 }  // namespace whead_kv_impl

@@ -35,6 +35,15 @@ struct AttendArgs {
   int small;    // all units are less than 2^31
 };
 
+// The rows of a tile for entries of at most `rows` rows a KV head: up to 32 for the kernel of few rows (kv_attend.cu), above for that of many.
+inline int tile_rows(int head_dim, int64_t rows) {
+  if (rows <= 8) return 8;
+  if (rows <= 16 || head_dim == 256) return 16;
+  return rows <= 32 ? 32 : rows <= 128 ? 128 : 256;
+}
+// Most items of a launch: whoever looks through them steps by up to 1024 beyond the last, in ints.
+constexpr int64_t kMaxItems = INT32_MAX - 4096;
+
 // Attention of more than a few rows a KV head (kv_attend_tiles.cu); head_dim 64 or 128.
 int launch_tiles(const struct HostCache& h, const AttendArgs& a, int max_q);
 

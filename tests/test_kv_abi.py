@@ -100,6 +100,14 @@ def test_attend_refuses(L, kw, code):
     assert L.whead_kv_attend(ctypes.addressof(p), ctypes.addressof(a)) == code
 
 
+def test_attend_refuses_more_items_than_its_scans_hold(L):
+    """512 x 4,194,303 row tiles end 513 below 2^31: a scan of 1,024 items a step would step past it. What total rules out is no item."""
+    p = params(max_seqs=4096)
+    call = lambda **kw: L.whead_kv_attend(ctypes.addressof(p), ctypes.addressof(keep := attend_args(**dict(dict(n=512, heads=8, indptr=FAKE), **kw))))  # noqa: E731
+    assert call(total=4194303 * 256, max_q=4194303 * 256) == wh.ERR_UNSUPPORTED
+    assert call(total=2 ** 31 - 2, max_q=2 ** 30 - 1) == wh.ERR_UNSUPPORTED
+
+
 def test_other_calls_refuse(L):
     p, x = params(), ctypes.c_void_p(FAKE)
     q = ctypes.addressof(p)
