@@ -314,9 +314,10 @@ __global__ void __launch_bounds__(kPlan, 1) append_plan(Cache c, AppendArgs a) {
   }
 }
 
-// One block of 16 channels' scale byte and the factor 1 / (s g) that its codes are formed with.
+// One block of 16 channels' scale byte and the factor 1 / (s g) that its codes are formed with. The maximum passes over a NaN beside
+// numbers; of nothing but NaN it is one, and counts as zero: a NaN scale would reach every row whose masks hide the token.
 __device__ __forceinline__ uint32_t block_scale(float amax, float g, float& inv) {
-  const float r = __fdiv_rn(amax, __fmul_rn(6.0f, g));
+  const float r = __fdiv_rn(fmaxf(amax, 0.0f), __fmul_rn(6.0f, g));
   const uint32_t byte = __nv_cvt_float_to_fp8(r, __NV_SATFINITE, __NV_E4M3);
   inv = __frcp_rn(__fmul_rn(e4m3_to_float((uint8_t)byte), g));
   return byte;

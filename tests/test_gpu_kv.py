@@ -549,3 +549,30 @@ def test_other_streams_and_graphs(torch, kv):
             side.synchronize()
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and torch.equal(c.state, want[2])
         assert c.status() == 0
+
+
+@pytest.mark.parametrize("t,group,option", [(2, 4, "causal"), (2, 4, "window"), (2, 4, "tree"), (40, 4, "causal"), (40, 2, "window"), (40, 4, "tree")])
+def test_a_token_of_nothing_but_nan(torch, kv, t, group, option):
+    """A token, and a block of 16 channels, that hold no number at all are held as zeros: where they are seen, and where a mask hides them."""
+    h, d, lens = 2, 128, [90, 61]
+    c = make(kv, torch, 2, 96, h, d, 32)
+    k, v = randn(torch, (sum(lens), h, d), torch.bfloat16, 31), randn(torch, (sum(lens), h, d), torch.bfloat16, 32)
+    for x in (k, v):
+        x[[0, 50, 88, 89, 95, 150]] = float("nan")
+        x[70, :, 16:32] = float("nan")
+    ip = torch.tensor([0, 90, 151], dtype=torch.int32, device="cuda")
+    c.append(k, v, ip)
+    got = c.read(torch.zeros(2, dtype=torch.int32, device="cuda"), 90, dtype=torch.float32)
+    hk, hv = held(torch, k, c.k_scale), held(torch, v, c.v_scale)
+    for y, w in zip(got, (hk, hv)):
+        np.testing.assert_array_equal(y[0].cpu().numpy(), w[:90])
+        np.testing.assert_array_equal(y[1, :61].cpu().numpy(), w[90:])
+    kvs = [(hk[a:b].astype(np.float64), hv[a:b].astype(np.float64)) for a, b in ((0, 90), (90, 151))]
+    more = {"window": {"window": 3}, "causal": {}}.get(option)
+    if more is None:
+        bits = torch.ones(2 * t, dtype=torch.int64, device="cuda") << torch.arange(t, device="cuda").repeat(2)
+        more = {"tree": torch.where(torch.arange(2 * t, device="cuda") % t == t - 1, 1, bits)}  # the last sees the first, the others themselves
+    q = randn(torch, (2 * t, h * group, d), torch.bfloat16, 33)
+    out, lse = c.attend(q, **more)
+    assert c.status() == 0
+    check(torch, c, kvs, q, out, lse, [t, t], **more)
