@@ -96,7 +96,7 @@ typedef struct {
   int64_t q_token_stride, q_head_stride; /* in elements */
   int32_t n;                /* entries */
   int32_t heads;            /* query heads, a multiple of kv_heads; head a reads KV head a / (heads / kv_heads) */
-  int32_t max_q;            /* no entry has more query tokens than this */
+  int32_t max_q;            /* no entry may have more query tokens than this */
   int32_t dtype;            /* WHEAD_KV_BF16 or WHEAD_KV_F16, for q and out */
   int32_t causal;
   int32_t window;           /* 0, or the number of latest keys that a token sees (needs causal) */
@@ -109,6 +109,8 @@ typedef struct {
  * stands at position p = L - T + t, so that append comes before attend. It sees the keys j < L, and of those, with
  * causal, j <= p; with a window, j > p - window; with a tree, for j >= L - T, those whose bit j - (L - T) is set in its
  * mask. A query that sees none gives zeros and lse -inf. Scores, softmax and sums are in fp32.
+ * Device errors: WHEAD_ERR_INVALID_ARG for an entry whose offsets are out of order or past total, or that has more than max_q
+ * tokens (its rows of out and lse are not written, nor are rows that belong to no entry), and for a slot that is none.
  */
 int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* args);
 

@@ -628,6 +628,7 @@ extern "C" int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* x
   a.q_head_stride = x->q_head_stride;
   a.n = x->n;
   a.each = (int)(x->total / x->n);
+  a.max_q = max_q;
   a.heads = x->heads;
   set_group(&a, group);
   a.row_tiles = 1;

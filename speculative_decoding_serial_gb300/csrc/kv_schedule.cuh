@@ -26,7 +26,7 @@ struct AttendArgs {
   const int32_t* slots;
   const unsigned long long* tree;
   int64_t total, q_token_stride, q_head_stride;
-  int n, each, heads, group, group_shift, row_tiles, dtype, causal, window, tree_words;
+  int n, each, max_q, heads, group, group_shift, row_tiles, dtype, causal, window, tree_words;
   uint32_t group_mul;  // row / group = (row * group_mul >> 32 + row) >> group_shift, for rows below 2^31
   float scale;
   bool wide_q, wide_q16;  // query rows can be read 8, 16 bytes at a time
@@ -82,7 +82,7 @@ __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, i
   if (t.len == 0) t.slot = 0;
   if (a.indptr) {
     const int lo = a.indptr[i], hi = a.indptr[i + 1];
-    const bool ok = lo >= 0 && hi >= lo && hi <= a.total;
+    const bool ok = lo >= 0 && hi >= lo && hi <= a.total && hi - lo <= a.max_q;  // the row tiles and the join's blocks are for max_q
     if (!ok) set_status(c, WHEAD_ERR_INVALID_ARG);
     t.first = ok ? lo : 0;
     t.tokens = ok ? hi - lo : 0;
@@ -92,7 +92,6 @@ __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, i
   }
   const int64_t all = (int64_t)t.tokens * a.group;
   const int64_t row0 = (int64_t)m * tile_rows;
-  if (m == a.row_tiles - 1 && row0 + tile_rows < all) set_status(c, WHEAD_ERR_INVALID_ARG);  // more tokens than max_q
   t.row0 = (int)row0;
   t.rows = (int)(all - row0 < 0 ? 0 : all - row0 < tile_rows ? all - row0 : tile_rows);
   t.unit0 = t.units = 0;

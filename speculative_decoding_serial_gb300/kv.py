@@ -223,8 +223,9 @@ class KvCache:
         last tokens, so append them first. A token sees its slot's keys, with causal those up to itself, with a window the
         latest `window` of these. tree (int64, (total,) or (total, words)): for each token, the bits of the entry's own
         tokens that it sees, besides everything before them. scale defaults to head_dim ** -0.5. With indptr, max_q says
-        how many query tokens an entry has at most (default: total). A token that sees nothing gets zeros and -inf.
-        out (as q, contiguous) and lse (total, heads) float32 may be given."""
+        how many query tokens an entry has at most (default: total); one that has more is reported by status() and its rows are
+        not written. A token that sees nothing gets zeros and -inf. out (as q, contiguous) and lse (total, heads) float32 may
+        be given."""
         torch = self._torch
         n, ip, sl = self._entries(indptr, slots)
         shape, strides = q.shape, q.stride()

@@ -576,3 +576,24 @@ def test_a_token_of_nothing_but_nan(torch, kv, t, group, option):
     out, lse = c.attend(q, **more)
     assert c.status() == 0
     check(torch, c, kvs, q, out, lse, [t, t], **more)
+
+
+@pytest.mark.parametrize("d,group,most,count", [(128, 4, 17, 32), (128, 4, 3, 4), (64, 2, 70, 100), (64, 1, 3, 8), (256, 1, 5, 8), (128, 4, 17, 200), (64, 4, 2, 40)])
+def test_attend_more_tokens_than_max_q(torch, kv, d, group, most, count):
+    """Reported, whether the row tile has room for them or not; that entry's rows are left alone and the others' are right."""
+    h, lens = 2, [3000, 2900, 64]
+    c = make(kv, torch, 3, 3000, h, d, 64, seed=d)
+    kvs = fill(torch, c, lens, 41)
+    counts = [most, count, 1]
+    ip = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    q = randn(torch, (sum(counts), h * group, d), torch.bfloat16, 42)
+    out, lse = torch.full_like(q, 7.0), torch.full((sum(counts), h * group), 9.0, device="cuda")
+    c.attend(q, ip, max_q=most, out=out, lse=lse)
+    assert c.status() == -1
+    assert (out[most:most + count] == 7.0).all() and (lse[most:most + count] == 9.0).all()
+    keep = torch.ones(sum(counts), dtype=torch.bool, device="cuda")
+    keep[most:most + count] = False
+    check(torch, c, [kvs[0], kvs[2]], q[keep], out[keep], lse[keep], [most, 1])
+    c.attend(q, ip, max_q=max(counts), out=out, lse=lse)
+    assert c.status() == 0
+    check(torch, c, kvs, q, out, lse, counts, rows=(0, 1, count - 1))
