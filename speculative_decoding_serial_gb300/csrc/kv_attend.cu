@@ -200,7 +200,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
     const int h = now.h, u0 = now.u0, u1 = now.u1;
     int live_end = fetch.end;
     // query rows: from a power of two to f16, as operands
-    const float to_log2 = a.scale * c.k_scale[h] * kLog2e;
+    const float k_scale = c.k_scale[h];
     uint2 q[S::kQInRegs ? NT : 1][S::kQInRegs ? NB : 1];
     float f[NT][2];
     if (!S::kQInRegs) named_sync<kConsumers>(1);
@@ -223,8 +223,9 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 1));
         top = __vmaxu2(top, __shfl_xor_sync(~0u, top, 2));
         top = max(top & 0xFFFFu, top >> 16);
-        // 2^e <= largest < 2^(e + 1) (an f16 below 2^-14 counts as one just there), in the range whose powers of two are normal both ways
-        const int e = min(max(a.dtype == WHEAD_KV_BF16 ? (int)(top >> 7) - 127 : max((int)(top >> 10), 1) - 15, -100), 100);
+        // 2^e <= largest < 2^(e + 1) (an f16 below 2^-14 counts as one just there). Both powers of two are normal for every bf16 exponent
+        // from -100 up; a row below counts as one there, where bf16's smallest step is still one that f16 holds.
+        const int e = max(a.dtype == WHEAD_KV_BF16 ? (int)(top >> 7) - 127 : max((int)(top >> 10), 1) - 15, -100);
         const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23), down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -234,10 +235,11 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
           else s_q[(nt * NB + b) * 32 + lane] = w;
         }
         if constexpr (S::kQInRegs) {
-          f[i][0] = __shfl_sync(~0u, down, t * 8) * to_log2;
-          f[i][1] = __shfl_sync(~0u, down, t * 8 + 4) * to_log2;
+          // the row's power of two first: it may be what the scale takes back
+          f[i][0] = __shfl_sync(~0u, down, t * 8) * a.scale * k_scale * kLog2e;
+          f[i][1] = __shfl_sync(~0u, down, t * 8 + 4) * a.scale * k_scale * kLog2e;
         } else if (t == 0) {
-          s_c[nt * 8 + g] = down * to_log2;
+          s_c[nt * 8 + g] = down * a.scale * k_scale * kLog2e;
         }
       }
     }

@@ -499,7 +499,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
         // The thread's query row, from a power of two to f16. All of its loads are under way before it looks at one. (Rows fetched by bulk
         // or asynchronous copies took 4,500 cycles to ask for: those are issued lane by lane.) The sign of the scale goes into the
         // row, so that f is positive and scores need it only after their maximum is known.
-        const float to_log2 = a.scale * c.k_scale[sg.h] * kLog2e;
+        const float k_scale = c.k_scale[sg.h];
         const int row = tile.row0 + r, tok = row_token(a, row);
         uint4 x[D / 8];
 #pragma unroll
@@ -526,10 +526,11 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
         }
         big = __vmaxu2(big, also);
         big = max(big & 0xFFFFu, big >> 16);
-        // 2^e <= largest < 2^(e + 1) (an f16 below 2^-14 counts as one just there), in the range whose powers of two are normal both ways
-        const int e = min(max(a.dtype == WHEAD_KV_BF16 ? (int)(big >> 7) - 127 : max((int)(big >> 10), 1) - 15, -100), 100);
-        const float up = copysignf(__uint_as_float((uint32_t)(127 + 13 - e) << 23), to_log2);
-        f = __uint_as_float((uint32_t)(127 - 13 + e) << 23) * fabsf(to_log2);
+        // 2^e <= largest < 2^(e + 1), from -100 up, as in kv_attend.cu; the row's power of two first: it may be what the scale takes back
+        const int e = max(a.dtype == WHEAD_KV_BF16 ? (int)(big >> 7) - 127 : max((int)(big >> 10), 1) - 15, -100);
+        const float factor = __uint_as_float((uint32_t)(127 - 13 + e) << 23) * a.scale * k_scale * kLog2e;
+        const float up = copysignf(__uint_as_float((uint32_t)(127 + 13 - e) << 23), factor);
+        f = fabsf(factor);
         uint8_t* to = smem + S::kOffQ + t * S::kQ + (quarter * 32 + lane) * 128;
         auto put = [&](auto bf16) {
           constexpr int kType = decltype(bf16)::value ? WHEAD_KV_BF16 : WHEAD_KV_F16;

@@ -597,3 +597,18 @@ def test_attend_more_tokens_than_max_q(torch, kv, d, group, most, count):
     c.attend(q, ip, max_q=max(counts), out=out, lse=lse)
     assert c.status() == 0
     check(torch, c, kvs, q, out, lse, counts, rows=(0, 1, count - 1))
+
+
+@pytest.mark.parametrize("t", [1, 40])
+@pytest.mark.parametrize("power", [124, 104, -104, -122, -130])
+def test_attend_query_rows_over_the_types_range(torch, kv, t, power):
+    """Rows of bf16 up to its largest values and down among those below its normal ones, with the scale the other way."""
+    h, d, group = 1, 128, 4
+    c = make(kv, torch, 1, 200, h, d, 16)
+    kvs = fill(torch, c, [200], 3)
+    q = randn(torch, (t, group, d), torch.float32, 4).mul(2.0 ** (power / 2)).mul(2.0 ** (power / 2)).bfloat16()
+    assert torch.isfinite(q).all() and q.any()
+    scale = d ** -0.5 * 2.0 ** -max(power, -126)
+    out, lse = c.attend(q, scale=scale)
+    assert c.status() == 0
+    check(torch, c, kvs, q, out, lse, [t], scale=scale)
