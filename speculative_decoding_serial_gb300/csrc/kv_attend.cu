@@ -251,12 +251,6 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         f[nt][1] = s_c[nt * 8 + 2 * t + 1];
       }
     }
-    // a zero factor becomes one that leaves all scores at zero, so that a masked product can be one whose score is -inf
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (fabsf(f[nt][e]) < 1e-37f) f[nt][e] = 1e-37f;
     float o[NT][NB][4];
     float m[NT][2], l[NT][2];
 #pragma unroll
@@ -304,6 +298,14 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
           }
         }
       }
+      // from sums of products to scores, rounded before the reference is taken off: the difference of a score and itself is then zero,
+      // however large both are (in one multiply-add it would be the product's rounding, and p anything)
+#pragma unroll
+      for (int w = 0; w < G; ++w)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[w][nt][k] = __fmul_rn(sc[w][nt][k], f[nt][k & 1]);
 #pragma unroll
       for (int w = 0; w < G; ++w) {
         if (key0 + w * 16 < free_lo || key0 + w * 16 + 16 > free_hi) {
@@ -321,9 +323,8 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const RowView view = row_view(a, tile, tile.row0 + nt * 8 + 2 * t + e);
-              // a masked product becomes the one whose score is -inf
-              if (!sees(view, key0 + w * 16 + g)) sc[w][nt][e] = -copysignf(INFINITY, f[nt][e]);
-              if (!sees(view, key0 + w * 16 + g + 8)) sc[w][nt][e + 2] = -copysignf(INFINITY, f[nt][e]);
+              if (!sees(view, key0 + w * 16 + g)) sc[w][nt][e] = -INFINITY;
+              if (!sees(view, key0 + w * 16 + g + 8)) sc[w][nt][e + 2] = -INFINITY;
             }
         }
       }
@@ -334,7 +335,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         for (int w = 0; w < G; ++w)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            d[w][nt][k] = fmaf(sc[w][nt][k], f[nt][k & 1], -m[nt][k & 1]);
+            d[w][nt][k] = sc[w][nt][k] - m[nt][k & 1];
             top = fmaxf(top, d[w][nt][k]);
           }
       if (__any_sync(~0u, top > kSlack)) {
@@ -345,7 +346,7 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
           for (int e = 0; e < 2; ++e) {
             float x = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < G; ++w) x = fmaxf(x, fmaxf(sc[w][nt][e] * f[nt][e], sc[w][nt][e + 2] * f[nt][e]));
+            for (int w = 0; w < G; ++w) x = fmaxf(x, fmaxf(sc[w][nt][e], sc[w][nt][e + 2]));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
             x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
@@ -355,8 +356,8 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
             l[nt][e] *= r[e];
 #pragma unroll
             for (int w = 0; w < G; ++w) {
-              d[w][nt][e] = fmaf(sc[w][nt][e], f[nt][e], -now);
-              d[w][nt][e + 2] = fmaf(sc[w][nt][e + 2], f[nt][e], -now);
+              d[w][nt][e] = sc[w][nt][e] - now;
+              d[w][nt][e + 2] = sc[w][nt][e + 2] - now;
             }
           }
 #pragma unroll

@@ -100,10 +100,10 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&x)[
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // two fp32 operations in one instruction
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
-  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n"
-      " mov.b64 {%0, %1}, d;\n}\n" : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -143,10 +143,13 @@ __device__ __forceinline__ float row_max(uint32_t st, const uint32_t (&seen)[2])
   return fmaxf(a0, a1);
 }
 
-// p = 2^(score f - m) of a row's scores, as f16 pairs, their sum, and the largest exponent: one pass, on the guess that m still does.
+// p = 2^((x - ref) f) of a row's products x, as f16 pairs, their sum, and the largest x: one pass, on the guess that the reference still
+// does. The reference is a product, or near one, and is taken off before the factor comes: the difference of x and itself is zero,
+// however large the scores are. (2^(x f - m) in one multiply-add is off by the rounding of m = ref f: for scores past 2^24 p would be any
+// power of two, or infinite. It took 303 us where this takes 306, 2 prompts of 2,048 tokens, and 139 where 146 with a window of 1,024.)
 template <bool MASKED>
-__device__ __forceinline__ float row_exp(uint32_t st, const uint32_t (&seen)[2], float f, float m, float2& sum, uint32_t (&p)[2][16]) {
-  const float2 f2 = make_float2(f, f), m2 = make_float2(-m, -m);
+__device__ __forceinline__ float row_exp(uint32_t st, const uint32_t (&seen)[2], float f, float ref, float2& sum, uint32_t (&p)[2][16]) {
+  const float2 f2 = make_float2(f, f), off = make_float2(-ref, -ref);
   float2 s0 = make_float2(0.f, 0.f), s1 = s0;
   float t0 = -INFINITY, t1 = -INFINITY;
   uint32_t ahead[2][16];
@@ -158,13 +161,14 @@ __device__ __forceinline__ float row_exp(uint32_t st, const uint32_t (&seen)[2],
     if (i < 3) tmem_load16(st + i * 16 + 16, ahead[(i + 1) & 1]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      float2 d = fma2(make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), f2, m2);
+      float2 d = make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
       if (MASKED) {
         d.x = (seen[i / 2] >> (i % 2 * 16 + 2 * k)) & 1 ? d.x : -INFINITY;
         d.y = (seen[i / 2] >> (i % 2 * 16 + 2 * k + 1)) & 1 ? d.y : -INFINITY;
       }
       if (k & 1) t1 = max3(t1, d.x, d.y);
       else t0 = max3(t0, d.x, d.y);
+      d = mul2(add2(d, off), f2);
       d.x = ex2(d.x);
       d.y = ex2(d.y);
       if (k & 1) s1 = add2(s1, d);
@@ -530,7 +534,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
         const int e = max(a.dtype == WHEAD_KV_BF16 ? (int)(big >> 7) - 127 : max((int)(big >> 10), 1) - 15, -100);
         const float factor = __uint_as_float((uint32_t)(127 - 13 + e) << 23) * a.scale * k_scale * kLog2e;
         const float up = copysignf(__uint_as_float((uint32_t)(127 + 13 - e) << 23), factor);
-        f = fabsf(factor);
+        f = fmaxf(fabsf(factor), 1e-30f);  // positive: products stay below 2^34, so that scores of less are zero all the same
         uint8_t* to = smem + S::kOffQ + t * S::kQ + (quarter * 32 + lane) * 128;
         auto put = [&](auto bf16) {
           constexpr int kType = decltype(bf16)::value ? WHEAD_KV_BF16 : WHEAD_KV_F16;
@@ -561,7 +565,8 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
         free_lo = lo;
       }
       bool fresh = true;  // some row of the warp has no reference yet
-      float m = kNoKey;
+      float ref = kNoKey;  // in units of the products; m = ref f
+      const float bias = __fdividef(kBias, f);
       float2 l = make_float2(0.f, 0.f);
       for (int u = sg.u0; u < sg.u1; ++u, ++n) {
         const int key0 = (tile.unit0 + u) * kBlock;
@@ -590,15 +595,16 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
           }
           if (fresh) {  // a row's first keys: its reference is their maximum
             const float top = masked ? row_max<true>(st, seen) : row_max<false>(st, seen);
-            if (m == kNoKey && top != -INFINITY) m = top * f - kBias;
-            fresh = __any_sync(~0u, m == kNoKey);
+            if (ref == kNoKey && top > kNoKey) ref = top - bias;
+            fresh = __any_sync(~0u, ref == kNoKey);
           }
           uint32_t p[2][16];
           float2 sum;
-          const float top = masked ? row_exp<true>(st, seen, f, m, sum, p) : row_exp<false>(st, seen, f, m, sum, p);
-          if (__any_sync(~0u, top > kSlack)) {  // some p came out too large: the reference goes up, what there is comes down, once more
-            const float up = top > kSlack ? top - kBias : 0.0f, rr = ex2(-up);
-            m += up;
+          const float top = masked ? row_exp<true>(st, seen, f, ref, sum, p) : row_exp<false>(st, seen, f, ref, sum, p);
+          const bool over = (top - ref) * f > kSlack;
+          if (__any_sync(~0u, over)) {  // some p came out too large: the reference goes up, what there is comes down, once more
+            const float now = over ? top - bias : ref, rr = over ? ex2((ref - now) * f) : 1.0f;
+            ref = now;
             l.x *= rr;
             l.y *= rr;
             if (u > sg.u0 || h > 0) {  // after the products of the half before
@@ -615,7 +621,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
                 tmem_store16(ot + i * 16, x);
               }
             }
-            masked ? row_exp<true>(st, seen, f, m, sum, p) : row_exp<false>(st, seen, f, m, sum, p);
+            masked ? row_exp<true>(st, seen, f, ref, sum, p) : row_exp<false>(st, seen, f, ref, sum, p);
           }
           l = add2(l, sum);
           tmem_store16(st, p[0]);  // over the scores
@@ -633,12 +639,16 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       const bool live = r < tile.rows;
       const int tok = row_token(a, row), head = sg.h * a.group + row - tok * a.group;
       const bool whole = sg.u0 == 0 && sg.u1 == tile.units;
-      const float ll = l.x + l.y;
+      const float m = __fmul_rn(ref, f);
+      // a part's m is rounded: what that took from it goes into its sums, up to what they bear (past that the reference is the score of
+      // one of the keys, and every part's the same for the same score)
+      const float back = whole ? 1.0f : ex2(fminf(fmaxf(__fmaf_rn(ref, f, -m), -16.0f), 16.0f));
+      const float ll = (l.x + l.y) * back;
       constexpr int kPart = S::kRows * (D + 2);
       const int64_t out_row = (int64_t)(tile.first + tok) * a.heads + head;
       const float gv = c.v_scale[sg.h];
       float* part = c.partial + (int64_t)part_slot(start, sg, blockIdx.x) * kPart;
-      const float scale = whole ? (ll != 0.0f ? gv / ll : 0.0f) : 1.0f;
+      const float scale = whole ? (ll != 0.0f ? gv / ll : 0.0f) : back;
 #pragma unroll 1
       for (int i = 0; i < D / 16; ++i) {
         uint32_t x[16];
@@ -674,7 +684,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
         continue;
       }
       if (live) {
-        __stcg(part + r, m);
+        __stcg(part + r, ll == 0.0f ? kNoKey : m);
         __stcg(part + S::kRows + r, ll);
       }
     }

@@ -18,7 +18,7 @@ constexpr int kMaxCtas = 2048;        // most CTAs of an attend launch (partial 
 constexpr int kRegionPages = WHEAD_KV_MAX_BLOCK / 16 + 1;  // pages that a block's tokens can lie in
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoKey = -1e30f;  // a running maximum before the first key
+constexpr float kNoKey = -3.402823466e38f;  // a running maximum before the first key: fp32's lowest, so that every score may follow it
 
 // Workspace: the control words, then per-slot arrays, then the attention's counters and partial results.
 struct Ctl {

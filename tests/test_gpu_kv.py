@@ -612,3 +612,63 @@ def test_attend_query_rows_over_the_types_range(torch, kv, t, power):
     out, lse = c.attend(q, scale=scale)
     assert c.status() == 0
     check(torch, c, kvs, q, out, lse, [t], scale=scale)
+
+
+@pytest.mark.parametrize("factor", [-2.0 ** 110, -2.0 ** 33, 2.0 ** 33, 2.0 ** 110])
+@pytest.mark.parametrize("d,group,t", [(128, 4, 1), (64, 4, 2), (128, 4, 5), (64, 2, 40), (128, 2, 130), (256, 1, 3)])
+def test_attend_equal_scores_of_any_size(torch, kv, d, group, t, factor):
+    """Keys that are all alike, with scores from 1e9 to 1e33 of either sign: every one counts the same, in one CTA or in many."""
+    h, L = 2, 2500
+    c = make(kv, torch, 2, L, h, d, 64)
+    base = randn(torch, (1, h, d), torch.bfloat16, 51)
+    v = randn(torch, (L + 20, h, d), torch.bfloat16, 52)
+    c.append(base.expand(L + 20, h, d), v, torch.tensor([0, L, L + 20], dtype=torch.int32, device="cuda"))
+    k = held(torch, base, c.k_scale).astype(np.float64)[0]
+    vv = held(torch, v, c.v_scale).astype(np.float64)
+    q = (base.float() * factor).bfloat16()[:, :, None].expand(2 * t, h, group, d).reshape(2 * t, h * group, d).contiguous()
+    out, lse = c.attend(q)
+    assert c.status() == 0
+    o, l, qq = out.double().cpu().numpy(), lse.double().cpu().numpy(), q.double().cpu().numpy()
+    for i, (lo, n) in enumerate(((0, L), (L, 20))):
+        for row in range(t):
+            see = max(n - t + row + 1, 0)
+            for a in range(h * group):
+                x, at = vv[lo:lo + see, a // group], (i * t + row, a)
+                if not see:
+                    assert not o[at].any() and l[at] == -np.inf
+                    continue
+                # p is the same for all: what is left of the bounds above is the rounding of the sums and of the output
+                tol = 2.0 ** -8 * np.abs(x.mean(0)) + (see + 256) * 2.0 ** -25 * np.abs(x).mean(0) + 2.0 ** -24 * np.abs(x).max()
+                assert (np.abs(o[at] - x.mean(0)) <= tol).all(), at
+                want = k[a // group] @ qq[at] * d ** -0.5 + np.log(see)
+                assert abs(want) > 1e9 and abs(l[at] - want) <= (d + 8) * 2.0 ** -23 * abs(want), at
+
+
+@pytest.mark.parametrize("t", [1, 3, 40, 130])
+@pytest.mark.parametrize("factor", [2.0 ** 28, 2.0 ** 100])
+def test_attend_large_scores_that_grow(torch, kv, t, factor):
+    """Runs of like keys whose scores, far past the 24 bits of an fp32 number, grow from run to run: the latest run alone counts."""
+    h, d, group, L, run = 8, 128, 2, 6000, 500
+    c = make(kv, torch, 2, L, h, d, 64)
+    base = randn(torch, (1, h, d), torch.float32, 53)
+    k = (base * 0.2 * 1.25 ** torch.arange(L // run).cuda().repeat_interleave(run)[:, None, None]).bfloat16()
+    v = randn(torch, (L, h, d), torch.bfloat16, 54)
+    for slot in range(2):
+        c.append(k, v, slots=torch.tensor([slot], dtype=torch.int32, device="cuda"))
+    kk, vv = (held(torch, x, g).astype(np.float64) for x, g in ((k[::run], c.k_scale), (v, c.v_scale)))
+    q = (base * factor).bfloat16().repeat_interleave(group, 1).expand(2 * t, h * group, d).contiguous()
+    scores = np.einsum("rhd,hd->rh", kk, q[0, ::group].double().cpu().numpy())
+    assert (scores[0] > 1e8).all() and (scores[1:] > 1.1 * scores[:-1]).all()
+    out, lse = c.attend(q)
+    assert c.status() == 0
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for i in range(2):
+        for row in sorted({0, t // 2, t - 1}):
+            see = L - t + row + 1
+            first = (see - 1) // run * run
+            for a in range(h * group):
+                x, at = vv[first:see, a // group], (i * t + row, a)
+                tol = 2.0 ** -8 * np.abs(x.mean(0)) + (see + 256) * 2.0 ** -25 * np.abs(x).mean(0) + 2.0 ** -24 * np.abs(x).max()
+                assert (np.abs(o[at] - x.mean(0)) <= tol).all(), at
+                want = scores[first // run, a // group] * d ** -0.5
+                assert abs(l[at] - want) <= (d + 8) * 2.0 ** -23 * want, at
