@@ -20,7 +20,7 @@ from . import whead as _wh
 
 BF16, F16, F32 = 0, 1, 2
 MAX_BLOCK = 256
-INT_MAX = 2 ** 31 - 1
+INT_MIN, INT_MAX = -2 ** 31, 2 ** 31 - 1
 
 # Every symbol include/whead_kv.h declares.
 EXPORTS = ("whead_kv_page_bytes", "whead_kv_workspace_bytes", "whead_kv_append", "whead_kv_read", "whead_kv_attend",
@@ -250,8 +250,8 @@ class KvCache:
             words, bits = 1 if tree.dim() == 1 else tree.shape[1], tree.data_ptr()
         if max_q is None:
             max_q = total if indptr is not None else total // max(n, 1)
-        if window > INT_MAX or max_q > INT_MAX:
-            raise ValueError("window and max_q have to be below 2^31")
+        if not (INT_MIN <= window <= INT_MAX and INT_MIN <= max_q <= INT_MAX):  # ctypes would wrap them; the library refuses what is negative
+            raise ValueError("0 <= window, max_q < 2^31 is wanted")
         a = KvAttendArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr(), ip, sl, bits, total, strides[0], strides[1], n, heads, max_q, code,
                          bool(causal), window, words, self._scale if scale is None else scale)
         self._call(self._lib.whead_kv_attend, ctypes.addressof(a))

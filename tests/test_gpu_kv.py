@@ -672,3 +672,16 @@ def test_attend_large_scores_that_grow(torch, kv, t, factor):
                 assert (np.abs(o[at] - x.mean(0)) <= tol).all(), at
                 want = scores[first // run, a // group] * d ** -0.5
                 assert abs(l[at] - want) <= (d + 8) * 2.0 ** -23 * want, at
+
+
+def test_sizes_that_do_not_fit_are_refused(torch, kv):
+    """Windows and most tokens of an entry that wrap to a right number in 32 bits."""
+    c = make(kv, torch, 2, 64, 1, 64, 16)
+    fill(torch, c, [20, 30], 61)
+    q = randn(torch, (2, 1, 64), torch.bfloat16, 62)
+    for bad in (-2 ** 32, -2 ** 32 + 5, -2 ** 31, 2 ** 32, 2 ** 32 + 5, -1):
+        with pytest.raises((ValueError, RuntimeError)):
+            c.attend(q, window=bad)
+        with pytest.raises((ValueError, RuntimeError)):
+            c.attend(q, max_q=bad)
+    assert c.status() == 0
