@@ -685,3 +685,17 @@ def test_sizes_that_do_not_fit_are_refused(torch, kv):
         with pytest.raises((ValueError, RuntimeError)):
             c.attend(q, max_q=bad)
     assert c.status() == 0
+
+
+def test_gradients_are_refused(torch, kv):
+    c = make(kv, torch, 1, 64, 2, 64, 16)
+    x = randn(torch, (4, 2, 64), torch.bfloat16, 63)
+    y = x.clone().requires_grad_()
+    for call in (lambda: c.append(y, x), lambda: c.append(x, y), lambda: c.attend(y)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    assert c.lens.item() == 0
+    with torch.no_grad():
+        c.append(y, y)
+        out, _ = c.attend(y)
+    assert c.lens.item() == 4 and not out.requires_grad and c.status() == 0
