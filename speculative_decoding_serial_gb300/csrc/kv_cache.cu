@@ -362,6 +362,7 @@ __global__ void __launch_bounds__(D) append_write(const __grid_constant__ Cache 
   const int total = c.ctl->total;
   for (int x = blockIdx.x; x < total; x += gridDim.x) {
     const int4 what = __ldcg(reinterpret_cast<const int4*>(c.partial) + x);  // an AppendGroup
+    if (!is_page(c, what.x)) continue;                                       // a table that is not this cache's
     const int lo = what.y >> 8 & 0xFF, hi = what.y >> 16;                    // new tokens of the group: lo .. hi - 1
     const bool whole = lo == 0 && hi == 16;
     const int64_t row0 = (int64_t)((uint64_t)(uint32_t)what.z | (uint64_t)(uint32_t)what.w << 32);  // row of k, v of the group's first token
@@ -720,13 +721,14 @@ __global__ void __launch_bounds__(128) compact_move(Cache c, CompactArgs a) {
   for (int x = threadIdx.x; x < ng * (kGroup / 16); x += blockDim.x) {
     const int gr = lo + x / (kGroup / 16), off = x % (kGroup / 16);
     const int page = before[gr / gpp - first];
-    if ((unsigned)page < (unsigned)c.num_pages)
-      reinterpret_cast<uint4*>(groups)[x] = reinterpret_cast<const uint4*>(group_ptr<D>(c, page, h, gr * 16))[off];
+    reinterpret_cast<uint4*>(groups)[x] = is_page(c, page) ? reinterpret_cast<const uint4*>(group_ptr<D>(c, page, h, gr * 16))[off] : make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   for (int y = threadIdx.x >> 5; y < hi - lo; y += blockDim.x >> 5) {
-    uint8_t* out = group_ptr<D>(c, after[(lo + y) / gpp - first], h, (lo + y) * 16);
+    const int page = after[(lo + y) / gpp - first];
+    if (!is_page(c, page)) continue;
+    uint8_t* out = group_ptr<D>(c, page, h, (lo + y) * 16);
     const int* m = from + y * 16;
     const int k0 = m[g], k1 = m[g + 8];
     const int v[4] = {m[2 * t], m[2 * t + 1], m[2 * t + 8], m[2 * t + 9]};

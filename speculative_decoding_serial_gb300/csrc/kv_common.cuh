@@ -215,13 +215,17 @@ __device__ __forceinline__ void named_sync(int id) {
 
 __device__ __forceinline__ void set_status(const Cache& c, int code) { atomicCAS(&c.ctl->status, 0, code); }
 
-// Group `pos / 16` of head h in a slot's page; pages out of range read page 0 and are reported.
+// Whether a table's entry is a page of the pool; reported where it is not.
+__device__ __forceinline__ bool is_page(const Cache& c, int page) {
+  if ((unsigned)page < (unsigned)c.num_pages) return true;
+  set_status(c, WHEAD_ERR_INTERNAL);
+  return false;
+}
+
+// Group `pos / 16` of head h in a slot's page, to read: pages out of range read page 0. Who writes asks is_page first.
 template <int D>
 __device__ __forceinline__ uint8_t* group_ptr(const Cache& c, int page, int h, int pos) {
-  if ((unsigned)page >= (unsigned)c.num_pages) {
-    set_status(c, WHEAD_ERR_INTERNAL);
-    page = 0;
-  }
+  if (!is_page(c, page)) page = 0;
   const int in_page = (pos & (c.page_size - 1)) >> 4;
   return c.pool + (((int64_t)page * c.kv_heads + h) * (c.page_size >> 4) + in_page) * (18 * D);
 }

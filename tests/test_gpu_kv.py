@@ -699,3 +699,19 @@ def test_gradients_are_refused(torch, kv):
         c.append(y, y)
         out, _ = c.attend(y)
     assert c.lens.item() == 4 and not out.requires_grad and c.status() == 0
+
+
+@pytest.mark.parametrize("page", [-1, 5, 2 ** 31 - 1])
+def test_a_table_that_names_no_page_is_not_written_through(torch, kv, page):
+    """A caller's table whose entry is no page: append and compact report it and write nowhere."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    c = kv.KvCache(5, 16, 2, 64, 2, 2)
+    x = randn(torch, (40, 2, 64), torch.bfloat16, 64)
+    c.append(x[:30], x[:30], i32([0, 10, 30]))
+    assert c.status() == 0
+    c.tables[1, 1] = page
+    pool = c.pool.clone()
+    c.compact(i32([17]), i32([[1, 2]]), i32([2]), i32([1]))
+    assert c.status() == -6 and torch.equal(c.pool, pool)
+    c.append(x[:1], x[:1], slots=i32([1]))
+    assert c.status() == -6 and torch.equal(c.pool, pool)
