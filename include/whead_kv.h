@@ -118,7 +118,8 @@ int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* args);
  * Keeps part of a block at a slot's end: of the tokens from position start[i] on, those at start[i] + keep[i][j],
  * j < count[i], move to start[i] + j; the length becomes start[i] + count[i] and pages past it lose this slot's
  * reference. keep: n x keep_width, each row's first count[i] offsets ascending and below lens - start; offsets
- * are at most WHEAD_KV_MAX_BLOCK - 1. count[i] = 0 cuts the slot at start[i] (NULL keep and count: for all).
+ * are at most WHEAD_KV_MAX_BLOCK - 1. count[i] = 0 cuts the slot at start[i] (NULL keep and count: for all). keep may be
+ * NULL where keep_width is 0.
  * Device errors: WHEAD_ERR_NO_PAGES, WHEAD_ERR_INVALID_ARG.
  */
 #define WHEAD_KV_MAX_BLOCK 256

@@ -945,7 +945,7 @@ int whead_kv_compact(const whead_kv* kv, const int32_t* start, const int32_t* ke
   if (!kv || n < 0 || n > kv->max_seqs || keep_width < 0 || keep_width > WHEAD_KV_MAX_BLOCK) return WHEAD_ERR_INVALID_ARG;
   HostCache h;
   if (n == 0) return host_cache(kv, &h);
-  if (!start || (keep != nullptr) != (count != nullptr) || (!keep && keep_width > 0)) return WHEAD_ERR_INVALID_ARG;
+  if (!start || (keep && !count) || (!keep && keep_width > 0)) return WHEAD_ERR_INVALID_ARG;  // an empty keep may have no address
   if (!aligned(start, 4) || !aligned(keep, 4) || !aligned(count, 4) || !aligned(slots, 4)) return WHEAD_ERR_INVALID_ARG;
   int rc = host_cache(kv, &h);
   if (rc != WHEAD_OK) return rc;

@@ -715,3 +715,15 @@ def test_a_table_that_names_no_page_is_not_written_through(torch, kv, page):
     assert c.status() == -6 and torch.equal(c.pool, pool)
     c.append(x[:1], x[:1], slots=i32([1]))
     assert c.status() == -6 and torch.equal(c.pool, pool)
+
+
+def test_compact_that_keeps_no_column(torch, kv):
+    """keep without a column keeps nothing, as keep with columns and counts of zero does."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    c = kv.KvCache(8, 16, 1, 64, 2, 4)
+    x = randn(torch, (60, 1, 64), torch.bfloat16, 65)
+    c.append(x, x)
+    c.compact(i32([17, 3]), torch.empty(2, 0, dtype=torch.int32, device="cuda"), i32([0, 0]))
+    assert c.status() == 0 and c.lens.tolist() == [17, 3] and int((c.refs > 0).sum()) == 3
+    c.compact(i32([17, 3]), torch.empty(2, 0, dtype=torch.int32, device="cuda"), i32([0, 1]))  # a count past the row
+    assert c.status() == -1 and c.lens.tolist() == [17, 3]
