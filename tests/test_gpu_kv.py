@@ -727,3 +727,41 @@ def test_compact_that_keeps_no_column(torch, kv):
     assert c.status() == 0 and c.lens.tolist() == [17, 3] and int((c.refs > 0).sum()) == 3
     c.compact(i32([17, 3]), torch.empty(2, 0, dtype=torch.int32, device="cuda"), i32([0, 1]))  # a count past the row
     assert c.status() == -1 and c.lens.tolist() == [17, 3]
+
+
+@pytest.mark.parametrize("lens,t,d,page,dtype,more", [
+    ([6000, 2987], 300, 128, 64, "bfloat16", {}),                     # two tiles, some 20 blocks a CTA
+    ([5003, 4000], 261, 64, 16, "float16", {"window": 1500}),
+    ([4000, 4999], 200, 128, 128, "float16", {"causal": False}),
+    ([9000, 3000, 6001], 17, 128, 64, "bfloat16", {}),                # one tile, some 6
+    ([9000, 3000, 6001], 20, 64, 32, "float16", {"causal": False}),
+])
+def test_attend_many_blocks_a_cta(torch, kv, lens, t, d, page, dtype, more):
+    """CTAs that go through many blocks of keys and several items: every buffer and barrier comes round again."""
+    h, group, n = 8, 4, len(lens)
+    c = make(kv, torch, n, max(lens), h, d, page, seed=t)
+    kvs = fill(torch, c, lens, 71)
+    q = randn(torch, (n * t, h * group, d), getattr(torch, dtype), 72) * 1.5
+    out, lse = c.attend(q, **more)
+    assert c.status() == 0
+    check(torch, c, kvs, q, out, lse, [t] * n, rows=(0, 1, t // 2, t - 1), **more)
+    again = c.attend(q, **more)
+    assert torch.equal(out.view(torch.int16), again[0].view(torch.int16)) and torch.equal(lse.view(torch.int32), again[1].view(torch.int32))
+
+
+@pytest.mark.parametrize("t", [40, 130])
+def test_attend_growing_scores_over_many_blocks(torch, kv, t):
+    """Scores that grow from block to block within a CTA, for one tile and two: outputs in tensor memory come down again and again."""
+    h, d, L = 8, 128, 6000
+    c = make(kv, torch, 2, L, h, d, 64)
+    base = randn(torch, (1, h, d), torch.float32, 5)
+    for s, top in enumerate((4.0, 40.0)):
+        k = (base * torch.linspace(0.01, top, L).cuda()[:, None, None]).to(torch.bfloat16)
+        c.append(k, randn(torch, (L, h, d), torch.bfloat16, 6 + s), slots=torch.tensor([s], dtype=torch.int32, device="cuda"))
+    assert c.status() == 0
+    kk, vv = c.read(torch.zeros(2, dtype=torch.int32, device="cuda"), L, dtype=torch.float32)
+    kvs = [(kk[i].double().cpu().numpy(), vv[i].double().cpu().numpy()) for i in range(2)]
+    q = base.repeat_interleave(2, 1).expand(2 * t, 2 * h, d).to(torch.float16).contiguous()
+    out, lse = c.attend(q)
+    assert c.status() == 0
+    check(torch, c, kvs, q, out, lse, [t, t], rows=(0, t // 2, t - 1))
