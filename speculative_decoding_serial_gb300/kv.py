@@ -230,9 +230,9 @@ class KvCache:
         last tokens, so append them first. A token sees its slot's keys, with causal those up to itself, with a window the
         latest `window` of these. tree (int64, (total,) or (total, words)): for each token, the bits of the entry's own
         tokens that it sees, besides everything before them. scale defaults to head_dim ** -0.5. With indptr, max_q says
-        how many query tokens an entry has at most (default: total); one that has more is reported by status() and its rows are
-        not written. A token that sees nothing gets zeros and -inf. out (as q, contiguous) and lse (total, heads) float32 may
-        be given."""
+        how many query tokens an entry has at most (default: total, or as many as tree has bits for); one that has more is
+        reported by status() and its rows are not written. A token that sees nothing gets zeros and -inf. out (as q,
+        contiguous) and lse (total, heads) float32 may be given."""
         torch = self._torch
         n, ip, sl = self._entries(indptr, slots)
         shape, strides = q.shape, q.stride()
@@ -258,7 +258,7 @@ class KvCache:
                 raise ValueError("tree: a contiguous int64 tensor (total,) or (total, words) is wanted")
             words, bits = 1 if tree.dim() == 1 else tree.shape[1], tree.data_ptr()
         if max_q is None:
-            max_q = total if indptr is not None else total // max(n, 1)
+            max_q = total // max(n, 1) if indptr is None else min(total, 64 * words) if words else total
         if not (INT_MIN <= window <= INT_MAX and INT_MIN <= max_q <= INT_MAX):  # ctypes would wrap them; the library refuses what is negative
             raise ValueError("0 <= window, max_q < 2^31 is wanted")
         a = KvAttendArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr(), ip, sl, bits, total, strides[0], strides[1], n, heads, max_q, code,

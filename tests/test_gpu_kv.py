@@ -765,3 +765,25 @@ def test_attend_growing_scores_over_many_blocks(torch, kv, t):
     out, lse = c.attend(q)
     assert c.status() == 0
     check(torch, c, kvs, q, out, lse, [t, t], rows=(0, t // 2, t - 1))
+
+
+@pytest.mark.parametrize("d,group", [(64, 4), (256, 1)])
+def test_attend_ragged_trees(torch, kv, d, group):
+    """Masks of one word for entries whose tokens together are more than 64, without max_q: the words say how many tokens an entry may have."""
+    h, lens, counts = 2, [300, 45, 120], [33, 20, 40]
+    c = make(kv, torch, 3, 320, h, d, 32, seed=d)
+    kvs = fill(torch, c, lens, 81)
+    b, g = [], np.random.RandomState(82)
+    for n in counts:
+        own = []
+        for u in range(n):
+            own.append((own[g.randint(u)] if u else 0) | 1 << u)
+        b += own
+    tree = torch.tensor(np.array(b, np.uint64).view(np.int64), device="cuda")
+    ip = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    q = randn(torch, (sum(counts), h * group, d), torch.bfloat16, 83)
+    out, lse = c.attend(q, ip, tree=tree)
+    assert c.status() == 0
+    check(torch, c, kvs, q, out, lse, counts, tree=tree)
+    c.attend(q, torch.tensor([0, 5, 6, 93], dtype=torch.int32, device="cuda"), tree=tree)  # 87 tokens
+    assert c.status() == -1
