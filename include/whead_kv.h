@@ -108,7 +108,8 @@ typedef struct {
  * Attention of each entry's query tokens over its slot's keys and values. With T query tokens and length L, query t
  * stands at position p = L - T + t, so that append comes before attend. It sees the keys j < L, and of those, with
  * causal, j <= p; with a window, j > p - window; with a tree, for j >= L - T, those whose bit j - (L - T) is set in its
- * mask. A query that sees none gives zeros and lse -inf. Scores, softmax and sums are in fp32.
+ * mask. A query that sees none gives zeros and lse -inf. Scores, which may be of any finite size, maxima, exponentials and sums
+ * are in fp32; the exponentials are rounded to f16 (2^-11 at most) where they meet the values.
  * Device errors: WHEAD_ERR_INVALID_ARG for an entry whose offsets are out of order or past total, or that has more than max_q
  * tokens (its rows of out and lse are not written, nor are rows that belong to no entry), and for a slot that is none.
  */

@@ -2,20 +2,23 @@
 //
 // For a row q and the visible keys k_j and values v_j of its KV head: o = sum_j p_j v_j / l, p_j = 2^(s_j - m),
 // s_j = scale log2(e) q.k_j, l = sum_j p_j, lse = ln 2 (m + log2 l). m is any reference near the largest s; here it is a running
-// one that is raised only when a score passes it by 2^kSlack, so that most tiles rescale nothing.
+// one that is raised only when a score passes it by kSlack, so that most tiles rescale nothing.
 //
 // This file: few rows of a KV head, on mma.sync. S^T = K Q^T and O^T = V^T P^T have the keys and the channels on the 16-row side and
 // the query rows on the side of 8, so that one token's 4 rows waste half a tile and not three quarters; the groups of the cache lie in
 // the operands' lane order. Bound by the cache's bytes where there are enough: 32 sequences on 2,000 to 32,768 keys, one token, 654 MB in
-// 119 us, 5.5 TB/s, 82 % of the measured copy rate; what is missing is the spread of the CTAs' ends (93 to 119 us: the memory's
-// share of an SM differs) and the unpacking, some 70 % of the issue slots. 16 on 300 to 8,200 keys (78 MB, 24 us, 3.3 TB/s) and
-// below: a CTA's start, 4 us, and the joining of the parts.
+// 120 us, 5.5 TB/s, 82 % of the measured copy rate; what is missing is the spread of the CTAs' ends (93 to 119 us: the memory's
+// share of an SM differs) and the issue slots, of which 61 % are in use, most of them for the unpacking. 16 on 300 to 8,200 keys (78 MB,
+// 24 us, 3.3 TB/s) and below: a CTA's start, 4 us, and the joining of the parts. 256 channels, 4 heads a KV head: 16 on 300 to 8,200
+// keys, one token, 83 MB in 28 us, 3.0 TB/s; with many rows every 16 unpack the keys again (2 x 512 tokens on 2,000 to 4,000 keys, 59 GFLOP
+// in 283 us, 0.2 PFLOP/s; 8 x 17 on 900 to 6,100, 37 MB in 55 us).
 //
 // Arithmetic. A held value without its head's fp32 factor is e2m1 x e4m3: 6 significant bits, at most 2688 and a multiple of
 // 2^-10, so f16 holds it exactly, and the factor goes into the scores' scale (keys) and the output (values). A query
 // row is scaled by a power of two to a largest value in [2^13, 2^14): bf16 and f16 rows then are f16 without rounding,
-// but for parts below 2^-38 of the row's largest. Products are exact and their sums are fp32. p is rounded to f16 (2^-12
-// relative, which is below the output's own rounding for bf16 and equal to it for f16); l sums what is not rounded.
+// but for parts below 2^-38 of the row's largest. Products are exact and their sums are fp32. p is rounded to f16, the operand type of the
+// product with the values (2^-11 relative at most: an eighth of the output's own rounding for bf16, as much for f16, whose outputs
+// are off by 0.00028 of their norm for 0.00021 with p in fp32); l sums what is not rounded.
 #include "kv_schedule.cuh"
 
 #include <algorithm>
@@ -299,7 +302,8 @@ __global__ void __launch_bounds__((Shape<D, NT>::kThreads), (Shape<D, NT>::kCtas
         }
       }
       // from sums of products to scores, rounded before the reference is taken off: the difference of a score and itself is then zero,
-      // however large both are (in one multiply-add it would be the product's rounding, and p anything)
+      // however large both are (in one multiply-add it would be the product's rounding, and p anything; 32 sequences on 2,000 to 32,768
+      // keys took 119.4 us so, 119.9 now)
 #pragma unroll
       for (int w = 0; w < G; ++w)
 #pragma unroll
@@ -642,10 +646,6 @@ extern "C" int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* x
   a.scale = x->scale;
   a.wide_q16 = aligned(x->q, 16) && x->q_token_stride % 8 == 0 && x->q_head_stride % 8 == 0;
   a.wide_q = aligned(x->q, 8) && x->q_token_stride % 4 == 0 && x->q_head_stride % 4 == 0;
-  // Up to 32 rows the keys' bytes and their unpacking are the work, and the rows ride along in one pass; above, every 32 rows would
-  // unpack the keys again, and the tiles' products cost the same for 36 rows as for 128. 64 sequences on 8,192 keys, 8 KV heads, by rows
-  // and tiles: 32 rows 268 and 399 us, 36 rows 510 and 403; 16 on 4,096: 44 and 61, 80 and 54.
-  // Fewer rows have kernels of fewer registers: 4 rows by the kernel for 32 take 254 us, by their own 113.
   if (tile > 32) return launch_tiles(h, a, max_q);
   switch (kv->head_dim) {
     case 64: return tile == 8 ? launch_rows<64, 1>(h, a, max_q) : tile == 16 ? launch_rows<64, 2>(h, a, max_q) : launch_rows<64, 4>(h, a, max_q);

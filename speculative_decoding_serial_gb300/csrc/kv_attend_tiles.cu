@@ -9,13 +9,14 @@
 // issued by halves of 64 keys, each as soon as the product with P has read that half, and the softmax starts on the first (this and the two issuing
 // warps: 2 prompts of 2,048 tokens 344 -> 300 us).
 //
-// What bounds it: for prompts the softmax, one thread a row. At 128 keys a row and block its 128 exponentials, as many
-// multiply-adds, maxima, additions and half as many packings are some 600 issue slots of a warp; eight such warps and the eight that
-// unpack share four schedulers. 2 x 2048 tokens on 4,100 and 6,200 keys, 32 query heads on 8: 297 us, 1.03 PFLOP/s, 54 % of the
-// measured rate of large matrix products. Two threads a row (half the chain, but a trade of maxima and sums through shared memory
-// for every block) and blocks of 64 keys (twice the barriers) were slower. For a few tokens a sequence (8 x 17, 31 MB: 30 us) what a
-// CTA does once (tensor memory, query rows, the first blocks, its part for the joining) and the chain through one block: copy,
-// unpack, QK, softmax, PV.
+// What holds it back. Prompts: no unit is full (53 % of the issue slots, 46 % of the tensor pipe, 41 % of the ALU, 23 % of the
+// exponentials); the roles wait for one another, the longest of them the softmax, one thread a row. At 128 keys a row and block its 128
+// exponentials, as many differences, products, maxima, additions and half as many packings are some 650 issue slots of a warp; eight
+// such warps and the eight that unpack share four schedulers. 2 x 2048 tokens on 4,100 and 6,200 keys, 32 query heads on 8: 303 us,
+// 1.01 PFLOP/s, 53 % of the measured rate of large matrix products; 64 channels 227 us. Two threads a row (half the chain, but a
+// trade of maxima and sums through shared memory for every block) and blocks of 64 keys (twice the barriers) were slower. For a few
+// tokens a sequence (8 x 17, 31 MB: 30 us) what a CTA does once (tensor memory, query rows, the first blocks, its part for the joining)
+// and the chain through one block: copy, unpack, QK, softmax, PV.
 //
 // Shared memory holds operands in rows of 128 bytes (64 f16), 8 rows to an atom of 1024 bytes, 16-byte chunks swizzled by the row.
 // Channels 16 b + 8 s .. + 7 of a query row or key lie in chunk 4 s + b % 4 of the row, not 2 b + s: a warp's stores of a block's keys
@@ -146,7 +147,8 @@ __device__ __forceinline__ float row_max(uint32_t st, const uint32_t (&seen)[2])
 // p = 2^((x - ref) f) of a row's products x, as f16 pairs, their sum, and the largest x: one pass, on the guess that the reference still
 // does. The reference is a product, or near one, and is taken off before the factor comes: the difference of x and itself is zero,
 // however large the scores are. (2^(x f - m) in one multiply-add is off by the rounding of m = ref f: for scores past 2^24 p would be any
-// power of two, or infinite. It took 303 us where this takes 306, 2 prompts of 2,048 tokens, and 139 where 146 with a window of 1,024.)
+// power of two, or infinite. 2 prompts of 2,048 tokens took 300 us so and take 303, with a window of 1,024 135 and 141, with 64 channels
+// 222 and 227.)
 template <bool MASKED>
 __device__ __forceinline__ float row_exp(uint32_t st, const uint32_t (&seen)[2], float f, float ref, float2& sum, uint32_t (&p)[2][16]) {
   const float2 f2 = make_float2(f, f), off = make_float2(-ref, -ref);

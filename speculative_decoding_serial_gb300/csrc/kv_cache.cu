@@ -209,7 +209,7 @@ __device__ __forceinline__ void append_entry(const Cache& c, const AppendArgs& a
 }
 
 // One group that an append writes, as the writing kernel needs it: one load away, instead of a search and four dependent loads in every
-// CTA (33,000 tokens of 8 heads of 128 channels: this and the scales worked out once took the writing from 109 to 47 us).
+// CTA (26,968 tokens of 8 heads of 128 channels: this and the scales worked out once took the writing from 109 to 47 us).
 struct __align__(16) AppendGroup {
   int page;    // of the pool
   int place;   // of the group in the page, the first new token in bits 8.., the one past the last in bits 16..
@@ -349,8 +349,8 @@ __device__ __forceinline__ void max_scatter(float (&x)[N]) {
 // A warp quantizes 64 channels of the keys, or of the values, of the new tokens of one group of one head; a CTA has all of the
 // group's. Its loads are all under way before the first is used (one loop over the blocks took 27 us for a single token: its stores kept
 // the next block's loads back). A group's owner is the only writer of its words, so the codes of two tokens that share a byte
-// do not race; what an owner does not write of a word it reads first. Bound by latency for single tokens. Prompts: 33,000
-// tokens, 8 heads of 128 channels, 174 MB of inputs and groups in 47 us, 3.7 TB/s, 55 % of the measured copy rate: a short CTA a
+// do not race; what an owner does not write of a word it reads first. Bound by latency for single tokens. Prompts: 26,968
+// tokens, 8 heads of 128 channels, 141.5 MB of inputs and groups in 47 us, 3.0 TB/s, 45 % of the measured copy rate: a short CTA a
 // group and head loads, works and stores in turn, and what others have under way does not fill the gaps.
 template <int D, int DTYPE>
 __global__ void __launch_bounds__(D) append_write(const __grid_constant__ Cache c, const __grid_constant__ AppendArgs a) {
@@ -916,7 +916,7 @@ int whead_kv_append(const whead_kv* kv, const void* k, const void* v, int32_t dt
   a.wide_k = aligned(k, 4 * e) && k_token_stride % 4 == 0 && k_head_stride % 4 == 0;
   a.wide_v = aligned(v, 2 * e) && v_token_stride % 2 == 0 && v_head_stride % 2 == 0;
   const int64_t groups = std::min(total / 16 + 2 * (int64_t)n, total);  // most that the tokens can touch
-  if (groups > h.c.partial_floats / 4) return WHEAD_ERR_UNSUPPORTED;    // more than the workspace can list: some 40 million tokens
+  if (groups > h.c.partial_floats / 4) return WHEAD_ERR_UNSUPPORTED;    // more than the workspace can list: some 20 million tokens of 64 channels
   const int st = launch_after(append_plan, dim3(1), kPlan, 0, h.stream, h.c, a);
   if (st != WHEAD_OK) return st;
   const dim3 grid((unsigned)std::min<int64_t>(groups, 65535 * 4), kv->kv_heads);
