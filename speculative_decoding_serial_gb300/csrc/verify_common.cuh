@@ -1,0 +1,325 @@
+// verify_common.cuh — what the kernels over rows of logits share: vectors of logits, one pass over a part of a row, and the joining of its parts.
+//
+// A row of V logits is taken in vectors of 16 bytes, 32 of them (one a lane, 512 bytes) being a group; a row's first and last
+// vector may lie across its ends, since rows start anywhere. A cluster of CTAs has a row, each CTA a run of its groups.
+#pragma once
+
+#include "../../include/whead_verify.h"
+#include "kv_common.cuh"
+
+#include <cooperative_groups.h>
+
+namespace whead_verify_impl {
+
+using whead_kv_impl::after_previous;
+using whead_kv_impl::aligned;
+using whead_kv_impl::ex2;
+using whead_kv_impl::kLn2;
+using whead_kv_impl::kLog2e;
+using whead_kv_impl::kMaxDevices;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kAhead = 4;          // vectors of a thread under way
+constexpr int kMaxCluster = 16;
+constexpr float kLowest = -3.402823466e38f;
+
+// Types: values in a vector, and keys, whole numbers in the values' order (-0 counts as +0).
+template <int DT>
+struct Type {
+  static constexpr int kPer = DT == WHEAD_F32 ? 4 : 8;
+  static constexpr int kSize = DT == WHEAD_F32 ? 4 : 2;
+  static constexpr int kKeyBits = DT == WHEAD_F32 ? 32 : 16;
+  static constexpr uint32_t kNone = DT == WHEAD_F32 ? 0xFF800000u : DT == WHEAD_BF16 ? 0xFF80FF80u : 0xFC00FC00u;  // -inf, as a vector holds it
+  static constexpr uint32_t kNoneKey = DT == WHEAD_F32 ? 0x007FFFFFu : DT == WHEAD_BF16 ? 0x007Fu : 0x03FFu;
+};
+
+template <int DT>
+__device__ __forceinline__ uint32_t key_of(float x) {
+  x += 0.0f;
+  if constexpr (DT == WHEAD_F32) {
+    const uint32_t b = __float_as_uint(x);
+    return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+  } else {
+    const uint32_t b = DT == WHEAD_BF16 ? __float_as_uint(x) >> 16 : (uint32_t)__half_as_ushort(__float2half_rn(x));
+    return b & 0x8000u ? b ^ 0xFFFFu : b | 0x8000u;
+  }
+}
+template <int DT>
+__device__ __forceinline__ float value_of(uint32_t key) {
+  if constexpr (DT == WHEAD_F32) {
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+  } else {
+    const uint32_t b = key & 0x8000u ? key ^ 0x8000u : key ^ 0xFFFFu;
+    return DT == WHEAD_BF16 ? __uint_as_float(b << 16) : __half2float(__ushort_as_half((unsigned short)b));
+  }
+}
+
+__device__ __forceinline__ float load_one(const void* p, int64_t at, int dtype) {
+  if (dtype == WHEAD_F32) return __ldg(static_cast<const float*>(p) + at);
+  const unsigned short b = __ldg(static_cast<const unsigned short*>(p) + at);
+  return dtype == WHEAD_BF16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
+}
+
+// A row: where its first vector is (16-byte aligned, at or before its first value), how many values of it come before the row, and
+// how many the row has.
+struct Row {
+  const char* base;
+  int off, V;
+};
+template <int DT>
+__device__ __forceinline__ Row row_at(const void* logits, int64_t at, int V) {
+  const char* p = static_cast<const char*>(logits) + at * Type<DT>::kSize;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return Row{reinterpret_cast<const char*>(a & ~(uintptr_t)15), (int)(a & 15) / Type<DT>::kSize, V};
+}
+template <int DT>
+__device__ __forceinline__ int row_groups(const Row& r) { return (r.off + r.V + 32 * Type<DT>::kPer - 1) / (32 * Type<DT>::kPer); }
+
+// Vector j of a row; places outside the row hold -inf.
+template <int DT>
+__device__ __forceinline__ uint4 load_vector(const Row& r, int j) {
+  constexpr int N = Type<DT>::kPer;
+  const int first = j * N - r.off;
+  uint4 v;
+  if (first >= 0 && first + N <= r.V) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(r.base + (int64_t)j * 16));
+    return v;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    w[k] = Type<DT>::kNone;
+    if constexpr (DT == WHEAD_F32) {
+      if ((unsigned)(first + k) < (unsigned)r.V) w[k] = __ldg(reinterpret_cast<const uint32_t*>(r.base) + (int64_t)j * 4 + k);
+    } else {
+      const unsigned short* p = reinterpret_cast<const unsigned short*>(r.base) + (int64_t)j * 8 + 2 * k;
+      if ((unsigned)(first + 2 * k) < (unsigned)r.V) w[k] = (w[k] & 0xFFFF0000u) | __ldg(p);
+      if ((unsigned)(first + 2 * k + 1) < (unsigned)r.V) w[k] = (w[k] & 0xFFFFu) | (uint32_t)__ldg(p + 1) << 16;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int DT>
+__device__ __forceinline__ void values_of(const uint4& v, float (&x)[Type<DT>::kPer]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (DT == WHEAD_F32) {
+      x[k] = __uint_as_float(w[k]);
+    } else if constexpr (DT == WHEAD_BF16) {
+      x[2 * k] = __uint_as_float(w[k] << 16);
+      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    } else {
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      x[2 * k] = y.x;
+      x[2 * k + 1] = y.y;
+    }
+  }
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// The largest value of a vector, NaN left out.
+template <int DT>
+__device__ __forceinline__ float largest(const uint4& v) {
+  if constexpr (DT == WHEAD_F32) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else if constexpr (DT == WHEAD_BF16) {
+    auto as = [](const uint32_t& w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const float2 m = __bfloat1622float2(__hmax2(__hmax2(as(v.x), as(v.y)), __hmax2(as(v.z), as(v.w))));
+    return fmaxf(m.x, m.y);
+  } else {
+    auto as = [](const uint32_t& w) { return *reinterpret_cast<const __half2*>(&w); };
+    const float2 m = __half22float2(__hmax2(__hmax2(as(v.x), as(v.y)), __hmax2(as(v.z), as(v.w))));
+    return fmaxf(m.x, m.y);
+  }
+}
+
+// The same, NaN if the vector holds one.
+template <int DT>
+__device__ __forceinline__ float largest_nan(const uint4& v) {
+  if constexpr (DT == WHEAD_F32) {
+    return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+  } else if constexpr (DT == WHEAD_BF16) {
+    auto as = [](const uint32_t& w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const float2 m = __bfloat1622float2(__hmax2_nan(__hmax2_nan(as(v.x), as(v.y)), __hmax2_nan(as(v.z), as(v.w))));
+    return max_nan(m.x, m.y);
+  } else {
+    auto as = [](const uint32_t& w) { return *reinterpret_cast<const __half2*>(&w); };
+    const float2 m = __half22float2(__hmax2_nan(__hmax2_nan(as(v.x), as(v.y)), __hmax2_nan(as(v.z), as(v.w))));
+    return max_nan(m.x, m.y);
+  }
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+// A part's sums: s of 2^d and a of d 2^d, d = (x - ref) c with c = log2(e) / T. The difference is formed before the product, so that it
+// is right for any two finite logits (x c - ref c in one multiply-add would be infinite for rows at the type's lowest value).
+struct Sums {
+  float ref, s, a;
+};
+// The same sums for another reference. A part without a value has s = a = 0 and any reference.
+__device__ __forceinline__ Sums moved(const Sums& p, float ref, float c) {
+  if (p.s == 0.0f) return Sums{ref, 0.0f, 0.0f};
+  const float d = max_nan((p.ref - ref) * c, -1e4f), f = ex2(d);
+  return Sums{ref, p.s * f, f == 0.0f ? 0.0f : (p.a + p.s * d) * f};
+}
+
+// One thread's way through its vectors. `ref` is raised when a vector's largest value passes it by kSlack (in log2 units), so that most
+// vectors change nothing; sums then reach 2^kSlack times their number, and a, which loses kSlack units of 2^-24 when it is moved to the
+// row's largest, costs the entropy 5e-7 at most.
+constexpr float kSlack = 8.0f;
+struct Pass {
+  float ref, top;
+  float2 s, a;
+};
+__device__ __forceinline__ void begin(Pass& p) {
+  p.ref = kLowest;
+  p.top = -INFINITY;
+  p.s = p.a = make_float2(0.0f, 0.0f);
+}
+// Adds a vector, whose largest value is `high`. NaN and +inf end in s: NaN by itself, +inf as its own reference (inf - inf). -inf and
+// what lies below the reference by more than 2^-200 add nothing: d is cut off there, so that a never meets 0 x inf.
+template <int DT, bool ENTROPY>
+__device__ __forceinline__ void take(Pass& p, const uint4& raw, float high, float c) {
+  constexpr int N = Type<DT>::kPer;
+  float x[N];
+  values_of<DT>(raw, x);
+  p.top = fmaxf(p.top, high);
+  if ((high - p.ref) * c > kSlack) {
+    const float d = fmaxf((p.ref - high) * c, -1e4f), f = ex2(d);
+    if (ENTROPY) p.a = mul2(fma2(p.s, make_float2(d, d), p.a), make_float2(f, f));
+    p.s = mul2(p.s, make_float2(f, f));
+    p.ref = high;
+  }
+  const float2 off = make_float2(-p.ref, -p.ref), c2 = make_float2(c, c);
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    float2 d = mul2(add2(make_float2(x[k], x[k + 1]), off), c2);
+    if (ENTROPY) d = make_float2(max_nan(d.x, -200.0f), max_nan(d.y, -200.0f));
+    const float2 e = make_float2(ex2(d.x), ex2(d.y));
+    p.s = add2(p.s, e);
+    if (ENTROPY) p.a = fma2(e, d, p.a);
+  }
+}
+
+// Two parts' sums and largest values as one, with the largest value as the reference.
+__device__ __forceinline__ Sums joined(const Sums& p, const Sums& q, float top, float c) {
+  const Sums x = moved(p, top, c), y = moved(q, top, c);
+  return Sums{top, x.s + y.s, x.a + y.a};
+}
+// Over a warp; every lane gets them.
+__device__ __forceinline__ Sums warp_joined(const Pass& p, float c, float& top) {
+  top = p.top;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  Sums r = moved(Sums{p.ref, p.s.x + p.s.y, p.a.x + p.a.y}, top, c);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    r.s += __shfl_xor_sync(~0u, r.s, o);
+    r.a += __shfl_xor_sync(~0u, r.a, o);
+  }
+  return r;
+}
+
+// Runs of groups: CTA `rank` of `ctas` has groups run_begin(rank) .. run_begin(rank + 1) - 1.
+__device__ __forceinline__ int run_begin(int groups, int ctas, int rank) { return (int)((int64_t)groups * rank / ctas); }
+
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned n;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned n;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
+  return n;
+}
+
+// Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC'11).
+__device__ __forceinline__ uint4 philox(uint4 x, uint64_t seed) {
+  uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = (uint64_t)x.x * 0xD2511F53u, b = (uint64_t)x.z * 0xCD9E8D57u;
+    x = make_uint4((uint32_t)(b >> 32) ^ x.y ^ k0, (uint32_t)b, (uint32_t)(a >> 32) ^ x.w ^ k1, (uint32_t)a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return x;
+}
+
+// ---------------------------------------------------------------- host
+
+inline bool is_dtype(int dtype) { return dtype == WHEAD_BF16 || dtype == WHEAD_F16 || dtype == WHEAD_F32; }
+inline int dtype_size(int dtype) { return dtype == WHEAD_F32 ? 4 : 2; }
+
+// log2(e) / T in fp32 has to be a normal number.
+inline bool good_temperature(double t) {
+  const double c = 1.4426950408889634 / t;
+  return t > 0 && c > 1.2e-38 && c < 3.4e38;
+}
+
+// CTAs of a cluster for each of `rows` rows of `bytes`. More CTAs a row while the device has room for them, down to 8 KB each.
+inline int cluster_for(int64_t rows, int64_t bytes, int sms) {
+  int c = 1;
+  while (c < kMaxCluster && rows * c * 2 <= (int64_t)sms * 6 && bytes / (2 * c) >= 8192) c *= 2;
+  return c;
+}
+
+// A launch of `clusters` clusters of `ctas` CTAs, placed while the kernel before it in the stream still runs (it waits for its end).
+template <typename... P, typename... A>
+int launch_clusters(void (*kernel)(P...), int64_t clusters, int ctas, int threads, size_t smem, cudaStream_t stream, std::atomic<bool> (&granted)[kMaxDevices],
+                    int device, A... args) {
+  if (!granted[device].load(std::memory_order_relaxed)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return WHEAD_ERR_CUDA;
+    }
+    granted[device].store(true, std::memory_order_relaxed);
+  }
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)ctas;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3((unsigned)(clusters * ctas));
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  config.attrs = at;
+  config.numAttrs = 2;
+  if (cudaLaunchKernelEx(&config, kernel, P(args)...) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return WHEAD_ERR_CUDA;
+  }
+  return WHEAD_OK;
+}
+
+}  // namespace whead_verify_impl
