@@ -1,6 +1,6 @@
 // verify_common.cuh — what the kernels over rows of logits share: vectors of logits, one pass over a part of a row, and the joining of its parts.
 //
-// A row of V logits is taken in vectors of 16 bytes, 32 of them (one a lane, 512 bytes) being a group; a row's first and last
+// A row of V logits is taken in vectors of 16 bytes, 64 of them (two a lane, 1 KB) being a group; a row's first and last
 // vector may lie across its ends, since rows start anywhere. A cluster of CTAs has a row, each CTA a run of its groups.
 #pragma once
 
@@ -19,7 +19,8 @@ using whead_kv_impl::kLog2e;
 using whead_kv_impl::kMaxDevices;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kAhead = 4;          // vectors of a thread under way
+constexpr int kGroup = 64;         // vectors of a group
+constexpr int kAhead = 2;          // groups of a warp under way
 constexpr int kMaxCluster = 16;
 constexpr float kLowest = -3.402823466e38f;
 
@@ -73,19 +74,20 @@ __device__ __forceinline__ Row row_at(const void* logits, int64_t at, int V) {
   return Row{reinterpret_cast<const char*>(a & ~(uintptr_t)15), (int)(a & 15) / Type<DT>::kSize, V};
 }
 template <int DT>
-__device__ __forceinline__ int row_groups(const Row& r) { return (r.off + r.V + 32 * Type<DT>::kPer - 1) / (32 * Type<DT>::kPer); }
+__device__ __forceinline__ int row_groups(const Row& r) { return (r.off + r.V + kGroup * Type<DT>::kPer - 1) / (kGroup * Type<DT>::kPer); }
+
+__device__ __forceinline__ uint4 load16(const char* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 
 // Vector j of a row; places outside the row hold -inf.
 template <int DT>
 __device__ __forceinline__ uint4 load_vector(const Row& r, int j) {
   constexpr int N = Type<DT>::kPer;
   const int first = j * N - r.off;
-  uint4 v;
-  if (first >= 0 && first + N <= r.V) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(r.base + (int64_t)j * 16));
-    return v;
-  }
+  if (first >= 0 && first + N <= r.V) return load16(r.base + (int64_t)j * 16);
   uint32_t w[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -176,61 +178,116 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
       : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
-// A part's sums: s of 2^d and a of d 2^d, d = (x - ref) c with c = log2(e) / T. The difference is formed before the product, so that it
-// is right for any two finite logits (x c - ref c in one multiply-add would be infinite for rows at the type's lowest value).
+// A part's sums: s of 2^d and a of d 2^d, with d = x c - k, c = log2(e) / T, k = ref c rounded: one multiply-add, exact but for its own
+// rounding, since k is what the sums refer to, whatever it was rounded from. From 2^23 on that rounding would be no small power of two any
+// more (rows at the type's lowest value, temperatures near 0): there d is (x - ref) c, the difference formed before the product,
+// which is right for any two finite logits.
 struct Sums {
   float ref, s, a;
 };
+__device__ __forceinline__ bool plain(float k) { return fabsf(k) < 0x1p23f; }
+// What d becomes less by when the reference goes from one value to another (at most 10,000: 2^-10000 is 0, and times 0 too).
+__device__ __forceinline__ float shift_of(float from, float to, float c) {
+  const float k0 = from * c, k1 = to * c;
+  return max_nan(plain(k0) && plain(k1) ? k0 - k1 : (from - to) * c, -1e4f);
+}
 // The same sums for another reference. A part without a value has s = a = 0 and any reference.
 __device__ __forceinline__ Sums moved(const Sums& p, float ref, float c) {
   if (p.s == 0.0f) return Sums{ref, 0.0f, 0.0f};
-  const float d = max_nan((p.ref - ref) * c, -1e4f), f = ex2(d);
+  const float d = shift_of(p.ref, ref, c), f = ex2(d);
   return Sums{ref, p.s * f, f == 0.0f ? 0.0f : (p.a + p.s * d) * f};
 }
 
-// One thread's way through its vectors. `ref` is raised when a vector's largest value passes it by kSlack (in log2 units), so that most
-// vectors change nothing; sums then reach 2^kSlack times their number, and a, which loses kSlack units of 2^-24 when it is moved to the
+// One thread's way through its groups. The reference is raised when a group's largest value passes it by kSlack (in log2 units), so that
+// most groups change nothing; sums then reach 2^kSlack times their number, and a, which loses kSlack units of 2^-24 when it is moved to the
 // row's largest, costs the entropy 5e-7 at most.
 constexpr float kSlack = 8.0f;
 struct Pass {
-  float ref, top;
+  float ref, k, limit, top;
+  bool careful;  // d may be -inf (then d 2^d would be NaN) or has to be formed from the difference
+  bool masked;   // -inf has been met
   float2 s, a;
 };
 __device__ __forceinline__ void begin(Pass& p) {
-  p.ref = kLowest;
-  p.top = -INFINITY;
+  p.ref = p.limit = kLowest;
+  p.k = p.top = -INFINITY;
+  p.careful = true;
+  p.masked = false;
   p.s = p.a = make_float2(0.0f, 0.0f);
 }
-// Adds a vector, whose largest value is `high`. NaN and +inf end in s: NaN by itself, +inf as its own reference (inf - inf). -inf and
-// what lies below the reference by more than 2^-200 add nothing: d is cut off there, so that a never meets 0 x inf.
-template <int DT, bool ENTROPY>
-__device__ __forceinline__ void take(Pass& p, const uint4& raw, float high, float c) {
+template <int DT, bool ENTROPY, bool CAREFUL>
+__device__ __forceinline__ void add_vector(Pass& p, const uint4& raw, float c) {
   constexpr int N = Type<DT>::kPer;
   float x[N];
   values_of<DT>(raw, x);
-  p.top = fmaxf(p.top, high);
-  if ((high - p.ref) * c > kSlack) {
-    const float d = fmaxf((p.ref - high) * c, -1e4f), f = ex2(d);
-    if (ENTROPY) p.a = mul2(fma2(p.s, make_float2(d, d), p.a), make_float2(f, f));
-    p.s = mul2(p.s, make_float2(f, f));
-    p.ref = high;
-  }
-  const float2 off = make_float2(-p.ref, -p.ref), c2 = make_float2(c, c);
+  const bool is_plain = plain(p.k);
 #pragma unroll
-  for (int k = 0; k < N; k += 2) {
-    float2 d = mul2(add2(make_float2(x[k], x[k + 1]), off), c2);
-    if (ENTROPY) d = make_float2(max_nan(d.x, -200.0f), max_nan(d.y, -200.0f));
+  for (int i = 0; i < N; i += 2) {
+    float2 d;
+    if (!CAREFUL || is_plain) d = fma2(make_float2(x[i], x[i + 1]), make_float2(c, c), make_float2(-p.k, -p.k));
+    else d = mul2(add2(make_float2(x[i], x[i + 1]), make_float2(-p.ref, -p.ref)), make_float2(c, c));
+    if (ENTROPY && CAREFUL) d = make_float2(max_nan(d.x, -200.0f), max_nan(d.y, -200.0f));
     const float2 e = make_float2(ex2(d.x), ex2(d.y));
     p.s = add2(p.s, e);
     if (ENTROPY) p.a = fma2(e, d, p.a);
   }
 }
-
-// Two parts' sums and largest values as one, with the largest value as the reference.
-__device__ __forceinline__ Sums joined(const Sums& p, const Sums& q, float top, float c) {
-  const Sums x = moved(p, top, c), y = moved(q, top, c);
-  return Sums{top, x.s + y.s, x.a + y.a};
+// Adds two vectors whose largest value is `high`. NaN and +inf end in s as NaN (+inf as its own reference: inf - inf). Values of -inf, or so
+// far below the reference that d is -inf, add nothing, but would make a NaN: where a is NaN and s is not, the vectors are added once more
+// with d cut off at -200, and so are the thread's later ones (cutting off always costs one instruction in six).
+template <int DT, bool ENTROPY>
+__device__ __forceinline__ void take(Pass& p, const uint4& v, const uint4& w, float high, float c) {
+  p.top = fmaxf(p.top, high);
+  if (high > p.limit) {
+    const float d = shift_of(p.ref, high, c), f = ex2(d);
+    if (ENTROPY) p.a = mul2(fma2(p.s, make_float2(d, d), p.a), make_float2(f, f));
+    p.s = mul2(p.s, make_float2(f, f));
+    p.ref = high;
+    p.k = high * c;
+    p.limit = high + kSlack / c;
+    p.careful = p.masked || !plain(p.k);
+  }
+  if (!p.careful) {
+    const float2 s = p.s, a = p.a;
+    add_vector<DT, ENTROPY, false>(p, v, c);
+    add_vector<DT, ENTROPY, false>(p, w, c);
+    if (!ENTROPY) return;
+    const float check = p.a.x + p.a.y;
+    if (check == check) return;
+    p.s = s;
+    p.a = a;
+    p.careful = p.masked = true;
+  }
+  add_vector<DT, ENTROPY, true>(p, v, c);
+  add_vector<DT, ENTROPY, true>(p, w, c);
 }
+
+// Over the groups g0 .. g1 - 1 of a row, a warp a group, two vectors of each a lane: f(group, vector, vector). Groups inside the row are
+// loaded without looking at its ends, kAhead of them at a time.
+template <int DT, typename F>
+__device__ __forceinline__ void over_groups(const Row& row, int g0, int g1, F f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int inner0 = row.off ? 1 : 0, inner1 = (row.off + row.V) / (kGroup * Type<DT>::kPer);
+  const int lo = max(g0, inner0), hi = min(g1, inner1);
+  const char* at = row.base + ((int64_t)(lo + warp) * kGroup + lane) * 16;
+  for (int g = lo + warp; g < hi; g += kWarps * kAhead, at += kWarps * kAhead * kGroup * 16) {
+    uint4 v[kAhead], w[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (g + k * kWarps < hi) {
+        v[k] = load16(at + k * kWarps * kGroup * 16);
+        w[k] = load16(at + k * kWarps * kGroup * 16 + 512);
+      }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (g + k * kWarps < hi) f(g + k * kWarps, v[k], w[k]);
+  }
+  // the groups across the row's ends
+  if (warp >= 2) return;
+  const int g = warp == 0 ? 0 : max(inner0, inner1);
+  if (g >= g0 && g < g1 && (warp || inner0)) f(g, load_vector<DT>(row, g * kGroup + lane), load_vector<DT>(row, g * kGroup + 32 + lane));
+}
+
 // Over a warp; every lane gets them.
 __device__ __forceinline__ Sums warp_joined(const Pass& p, float c, float& top) {
   top = p.top;
@@ -245,19 +302,15 @@ __device__ __forceinline__ Sums warp_joined(const Pass& p, float c, float& top) 
   return r;
 }
 
+// Largest of a warp's values, NaN left out.
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Runs of groups: CTA `rank` of `ctas` has groups run_begin(rank) .. run_begin(rank + 1) - 1.
 __device__ __forceinline__ int run_begin(int groups, int ctas, int rank) { return (int)((int64_t)groups * rank / ctas); }
-
-__device__ __forceinline__ unsigned cluster_size() {
-  unsigned n;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
-__device__ __forceinline__ unsigned cluster_rank() {
-  unsigned n;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
-  return n;
-}
 
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC'11).
 __device__ __forceinline__ uint4 philox(uint4 x, uint64_t seed) {

@@ -58,15 +58,7 @@ __device__ __forceinline__ void row_sums(const VerifyArgs& a, const Row& row, in
   const int groups = row_groups<DT>(row), g0 = run_begin(groups, a.ctas, rank), g1 = run_begin(groups, a.ctas, rank + 1);
   Pass p;
   begin(p);
-  for (int g = g0 + warp; g < g1; g += kWarps * kAhead) {
-    uint4 raw[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (g + k * kWarps < g1) raw[k] = load_vector<DT>(row, (g + k * kWarps) * 32 + lane);
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (g + k * kWarps < g1) take<DT, false>(p, raw[k], largest<DT>(raw[k]), c);
-  }
+  over_groups<DT>(row, g0, g1, [&](int, const uint4& v, const uint4& w) { take<DT, false>(p, v, w, fmaxf(largest<DT>(v), largest<DT>(w)), c); });
   float top;
   const Sums w = warp_joined(p, c, top);
   if (lane == 0) {
@@ -131,22 +123,15 @@ __device__ __forceinline__ void row_token(const VerifyArgs& a, const Row& row, i
   float top = -INFINITY;
   int at = INT_MAX;
   bool bad = false;
-  for (int g = g0 + warp; g < g1; g += kWarps * kAhead) {
-    uint4 raw[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (g + k * kWarps < g1) raw[k] = load_vector<DT>(row, (g + k * kWarps) * 32 + lane);
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (g + k * kWarps < g1) {
-        const float high = largest_nan<DT>(raw[k]);
-        bad |= !(high < INFINITY);
-        if (high > top) {
-          top = high;
-          at = (g + k * kWarps) * 32 + lane;
-        }
-      }
-  }
+  over_groups<DT>(row, g0, g1, [&](int g, const uint4& v, const uint4& w) {
+    const float first = largest_nan<DT>(v), second = largest_nan<DT>(w), high = max_nan(first, second);
+    bad |= !(high < INFINITY);
+    const int j = g * kGroup + (first == high ? lane : 32 + lane);
+    if (high > top || (high == top && j < at)) {  // a row's first group may come last
+      top = high;
+      at = j;
+    }
+  });
   bad = __any_sync(~0u, bad);
   warp_first(top, at);
   if (lane == 0) {
@@ -181,7 +166,7 @@ __device__ __forceinline__ void row_token(const VerifyArgs& a, const Row& row, i
   }
   if (rank == 0 && tid == 0) {
     int token = -1;
-    if (!bad && at != INT_MAX) {
+    if (!bad && top > -INFINITY) {
       float x[N];
       values_of<DT>(load_vector<DT>(row, at), x);
 #pragma unroll

@@ -3,7 +3,7 @@
 // With d_v = (x_v - m) log2(e) / T, m the row's largest: s = sum 2^d, a = sum d 2^d; lse = m / T + ln s, log p(v) = ln 2 (d_v - log2 s),
 // H = ln 2 (log2 s - a / s), whose two terms have one sign. Every thread has a running m of its own (verify_common.cuh).
 //
-// Alternatives. The pass keeps the largest value of every group of 32 vectors (512 bytes of the row) in shared memory. The `top` best
+// Alternatives. The pass keeps the largest value of every group (1 KB of the row) in shared memory. The `top` best
 // tokens lie in the `top` groups that come first by (largest value, index): were one outside them, each of them would have a token that
 // comes before it. So once the pass has ended, those groups are found, read again, and their values ranked: work that does
 // not depend on the order of the logits, where lists kept in the pass would.
@@ -20,7 +20,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kMaxRuns = 4224;  // largest values kept by a CTA: of groups, or of runs of 2^shift groups in rows of more (2^24 logits: shift 5)
+constexpr int kMaxRuns = 4224;  // largest values kept by a CTA: of groups, or of runs of 2^shift groups in rows of more (2^24 logits: shift 4)
 constexpr int kCandidates = 512;
 
 struct LogprobArgs {
@@ -50,7 +50,7 @@ struct Shared {
   unsigned long long best[WHEAD_MAX_TOP];                          // the CTA's, in order: key, then the complement of the token; 0: none
   unsigned long long all[kMaxCluster * WHEAD_MAX_TOP];             // the cluster's
   unsigned long long candidate[kCandidates];
-  uint32_t key[WHEAD_MAX_TOP * 32];                                // largest values of the picked groups' vectors, or of the picked runs' groups
+  uint32_t key[WHEAD_MAX_TOP * kGroup];                              // largest values of the picked groups' vectors, or of the picked runs' groups
 };
 
 // Of n keys in shared memory the `top` first by (key, index), by one warp: their indexes, ascending, into `list`, and how many they
@@ -133,28 +133,17 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_rows(const __grid_consta
   // ---- the pass
   Pass p;
   begin(p);
-  for (int g = g0 + warp; g < g1; g += kWarps * kAhead) {
-    uint4 raw[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (g + k * kWarps < g1) raw[k] = load_vector<DT>(row, (g + k * kWarps) * 32 + lane);
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int now = g + k * kWarps;
-      if (now < g1) {
-        const float high = largest<DT>(raw[k]);
-        take<DT, true>(p, raw[k], high, a.c);
-        if (TOP) {
-          const uint32_t key = __reduce_max_sync(~0u, key_of<DT>(high));
-          if (lane == 0) {
-            if (a.shift) atomicMax(&runs[(now >> a.shift) - (g0 >> a.shift)], key);
-            else runs[now - g0] = key;
-          }
-        }
+  over_groups<DT>(row, g0, g1, [&](int g, const uint4& v, const uint4& w) {
+    const float high = fmaxf(largest<DT>(v), largest<DT>(w));
+    take<DT, true>(p, v, w, high, a.c);
+    if (TOP) {
+      const float most = warp_max(high);
+      if (lane == 0) {
+        if (a.shift) atomicMax(&runs[(g >> a.shift) - (g0 >> a.shift)], key_of<DT>(most));
+        else runs[g - g0] = __float_as_uint(most);
       }
     }
-  }
+  });
   {
     float top;
     const Sums w = warp_joined(p, a.c, top);
@@ -165,15 +154,21 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_rows(const __grid_consta
   }
   __syncthreads();
   float top = s.part_top[0];
-  Sums sums = s.part[0];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s.part_top[w]);
+  Sums sums = moved(s.part[0], top, a.c);
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) {
-    const float both = fmaxf(top, s.part_top[w]);
-    sums = joined(sums, s.part[w], both, a.c);
-    top = both;
+    const Sums part = moved(s.part[w], top, a.c);
+    sums.s += part.s;
+    sums.a += part.a;
   }
   // ---- the CTA's best tokens
   if (TOP) {
+    if (!a.shift) {
+      for (int k = tid; k < n_runs; k += kThreads) runs[k] = key_of<DT>(__uint_as_float(runs[k]));
+      __syncthreads();
+    }
     auto choose = [&](const uint32_t* keys, int n) {
       if (warp == 0) {
         const uint32_t bound = pick<BITS>(keys, n, a.top, s.order, &s.picked);
@@ -181,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_rows(const __grid_consta
       }
       __syncthreads();
     };
+    auto key_at = [&](int j) { return key_of<DT>(largest<DT>(load_vector<DT>(row, j))); };
     // the groups
     choose(runs, n_runs);
     const int first = (g0 >> a.shift) << a.shift;
@@ -191,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_rows(const __grid_consta
       for (int e = warp; e < n; e += kWarps) {
         const int g = s.group[e >> a.shift] + (e & mask);
         const bool mine = g >= g0 && g < g1;
-        const uint32_t key = mine ? __reduce_max_sync(~0u, key_of<DT>(largest<DT>(load_vector<DT>(row, g * 32 + lane)))) : 0;
+        const uint32_t key = mine ? __reduce_max_sync(~0u, max(key_at(g * kGroup + lane), key_at(g * kGroup + 32 + lane))) : 0;
         if (lane == 0) s.key[e] = key;
       }
       __syncthreads();
@@ -205,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_rows(const __grid_consta
     uint32_t bound = s.bound;
     const int picked = s.picked;
     if (bound > Type<DT>::kNoneKey) {
-      for (int e = warp; e < picked; e += kWarps) {
-        const int j = s.group[e] * 32 + lane;
+      for (int e = warp; e < 2 * picked; e += kWarps) {
+        const int j = s.group[e / 2] * kGroup + e % 2 * 32 + lane;
         const uint4 raw = load_vector<DT>(row, j);
         if (key_of<DT>(largest<DT>(raw)) >= bound) offer<DT>(s, raw, j, row, bound);
       }
@@ -214,13 +210,13 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_rows(const __grid_consta
     __syncthreads();
     if (bound <= Type<DT>::kNoneKey || s.found > kCandidates) {
       // the same step once more, with the groups' vectors in the groups' place: the best tokens lie in no more vectors than they are
-      for (int e = warp; e < picked; e += kWarps) s.key[e * 32 + lane] = key_of<DT>(largest<DT>(load_vector<DT>(row, s.group[e] * 32 + lane)));
+      for (int e = tid; e < picked * kGroup; e += kThreads) s.key[e] = key_at(s.group[e / kGroup] * kGroup + e % kGroup);
       __syncthreads();
       if (tid == 0) s.found = 0;
-      choose(s.key, picked * 32);
+      choose(s.key, picked * kGroup);
       bound = s.bound;
       if (tid < s.picked) {
-        const int j = s.group[s.order[tid] / 32] * 32 + s.order[tid] % 32;
+        const int j = s.group[s.order[tid] / kGroup] * kGroup + s.order[tid] % kGroup;
         offer<DT>(s, load_vector<DT>(row, j), j, row, bound);
       }
       __syncthreads();
@@ -261,12 +257,18 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_rows(const __grid_consta
     }
     cluster.sync();  // nobody reads this CTA's shared memory after it
   }
-  const float log_s = log2f(sums.s);
+  const float log_s = log2f(sums.s), k = top * a.c;
   const bool none = sums.s == 0.0f, bad = isnan(sums.s);
-  const float inverse = (float)a.inverse;  // and not c ln 2: a token at the type's lowest value keeps its finite log probability
-  auto log_p = [&](float x) { return bad ? sums.s : none || x == -INFINITY ? -INFINITY : (x - top) * inverse - log_s * kLn2; };
+  auto log_p = [&](float x) {
+    if (bad) return sums.s;
+    if (none || x == -INFINITY) return -INFINITY;
+    // a token at the type's lowest value keeps its finite log probability
+    return plain(k) && plain(x * a.c) ? (__fmaf_rn(x, a.c, -k) - log_s) * kLn2 : (x - top) * (float)a.inverse - log_s * kLn2;
+  };
   if (rank == 0 && tid == 0) {
-    if (a.lse) a.lse[r] = bad ? sums.s : none ? -INFINITY : (float)(top * a.inverse) + log_s * kLn2;
+    // m / T itself, and what k was rounded by
+    const float off = plain(k) ? __fmaf_rn(top, a.c, -k) : 0.0f;
+    if (a.lse) a.lse[r] = bad ? sums.s : none ? -INFINITY : (float)(top * a.inverse) + (log_s - off) * kLn2;
     if (a.entropy) a.entropy[r] = bad ? sums.s : none ? 0.0f : fmaxf((log_s - sums.a / sums.s) * kLn2, 0.0f);
     if (a.logprob) a.logprob[r] = log_p(x_token);
   }
@@ -345,7 +347,7 @@ extern "C" int whead_logprobs(const whead_logprobs_args* x) {
   const int64_t bytes = x->V * dtype_size(x->dtype);
   a.ctas = cluster_for(rows, bytes, sms);
   // most groups of a CTA: a row's, one more for its start anywhere, over the CTAs
-  const int most = (int)((bytes / 512 + 2) / a.ctas + 1);
+  const int most = (int)((bytes / (kGroup * 16) + 2) / a.ctas + 1);
   while (((most >> a.shift) + 2) > kMaxRuns) ++a.shift;
   a.runs = (most >> a.shift) + 2;
   cudaStream_t stream = static_cast<cudaStream_t>(x->stream);
