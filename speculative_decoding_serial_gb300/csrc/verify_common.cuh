@@ -18,10 +18,18 @@ using whead_kv_impl::kLn2;
 using whead_kv_impl::kLog2e;
 using whead_kv_impl::kMaxDevices;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kGroup = 64;         // vectors of a group
-constexpr int kAhead = 2;          // groups of a warp under way
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;     // clusters of 16 do not all find room at once: 17 rows of 608 KB take 16 us by them, 9 by clusters of 8
+
+// Two forms of a CTA. For many rows: 256 threads, two groups a warp under way, the rest by the SM's other CTAs. For few rows: 512 threads that
+// ask for all of their groups at once and hold them, so that the call waits for memory once, not turn by turn.
+template <bool HELD>
+struct Form {
+  static constexpr int kThreads = HELD ? 512 : 256, kWarps = kThreads / 32;
+  static constexpr int kAhead = HELD ? 5 : 2;  // groups of a warp
+  static constexpr int kBytes = kWarps * kAhead * kGroup * 16;  // of a row that are under way
+  static constexpr int kCtas = HELD ? 2 : 6;
+};
 constexpr float kLowest = -3.402823466e38f;
 
 // Types: values in a vector, and keys, whole numbers in the values' order (-0 counts as +0).
@@ -263,9 +271,10 @@ __device__ __forceinline__ void take(Pass& p, const uint4& v, const uint4& w, fl
 }
 
 // Over the groups g0 .. g1 - 1 of a row, a warp a group, two vectors of each a lane: f(group, vector, vector). Groups inside the row are
-// loaded without looking at its ends, kAhead of them at a time.
-template <int DT, typename F>
+// loaded without looking at its ends, several of them at a time.
+template <int DT, bool HELD, typename F>
 __device__ __forceinline__ void over_groups(const Row& row, int g0, int g1, F f) {
+  constexpr int kWarps = Form<HELD>::kWarps, kAhead = Form<HELD>::kAhead;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int inner0 = row.off ? 1 : 0, inner1 = (row.off + row.V) / (kGroup * Type<DT>::kPer);
   const int lo = max(g0, inner0), hi = min(g1, inner1);
@@ -288,18 +297,35 @@ __device__ __forceinline__ void over_groups(const Row& row, int g0, int g1, F f)
   if (g >= g0 && g < g1 && (warp || inner0)) f(g, load_vector<DT>(row, g * kGroup + lane), load_vector<DT>(row, g * kGroup + 32 + lane));
 }
 
-// Over a warp; every lane gets them.
-__device__ __forceinline__ Sums warp_joined(const Pass& p, float c, float& top) {
-  top = p.top;
+// The groups that a warp of the form that holds them has: g0 + warp + k * kWarps, k < kAhead; what is not there holds -inf.
+template <int DT>
+struct Held {
+  static constexpr int kAhead = Form<true>::kAhead;
+  uint4 v[kAhead], w[kAhead];
+};
+template <int DT>
+__device__ __forceinline__ void hold_groups(const Row& row, int g0, int g1, Held<DT>& h) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int inner0 = row.off ? 1 : 0, inner1 = (row.off + row.V) / (kGroup * Type<DT>::kPer);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-  Sums r = moved(Sums{p.ref, p.s.x + p.s.y, p.a.x + p.a.y}, top, c);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    r.s += __shfl_xor_sync(~0u, r.s, o);
-    r.a += __shfl_xor_sync(~0u, r.a, o);
+  for (int k = 0; k < Held<DT>::kAhead; ++k) {
+    const int g = g0 + warp + k * Form<true>::kWarps;
+    if (g < g1 && g >= inner0 && g < inner1) {
+      const char* at = row.base + ((int64_t)g * kGroup + lane) * 16;
+      h.v[k] = load16(at);
+      h.w[k] = load16(at + 512);
+    }
   }
-  return r;
+#pragma unroll
+  for (int k = 0; k < Held<DT>::kAhead; ++k) {
+    const int g = g0 + warp + k * Form<true>::kWarps;
+    if (g >= g1) {
+      h.v[k] = h.w[k] = make_uint4(Type<DT>::kNone, Type<DT>::kNone, Type<DT>::kNone, Type<DT>::kNone);
+    } else if (g < inner0 || g >= inner1) {
+      h.v[k] = load_vector<DT>(row, g * kGroup + lane);
+      h.w[k] = load_vector<DT>(row, g * kGroup + 32 + lane);
+    }
+  }
 }
 
 // Largest of a warp's values, NaN left out.
@@ -309,8 +335,41 @@ __device__ __forceinline__ float warp_max(float x) {
   return r;
 }
 
+// Over a warp; every lane gets them.
+__device__ __forceinline__ Sums warp_joined(const Pass& p, float c) {
+  const float top = warp_max(p.top);
+  Sums r = moved(Sums{p.ref, p.s.x + p.s.y, p.a.x + p.a.y}, top, c);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    r.s += __shfl_xor_sync(~0u, r.s, o);
+    r.a += __shfl_xor_sync(~0u, r.a, o);
+  }
+  return r;
+}
+// Of n <= 16 parts, whose references are their largest values, by a warp; every lane gets them.
+__device__ __forceinline__ Sums parts_joined(const Sums* part, int n, float c) {
+  const int lane = threadIdx.x & 31;
+  Sums p = part[min(lane, n - 1)];
+  const float top = warp_max(p.ref);
+  if (lane >= n) p.s = p.a = 0.0f;
+  p = moved(p, top, c);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) {
+    p.s += __shfl_xor_sync(~0u, p.s, o);
+    p.a += __shfl_xor_sync(~0u, p.a, o);
+  }
+  return Sums{top, __shfl_sync(~0u, p.s, 0), __shfl_sync(~0u, p.a, 0)};
+}
+
 // Runs of groups: CTA `rank` of `ctas` has groups run_begin(rank) .. run_begin(rank + 1) - 1.
 __device__ __forceinline__ int run_begin(int groups, int ctas, int rank) { return (int)((int64_t)groups * rank / ctas); }
+
+// A cluster's CTAs write what they have into the first one's shared memory: once when all have started, and the first goes on when all
+// have written; the others need not wait for that.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+template <typename T>
+__device__ __forceinline__ T* in_first(T* p) { return cooperative_groups::this_cluster().map_shared_rank(p, 0); }
 
 // Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as 1, 2, 3", SC'11).
 __device__ __forceinline__ uint4 philox(uint4 x, uint64_t seed) {
@@ -336,11 +395,22 @@ inline bool good_temperature(double t) {
   return t > 0 && c > 1.2e-38 && c < 3.4e38;
 }
 
-// CTAs of a cluster for each of `rows` rows of `bytes`. More CTAs a row while the device has room for them, down to 8 KB each.
-inline int cluster_for(int64_t rows, int64_t bytes, int sms) {
+// Whether rows go by CTAs that hold their part, and how many CTAs a row has.
+struct Division {
+  bool held;
+  int ctas;
+};
+inline Division divide(int64_t rows, int64_t bytes, int sms) {
+  Division d{false, 1};
+  // held: as many CTAs as the row needs, then more while the device has room for them, down to 8 KB each
   int c = 1;
-  while (c < kMaxCluster && rows * c * 2 <= (int64_t)sms * 6 && bytes / (2 * c) >= 8192) c *= 2;
-  return c;
+  while (c < kMaxCluster && c * (Form<true>::kBytes - 2 * 1024) < bytes) c *= 2;
+  if (c * (Form<true>::kBytes - 2 * 1024) >= bytes && rows * c <= (int64_t)sms * Form<true>::kCtas) {
+    while (c < kMaxCluster && rows * c * 2 <= (int64_t)sms * Form<true>::kCtas && bytes / (2 * c) >= 8192) c *= 2;
+    return Division{true, c};
+  }
+  while (d.ctas < kMaxCluster && rows * d.ctas * 2 <= (int64_t)sms * Form<false>::kCtas && bytes / (2 * d.ctas) >= 32768) d.ctas *= 2;
+  return d;
 }
 
 // A launch of `clusters` clusters of `ctas` CTAs, placed while the kernel before it in the stream still runs (it waits for its end).
@@ -348,8 +418,7 @@ template <typename... P, typename... A>
 int launch_clusters(void (*kernel)(P...), int64_t clusters, int ctas, int threads, size_t smem, cudaStream_t stream, std::atomic<bool> (&granted)[kMaxDevices],
                     int device, A... args) {
   if (!granted[device].load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess) {
       (void)cudaGetLastError();
       return WHEAD_ERR_CUDA;
     }

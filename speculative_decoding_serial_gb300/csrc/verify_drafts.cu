@@ -41,144 +41,107 @@ struct VerifyArgs {
 
 __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int i) { return a.drafted ? min(max(__ldg(a.drafted + i), 0), a.gamma) : a.gamma; }
 
+// A part of a row's first largest value: the vector that holds it, and whether the part has NaN or +inf.
+struct First {
+  float top;
+  int at, bad;
+};
 struct RowShared {
-  Sums part[kWarps];
-  float part_top[kWarps];
-  int part_at[kWarps];
-  int part_bad[kWarps];
-  Sums mine;
-  float mine_top;
-  int mine_at, mine_bad;
+  Sums part[16];
+  Sums cluster[kMaxCluster];
+  First first[16];
+  First first_cluster[kMaxCluster];
 };
 
 // Largest value and sum of a row, by a cluster.
-template <int DT>
+template <int DT, bool HELD>
 __device__ __forceinline__ void row_sums(const VerifyArgs& a, const Row& row, int rank, float c, float2* to, RowShared& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = row_groups<DT>(row), g0 = run_begin(groups, a.ctas, rank), g1 = run_begin(groups, a.ctas, rank + 1);
+  if (a.ctas > 1) cluster_arrive();
   Pass p;
   begin(p);
-  over_groups<DT>(row, g0, g1, [&](int, const uint4& v, const uint4& w) { take<DT, false>(p, v, w, fmaxf(largest<DT>(v), largest<DT>(w)), c); });
-  float top;
-  const Sums w = warp_joined(p, c, top);
-  if (lane == 0) {
-    s.part[warp] = w;
-    s.part_top[warp] = top;
-  }
+  over_groups<DT, HELD>(row, g0, g1, [&](int, const uint4& v, const uint4& w) { take<DT, false>(p, v, w, fmaxf(largest<DT>(v), largest<DT>(w)), c); });
+  Sums q = warp_joined(p, c);
+  if (lane == 0) s.part[warp] = q;
   __syncthreads();
-  if (warp == 0) {
-    Sums q = s.part[lane & (kWarps - 1)];
-    top = s.part_top[lane & (kWarps - 1)];
-#pragma unroll
-    for (int o = kWarps / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    q = moved(q, top, c);
-#pragma unroll
-    for (int o = kWarps / 2; o; o >>= 1) q.s += __shfl_xor_sync(~0u, q.s, o);
-    if (lane == 0) {
-      s.mine = q;
-      s.mine_top = top;
-    }
-  }
   if (a.ctas > 1) {
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    if (rank == 0 && warp == 0) {
-      const int k = lane < a.ctas ? lane : 0;
-      top = *cluster.map_shared_rank(&s.mine_top, k);
-      Sums q = *cluster.map_shared_rank(&s.mine, k);
-      if (lane >= a.ctas) q.s = 0.0f;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-      q = moved(q, top, c);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) q.s += __shfl_xor_sync(~0u, q.s, o);
-      if (lane == 0) *to = make_float2(top, q.s);
+    cluster_wait();
+    if (warp == 0) {
+      q = parts_joined(s.part, Form<HELD>::kWarps, c);
+      if (lane == 0) *in_first(&s.cluster[rank]) = q;
     }
-    cluster.sync();
-  } else if (tid == 0) {
-    *to = make_float2(s.mine_top, s.mine.s);
+    __syncwarp();
+    cluster_arrive();
+    if (rank != 0) return;
+    cluster_wait();
+    if (warp == 0) q = parts_joined(s.cluster, a.ctas, c);
+  } else if (warp == 0) {
+    q = parts_joined(s.part, Form<HELD>::kWarps, c);
   }
+  if (tid == 0) *to = make_float2(q.ref, q.s);
 }
 
-// (largest value, its place) over a warp: of equal values the first place.
-__device__ __forceinline__ void warp_first(float& top, int& at) {
+__device__ __forceinline__ First warp_first(First f) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
-    const float y = __shfl_xor_sync(~0u, top, o);
-    const int z = __shfl_xor_sync(~0u, at, o);
-    if (y > top || (y == top && z < at)) {
-      top = y;
-      at = z;
+    const float y = __shfl_xor_sync(~0u, f.top, o);
+    const int z = __shfl_xor_sync(~0u, f.at, o);
+    if (y > f.top || (y == f.top && z < f.at)) {
+      f.top = y;
+      f.at = z;
     }
   }
+  f.bad = __any_sync(~0u, f.bad);
+  return f;
 }
 
 // Token of a row's largest value, by a cluster: the first vector that holds it, then its place there. -1 where the row has NaN, +inf or
 // nothing but -inf.
-template <int DT>
+template <int DT, bool HELD>
 __device__ __forceinline__ void row_token(const VerifyArgs& a, const Row& row, int rank, float2* to, RowShared& s) {
-  constexpr int N = Type<DT>::kPer;
+  constexpr int N = Type<DT>::kPer, WARPS = Form<HELD>::kWarps;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = row_groups<DT>(row), g0 = run_begin(groups, a.ctas, rank), g1 = run_begin(groups, a.ctas, rank + 1);
-  float top = -INFINITY;
-  int at = INT_MAX;
-  bool bad = false;
-  over_groups<DT>(row, g0, g1, [&](int g, const uint4& v, const uint4& w) {
-    const float first = largest_nan<DT>(v), second = largest_nan<DT>(w), high = max_nan(first, second);
-    bad |= !(high < INFINITY);
+  if (a.ctas > 1) cluster_arrive();
+  First f{-INFINITY, INT_MAX, 0};
+  over_groups<DT, HELD>(row, g0, g1, [&](int g, const uint4& v, const uint4& w) {
+    const float first = largest_nan<DT>(v), high = max_nan(first, largest_nan<DT>(w));
+    f.bad |= !(high < INFINITY);
     const int j = g * kGroup + (first == high ? lane : 32 + lane);
-    if (high > top || (high == top && j < at)) {  // a row's first group may come last
-      top = high;
-      at = j;
+    if (high > f.top || (high == f.top && j < f.at)) {  // a row's first group may come last
+      f.top = high;
+      f.at = j;
     }
   });
-  bad = __any_sync(~0u, bad);
-  warp_first(top, at);
-  if (lane == 0) {
-    s.part_top[warp] = top;
-    s.part_at[warp] = at;
-    s.part_bad[warp] = bad;
-  }
+  f = warp_first(f);
+  if (lane == 0) s.first[warp] = f;
   __syncthreads();
-  if (warp == 0) {
-    top = s.part_top[lane & (kWarps - 1)];
-    at = s.part_at[lane & (kWarps - 1)];
-    bad = __any_sync(~0u, s.part_bad[lane & (kWarps - 1)]);
-    warp_first(top, at);
-    if (lane == 0) {
-      s.mine_top = top;
-      s.mine_at = at;
-      s.mine_bad = bad;
-    }
-    __syncwarp();
-  }
+  if (a.ctas > 1) cluster_wait();
+  if (warp == 0) f = warp_first(s.first[lane & (WARPS - 1)]);
   if (a.ctas > 1) {
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    if (rank == 0 && warp == 0) {
-      const int k = lane < a.ctas ? lane : 0;
-      top = *cluster.map_shared_rank(&s.mine_top, k);
-      at = *cluster.map_shared_rank(&s.mine_at, k);
-      bad = __any_sync(~0u, *cluster.map_shared_rank(&s.mine_bad, k));
-      warp_first(top, at);
-    }
-    cluster.sync();
+    if (tid == 0) *in_first(&s.first_cluster[rank]) = f;
+    __syncwarp();
+    cluster_arrive();
+    if (rank != 0) return;
+    cluster_wait();
+    if (warp == 0) f = warp_first(s.first_cluster[lane < a.ctas ? lane : 0]);
   }
-  if (rank == 0 && tid == 0) {
+  if (tid == 0) {
     int token = -1;
-    if (!bad && top > -INFINITY) {
+    if (!f.bad && f.top > -INFINITY) {
       float x[N];
-      values_of<DT>(load_vector<DT>(row, at), x);
+      values_of<DT>(load_vector<DT>(row, f.at), x);
 #pragma unroll
       for (int k = N - 1; k >= 0; --k)
-        if (x[k] == top) token = at * N + k - row.off;
+        if (x[k] == f.top) token = f.at * N + k - row.off;
     }
     *to = make_float2(__int_as_float(token), 0.0f);
   }
 }
 
-template <bool GREEDY>
-__global__ void __launch_bounds__(kThreads, 6) verify_rows(const __grid_constant__ VerifyArgs a) {
+template <bool GREEDY, bool HELD>
+__global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) verify_rows(const __grid_constant__ VerifyArgs a) {
   after_previous();
   __shared__ RowShared s;
   const int r = blockIdx.x / a.ctas, rank = blockIdx.x - r * a.ctas;
@@ -195,8 +158,8 @@ __global__ void __launch_bounds__(kThreads, 6) verify_rows(const __grid_constant
   auto go = [&](auto type) {
     constexpr int DT = decltype(type)::value;
     const Row row = row_at<DT>(p, at, a.V);
-    if constexpr (GREEDY) row_token<DT>(a, row, rank, to, s);
-    else row_sums<DT>(a, row, rank, c, to, s);
+    if constexpr (GREEDY) row_token<DT, HELD>(a, row, rank, to, s);
+    else row_sums<DT, HELD>(a, row, rank, c, to, s);
   };
   if (dtype == WHEAD_BF16) go(std::integral_constant<int, WHEAD_BF16>{});
   else if (dtype == WHEAD_F16) go(std::integral_constant<int, WHEAD_F16>{});
@@ -379,20 +342,28 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
   write_said(a, i, stay, some ? s.stay : -1, tid, kDrawThreads);
 }
 
+template <bool GREEDY, bool HELD>
+int launch_rows(const VerifyArgs& a, int64_t rows, int device, cudaStream_t stream) {
+  static std::atomic<bool> granted[kMaxDevices];
+  return launch_clusters(verify_rows<GREEDY, HELD>, rows, a.ctas, Form<HELD>::kThreads, 0, stream, granted, device, a);
+}
+
 int launch(const VerifyArgs& from, int device, int sms, cudaStream_t stream) {
-  static std::atomic<bool> granted[3][kMaxDevices];
+  static std::atomic<bool> granted[kMaxDevices];
   VerifyArgs a = from;
   const bool greedy = a.inverse == 0.0;
   const int64_t rows = a.n * (a.gamma + 1) + (greedy || !a.draft ? 0 : a.n * a.gamma);
-  const int64_t bytes = (int64_t)a.V * (a.target_dtype == WHEAD_F32 ? 4 : 2);
-  a.ctas = cluster_for(rows, bytes, sms);
-  int rc = greedy ? launch_clusters(verify_rows<true>, rows, a.ctas, kThreads, 0, stream, granted[0], device, a)
-                  : launch_clusters(verify_rows<false>, rows, a.ctas, kThreads, 0, stream, granted[1], device, a);
+  const int64_t bytes = (int64_t)a.V * std::max(dtype_size(a.target_dtype), a.draft ? dtype_size(a.draft_dtype) : 0);
+  const Division d = divide(rows, bytes, sms);
+  a.ctas = d.ctas;
+  int rc;
+  if (greedy) rc = d.held ? launch_rows<true, true>(a, rows, device, stream) : launch_rows<true, false>(a, rows, device, stream);
+  else rc = d.held ? launch_rows<false, true>(a, rows, device, stream) : launch_rows<false, false>(a, rows, device, stream);
   if (rc != WHEAD_OK) return rc;
   if (greedy) return whead_kv_impl::launch_after(verify_greedy, dim3((unsigned)a.n), 32, 0, stream, a);
   a.ctas = 1;
   while (a.ctas < kMaxCluster && a.n * a.ctas * 2 <= (int64_t)sms * 3 && a.V / (2 * a.ctas) >= 4 * kDrawThreads) a.ctas *= 2;
-  return launch_clusters(verify_draw, a.n, a.ctas, kDrawThreads, 0, stream, granted[2], device, a);
+  return launch_clusters(verify_draw, a.n, a.ctas, kDrawThreads, 0, stream, granted, device, a);
 }
 
 }  // namespace

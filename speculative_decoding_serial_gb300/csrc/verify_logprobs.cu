@@ -3,25 +3,25 @@
 // With d_v = (x_v - m) log2(e) / T, m the row's largest: s = sum 2^d, a = sum d 2^d; lse = m / T + ln s, log p(v) = ln 2 (d_v - log2 s),
 // H = ln 2 (log2 s - a / s), whose two terms have one sign. Every thread has a running m of its own (verify_common.cuh).
 //
-// Alternatives. The pass keeps the largest value of every group (1 KB of the row) in shared memory. The `top` best
-// tokens lie in the `top` groups that come first by (largest value, index): were one outside them, each of them would have a token that
-// comes before it. So once the pass has ended, those groups are found, read again, and their values ranked: work that does
-// not depend on the order of the logits, where lists kept in the pass would.
+// Alternatives. The CTA's threads make 64 parts of its values; the `top`-th of the parts' largest values is a bound that at least `top`
+// values reach, and in rows without an order few more. The values that reach it are ranked by counting. Many rows: the pass keeps the
+// largest value of every group (1 KB of the row) in shared memory, and the groups that reach the bound are read again; few rows:
+// the CTA still holds its groups. Where more values reach the bound than there is room for, the groups with the best tokens are picked
+// exactly (pick_candidates). None of this is part of the pass, whose work does not depend on the order of the logits.
 #include "verify_common.cuh"
 
 #include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 namespace whead_verify_impl {
 
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr int kMaxRuns = 4224;  // largest values kept by a CTA: of groups, or of runs of 2^shift groups in rows of more (2^24 logits: shift 4)
-constexpr int kCandidates = 512;
+constexpr int kCandidates = 512, kListed = 128, kSubs = 64;
 
 struct LogprobArgs {
   const void* logits;
@@ -37,21 +37,24 @@ struct LogprobArgs {
   double inverse;  // 1 / T
 };
 
-struct Shared {
-  Sums part[kWarps];
-  float part_top[kWarps];
-  Sums mine;          // the CTA's, for the cluster
-  float mine_top;
-  int found;          // candidates
-  int picked;         // what pick() found: how many keys, their indexes, the bound
-  int order[WHEAD_MAX_TOP];
-  uint32_t bound;
-  int group[WHEAD_MAX_TOP];
-  unsigned long long best[WHEAD_MAX_TOP];                          // the CTA's, in order: key, then the complement of the token; 0: none
-  unsigned long long all[kMaxCluster * WHEAD_MAX_TOP];             // the cluster's
-  unsigned long long candidate[kCandidates];
-  uint32_t key[WHEAD_MAX_TOP * kGroup];                              // largest values of the picked groups' vectors, or of the picked runs' groups
+struct RowShared {
+  Sums part[16];          // the warps'
+  Sums cluster[kMaxCluster];
 };
+struct TopShared {
+  uint32_t bound;
+  int found, listed;                                    // candidates, groups
+  int list[kListed];
+  uint32_t sub[kSubs];                                  // largest values of the CTA's parts
+  unsigned long long candidate[kCandidates];            // key, then the complement of the token
+  unsigned long long best[kMaxCluster * WHEAD_MAX_TOP]; // each CTA's, in order; 0: none
+  // the way for rows whose candidates are too many
+  int picked;                                           // what pick() found: how many keys, their indexes
+  int order[WHEAD_MAX_TOP];
+  int group[WHEAD_MAX_TOP];
+  uint32_t key[WHEAD_MAX_TOP * kGroup];                 // largest values of the picked groups' vectors, or of the picked runs' groups
+};
+struct Nothing {};
 
 // Of n keys in shared memory the `top` first by (key, index), by one warp: their indexes, ascending, into `list`, and how many they
 // are. Returns a bound that all of them reach and none of those left out passes (0 where none is left out). Bit by bit, from the highest,
@@ -89,25 +92,70 @@ __device__ uint32_t pick(const uint32_t* keys, int n, int top, int* list, int* p
 }
 
 template <int DT>
-__device__ __forceinline__ void offer(Shared& s, const uint4& raw, int j, const Row& row, uint32_t bound) {
+__device__ __forceinline__ void offer(TopShared& s, const uint4& raw, int j, const Row& row, uint32_t bound) {
   constexpr int N = Type<DT>::kPer;
   float x[N];
   values_of<DT>(raw, x);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const uint32_t key = key_of<DT>(x[k]);
-    if (key >= bound && key > Type<DT>::kNoneKey) {
+    if (key >= bound) {
       const int at = atomicAdd(&s.found, 1);
       if (at < kCandidates) s.candidate[at] = (unsigned long long)key << 32 | (uint32_t)~(uint32_t)(j * N + k - row.off);
     }
   }
 }
 
-template <int DT, bool TOP>
-__global__ void __launch_bounds__(kThreads, 6) logprobs_rows(const __grid_constant__ LogprobArgs a) {
-  after_previous();
+// The way for a part of a row with too many values that reach the bound (many equal ones, or sorted ones): the groups that hold the best
+// tokens by pick(), then their vectors likewise; the best tokens lie in no more vectors than they are. runs: the groups' largest values.
+template <int DT, int THREADS>
+__device__ __noinline__ void pick_candidates(TopShared& s, const uint32_t* runs, int n_runs, int g0, int g1, int shift, int top, Row row) {
   constexpr int BITS = Type<DT>::kKeyBits;
-  __shared__ Shared s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto key_at = [&](int j) { return key_of<DT>(largest<DT>(load_vector<DT>(row, j))); };
+  auto choose = [&](const uint32_t* keys, int n) {
+    if (warp == 0) {
+      const uint32_t bound = pick<BITS>(keys, n, top, s.order, &s.picked);
+      if (lane == 0) s.bound = bound;
+    }
+    __syncthreads();
+  };
+  choose(runs, n_runs);
+  if (tid < s.picked) s.group[tid] = ((g0 >> shift) + s.order[tid]) << shift;
+  __syncthreads();
+  if (shift) {  // of the picked runs of groups
+    const int n = s.picked << shift, mask = (1 << shift) - 1;
+    for (int e = warp; e < n; e += THREADS / 32) {
+      const int g = s.group[e >> shift] + (e & mask);
+      const bool mine = g >= g0 && g < g1;
+      const uint32_t key = mine ? __reduce_max_sync(~0u, max(key_at(g * kGroup + lane), key_at(g * kGroup + 32 + lane))) : 0;
+      if (lane == 0) s.key[e] = key;
+    }
+    __syncthreads();
+    choose(s.key, n);
+    const int g = tid < s.picked ? s.group[s.order[tid] >> shift] + (s.order[tid] & mask) : 0;
+    __syncthreads();
+    if (tid < s.picked) s.group[tid] = g;
+    __syncthreads();
+  }
+  const int picked = s.picked;
+  for (int e = tid; e < picked * kGroup; e += THREADS) s.key[e] = key_at(s.group[e / kGroup] * kGroup + e % kGroup);
+  if (tid == 0) s.found = 0;
+  __syncthreads();
+  choose(s.key, picked * kGroup);
+  if (tid < s.picked) {
+    const int j = s.group[s.order[tid] / kGroup] * kGroup + s.order[tid] % kGroup;
+    offer<DT>(s, load_vector<DT>(row, j), j, row, max(s.bound, Type<DT>::kNoneKey + 1));
+  }
+  __syncthreads();
+}
+
+template <int DT, bool TOP, bool HELD>
+__global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) logprobs_rows(const __grid_constant__ LogprobArgs a) {
+  after_previous();
+  constexpr int THREADS = Form<HELD>::kThreads, WARPS = THREADS / 32;
+  __shared__ RowShared s;
+  __shared__ std::conditional_t<TOP, TopShared, Nothing> top_shared;
   extern __shared__ uint32_t runs[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = blockIdx.x / a.ctas, rank = blockIdx.x - r * a.ctas;
@@ -116,148 +164,137 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_rows(const __grid_consta
   const Row row = row_at<DT>(a.logits, at, a.V);
   const int groups = row_groups<DT>(row), g0 = run_begin(groups, a.ctas, rank), g1 = run_begin(groups, a.ctas, rank + 1);
   const int n_runs = g1 > g0 ? ((g1 - 1) >> a.shift) - (g0 >> a.shift) + 1 : 0;
-  if (TOP) {
-    if (a.shift) {
-      for (int k = tid; k < n_runs; k += kThreads) runs[k] = 0;
+  Held<DT> held;
+  if (HELD) hold_groups<DT>(row, g0, g1, held);
+  if constexpr (TOP) {
+    if (!HELD && a.shift) {
+      for (int k = tid; k < n_runs; k += THREADS) runs[k] = 0;
     }
-    if (tid == 0) s.found = 0;
-    if (tid < WHEAD_MAX_TOP) s.best[tid] = 0;
+    if (tid == 0) top_shared.found = top_shared.listed = 0;
+    if (tid < kMaxCluster * WHEAD_MAX_TOP) top_shared.best[tid] = 0;
     __syncthreads();
   }
-  int token = -1;
+  if (a.ctas > 1) cluster_arrive();
   float x_token = -INFINITY;
-  if (rank == 0 && tid == 0 && a.tokens) {
-    token = __ldg(a.tokens + r);
+  if (rank == 0 && a.tokens) {
+    const int token = __ldg(a.tokens + r);
     if ((unsigned)token < (unsigned)a.V) x_token = load_one(a.logits, at + token, DT);
   }
   // ---- the pass
   Pass p;
   begin(p);
-  over_groups<DT>(row, g0, g1, [&](int g, const uint4& v, const uint4& w) {
+  auto step = [&](int g, const uint4& v, const uint4& w) {
     const float high = fmaxf(largest<DT>(v), largest<DT>(w));
     take<DT, true>(p, v, w, high, a.c);
-    if (TOP) {
+    if (TOP && !HELD) {
       const float most = warp_max(high);
       if (lane == 0) {
         if (a.shift) atomicMax(&runs[(g >> a.shift) - (g0 >> a.shift)], key_of<DT>(most));
-        else runs[g - g0] = __float_as_uint(most);
+        else runs[g - g0] = key_of<DT>(most);
       }
     }
-  });
+  };
+  if constexpr (HELD) {
+#pragma unroll
+    for (int k = 0; k < Held<DT>::kAhead; ++k)
+      if (g0 + warp + k * WARPS < g1) step(0, held.v[k], held.w[k]);
+  } else {
+    over_groups<DT, false>(row, g0, g1, step);
+  }
   {
-    float top;
-    const Sums w = warp_joined(p, a.c, top);
-    if (lane == 0) {
-      s.part[warp] = w;
-      s.part_top[warp] = top;
-    }
+    const Sums w = warp_joined(p, a.c);
+    if (lane == 0) s.part[warp] = w;
+  }
+  if constexpr (TOP) {
+    constexpr int SUB = THREADS / kSubs;
+    uint32_t key = key_of<DT>(p.top);
+#pragma unroll
+    for (int o = 1; o < SUB; o <<= 1) key = max(key, __shfl_xor_sync(~0u, key, o));
+    if (tid % SUB == 0) top_shared.sub[tid / SUB] = key;
   }
   __syncthreads();
-  float top = s.part_top[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s.part_top[w]);
-  Sums sums = moved(s.part[0], top, a.c);
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) {
-    const Sums part = moved(s.part[w], top, a.c);
-    sums.s += part.s;
-    sums.a += part.a;
-  }
   // ---- the CTA's best tokens
-  if (TOP) {
-    if (!a.shift) {
-      for (int k = tid; k < n_runs; k += kThreads) runs[k] = key_of<DT>(__uint_as_float(runs[k]));
-      __syncthreads();
+  unsigned long long* best = nullptr;
+  if constexpr (TOP) {
+    TopShared& ts = top_shared;
+    // The CTA's values are in kSubs parts. The `top`-th of their largest values is one that `top` values reach, and on rows
+    // without an order few more do.
+    if (tid < kSubs) {
+      const uint32_t mine = ts.sub[tid];
+      int before = 0;
+#pragma unroll 16
+      for (int k = 0; k < kSubs; ++k) before += ts.sub[k] > mine || (ts.sub[k] == mine && k < tid);
+      if (before == a.top - 1) ts.bound = max(mine, Type<DT>::kNoneKey + 1);
     }
-    auto choose = [&](const uint32_t* keys, int n) {
-      if (warp == 0) {
-        const uint32_t bound = pick<BITS>(keys, n, a.top, s.order, &s.picked);
-        if (lane == 0) s.bound = bound;
-      }
-      __syncthreads();
-    };
-    auto key_at = [&](int j) { return key_of<DT>(largest<DT>(load_vector<DT>(row, j))); };
-    // the groups
-    choose(runs, n_runs);
-    const int first = (g0 >> a.shift) << a.shift;
-    if (tid < s.picked) s.group[tid] = first + (s.order[tid] << a.shift);
     __syncthreads();
-    if (a.shift) {  // of the picked runs of groups
-      const int n = s.picked << a.shift, mask = (1 << a.shift) - 1;
-      for (int e = warp; e < n; e += kWarps) {
-        const int g = s.group[e >> a.shift] + (e & mask);
-        const bool mine = g >= g0 && g < g1;
-        const uint32_t key = mine ? __reduce_max_sync(~0u, max(key_at(g * kGroup + lane), key_at(g * kGroup + 32 + lane))) : 0;
-        if (lane == 0) s.key[e] = key;
+    const uint32_t bound = ts.bound;
+    if constexpr (HELD) {
+#pragma unroll
+      for (int k = 0; k < Held<DT>::kAhead; ++k) {
+        const int j = (g0 + warp + k * WARPS) * kGroup + lane;
+        if (key_of<DT>(largest<DT>(held.v[k])) >= bound) offer<DT>(ts, held.v[k], j, row, bound);
+        if (key_of<DT>(largest<DT>(held.w[k])) >= bound) offer<DT>(ts, held.w[k], j + 32, row, bound);
       }
+    } else {
+      for (int k = tid; k < n_runs; k += THREADS)
+        if (runs[k] >= bound) {
+          const int place = atomicAdd(&ts.listed, 1);
+          if (place < kListed) ts.list[place] = k;
+        }
       __syncthreads();
-      choose(s.key, n);
-      const int g = tid < s.picked ? s.group[s.order[tid] >> a.shift] + (s.order[tid] & mask) : 0;
-      __syncthreads();
-      if (tid < s.picked) s.group[tid] = g;
-      __syncthreads();
-    }
-    // their values that reach the bound, where that is one and they are not too many
-    uint32_t bound = s.bound;
-    const int picked = s.picked;
-    if (bound > Type<DT>::kNoneKey) {
-      for (int e = warp; e < 2 * picked; e += kWarps) {
-        const int j = s.group[e / 2] * kGroup + e % 2 * 32 + lane;
-        const uint4 raw = load_vector<DT>(row, j);
-        if (key_of<DT>(largest<DT>(raw)) >= bound) offer<DT>(s, raw, j, row, bound);
+      const int listed = ts.listed << a.shift;
+      if (ts.listed <= kListed) {
+        for (int e = warp; e < 2 * listed; e += WARPS) {
+          const int g = (((g0 >> a.shift) + ts.list[e / 2 >> a.shift]) << a.shift) + (e / 2 & ((1 << a.shift) - 1)), j = g * kGroup + e % 2 * 32 + lane;
+          if (g < g0 || g >= g1) continue;
+          const uint4 raw = load_vector<DT>(row, j);
+          if (key_of<DT>(largest<DT>(raw)) >= bound) offer<DT>(ts, raw, j, row, bound);
+        }
       }
     }
     __syncthreads();
-    if (bound <= Type<DT>::kNoneKey || s.found > kCandidates) {
-      // the same step once more, with the groups' vectors in the groups' place: the best tokens lie in no more vectors than they are
-      for (int e = tid; e < picked * kGroup; e += kThreads) s.key[e] = key_at(s.group[e / kGroup] * kGroup + e % kGroup);
-      __syncthreads();
-      if (tid == 0) s.found = 0;
-      choose(s.key, picked * kGroup);
-      bound = s.bound;
-      if (tid < s.picked) {
-        const int j = s.group[s.order[tid] / kGroup] * kGroup + s.order[tid] % kGroup;
-        offer<DT>(s, load_vector<DT>(row, j), j, row, bound);
+    if (ts.found > kCandidates || ts.listed > kListed) {
+      if constexpr (HELD) {
+#pragma unroll
+        for (int k = 0; k < Held<DT>::kAhead; ++k) {
+          const float most = warp_max(fmaxf(largest<DT>(held.v[k]), largest<DT>(held.w[k])));
+          if (lane == 0 && g0 + warp + k * WARPS < g1) runs[warp + k * WARPS] = key_of<DT>(most);
+        }
+        __syncthreads();
       }
-      __syncthreads();
+      pick_candidates<DT, THREADS>(ts, runs, n_runs, g0, g1, a.shift, a.top, row);
     }
     // ranked by counting those that come before
-    const int found = s.found;
-    for (int e = tid; e < found; e += kThreads) {
-      const unsigned long long mine = s.candidate[e];
+    if (a.ctas > 1) cluster_wait();  // all have started
+    best = a.ctas > 1 ? in_first(ts.best) + rank * a.top : ts.best;
+    const int found = ts.found;
+    for (int e = tid; e < found; e += THREADS) {
+      const unsigned long long mine = ts.candidate[e];
       int before = 0;
-      for (int k = 0; k < found; ++k) before += s.candidate[k] > mine;
-      if (before < a.top) s.best[before] = mine;
+#pragma unroll 4
+      for (int k = 0; k < found; ++k) before += ts.candidate[k] > mine;
+      if (before < a.top) best[before] = mine;
     }
-    __syncthreads();
+  } else if (a.ctas > 1) {
+    cluster_wait();
   }
-  // ---- the cluster's parts
+  // ---- the cluster's parts, in its first CTA
+  Sums sums;
   if (a.ctas > 1) {
-    cg::cluster_group cluster = cg::this_cluster();
-    if (tid == 0) {
-      s.mine = sums;
-      s.mine_top = top;
+    if (warp == 0) {
+      sums = parts_joined(s.part, WARPS, a.c);
+      if (lane == 0) *in_first(&s.cluster[rank]) = sums;
     }
-    cluster.sync();
-    const int k = lane < a.ctas ? lane : 0;  // the same in every warp
-    const float other = *cluster.map_shared_rank(&s.mine_top, k);
-    Sums part = *cluster.map_shared_rank(&s.mine, k);
-    if (lane >= a.ctas) part.s = 0.0f;
-    top = other;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    sums = moved(part, top, a.c);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      sums.s += __shfl_xor_sync(~0u, sums.s, o);
-      sums.a += __shfl_xor_sync(~0u, sums.a, o);
-    }
-    if (TOP) {
-      for (int e = tid; e < a.ctas * a.top; e += kThreads) s.all[e] = cluster.map_shared_rank(s.best, e / a.top)[e % a.top];
-    }
-    cluster.sync();  // nobody reads this CTA's shared memory after it
+    __syncwarp();
+    cluster_arrive();
+    if (rank != 0) return;
+    cluster_wait();
+    sums = parts_joined(s.cluster, a.ctas, a.c);
+  } else {
+    if (TOP) __syncthreads();
+    sums = parts_joined(s.part, WARPS, a.c);
   }
-  const float log_s = log2f(sums.s), k = top * a.c;
+  const float top = sums.ref, log_s = log2f(sums.s), k = top * a.c;
   const bool none = sums.s == 0.0f, bad = isnan(sums.s);
   auto log_p = [&](float x) {
     if (bad) return sums.s;
@@ -265,48 +302,46 @@ __global__ void __launch_bounds__(kThreads, 6) logprobs_rows(const __grid_consta
     // a token at the type's lowest value keeps its finite log probability
     return plain(k) && plain(x * a.c) ? (__fmaf_rn(x, a.c, -k) - log_s) * kLn2 : (x - top) * (float)a.inverse - log_s * kLn2;
   };
-  if (rank == 0 && tid == 0) {
+  if (tid == 0) {
     // m / T itself, and what k was rounded by
     const float off = plain(k) ? __fmaf_rn(top, a.c, -k) : 0.0f;
     if (a.lse) a.lse[r] = bad ? sums.s : none ? -INFINITY : (float)(top * a.inverse) + (log_s - off) * kLn2;
     if (a.entropy) a.entropy[r] = bad ? sums.s : none ? 0.0f : fmaxf((log_s - sums.a / sums.s) * kLn2, 0.0f);
     if (a.logprob) a.logprob[r] = log_p(x_token);
   }
-  if (TOP) {
+  if constexpr (TOP) {
+    TopShared& ts = top_shared;
+    const int n = a.ctas * a.top;  // at most a place a thread
+    const unsigned long long mine = tid < n && !bad ? ts.best[tid] : 0ull;
+    int before = tid;
+    if (a.ctas > 1 && tid < n) {
+      before = 0;
+#pragma unroll 4
+      for (int e = 0; e < n; ++e) before += ts.best[e] > mine;
+    }
+    const int live = __syncthreads_count(mine != 0);
     int32_t* tokens = a.top_tokens + (int64_t)r * a.top;
     float* values = a.top_logprobs + (int64_t)r * a.top;
-    auto put = [&](int place, unsigned long long e) {
-      const bool is = e != 0 && !bad;
-      tokens[place] = is ? (int32_t)~(uint32_t)e : -1;
-      values[place] = is ? log_p(value_of<DT>((uint32_t)(e >> 32))) : bad ? sums.s : -INFINITY;
-    };
-    if (a.ctas == 1) {
-      if (tid < a.top) put(tid, s.best[tid]);
-    } else {
-      __syncthreads();
-      const int n = a.ctas * a.top;
-      int live = 0;
-      for (int e = warp; e < a.top; e += kWarps) {
-        const unsigned long long mine = s.best[e];
-        int before = 0;
-        live = 0;
-        for (int k = lane; k < n; k += 32) {
-          before += s.all[k] > mine;
-          live += s.all[k] != 0;
-        }
-        before = __reduce_add_sync(~0u, before);
-        live = __reduce_add_sync(~0u, live);
-        if (lane == 0 && mine != 0 && before < a.top) put(before, mine);
-        if (lane == 0 && rank == 0 && e >= live) put(e, 0ull);
-      }
+    if (mine != 0 && before < a.top) {
+      tokens[before] = (int32_t)~(uint32_t)mine;
+      values[before] = log_p(value_of<DT>((uint32_t)(mine >> 32)));
+    }
+    if (tid >= live && tid < a.top) {
+      tokens[tid] = -1;
+      values[tid] = bad ? sums.s : -INFINITY;
     }
   }
 }
 
-template <int DT, bool TOP>
+template <int DT, bool TOP, bool HELD>
 int launch(const LogprobArgs& a, int64_t rows, int device, cudaStream_t stream) {
   static std::atomic<bool> granted[kMaxDevices];
-  return launch_clusters(logprobs_rows<DT, TOP>, rows, a.ctas, kThreads, TOP ? a.runs * 4 : 0, stream, granted, device, a);
+  return launch_clusters(logprobs_rows<DT, TOP, HELD>, rows, a.ctas, Form<HELD>::kThreads, TOP ? a.runs * 4 : 0, stream, granted, device, a);
+}
+template <int DT>
+int launch(const LogprobArgs& a, bool held, int64_t rows, int device, cudaStream_t stream) {
+  if (held) return a.top ? launch<DT, true, true>(a, rows, device, stream) : launch<DT, false, true>(a, rows, device, stream);
+  return a.top ? launch<DT, true, false>(a, rows, device, stream) : launch<DT, false, false>(a, rows, device, stream);
 }
 
 }  // namespace
@@ -345,15 +380,16 @@ extern "C" int whead_logprobs(const whead_logprobs_args* x) {
   a.inverse = 1.0 / x->temperature;
   a.c = (float)(1.4426950408889634 / x->temperature);
   const int64_t bytes = x->V * dtype_size(x->dtype);
-  a.ctas = cluster_for(rows, bytes, sms);
+  const Division d = divide(rows, bytes, sms);
+  a.ctas = d.ctas;
   // most groups of a CTA: a row's, one more for its start anywhere, over the CTAs
   const int most = (int)((bytes / (kGroup * 16) + 2) / a.ctas + 1);
   while (((most >> a.shift) + 2) > kMaxRuns) ++a.shift;
   a.runs = (most >> a.shift) + 2;
   cudaStream_t stream = static_cast<cudaStream_t>(x->stream);
   switch (x->dtype) {
-    case WHEAD_BF16: return a.top ? launch<WHEAD_BF16, true>(a, rows, device, stream) : launch<WHEAD_BF16, false>(a, rows, device, stream);
-    case WHEAD_F16: return a.top ? launch<WHEAD_F16, true>(a, rows, device, stream) : launch<WHEAD_F16, false>(a, rows, device, stream);
-    default: return a.top ? launch<WHEAD_F32, true>(a, rows, device, stream) : launch<WHEAD_F32, false>(a, rows, device, stream);
+    case WHEAD_BF16: return launch<WHEAD_BF16>(a, d.held, rows, device, stream);
+    case WHEAD_F16: return launch<WHEAD_F16>(a, d.held, rows, device, stream);
+    default: return launch<WHEAD_F32>(a, d.held, rows, device, stream);
   }
 }
