@@ -22,14 +22,16 @@ constexpr int kGroup = 64;         // vectors of a group
 constexpr int kMaxCluster = 8;     // clusters of 16 do not all find room at once: 17 rows of 608 KB take 16 us by them, 9 by clusters of 8
 
 // Two forms of a CTA. For many rows: 256 threads, two groups a warp under way, the rest by the SM's other CTAs. For few rows: 512 threads that
-// ask for all of their groups at once and hold them, so that the call waits for memory once, not turn by turn.
+// ask for their whole part of the row at once, by copies to shared memory, so that the call waits for memory once, not turn by turn; the
+// loop over it is rolled, since code that runs once is fetched more slowly than it runs.
 template <bool HELD>
 struct Form {
   static constexpr int kThreads = HELD ? 512 : 256, kWarps = kThreads / 32;
-  static constexpr int kAhead = HELD ? 5 : 2;  // groups of a warp
-  static constexpr int kBytes = kWarps * kAhead * kGroup * 16;  // of a row that are under way
   static constexpr int kCtas = HELD ? 2 : 6;
 };
+constexpr int kAhead = 2;       // groups of a warp under way
+constexpr int kHeldGroups = 90; // of a CTA: two CTAs an SM
+
 constexpr float kLowest = -3.402823466e38f;
 
 // Types: values in a vector, and keys, whole numbers in the values' order (-0 counts as +0).
@@ -266,15 +268,15 @@ __device__ __forceinline__ void take(Pass& p, const uint4& v, const uint4& w, fl
     p.a = a;
     p.careful = p.masked = true;
   }
-  add_vector<DT, ENTROPY, true>(p, v, c);
-  add_vector<DT, ENTROPY, true>(p, w, c);
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) add_vector<DT, ENTROPY, true>(p, k ? w : v, c);
 }
 
 // Over the groups g0 .. g1 - 1 of a row, a warp a group, two vectors of each a lane: f(group, vector, vector). Groups inside the row are
 // loaded without looking at its ends, several of them at a time.
-template <int DT, bool HELD, typename F>
+template <int DT, typename F>
 __device__ __forceinline__ void over_groups(const Row& row, int g0, int g1, F f) {
-  constexpr int kWarps = Form<HELD>::kWarps, kAhead = Form<HELD>::kAhead;
+  constexpr int kWarps = Form<false>::kWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int inner0 = row.off ? 1 : 0, inner1 = (row.off + row.V) / (kGroup * Type<DT>::kPer);
   const int lo = max(g0, inner0), hi = min(g1, inner1);
@@ -297,35 +299,32 @@ __device__ __forceinline__ void over_groups(const Row& row, int g0, int g1, F f)
   if (g >= g0 && g < g1 && (warp || inner0)) f(g, load_vector<DT>(row, g * kGroup + lane), load_vector<DT>(row, g * kGroup + 32 + lane));
 }
 
-// The groups that a warp of the form that holds them has: g0 + warp + k * kWarps, k < kAhead; what is not there holds -inf.
+// The other form: the groups to shared memory, group g at 64 (g - g0), all under way at once; and then over them. A thread
+// takes what it has asked for itself, so that no barrier is needed before.
 template <int DT>
-struct Held {
-  static constexpr int kAhead = Form<true>::kAhead;
-  uint4 v[kAhead], w[kAhead];
-};
-template <int DT>
-__device__ __forceinline__ void hold_groups(const Row& row, int g0, int g1, Held<DT>& h) {
+__device__ __forceinline__ void hold_groups(const Row& row, int g0, int g1, uint4* held) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int inner0 = row.off ? 1 : 0, inner1 = (row.off + row.V) / (kGroup * Type<DT>::kPer);
-#pragma unroll
-  for (int k = 0; k < Held<DT>::kAhead; ++k) {
-    const int g = g0 + warp + k * Form<true>::kWarps;
-    if (g < g1 && g >= inner0 && g < inner1) {
-      const char* at = row.base + ((int64_t)g * kGroup + lane) * 16;
-      h.v[k] = load16(at);
-      h.w[k] = load16(at + 512);
+#pragma unroll 2
+  for (int g = g0 + warp; g < g1; g += Form<true>::kWarps) {
+    uint4* to = held + (g - g0) * kGroup + lane;
+    const int j = g * kGroup + lane;
+    if (g >= inner0 && g < inner1) {
+      const char* from = row.base + (int64_t)j * 16;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(whead_kv_impl::smem_u32(to)), "l"(from) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(whead_kv_impl::smem_u32(to + 32)), "l"(from + 512) : "memory");
+    } else {
+      to[0] = load_vector<DT>(row, j);
+      to[32] = load_vector<DT>(row, j + 32);
     }
   }
-#pragma unroll
-  for (int k = 0; k < Held<DT>::kAhead; ++k) {
-    const int g = g0 + warp + k * Form<true>::kWarps;
-    if (g >= g1) {
-      h.v[k] = h.w[k] = make_uint4(Type<DT>::kNone, Type<DT>::kNone, Type<DT>::kNone, Type<DT>::kNone);
-    } else if (g < inner0 || g >= inner1) {
-      h.v[k] = load_vector<DT>(row, g * kGroup + lane);
-      h.w[k] = load_vector<DT>(row, g * kGroup + 32 + lane);
-    }
-  }
+}
+template <typename F>
+__device__ __forceinline__ void over_held(int g0, int g1, const uint4* held, F f) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+  for (int g = g0 + warp; g < g1; g += Form<true>::kWarps) f(g, held[(g - g0) * kGroup + lane], held[(g - g0) * kGroup + 32 + lane]);
 }
 
 // Largest of a warp's values, NaN left out.
@@ -361,8 +360,8 @@ __device__ __forceinline__ Sums parts_joined(const Sums* part, int n, float c) {
   return Sums{top, __shfl_sync(~0u, p.s, 0), __shfl_sync(~0u, p.a, 0)};
 }
 
-// Runs of groups: CTA `rank` of `ctas` has groups run_begin(rank) .. run_begin(rank + 1) - 1.
-__device__ __forceinline__ int run_begin(int groups, int ctas, int rank) { return (int)((int64_t)groups * rank / ctas); }
+// Runs of groups: CTA `rank` of 1 << ctas_shift has groups run_begin(rank) .. run_begin(rank + 1) - 1.
+__device__ __forceinline__ int run_begin(int groups, int ctas_shift, int rank) { return (int)((unsigned)groups * (unsigned)rank >> ctas_shift); }
 
 // A cluster's CTAs write what they have into the first one's shared memory: once when all have started, and the first goes on when all
 // have written; the others need not wait for that.
@@ -395,30 +394,35 @@ inline bool good_temperature(double t) {
   return t > 0 && c > 1.2e-38 && c < 3.4e38;
 }
 
-// Whether rows go by CTAs that hold their part, and how many CTAs a row has.
+// Whether rows go by CTAs that hold their part, and how many CTAs a row has (a power of two), with most groups of a CTA.
 struct Division {
   bool held;
-  int ctas;
+  int shift, groups;
 };
 inline Division divide(int64_t rows, int64_t bytes, int sms) {
-  Division d{false, 1};
+  // groups of a row, with one more for its start anywhere, over 1 << shift CTAs
+  auto groups = [&](int shift) { return (int)(((bytes / (kGroup * 16) + 2) >> shift) + 1); };
+  auto room = [&](int shift, int ctas) { return (1 << shift) <= kMaxCluster && (rows << shift) <= (int64_t)sms * ctas; };
   // held: as many CTAs as the row needs, then more while the device has room for them, down to 8 KB each
-  int c = 1;
-  while (c < kMaxCluster && c * (Form<true>::kBytes - 2 * 1024) < bytes) c *= 2;
-  if (c * (Form<true>::kBytes - 2 * 1024) >= bytes && rows * c <= (int64_t)sms * Form<true>::kCtas) {
-    while (c < kMaxCluster && rows * c * 2 <= (int64_t)sms * Form<true>::kCtas && bytes / (2 * c) >= 8192) c *= 2;
-    return Division{true, c};
+  int s = 0;
+  while ((1 << s) < kMaxCluster && groups(s) > kHeldGroups) ++s;
+  if (groups(s) <= kHeldGroups && room(s, Form<true>::kCtas)) {
+    while (room(s + 1, Form<true>::kCtas) && bytes >> (s + 1) >= 8192) ++s;
+    return Division{true, s, groups(s)};
   }
-  while (d.ctas < kMaxCluster && rows * d.ctas * 2 <= (int64_t)sms * Form<false>::kCtas && bytes / (2 * d.ctas) >= 32768) d.ctas *= 2;
-  return d;
+  s = 0;
+  while (room(s + 1, Form<false>::kCtas) && bytes >> (s + 1) >= 32768) ++s;
+  return Division{false, s, groups(s)};
 }
+
+constexpr int kMaxDynamic = 98 * 1024;  // shared memory that a launch may ask for
 
 // A launch of `clusters` clusters of `ctas` CTAs, placed while the kernel before it in the stream still runs (it waits for its end).
 template <typename... P, typename... A>
 int launch_clusters(void (*kernel)(P...), int64_t clusters, int ctas, int threads, size_t smem, cudaStream_t stream, std::atomic<bool> (&granted)[kMaxDevices],
                     int device, A... args) {
   if (!granted[device].load(std::memory_order_relaxed)) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamic) != cudaSuccess) {
       (void)cudaGetLastError();
       return WHEAD_ERR_CUDA;
     }

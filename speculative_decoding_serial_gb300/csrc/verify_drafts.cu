@@ -31,7 +31,7 @@ struct VerifyArgs {
   int32_t* count;
   float2* stats;    // n x (gamma + 1) rows of the target, then n x gamma of the drafts: (largest, sum); at temperature 0 (token, -)
   int64_t target_stride_n, target_stride_t, draft_stride_n, draft_stride_t;
-  int V, gamma, ctas, target_dtype, draft_dtype;
+  int V, gamma, ctas_shift, held, target_dtype, draft_dtype;
   uint32_t step;
   int64_t n;
   float c, draft_c;              // log2(e) / T
@@ -55,17 +55,20 @@ struct RowShared {
 
 // Largest value and sum of a row, by a cluster.
 template <int DT, bool HELD>
-__device__ __forceinline__ void row_sums(const VerifyArgs& a, const Row& row, int rank, float c, float2* to, RowShared& s) {
+__device__ __forceinline__ void row_sums(const VerifyArgs& a, const Row& row, int rank, float c, float2* to, uint4* held, RowShared& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int groups = row_groups<DT>(row), g0 = run_begin(groups, a.ctas, rank), g1 = run_begin(groups, a.ctas, rank + 1);
-  if (a.ctas > 1) cluster_arrive();
+  const int groups = row_groups<DT>(row), ctas = 1 << a.ctas_shift, g0 = run_begin(groups, a.ctas_shift, rank), g1 = run_begin(groups, a.ctas_shift, rank + 1);
+  if (ctas > 1) cluster_arrive();  // before the loads: it waits for what is under way
+  if (HELD) hold_groups<DT>(row, g0, g1, held);
   Pass p;
   begin(p);
-  over_groups<DT, HELD>(row, g0, g1, [&](int, const uint4& v, const uint4& w) { take<DT, false>(p, v, w, fmaxf(largest<DT>(v), largest<DT>(w)), c); });
+  auto step = [&](int, const uint4& v, const uint4& w) { take<DT, false>(p, v, w, fmaxf(largest<DT>(v), largest<DT>(w)), c); };
+  if (HELD) over_held(g0, g1, held, step);
+  else over_groups<DT>(row, g0, g1, step);
   Sums q = warp_joined(p, c);
   if (lane == 0) s.part[warp] = q;
   __syncthreads();
-  if (a.ctas > 1) {
+  if (ctas > 1) {
     cluster_wait();
     if (warp == 0) {
       q = parts_joined(s.part, Form<HELD>::kWarps, c);
@@ -75,7 +78,7 @@ __device__ __forceinline__ void row_sums(const VerifyArgs& a, const Row& row, in
     cluster_arrive();
     if (rank != 0) return;
     cluster_wait();
-    if (warp == 0) q = parts_joined(s.cluster, a.ctas, c);
+    if (warp == 0) q = parts_joined(s.cluster, ctas, c);
   } else if (warp == 0) {
     q = parts_joined(s.part, Form<HELD>::kWarps, c);
   }
@@ -99,13 +102,14 @@ __device__ __forceinline__ First warp_first(First f) {
 // Token of a row's largest value, by a cluster: the first vector that holds it, then its place there. -1 where the row has NaN, +inf or
 // nothing but -inf.
 template <int DT, bool HELD>
-__device__ __forceinline__ void row_token(const VerifyArgs& a, const Row& row, int rank, float2* to, RowShared& s) {
+__device__ __forceinline__ void row_token(const VerifyArgs& a, const Row& row, int rank, float2* to, uint4* held, RowShared& s) {
   constexpr int N = Type<DT>::kPer, WARPS = Form<HELD>::kWarps;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int groups = row_groups<DT>(row), g0 = run_begin(groups, a.ctas, rank), g1 = run_begin(groups, a.ctas, rank + 1);
-  if (a.ctas > 1) cluster_arrive();
+  const int groups = row_groups<DT>(row), ctas = 1 << a.ctas_shift, g0 = run_begin(groups, a.ctas_shift, rank), g1 = run_begin(groups, a.ctas_shift, rank + 1);
+  if (ctas > 1) cluster_arrive();  // before the loads: it waits for what is under way
+  if (HELD) hold_groups<DT>(row, g0, g1, held);
   First f{-INFINITY, INT_MAX, 0};
-  over_groups<DT, HELD>(row, g0, g1, [&](int g, const uint4& v, const uint4& w) {
+  auto step = [&](int g, const uint4& v, const uint4& w) {
     const float first = largest_nan<DT>(v), high = max_nan(first, largest_nan<DT>(w));
     f.bad |= !(high < INFINITY);
     const int j = g * kGroup + (first == high ? lane : 32 + lane);
@@ -113,19 +117,21 @@ __device__ __forceinline__ void row_token(const VerifyArgs& a, const Row& row, i
       f.top = high;
       f.at = j;
     }
-  });
+  };
+  if (HELD) over_held(g0, g1, held, step);
+  else over_groups<DT>(row, g0, g1, step);
   f = warp_first(f);
   if (lane == 0) s.first[warp] = f;
   __syncthreads();
-  if (a.ctas > 1) cluster_wait();
+  if (ctas > 1) cluster_wait();
   if (warp == 0) f = warp_first(s.first[lane & (WARPS - 1)]);
-  if (a.ctas > 1) {
+  if (ctas > 1) {
     if (tid == 0) *in_first(&s.first_cluster[rank]) = f;
     __syncwarp();
     cluster_arrive();
     if (rank != 0) return;
     cluster_wait();
-    if (warp == 0) f = warp_first(s.first_cluster[lane < a.ctas ? lane : 0]);
+    if (warp == 0) f = warp_first(s.first_cluster[lane < ctas ? lane : 0]);
   }
   if (tid == 0) {
     int token = -1;
@@ -144,7 +150,8 @@ template <bool GREEDY, bool HELD>
 __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) verify_rows(const __grid_constant__ VerifyArgs a) {
   after_previous();
   __shared__ RowShared s;
-  const int r = blockIdx.x / a.ctas, rank = blockIdx.x - r * a.ctas;
+  extern __shared__ __align__(16) uint4 held[];
+  const int r = blockIdx.x >> a.ctas_shift, rank = blockIdx.x - (r << a.ctas_shift);
   const int targets = (int)a.n * (a.gamma + 1);
   const bool of_target = GREEDY || r < targets;
   const int each = of_target ? a.gamma + 1 : a.gamma, k = of_target ? r : r - targets;
@@ -158,8 +165,8 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) v
   auto go = [&](auto type) {
     constexpr int DT = decltype(type)::value;
     const Row row = row_at<DT>(p, at, a.V);
-    if constexpr (GREEDY) row_token<DT, HELD>(a, row, rank, to, s);
-    else row_sums<DT, HELD>(a, row, rank, c, to, s);
+    if constexpr (GREEDY) row_token<DT, HELD>(a, row, rank, to, held, s);
+    else row_sums<DT, HELD>(a, row, rank, c, to, held, s);
   };
   if (dtype == WHEAD_BF16) go(std::integral_constant<int, WHEAD_BF16>{});
   else if (dtype == WHEAD_F16) go(std::integral_constant<int, WHEAD_F16>{});
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
   after_previous();
   __shared__ DrawShared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int i = blockIdx.x / a.ctas, rank = blockIdx.x - i * a.ctas;
+  const int ctas = 1 << a.ctas_shift, i = blockIdx.x >> a.ctas_shift, rank = blockIdx.x & (ctas - 1);
   const int have = drafts_of(a, i);
   const float2* p_stats = a.stats + (int64_t)i * (a.gamma + 1);
   const float2* q_stats = a.stats + a.n * (a.gamma + 1) + (int64_t)i * a.gamma;
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
   bool whole = !rejected;  // draw from p itself
   for (int turn = 0; some && turn < 2; ++turn) {
     Best best{0.0f, 0.0f, -1, -1};
-    for (int g = rank * kDrawThreads + tid; g < (a.V + 3) / 4; g += a.ctas * kDrawThreads) {
+    for (int g = rank * kDrawThreads + tid; g < (a.V + 3) / 4; g += ctas * kDrawThreads) {
       float x[4], y[4];
       load_four_logits(a.target, p_at + 4 * g, a.target_dtype, p_wide, a.V - 4 * g, x);
       if (with_q && !whole) load_four_logits(a.draft, q_at + 4 * g, a.draft_dtype, q_wide, a.V - 4 * g, y);
@@ -308,11 +315,11 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
       add(best, s.part[w].k2, s.part[w].v2);
     }
     all = best;
-    if (a.ctas > 1) {
+    if (ctas > 1) {
       cg::cluster_group cluster = cg::this_cluster();
       if (tid == 0) s.mine[turn] = best;
       cluster.sync();
-      for (int k = 0; k < a.ctas; ++k) {
+      for (int k = 0; k < ctas; ++k) {
         if (k == rank) continue;
         const Best* y = cluster.map_shared_rank(&s.mine[turn], k);
         add(all, y->k1, y->v1);
@@ -324,7 +331,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
     if (all.v1 >= 0 || whole) break;
     whole = true;  // rounding left nothing of p - q
   }
-  if (a.ctas > 1) cg::this_cluster().sync();  // nobody reads this CTA's shared memory after it
+  if (ctas > 1) cg::this_cluster().sync();  // nobody reads this CTA's shared memory after it
   if (rank != 0) return;
   if (tid == 0) s.stay = all.v1;
   if (tid == 0 && all.v2 >= 0 && all.k1 - all.k2 <= kNear * all.k1) {
@@ -345,7 +352,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
 template <bool GREEDY, bool HELD>
 int launch_rows(const VerifyArgs& a, int64_t rows, int device, cudaStream_t stream) {
   static std::atomic<bool> granted[kMaxDevices];
-  return launch_clusters(verify_rows<GREEDY, HELD>, rows, a.ctas, Form<HELD>::kThreads, 0, stream, granted, device, a);
+  return launch_clusters(verify_rows<GREEDY, HELD>, rows, 1 << a.ctas_shift, Form<HELD>::kThreads, HELD ? a.held * kGroup * 16 : 0, stream, granted, device, a);
 }
 
 int launch(const VerifyArgs& from, int device, int sms, cudaStream_t stream) {
@@ -355,15 +362,16 @@ int launch(const VerifyArgs& from, int device, int sms, cudaStream_t stream) {
   const int64_t rows = a.n * (a.gamma + 1) + (greedy || !a.draft ? 0 : a.n * a.gamma);
   const int64_t bytes = (int64_t)a.V * std::max(dtype_size(a.target_dtype), a.draft ? dtype_size(a.draft_dtype) : 0);
   const Division d = divide(rows, bytes, sms);
-  a.ctas = d.ctas;
+  a.ctas_shift = d.shift;
+  a.held = d.groups;
   int rc;
   if (greedy) rc = d.held ? launch_rows<true, true>(a, rows, device, stream) : launch_rows<true, false>(a, rows, device, stream);
   else rc = d.held ? launch_rows<false, true>(a, rows, device, stream) : launch_rows<false, false>(a, rows, device, stream);
   if (rc != WHEAD_OK) return rc;
   if (greedy) return whead_kv_impl::launch_after(verify_greedy, dim3((unsigned)a.n), 32, 0, stream, a);
-  a.ctas = 1;
-  while (a.ctas < kMaxCluster && a.n * a.ctas * 2 <= (int64_t)sms * 3 && a.V / (2 * a.ctas) >= 4 * kDrawThreads) a.ctas *= 2;
-  return launch_clusters(verify_draw, a.n, a.ctas, kDrawThreads, 0, stream, granted, device, a);
+  a.ctas_shift = 0;
+  while ((2 << a.ctas_shift) <= kMaxCluster && a.n << (a.ctas_shift + 1) <= (int64_t)sms * 3 && a.V >> (a.ctas_shift + 1) >= 4 * kDrawThreads) ++a.ctas_shift;
+  return launch_clusters(verify_draw, a.n, 1 << a.ctas_shift, kDrawThreads, 0, stream, granted, device, a);
 }
 
 }  // namespace

@@ -21,7 +21,7 @@ namespace whead_verify_impl {
 namespace {
 
 constexpr int kMaxRuns = 4224;  // largest values kept by a CTA: of groups, or of runs of 2^shift groups in rows of more (2^24 logits: shift 4)
-constexpr int kCandidates = 512, kListed = 128, kSubs = 64;
+constexpr int kListed = 128, kVectors = 96, kCandidates = kVectors * 8, kSubs = 64;
 
 struct LogprobArgs {
   const void* logits;
@@ -32,9 +32,8 @@ struct LogprobArgs {
   int32_t* top_tokens;
   float* top_logprobs;
   int64_t stride_n, stride_t;
-  int t, V, top, ctas, shift, runs;  // runs: room for largest values
-  float c;
-  double inverse;  // 1 / T
+  int t, V, top, ctas_shift, shift, runs, held;  // runs: room for largest values; held: for groups
+  float c, inverse, inverse_low;                 // log2(e) / T, 1 / T, and what that was rounded by
 };
 
 struct RowShared {
@@ -43,16 +42,18 @@ struct RowShared {
 };
 struct TopShared {
   uint32_t bound;
-  int found, listed;                                    // candidates, groups
+  int found, listed, vectors;                                       // candidates, groups and vectors that reach the bound
   int list[kListed];
-  uint32_t sub[kSubs];                                  // largest values of the CTA's parts
-  unsigned long long candidate[kCandidates];            // key, then the complement of the token
-  unsigned long long best[kMaxCluster * WHEAD_MAX_TOP]; // each CTA's, in order; 0: none
-  // the way for rows whose candidates are too many
-  int picked;                                           // what pick() found: how many keys, their indexes
+  alignas(16) uint32_t sub[kSubs];                                  // largest values of the CTA's parts
+  uint4 vector[kVectors];
+  int vector_at[kVectors];
+  alignas(16) unsigned long long candidate[kCandidates];            // key, then the complement of the token
+  alignas(16) unsigned long long best[kMaxCluster * WHEAD_MAX_TOP]; // each CTA's, in order; 0: none
+  // the way for rows where too many values reach the bound
+  int picked;                                                       // what pick() found: how many keys, their indexes
   int order[WHEAD_MAX_TOP];
   int group[WHEAD_MAX_TOP];
-  uint32_t key[WHEAD_MAX_TOP * kGroup];                 // largest values of the picked groups' vectors, or of the picked runs' groups
+  uint32_t key[WHEAD_MAX_TOP * kGroup];                             // largest values of the picked groups' vectors, or of the picked runs' groups
 };
 struct Nothing {};
 
@@ -91,18 +92,34 @@ __device__ uint32_t pick(const uint32_t* keys, int n, int top, int* list, int* p
   return bound;
 }
 
-template <int DT>
-__device__ __forceinline__ void offer(TopShared& s, const uint4& raw, int j, const Row& row, uint32_t bound) {
-  constexpr int N = Type<DT>::kPer;
-  float x[N];
-  values_of<DT>(raw, x);
+// How many of n numbers in shared memory are greater.
+__device__ __forceinline__ int greater(const unsigned long long* x, int n, unsigned long long than) {
+  int count = 0, k = 0;
+  for (; k + 8 <= n; k += 8) {
+    ulonglong2 y[4];
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const uint32_t key = key_of<DT>(x[k]);
-    if (key >= bound) {
-      const int at = atomicAdd(&s.found, 1);
-      if (at < kCandidates) s.candidate[at] = (unsigned long long)key << 32 | (uint32_t)~(uint32_t)(j * N + k - row.off);
-    }
+    for (int i = 0; i < 4; ++i) y[i] = *reinterpret_cast<const ulonglong2*>(x + k + 2 * i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) count += (y[i].x > than) + (y[i].y > than);
+  }
+  for (; k < n; ++k) count += x[k] > than;
+  return count;
+}
+
+// Value e of vectors in shared memory.
+template <int DT>
+__device__ __forceinline__ float shared_one(const uint4* v, int e) {
+  if constexpr (DT == WHEAD_F32) return reinterpret_cast<const float*>(v)[e];
+  const unsigned short b = reinterpret_cast<const unsigned short*>(v)[e];
+  return DT == WHEAD_BF16 ? __uint_as_float((uint32_t)b << 16) : __half2float(__ushort_as_half(b));
+}
+
+// Keeps a vector, if there is room.
+__device__ __forceinline__ void keep(TopShared& s, const uint4& raw, int j) {
+  const int at = atomicAdd(&s.vectors, 1);
+  if (at < kVectors) {
+    s.vector[at] = raw;
+    s.vector_at[at] = j;
   }
 }
 
@@ -140,13 +157,14 @@ __device__ __noinline__ void pick_candidates(TopShared& s, const uint32_t* runs,
   }
   const int picked = s.picked;
   for (int e = tid; e < picked * kGroup; e += THREADS) s.key[e] = key_at(s.group[e / kGroup] * kGroup + e % kGroup);
-  if (tid == 0) s.found = 0;
+  if (tid == 0) s.vectors = 0;
   __syncthreads();
   choose(s.key, picked * kGroup);
   if (tid < s.picked) {
     const int j = s.group[s.order[tid] / kGroup] * kGroup + s.order[tid] % kGroup;
-    offer<DT>(s, load_vector<DT>(row, j), j, row, max(s.bound, Type<DT>::kNoneKey + 1));
+    keep(s, load_vector<DT>(row, j), j);
   }
+  if (tid == 0) s.bound = max(s.bound, Type<DT>::kNoneKey + 1);
   __syncthreads();
 }
 
@@ -156,51 +174,45 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
   constexpr int THREADS = Form<HELD>::kThreads, WARPS = THREADS / 32;
   __shared__ RowShared s;
   __shared__ std::conditional_t<TOP, TopShared, Nothing> top_shared;
-  extern __shared__ uint32_t runs[];
+  extern __shared__ __align__(16) uint4 held[];
+  uint32_t* runs = reinterpret_cast<uint32_t*>(held + (HELD ? a.held * kGroup : 0));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int r = blockIdx.x / a.ctas, rank = blockIdx.x - r * a.ctas;
-  const int i = r / a.t, t = r - i * a.t;
+  const int r = blockIdx.x >> a.ctas_shift, ctas = 1 << a.ctas_shift, rank = blockIdx.x & (ctas - 1);
+  const int i = a.t == 1 ? r : r / a.t, t = r - i * a.t;
   const int64_t at = i * a.stride_n + t * a.stride_t;
   const Row row = row_at<DT>(a.logits, at, a.V);
-  const int groups = row_groups<DT>(row), g0 = run_begin(groups, a.ctas, rank), g1 = run_begin(groups, a.ctas, rank + 1);
+  const int groups = row_groups<DT>(row), g0 = run_begin(groups, a.ctas_shift, rank), g1 = run_begin(groups, a.ctas_shift, rank + 1);
   const int n_runs = g1 > g0 ? ((g1 - 1) >> a.shift) - (g0 >> a.shift) + 1 : 0;
-  Held<DT> held;
-  if (HELD) hold_groups<DT>(row, g0, g1, held);
   if constexpr (TOP) {
+    if (tid == 0) {
+      top_shared.found = top_shared.listed = top_shared.vectors = 0;
+      top_shared.bound = ~0u;
+    }
+    if (tid < kMaxCluster * WHEAD_MAX_TOP) top_shared.best[tid] = 0;
     if (!HELD && a.shift) {
       for (int k = tid; k < n_runs; k += THREADS) runs[k] = 0;
+      __syncthreads();
     }
-    if (tid == 0) top_shared.found = top_shared.listed = 0;
-    if (tid < kMaxCluster * WHEAD_MAX_TOP) top_shared.best[tid] = 0;
-    __syncthreads();
   }
-  if (a.ctas > 1) cluster_arrive();
-  float x_token = -INFINITY;
-  if (rank == 0 && a.tokens) {
-    const int token = __ldg(a.tokens + r);
-    if ((unsigned)token < (unsigned)a.V) x_token = load_one(a.logits, at + token, DT);
-  }
+  if (ctas > 1) cluster_arrive();  // before the loads: it waits for what is under way
+  if (HELD) hold_groups<DT>(row, g0, g1, held);
+  const int token = rank == 0 && a.tokens ? __ldg(a.tokens + r) : -1;
   // ---- the pass
   Pass p;
   begin(p);
   auto step = [&](int g, const uint4& v, const uint4& w) {
     const float high = fmaxf(largest<DT>(v), largest<DT>(w));
     take<DT, true>(p, v, w, high, a.c);
-    if (TOP && !HELD) {
+    if (TOP) {
       const float most = warp_max(high);
       if (lane == 0) {
-        if (a.shift) atomicMax(&runs[(g >> a.shift) - (g0 >> a.shift)], key_of<DT>(most));
+        if (!HELD && a.shift) atomicMax(&runs[(g >> a.shift) - (g0 >> a.shift)], key_of<DT>(most));
         else runs[g - g0] = key_of<DT>(most);
       }
     }
   };
-  if constexpr (HELD) {
-#pragma unroll
-    for (int k = 0; k < Held<DT>::kAhead; ++k)
-      if (g0 + warp + k * WARPS < g1) step(0, held.v[k], held.w[k]);
-  } else {
-    over_groups<DT, false>(row, g0, g1, step);
-  }
+  if (HELD) over_held(g0, g1, held, step);
+  else over_groups<DT>(row, g0, g1, step);
   {
     const Sums w = warp_joined(p, a.c);
     if (lane == 0) s.part[warp] = w;
@@ -214,73 +226,68 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
   }
   __syncthreads();
   // ---- the CTA's best tokens
-  unsigned long long* best = nullptr;
   if constexpr (TOP) {
     TopShared& ts = top_shared;
     // The CTA's values are in kSubs parts. The `top`-th of their largest values is one that `top` values reach, and on rows
-    // without an order few more do.
+    // without an order few more do. It is the lowest that fewer than `top` are greater than.
     if (tid < kSubs) {
       const uint32_t mine = ts.sub[tid];
       int before = 0;
-#pragma unroll 16
-      for (int k = 0; k < kSubs; ++k) before += ts.sub[k] > mine || (ts.sub[k] == mine && k < tid);
-      if (before == a.top - 1) ts.bound = max(mine, Type<DT>::kNoneKey + 1);
+#pragma unroll
+      for (int k = 0; k < kSubs; k += 4) {
+        const uint4 y = *reinterpret_cast<const uint4*>(ts.sub + k);
+        before += (y.x > mine) + (y.y > mine) + (y.z > mine) + (y.w > mine);
+      }
+      const uint32_t low = __reduce_min_sync(~0u, before < a.top ? mine : ~0u);
+      if (lane == 0) atomicMin(&ts.bound, low);
     }
     __syncthreads();
-    const uint32_t bound = ts.bound;
-    if constexpr (HELD) {
-#pragma unroll
-      for (int k = 0; k < Held<DT>::kAhead; ++k) {
-        const int j = (g0 + warp + k * WARPS) * kGroup + lane;
-        if (key_of<DT>(largest<DT>(held.v[k])) >= bound) offer<DT>(ts, held.v[k], j, row, bound);
-        if (key_of<DT>(largest<DT>(held.w[k])) >= bound) offer<DT>(ts, held.w[k], j + 32, row, bound);
+    uint32_t bound = max(ts.bound, Type<DT>::kNoneKey + 1);
+    float least = value_of<DT>(bound);
+    // the groups that reach it, and of those the vectors
+    for (int k = tid; k < n_runs; k += THREADS)
+      if (runs[k] >= bound) {
+        const int place = atomicAdd(&ts.listed, 1);
+        if (place < kListed) ts.list[place] = k;
       }
-    } else {
-      for (int k = tid; k < n_runs; k += THREADS)
-        if (runs[k] >= bound) {
-          const int place = atomicAdd(&ts.listed, 1);
-          if (place < kListed) ts.list[place] = k;
-        }
-      __syncthreads();
-      const int listed = ts.listed << a.shift;
-      if (ts.listed <= kListed) {
-        for (int e = warp; e < 2 * listed; e += WARPS) {
-          const int g = (((g0 >> a.shift) + ts.list[e / 2 >> a.shift]) << a.shift) + (e / 2 & ((1 << a.shift) - 1)), j = g * kGroup + e % 2 * 32 + lane;
-          if (g < g0 || g >= g1) continue;
-          const uint4 raw = load_vector<DT>(row, j);
-          if (key_of<DT>(largest<DT>(raw)) >= bound) offer<DT>(ts, raw, j, row, bound);
-        }
+    __syncthreads();
+    const int listed = ts.listed <= kListed ? ts.listed << a.shift : 0;
+#pragma unroll 4
+    for (int e = warp; e < 2 * listed; e += WARPS) {
+      const int g = (((g0 >> a.shift) + ts.list[e / 2 >> a.shift]) << a.shift) + (e / 2 & ((1 << a.shift) - 1)), j = g * kGroup + e % 2 * 32 + lane;
+      if (g >= g0 && g < g1) {
+        const uint4 raw = HELD ? held[j - g0 * kGroup] : load_vector<DT>(row, j);
+        if (largest<DT>(raw) >= least) keep(ts, raw, j);
       }
     }
     __syncthreads();
-    if (ts.found > kCandidates || ts.listed > kListed) {
-      if constexpr (HELD) {
-#pragma unroll
-        for (int k = 0; k < Held<DT>::kAhead; ++k) {
-          const float most = warp_max(fmaxf(largest<DT>(held.v[k]), largest<DT>(held.w[k])));
-          if (lane == 0 && g0 + warp + k * WARPS < g1) runs[warp + k * WARPS] = key_of<DT>(most);
-        }
-        __syncthreads();
-      }
+    if (ts.vectors > kVectors || ts.listed > kListed) {
       pick_candidates<DT, THREADS>(ts, runs, n_runs, g0, g1, a.shift, a.top, row);
+      least = value_of<DT>(ts.bound);
     }
+    // their values that reach it
+    constexpr int N = Type<DT>::kPer;
+    for (int e = tid; e < ts.vectors * N; e += THREADS) {
+      const float x = shared_one<DT>(ts.vector, e);
+      if (x >= least) ts.candidate[atomicAdd(&ts.found, 1)] = (unsigned long long)key_of<DT>(x) << 32 | (uint32_t)~(uint32_t)(ts.vector_at[e / N] * N + e % N - row.off);
+    }
+    __syncthreads();
+    if (ctas > 1) cluster_wait();  // all have started
     // ranked by counting those that come before
-    if (a.ctas > 1) cluster_wait();  // all have started
-    best = a.ctas > 1 ? in_first(ts.best) + rank * a.top : ts.best;
+    unsigned long long* best = ctas > 1 ? in_first(ts.best) + rank * a.top : ts.best;
     const int found = ts.found;
     for (int e = tid; e < found; e += THREADS) {
       const unsigned long long mine = ts.candidate[e];
-      int before = 0;
-#pragma unroll 4
-      for (int k = 0; k < found; ++k) before += ts.candidate[k] > mine;
+      const int before = greater(ts.candidate, found, mine);
       if (before < a.top) best[before] = mine;
     }
-  } else if (a.ctas > 1) {
+  } else if (ctas > 1) {
     cluster_wait();
   }
   // ---- the cluster's parts, in its first CTA
+  const float x_token = (unsigned)token < (unsigned)a.V ? load_one(a.logits, at + token, DT) : -INFINITY;
   Sums sums;
-  if (a.ctas > 1) {
+  if (ctas > 1) {
     if (warp == 0) {
       sums = parts_joined(s.part, WARPS, a.c);
       if (lane == 0) *in_first(&s.cluster[rank]) = sums;
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
     cluster_arrive();
     if (rank != 0) return;
     cluster_wait();
-    sums = parts_joined(s.cluster, a.ctas, a.c);
+    sums = parts_joined(s.cluster, ctas, a.c);
   } else {
     if (TOP) __syncthreads();
     sums = parts_joined(s.part, WARPS, a.c);
@@ -300,25 +307,21 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
     if (bad) return sums.s;
     if (none || x == -INFINITY) return -INFINITY;
     // a token at the type's lowest value keeps its finite log probability
-    return plain(k) && plain(x * a.c) ? (__fmaf_rn(x, a.c, -k) - log_s) * kLn2 : (x - top) * (float)a.inverse - log_s * kLn2;
+    return plain(k) && plain(x * a.c) ? (__fmaf_rn(x, a.c, -k) - log_s) * kLn2 : (x - top) * a.inverse - log_s * kLn2;
   };
-  if (tid == 0) {
+  if (tid == THREADS - 32) {  // not the warps that write alternatives
     // m / T itself, and what k was rounded by
     const float off = plain(k) ? __fmaf_rn(top, a.c, -k) : 0.0f;
-    if (a.lse) a.lse[r] = bad ? sums.s : none ? -INFINITY : (float)(top * a.inverse) + (log_s - off) * kLn2;
-    if (a.entropy) a.entropy[r] = bad ? sums.s : none ? 0.0f : fmaxf((log_s - sums.a / sums.s) * kLn2, 0.0f);
+    if (a.lse) a.lse[r] = bad ? sums.s : none ? -INFINITY : plain(k) ? __fmaf_rn(top, a.inverse, __fmaf_rn(top, a.inverse_low, (log_s - off) * kLn2)) : top * a.inverse + log_s * kLn2;
+    if (a.entropy) a.entropy[r] = bad ? sums.s : none ? 0.0f : fmaxf((log_s - __fdividef(sums.a, sums.s)) * kLn2, 0.0f);
     if (a.logprob) a.logprob[r] = log_p(x_token);
   }
   if constexpr (TOP) {
     TopShared& ts = top_shared;
-    const int n = a.ctas * a.top;  // at most a place a thread
+    const int n = ctas * a.top;  // at most a place a thread
     const unsigned long long mine = tid < n && !bad ? ts.best[tid] : 0ull;
     int before = tid;
-    if (a.ctas > 1 && tid < n) {
-      before = 0;
-#pragma unroll 4
-      for (int e = 0; e < n; ++e) before += ts.best[e] > mine;
-    }
+    if (ctas > 1 && mine != 0) before = greater(ts.best, n, mine);
     const int live = __syncthreads_count(mine != 0);
     int32_t* tokens = a.top_tokens + (int64_t)r * a.top;
     float* values = a.top_logprobs + (int64_t)r * a.top;
@@ -336,7 +339,7 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
 template <int DT, bool TOP, bool HELD>
 int launch(const LogprobArgs& a, int64_t rows, int device, cudaStream_t stream) {
   static std::atomic<bool> granted[kMaxDevices];
-  return launch_clusters(logprobs_rows<DT, TOP, HELD>, rows, a.ctas, Form<HELD>::kThreads, TOP ? a.runs * 4 : 0, stream, granted, device, a);
+  return launch_clusters(logprobs_rows<DT, TOP, HELD>, rows, 1 << a.ctas_shift, Form<HELD>::kThreads, (HELD ? a.held * kGroup * 16 : 0) + (TOP ? a.runs * 4 : 0), stream, granted, device, a);
 }
 template <int DT>
 int launch(const LogprobArgs& a, bool held, int64_t rows, int device, cudaStream_t stream) {
@@ -377,15 +380,14 @@ extern "C" int whead_logprobs(const whead_logprobs_args* x) {
   a.t = (int)x->t;
   a.V = (int)x->V;
   a.top = x->top;
-  a.inverse = 1.0 / x->temperature;
+  a.inverse = (float)(1.0 / x->temperature);
+  a.inverse_low = (float)(1.0 / x->temperature - a.inverse);
   a.c = (float)(1.4426950408889634 / x->temperature);
-  const int64_t bytes = x->V * dtype_size(x->dtype);
-  const Division d = divide(rows, bytes, sms);
-  a.ctas = d.ctas;
-  // most groups of a CTA: a row's, one more for its start anywhere, over the CTAs
-  const int most = (int)((bytes / (kGroup * 16) + 2) / a.ctas + 1);
-  while (((most >> a.shift) + 2) > kMaxRuns) ++a.shift;
-  a.runs = (most >> a.shift) + 2;
+  const Division d = divide(rows, x->V * dtype_size(x->dtype), sms);
+  a.ctas_shift = d.shift;
+  a.held = d.groups;
+  while (((d.groups >> a.shift) + 2) > kMaxRuns) ++a.shift;
+  a.runs = (d.groups >> a.shift) + 2;
   cudaStream_t stream = static_cast<cudaStream_t>(x->stream);
   switch (x->dtype) {
     case WHEAD_BF16: return launch<WHEAD_BF16>(a, d.held, rows, device, stream);
