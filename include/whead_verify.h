@@ -58,7 +58,7 @@ typedef struct {
   int32_t* said;           /* n x (gamma + 1): the drafts that stay, the token after them, -1 for the rest */
   int32_t* count;          /* n: 1 + how many drafts stay */
   int64_t target_stride_n, target_stride_t, draft_stride_n, draft_stride_t;
-  int64_t n;               /* n * (2 gamma + 1) < 2^27 */
+  int64_t n;               /* n * (2 gamma + 2) < 2^27 */
   int64_t V;               /* 1 <= V < 2^24 */
   int32_t gamma;           /* 0..WHEAD_MAX_DRAFTS */
   int32_t target_dtype, draft_dtype;

@@ -345,11 +345,10 @@ __device__ __forceinline__ Sums warp_joined(const Pass& p, float c) {
   }
   return r;
 }
-// Of n <= 16 parts, whose references are their largest values, by a warp; every lane gets them.
-__device__ __forceinline__ Sums parts_joined(const Sums* part, int n, float c) {
+// Of n <= 16 parts, whose references are their largest values and of which lane k < n has the k-th, by a warp; every lane gets them.
+__device__ __forceinline__ Sums parts_joined(Sums p, int n, float c) {
   const int lane = threadIdx.x & 31;
-  Sums p = part[min(lane, n - 1)];
-  const float top = warp_max(p.ref);
+  const float top = warp_max(lane < n ? p.ref : -INFINITY);
   if (lane >= n) p.s = p.a = 0.0f;
   p = moved(p, top, c);
 #pragma unroll

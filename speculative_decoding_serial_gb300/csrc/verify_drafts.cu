@@ -1,9 +1,13 @@
 // verify_drafts.cu — which drafts stay under the target's logits, and the token after them.
 //
-// Two kernels. The first takes every row of logits once: at temperature 0 its largest value's token, else its largest value and its sum of
-// exponentials. The second, a cluster an entry, finds the first draft that does not stay and draws the token of that row: the largest of
-// r_v / E_v with r = max(p - q, 0), E = -log U. Since E >= 1 - U, only a token with r_v / (1 - U) above the best so far needs its
-// logarithm; 1 - U is known exactly from the word.
+// Two kernels. The first takes rows of logits: at temperature 0 their largest value's token, else their largest value and sum of
+// exponentials, a CTA a part of a row. The second, for each entry, joins the parts, finds the first draft that does not stay and draws the
+// token of that row: the largest of r_v / E_v with r = max(p - q, 0), E = -log U. Since E >= 1 - U, only a token with r_v / (1 - U)
+// above the best so far needs its logarithm; 1 - U is known exactly from the word.
+//
+// Rows after the first draft that does not stay are not needed. Where there are more rows than the device takes at once, CTAs come in the order of
+// the drafts' places, whoever finishes a place decides on its draft, and parts of later places that find theirs decided return
+// at once. Results do not depend on how many do: whoever decides joins the same parts in the same order.
 //
 // What is near a border is settled in fp64: a draft whose U q and p differ by less than 2^-16 of p, and the two best tokens where they do.
 #include "verify_common.cuh"
@@ -12,15 +16,15 @@
 #include <atomic>
 #include <climits>
 #include <cmath>
+#include <type_traits>
 
 namespace whead_verify_impl {
 
 namespace {
 
-namespace cg = cooperative_groups;
-
 constexpr float kNear = 0x1p-16f;
 constexpr int kDrawThreads = 512, kDrawWarps = kDrawThreads / 32;
+constexpr int kMaxParts = 16;  // of a row
 
 struct VerifyArgs {
   const void* target;
@@ -29,62 +33,75 @@ struct VerifyArgs {
   const int32_t* drafted;
   int32_t* said;
   int32_t* count;
-  float2* stats;    // n x (gamma + 1) rows of the target, then n x gamma of the drafts: (largest, sum); at temperature 0 (token, -)
+  float2* parts;     // n x (gamma + 1) x (target, draft) x parts: (largest, sum); at temperature 0 (largest or NaN, token)
+  int32_t* first;    // n: the first place whose draft is known not to stay; NULL: all rows are taken
+  int32_t* arrived;  // n x (gamma + 1): parts of a place that are done
   int64_t target_stride_n, target_stride_t, draft_stride_n, draft_stride_t;
-  int V, gamma, ctas_shift, held, target_dtype, draft_dtype;
+  int V, gamma, n, parts_shift, ctas_shift, held, target_dtype, draft_dtype;
   uint32_t step;
-  int64_t n;
   float c, draft_c;              // log2(e) / T
   double inverse, draft_inverse; // 1 / T
   uint64_t seed;
 };
 
 __device__ __forceinline__ int drafts_of(const VerifyArgs& a, int i) { return a.drafted ? min(max(__ldg(a.drafted + i), 0), a.gamma) : a.gamma; }
+__device__ __forceinline__ float2* parts_of(const VerifyArgs& a, int i, int t, int of_draft) {
+  return a.parts + ((((int64_t)i * (a.gamma + 1) + t) * 2 + of_draft) << a.parts_shift);
+}
+__device__ __forceinline__ float uniform(uint32_t w) { return ((float)(w >> 9) + 0.5f) * 0x1p-23f; }
 
-// A part of a row's first largest value: the vector that holds it, and whether the part has NaN or +inf.
+// A row's largest value and sum, by a warp, from its parts; every lane gets them.
+__device__ __forceinline__ float2 row_sums(const VerifyArgs& a, int i, int t, int of_draft) {
+  const int lane = threadIdx.x & 31, n = 1 << a.parts_shift;
+  const float2 x = __ldcg(parts_of(a, i, t, of_draft) + min(lane, n - 1));
+  const Sums s = parts_joined(Sums{x.x, x.y, 0.0f}, n, of_draft ? a.draft_c : a.c);
+  return make_float2(s.ref, s.s);
+}
+// Whether a row has a distribution.
+__device__ __forceinline__ bool sound(float2 x) { return x.y > 0.0f && x.y < INFINITY; }
+
+// The token of a row's largest value, from its parts; -1 where the row has NaN, +inf or nothing but -inf.
+__device__ __forceinline__ int row_token(const VerifyArgs& a, int i, int t) {
+  const float2* part = parts_of(a, i, t, 0);
+  float top = -INFINITY;
+  int token = -1;
+  bool bad = false;
+  for (int k = 0; k < 1 << a.parts_shift; ++k) {
+    const float2 x = __ldcg(part + k);
+    bad |= !(x.x < INFINITY);
+    if (x.x > top) {
+      top = x.x;
+      token = __float_as_int(x.y);
+    }
+  }
+  return bad ? -1 : token;
+}
+
+// Whether draft t stays, given that all before it do.
+__device__ __forceinline__ bool draft_stays(const VerifyArgs& a, int i, int t, int x, float2 ps, float2 qs) {
+  if ((unsigned)x >= (unsigned)a.V || !sound(ps) || !sound(qs)) return false;
+  const float xp = load_one(a.target, i * a.target_stride_n + t * a.target_stride_t + x, a.target_dtype);
+  const float xq = a.draft ? load_one(a.draft, i * a.draft_stride_n + t * a.draft_stride_t + x, a.draft_dtype) : 0.0f;
+  const float u = uniform(philox(make_uint4(0u, a.step + t, (uint32_t)i, 2u), a.seed).x);
+  const float p = ex2((xp - ps.x) * a.c) / ps.y, q = a.draft ? ex2((xq - qs.x) * a.draft_c) / qs.y : 1.0f;
+  if (fabsf(u * q - p) > kNear * p && p >= 1e-30f) return u * q < p;
+  const double dp = exp(((double)xp - ps.x) * a.inverse) / ps.y, dq = a.draft ? exp(((double)xq - qs.x) * a.draft_inverse) / qs.y : 1.0;
+  return u * dq < dp;
+}
+
+// Values for `first` and `arrived` before the rows.
+__global__ void __launch_bounds__(256) verify_begin(const __grid_constant__ VerifyArgs a) {
+  after_previous();
+  const int k = blockIdx.x * 256 + threadIdx.x;
+  if (k < a.n) a.first[k] = INT_MAX;
+  if (k < a.n * (a.gamma + 1)) a.arrived[k] = 0;
+}
+
+// A part of a row's first largest value: its vector, and whether the part has NaN or +inf.
 struct First {
   float top;
   int at, bad;
 };
-struct RowShared {
-  Sums part[16];
-  Sums cluster[kMaxCluster];
-  First first[16];
-  First first_cluster[kMaxCluster];
-};
-
-// Largest value and sum of a row, by a cluster.
-template <int DT, bool HELD>
-__device__ __forceinline__ void row_sums(const VerifyArgs& a, const Row& row, int rank, float c, float2* to, uint4* held, RowShared& s) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int groups = row_groups<DT>(row), ctas = 1 << a.ctas_shift, g0 = run_begin(groups, a.ctas_shift, rank), g1 = run_begin(groups, a.ctas_shift, rank + 1);
-  if (ctas > 1) cluster_arrive();  // before the loads: it waits for what is under way
-  if (HELD) hold_groups<DT>(row, g0, g1, held);
-  Pass p;
-  begin(p);
-  auto step = [&](int, const uint4& v, const uint4& w) { take<DT, false>(p, v, w, fmaxf(largest<DT>(v), largest<DT>(w)), c); };
-  if (HELD) over_held(g0, g1, held, step);
-  else over_groups<DT>(row, g0, g1, step);
-  Sums q = warp_joined(p, c);
-  if (lane == 0) s.part[warp] = q;
-  __syncthreads();
-  if (ctas > 1) {
-    cluster_wait();
-    if (warp == 0) {
-      q = parts_joined(s.part, Form<HELD>::kWarps, c);
-      if (lane == 0) *in_first(&s.cluster[rank]) = q;
-    }
-    __syncwarp();
-    cluster_arrive();
-    if (rank != 0) return;
-    cluster_wait();
-    if (warp == 0) q = parts_joined(s.cluster, ctas, c);
-  } else if (warp == 0) {
-    q = parts_joined(s.part, Form<HELD>::kWarps, c);
-  }
-  if (tid == 0) *to = make_float2(q.ref, q.s);
-}
-
 __device__ __forceinline__ First warp_first(First f) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
@@ -99,50 +116,58 @@ __device__ __forceinline__ First warp_first(First f) {
   return f;
 }
 
-// Token of a row's largest value, by a cluster: the first vector that holds it, then its place there. -1 where the row has NaN, +inf or
-// nothing but -inf.
-template <int DT, bool HELD>
-__device__ __forceinline__ void row_token(const VerifyArgs& a, const Row& row, int rank, float2* to, uint4* held, RowShared& s) {
+struct RowShared {
+  Sums part[16];
+  First first[16];
+  int last;
+};
+
+// One part of a row by a CTA; its first thread gets what `parts` holds.
+template <int DT, bool GREEDY, bool HELD>
+__device__ __forceinline__ float2 row_part(const VerifyArgs& a, const Row& row, int part, float c, uint4* held, RowShared& s) {
   constexpr int N = Type<DT>::kPer, WARPS = Form<HELD>::kWarps;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int groups = row_groups<DT>(row), ctas = 1 << a.ctas_shift, g0 = run_begin(groups, a.ctas_shift, rank), g1 = run_begin(groups, a.ctas_shift, rank + 1);
-  if (ctas > 1) cluster_arrive();  // before the loads: it waits for what is under way
+  const int groups = row_groups<DT>(row), g0 = run_begin(groups, a.parts_shift, part), g1 = run_begin(groups, a.parts_shift, part + 1);
   if (HELD) hold_groups<DT>(row, g0, g1, held);
-  First f{-INFINITY, INT_MAX, 0};
-  auto step = [&](int g, const uint4& v, const uint4& w) {
-    const float first = largest_nan<DT>(v), high = max_nan(first, largest_nan<DT>(w));
-    f.bad |= !(high < INFINITY);
-    const int j = g * kGroup + (first == high ? lane : 32 + lane);
-    if (high > f.top || (high == f.top && j < f.at)) {  // a row's first group may come last
-      f.top = high;
-      f.at = j;
-    }
-  };
-  if (HELD) over_held(g0, g1, held, step);
-  else over_groups<DT>(row, g0, g1, step);
-  f = warp_first(f);
-  if (lane == 0) s.first[warp] = f;
-  __syncthreads();
-  if (ctas > 1) cluster_wait();
-  if (warp == 0) f = warp_first(s.first[lane & (WARPS - 1)]);
-  if (ctas > 1) {
-    if (tid == 0) *in_first(&s.first_cluster[rank]) = f;
-    __syncwarp();
-    cluster_arrive();
-    if (rank != 0) return;
-    cluster_wait();
-    if (warp == 0) f = warp_first(s.first_cluster[lane < ctas ? lane : 0]);
-  }
-  if (tid == 0) {
+  if constexpr (GREEDY) {
+    First f{-INFINITY, INT_MAX, 0};
+    auto step = [&](int g, const uint4& v, const uint4& w) {
+      const float first = largest_nan<DT>(v), high = max_nan(first, largest_nan<DT>(w));
+      f.bad |= !(high < INFINITY);
+      const int j = g * kGroup + (first == high ? lane : 32 + lane);
+      if (high > f.top || (high == f.top && j < f.at)) {  // a row's first group may come last
+        f.top = high;
+        f.at = j;
+      }
+    };
+    if (HELD) over_held(g0, g1, held, step);
+    else over_groups<DT>(row, g0, g1, step);
+    f = warp_first(f);
+    if (lane == 0) s.first[warp] = f;
+    __syncthreads();
+    if (warp != 0) return make_float2(0.0f, 0.0f);
+    f = warp_first(s.first[lane & (WARPS - 1)]);
     int token = -1;
-    if (!f.bad && f.top > -INFINITY) {
+    if (lane == 0 && !f.bad && f.top > -INFINITY) {
       float x[N];
       values_of<DT>(load_vector<DT>(row, f.at), x);
 #pragma unroll
       for (int k = N - 1; k >= 0; --k)
         if (x[k] == f.top) token = f.at * N + k - row.off;
     }
-    *to = make_float2(__int_as_float(token), 0.0f);
+    return make_float2(f.bad ? NAN : f.top, __int_as_float(token));
+  } else {
+    Pass p;
+    begin(p);
+    auto step = [&](int, const uint4& v, const uint4& w) { take<DT, false>(p, v, w, fmaxf(largest<DT>(v), largest<DT>(w)), c); };
+    if (HELD) over_held(g0, g1, held, step);
+    else over_groups<DT>(row, g0, g1, step);
+    Sums q = warp_joined(p, c);
+    if (lane == 0) s.part[warp] = q;
+    __syncthreads();
+    if (warp != 0) return make_float2(0.0f, 0.0f);
+    q = parts_joined(s.part[min(lane, WARPS - 1)], WARPS, c);
+    return make_float2(q.ref, q.s);
   }
 }
 
@@ -151,26 +176,45 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) v
   after_previous();
   __shared__ RowShared s;
   extern __shared__ __align__(16) uint4 held[];
-  const int r = blockIdx.x >> a.ctas_shift, rank = blockIdx.x - (r << a.ctas_shift);
-  const int targets = (int)a.n * (a.gamma + 1);
-  const bool of_target = GREEDY || r < targets;
-  const int each = of_target ? a.gamma + 1 : a.gamma, k = of_target ? r : r - targets;
-  const int i = k / each, t = k - i * each;
-  if (t >= drafts_of(a, i) + (of_target ? 1 : 0)) return;  // the whole cluster
-  const void* p = of_target ? a.target : a.draft;
-  const int64_t at = of_target ? i * a.target_stride_n + t * a.target_stride_t : i * a.draft_stride_n + t * a.draft_stride_t;
-  const int dtype = of_target ? a.target_dtype : a.draft_dtype;
-  const float c = of_target ? a.c : a.draft_c;
-  float2* to = a.stats + r;
-  auto go = [&](auto type) {
-    constexpr int DT = decltype(type)::value;
-    const Row row = row_at<DT>(p, at, a.V);
-    if constexpr (GREEDY) row_token<DT, HELD>(a, row, rank, to, held, s);
-    else row_sums<DT, HELD>(a, row, rank, c, to, held, s);
-  };
-  if (dtype == WHEAD_BF16) go(std::integral_constant<int, WHEAD_BF16>{});
-  else if (dtype == WHEAD_F16) go(std::integral_constant<int, WHEAD_F16>{});
-  else go(std::integral_constant<int, WHEAD_F32>{});
+  const int tid = threadIdx.x, pair = a.draft ? 1 : 0;
+  // parts of a row, then target and draft, then entries, then places
+  const unsigned rest = blockIdx.x >> a.parts_shift;
+  const int part = blockIdx.x & ((1 << a.parts_shift) - 1), of_draft = rest & pair, t = (rest >> pair) / a.n, i = (rest >> pair) - t * a.n;
+  const int have = drafts_of(a, i);
+  if (t + of_draft > have) return;
+  if (a.first) {
+    if (__syncthreads_or(tid == 0 && *(volatile const int32_t*)(a.first + i) < t)) return;
+  }
+  const void* p = of_draft ? a.draft : a.target;
+  const int64_t at = of_draft ? i * a.draft_stride_n + t * a.draft_stride_t : i * a.target_stride_n + t * a.target_stride_t;
+  const int dtype = of_draft ? a.draft_dtype : a.target_dtype;
+  const float c = of_draft ? a.draft_c : a.c;
+  float2 mine;
+  if (dtype == WHEAD_BF16) mine = row_part<WHEAD_BF16, GREEDY, HELD>(a, row_at<WHEAD_BF16>(p, at, a.V), part, c, held, s);
+  else if (dtype == WHEAD_F16) mine = row_part<WHEAD_F16, GREEDY, HELD>(a, row_at<WHEAD_F16>(p, at, a.V), part, c, held, s);
+  else mine = row_part<WHEAD_F32, GREEDY, HELD>(a, row_at<WHEAD_F32>(p, at, a.V), part, c, held, s);
+  if (tid >= 32) return;
+  if (tid == 0) {
+    __stcg(parts_of(a, i, t, of_draft) + part, mine);
+    s.last = 0;
+    if (a.first && t < have) {
+      unsigned done;
+      asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(done) : "l"(a.arrived + (int64_t)i * (a.gamma + 1) + t) : "memory");
+      s.last = done + 1 == (1u + pair) << a.parts_shift;
+    }
+  }
+  __syncwarp();
+  if (!s.last) return;
+  // the place is done: its draft is decided on
+  const int x = a.tokens[(int64_t)i * a.gamma + t];
+  bool stays;
+  if constexpr (GREEDY) {
+    stays = x >= 0 && row_token(a, i, t) == x;
+  } else {
+    const float2 ps = row_sums(a, i, t, 0), qs = pair ? row_sums(a, i, t, 1) : make_float2(0.0f, 1.0f);
+    stays = draft_stays(a, i, t, x, ps, qs);
+  }
+  if (tid == 0 && !stays) atomicMin(a.first + i, t);
 }
 
 // One entry's row of `said`, and its count.
@@ -179,21 +223,20 @@ __device__ __forceinline__ void write_said(const VerifyArgs& a, int i, int stay,
   if (tid == 0) a.count[i] = stay + 1;
 }
 
-__global__ void __launch_bounds__(32) verify_greedy(const __grid_constant__ VerifyArgs a) {
+// Temperature 0, an entry a CTA, a place a thread.
+__global__ void __launch_bounds__(256) verify_greedy(const __grid_constant__ VerifyArgs a) {
   after_previous();
-  const int i = blockIdx.x, lane = threadIdx.x, have = drafts_of(a, i);
-  const float2* stats = a.stats + (int64_t)i * (a.gamma + 1);
-  int stay = have;
-  for (int base = 0; base < have; base += 32) {
-    const int t = base + lane;
-    const bool stops = t < have && (a.tokens[(int64_t)i * a.gamma + t] < 0 || __float_as_int(stats[t].x) != a.tokens[(int64_t)i * a.gamma + t]);
-    const unsigned b = __ballot_sync(~0u, stops);
-    if (b) {
-      stay = base + __ffs(b) - 1;
-      break;
-    }
-  }
-  write_said(a, i, stay, __float_as_int(stats[stay].x), lane, 32);
+  __shared__ int stay, next;
+  const int i = blockIdx.x, t = threadIdx.x, have = drafts_of(a, i);
+  const int known = a.first ? min(a.first[i], have) : have;  // the rows up to here are done
+  if (t == 0) stay = known;
+  const int x = t < known ? a.tokens[(int64_t)i * a.gamma + t] : -1, token = t <= known ? row_token(a, i, t) : -1;
+  __syncthreads();
+  if (t < known && (x < 0 || token != x)) atomicMin(&stay, t);
+  __syncthreads();
+  if (t == stay) next = token;
+  __syncthreads();
+  write_said(a, i, stay, next, t, blockDim.x);
 }
 
 // The best two tokens seen: keys r / E, of equal ones the lower token first; token -1: none.
@@ -213,14 +256,22 @@ __device__ __forceinline__ void add(Best& b, float k, int v) {
     b.v2 = v;
   }
 }
+__device__ __forceinline__ Best warp_best(Best b) {
+#pragma unroll 1
+  for (int o = 16; o; o >>= 1) {
+    const Best y{__shfl_xor_sync(~0u, b.k1, o), __shfl_xor_sync(~0u, b.k2, o), __shfl_xor_sync(~0u, b.v1, o), __shfl_xor_sync(~0u, b.v2, o)};
+    add(b, y.k1, y.v1);
+    add(b, y.k2, y.v2);
+  }
+  return b;
+}
 
 struct DrawShared {
-  int stay;
+  int stay, next;
+  float2 ps[WHEAD_MAX_DRAFTS + 1], qs[WHEAD_MAX_DRAFTS + 1];
   Best part[kDrawWarps];
-  Best mine[2];  // for the cluster, of the residual and of the target
+  Best cluster[kMaxCluster];
 };
-
-__device__ __forceinline__ float uniform(uint32_t w) { return ((float)(w >> 9) + 0.5f) * 0x1p-23f; }
 
 // Four logits from `at` on, of which `live` are there; `wide`: they can be read as one.
 __device__ __forceinline__ void load_four_logits(const void* p, int64_t at, int dtype, bool wide, int live, float (&x)[4]) {
@@ -239,138 +290,186 @@ __device__ __forceinline__ void load_four_logits(const void* p, int64_t at, int 
   }
 }
 
+// The row that a token is drawn from.
+struct DrawRow {
+  int64_t p_at, q_at;
+  float2 ps, qs;
+  int stay, drafted;       // the draft that does not stay, -1: none
+  bool q, p_wide, q_wide;  // q: there is a row of the draft's to take off
+};
+
+// The best tokens of four at a time, from `from` on in steps; `whole`: of p itself, else of max(p - q, 0).
+__device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int i, int from, int step, bool whole) {
+  constexpr int kTurn = 3;  // loads under way
+  Best best{0.0f, 0.0f, -1, -1};
+  const float p_inv = 1.0f / d.ps.y, q_inv = 1.0f / d.qs.y;
+  const bool with_q = d.q && !whole;
+  const int quads = (a.V + 3) / 4;
+  for (int g0 = from; g0 < quads; g0 += kTurn * step) {
+    float x[kTurn][4], y[kTurn][4];
+#pragma unroll
+    for (int n = 0; n < kTurn; ++n) {
+      const int g = g0 + n * step;
+      if (g < quads) {
+        load_four_logits(a.target, d.p_at + 4 * g, a.target_dtype, d.p_wide, a.V - 4 * g, x[n]);
+        if (with_q) load_four_logits(a.draft, d.q_at + 4 * g, a.draft_dtype, d.q_wide, a.V - 4 * g, y[n]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kTurn; ++n) {
+      const int g = g0 + n * step;
+      if (g >= quads) break;
+      float r[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        r[k] = ex2((x[n][k] - d.ps.x) * a.c) * p_inv;
+        if (with_q) r[k] -= ex2((y[n][k] - d.qs.x) * a.draft_c) * q_inv;
+        else if (!whole && !a.draft && 4 * g + k == d.drafted) r[k] = 0.0f;
+      }
+      if (!(fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3])) > 0.0f)) continue;
+      const uint4 word = philox(make_uint4((uint32_t)g, a.step + d.stay, (uint32_t)i, 1u), a.seed);
+      const uint32_t w[4] = {word.x, word.y, word.z, word.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float rest = (float)(0x800000u - (w[k] >> 9)) - 0.5f;  // (1 - U) 2^23, exactly
+        if (r[k] > 0.0f && r[k] * 8388736.0f > best.k1 * rest) add(best, r[k] / -logf(uniform(w[k])), 4 * g + k);
+      }
+    }
+  }
+  return best;
+}
+
+// The best of a CTA, in its first warp.
+__device__ __forceinline__ Best cta_best(Best b, DrawShared& s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  b = warp_best(b);
+  if (lane == 0) s.part[warp] = b;
+  __syncthreads();
+  if (warp == 0) {
+    b = lane < kDrawWarps ? s.part[lane] : Best{0.0f, 0.0f, -1, -1};
+    b = warp_best(b);
+  }
+  return b;
+}
+
 __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_constant__ VerifyArgs a) {
   after_previous();
   __shared__ DrawShared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ctas = 1 << a.ctas_shift, i = blockIdx.x >> a.ctas_shift, rank = blockIdx.x & (ctas - 1);
   const int have = drafts_of(a, i);
-  const float2* p_stats = a.stats + (int64_t)i * (a.gamma + 1);
-  const float2* q_stats = a.stats + a.n * (a.gamma + 1) + (int64_t)i * a.gamma;
+  const int known = a.first ? min(a.first[i], have) : have;  // the rows up to here are done
   const int32_t* tokens = a.tokens + (int64_t)i * a.gamma;
-  if (tid == 0) s.stay = have;
+  if (ctas > 1) cluster_arrive();
+  if (tid == 0) s.stay = known;
   __syncthreads();
-  auto sound = [](float2 x) { return x.y > 0.0f && x.y < INFINITY; };
-  if (tid < have) {
-    const int x = tokens[tid];
-    const float2 ps = p_stats[tid], qs = a.draft ? q_stats[tid] : make_float2(0.0f, 1.0f);
-    bool stays = false;
-    if ((unsigned)x < (unsigned)a.V && sound(ps) && sound(qs)) {
-      const float xp = load_one(a.target, i * a.target_stride_n + tid * a.target_stride_t + x, a.target_dtype);
-      const float xq = a.draft ? load_one(a.draft, i * a.draft_stride_n + tid * a.draft_stride_t + x, a.draft_dtype) : 0.0f;
-      const float u = uniform(philox(make_uint4(0u, a.step + tid, (uint32_t)i, 2u), a.seed).x);
-      const float p = ex2((xp - ps.x) * a.c) / ps.y, q = a.draft ? ex2((xq - qs.x) * a.draft_c) / qs.y : 1.0f;
-      stays = u * q < p;
-      if (fabsf(u * q - p) <= kNear * p || p < 1e-30f) {
-        const double dp = exp(((double)xp - ps.x) * a.inverse) / ps.y, dq = a.draft ? exp(((double)xq - qs.x) * a.draft_inverse) / qs.y : 1.0;
-        stays = u * dq < dp;
-      }
+  for (int t = warp; t <= known; t += kDrawWarps) {
+    const int x = t < have ? tokens[t] : -1;
+    const float2 ps = row_sums(a, i, t, 0), qs = t < have && a.draft ? row_sums(a, i, t, 1) : make_float2(0.0f, 1.0f);
+    if (lane == 0) {
+      s.ps[t] = ps;
+      s.qs[t] = qs;
+      if (t < known && !draft_stays(a, i, t, x, ps, qs)) atomicMin(&s.stay, t);
     }
-    if (!stays) atomicMin(&s.stay, tid);
   }
   __syncthreads();
-  const int stay = s.stay;
-  const float2 ps = p_stats[stay];
-  const bool some = sound(ps), rejected = stay < have;
-  const float2 qs = rejected && a.draft ? q_stats[stay] : make_float2(0.0f, 1.0f);
-  const int drafted = rejected ? tokens[stay] : -1;
-  const bool with_q = rejected && a.draft && sound(qs);  // a row q of logits to take off
-  const int64_t p_at = i * a.target_stride_n + stay * a.target_stride_t, q_at = i * a.draft_stride_n + stay * a.draft_stride_t;
+  DrawRow d;
+  d.stay = s.stay;
+  d.ps = s.ps[d.stay];
+  d.qs = s.qs[d.stay];
+  const bool some = sound(d.ps), rejected = d.stay < have;
+  d.drafted = rejected ? tokens[d.stay] : -1;
+  d.q = rejected && a.draft && sound(d.qs);
+  d.p_at = i * a.target_stride_n + d.stay * a.target_stride_t;
+  d.q_at = i * a.draft_stride_n + d.stay * a.draft_stride_t;
   const int p_size = a.target_dtype == WHEAD_F32 ? 4 : 2, q_size = a.draft_dtype == WHEAD_F32 ? 4 : 2;
-  const bool p_wide = ((reinterpret_cast<uintptr_t>(a.target) + p_at * p_size) & (4 * p_size - 1)) == 0;
-  const bool q_wide = with_q && ((reinterpret_cast<uintptr_t>(a.draft) + q_at * q_size) & (4 * q_size - 1)) == 0;
-  const float p_inv = 1.0f / ps.y, q_inv = 1.0f / qs.y;
-  Best all{0.0f, 0.0f, -1, -1};
-  bool whole = !rejected;  // draw from p itself
-  for (int turn = 0; some && turn < 2; ++turn) {
-    Best best{0.0f, 0.0f, -1, -1};
-    for (int g = rank * kDrawThreads + tid; g < (a.V + 3) / 4; g += ctas * kDrawThreads) {
-      float x[4], y[4];
-      load_four_logits(a.target, p_at + 4 * g, a.target_dtype, p_wide, a.V - 4 * g, x);
-      if (with_q && !whole) load_four_logits(a.draft, q_at + 4 * g, a.draft_dtype, q_wide, a.V - 4 * g, y);
-      const uint4 word = philox(make_uint4((uint32_t)g, a.step + stay, (uint32_t)i, 1u), a.seed);
-      const uint32_t w[4] = {word.x, word.y, word.z, word.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float r = ex2((x[k] - ps.x) * a.c) * p_inv;
-        if (!whole) {
-          if (with_q) r -= ex2((y[k] - qs.x) * a.draft_c) * q_inv;
-          else if (!a.draft && 4 * g + k == drafted) r = 0.0f;
-        }
-        const float rest = (float)(0x800000u - (w[k] >> 9)) - 0.5f;  // (1 - U) 2^23, exactly
-        if (r > 0.0f && r * 8388736.0f > best.k1 * rest) add(best, r / -logf(uniform(w[k])), 4 * g + k);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const Best y{__shfl_xor_sync(~0u, best.k1, o), __shfl_xor_sync(~0u, best.k2, o), __shfl_xor_sync(~0u, best.v1, o), __shfl_xor_sync(~0u, best.v2, o)};
-      add(best, y.k1, y.v1);
-      add(best, y.k2, y.v2);
-    }
-    if (lane == 0) s.part[warp] = best;
-    __syncthreads();
-    for (int w = 0; w < kDrawWarps; ++w) {
-      if (w == warp) continue;
-      add(best, s.part[w].k1, s.part[w].v1);
-      add(best, s.part[w].k2, s.part[w].v2);
-    }
-    all = best;
-    if (ctas > 1) {
-      cg::cluster_group cluster = cg::this_cluster();
-      if (tid == 0) s.mine[turn] = best;
-      cluster.sync();
-      for (int k = 0; k < ctas; ++k) {
-        if (k == rank) continue;
-        const Best* y = cluster.map_shared_rank(&s.mine[turn], k);
-        add(all, y->k1, y->v1);
-        add(all, y->k2, y->v2);
-      }
-    } else {
-      __syncthreads();
-    }
-    if (all.v1 >= 0 || whole) break;
-    whole = true;  // rounding left nothing of p - q
+  d.p_wide = ((reinterpret_cast<uintptr_t>(a.target) + d.p_at * p_size) & (4 * p_size - 1)) == 0;
+  d.q_wide = d.q && ((reinterpret_cast<uintptr_t>(a.draft) + d.q_at * q_size) & (4 * q_size - 1)) == 0;
+  bool whole = !rejected;
+  Best best{0.0f, 0.0f, -1, -1};
+  if (some) best = draw(a, d, i, rank * kDrawThreads + tid, ctas * kDrawThreads, whole);
+  best = cta_best(best, s);
+  if (ctas > 1) {
+    cluster_wait();  // all have started
+    if (tid == 0) *in_first(&s.cluster[rank]) = best;
+    __syncwarp();
+    cluster_arrive();
+    if (rank != 0) return;
+    cluster_wait();
+    if (warp == 0) best = warp_best(lane < ctas ? s.cluster[lane] : Best{0.0f, 0.0f, -1, -1});
   }
-  if (ctas > 1) cg::this_cluster().sync();  // nobody reads this CTA's shared memory after it
-  if (rank != 0) return;
-  if (tid == 0) s.stay = all.v1;
-  if (tid == 0 && all.v2 >= 0 && all.k1 - all.k2 <= kNear * all.k1) {
+  if (tid == 0) s.next = best.v1;
+  __syncthreads();
+  if (some && !whole && s.next < 0) {  // rounding left nothing of p - q
+    whole = true;
+    best = cta_best(draw(a, d, i, tid, kDrawThreads, true), s);
+    if (tid == 0) s.next = best.v1;
+  }
+  if (tid == 0 && best.v2 >= 0 && best.k1 - best.k2 <= kNear * best.k1) {
     auto key = [&](int v) {
-      double r = exp(((double)load_one(a.target, p_at + v, a.target_dtype) - ps.x) * a.inverse) / ps.y;
-      if (!whole && with_q) r -= exp(((double)load_one(a.draft, q_at + v, a.draft_dtype) - qs.x) * a.draft_inverse) / qs.y;
-      const uint4 word = philox(make_uint4((uint32_t)v >> 2, a.step + stay, (uint32_t)i, 1u), a.seed);
+      double r = exp(((double)load_one(a.target, d.p_at + v, a.target_dtype) - d.ps.x) * a.inverse) / d.ps.y;
+      if (!whole && d.q) r -= exp(((double)load_one(a.draft, d.q_at + v, a.draft_dtype) - d.qs.x) * a.draft_inverse) / d.qs.y;
+      const uint4 word = philox(make_uint4((uint32_t)v >> 2, a.step + d.stay, (uint32_t)i, 1u), a.seed);
       const uint32_t w = v & 2 ? (v & 1 ? word.w : word.z) : (v & 1 ? word.y : word.x);
       return r / -log((double)uniform(w));
     };
-    const double k1 = key(all.v1), k2 = key(all.v2);
-    if (k2 > k1 || (k2 == k1 && all.v2 < all.v1)) s.stay = all.v2;
+    const double k1 = key(best.v1), k2 = key(best.v2);
+    if (k2 > k1 || (k2 == k1 && best.v2 < best.v1)) s.next = best.v2;
   }
   __syncthreads();
-  write_said(a, i, stay, some ? s.stay : -1, tid, kDrawThreads);
+  write_said(a, i, d.stay, s.next, tid, kDrawThreads);
 }
 
 template <bool GREEDY, bool HELD>
-int launch_rows(const VerifyArgs& a, int64_t rows, int device, cudaStream_t stream) {
+int launch_rows(const VerifyArgs& a, int64_t ctas, int device, cudaStream_t stream) {
   static std::atomic<bool> granted[kMaxDevices];
-  return launch_clusters(verify_rows<GREEDY, HELD>, rows, 1 << a.ctas_shift, Form<HELD>::kThreads, HELD ? a.held * kGroup * 16 : 0, stream, granted, device, a);
+  return launch_clusters(verify_rows<GREEDY, HELD>, ctas, 1, Form<HELD>::kThreads, HELD ? a.held * kGroup * 16 : 0, stream, granted, device, a);
+}
+
+// Parts of a row, as a power of two: by the entries alone, so that the workspace's size does not depend on the device or on V.
+int most_parts_shift(int64_t n) {
+  int s = 4;
+  while (s > 0 && n << s > 512) --s;
+  return s;
+}
+static_assert(kMaxParts == 1 << 4, "");
+
+struct Layout {
+  int64_t first, arrived, total;
+};
+Layout layout(int64_t n, int gamma) {
+  const int64_t places = n * (gamma + 1);
+  Layout l;
+  l.first = whead_kv_impl::align256((places * 2 << most_parts_shift(n)) * (int64_t)sizeof(float2));
+  l.arrived = l.first + whead_kv_impl::align256(n * 4);
+  l.total = l.arrived + whead_kv_impl::align256(places * 4);
+  return l;
 }
 
 int launch(const VerifyArgs& from, int device, int sms, cudaStream_t stream) {
   static std::atomic<bool> granted[kMaxDevices];
   VerifyArgs a = from;
   const bool greedy = a.inverse == 0.0;
-  const int64_t rows = a.n * (a.gamma + 1) + (greedy || !a.draft ? 0 : a.n * a.gamma);
-  const int64_t bytes = (int64_t)a.V * std::max(dtype_size(a.target_dtype), a.draft ? dtype_size(a.draft_dtype) : 0);
-  const Division d = divide(rows, bytes, sms);
-  a.ctas_shift = d.shift;
-  a.held = d.groups;
-  int rc;
-  if (greedy) rc = d.held ? launch_rows<true, true>(a, rows, device, stream) : launch_rows<true, false>(a, rows, device, stream);
-  else rc = d.held ? launch_rows<false, true>(a, rows, device, stream) : launch_rows<false, false>(a, rows, device, stream);
+  const int pair = a.draft ? 1 : 0;
+  const int64_t places = (int64_t)a.n * (a.gamma + 1), bytes = (int64_t)a.V * std::max(dtype_size(a.target_dtype), pair ? dtype_size(a.draft_dtype) : 0);
+  // parts of 16 KB or more, as many as there is room for (by the entries)
+  const int most = most_parts_shift(a.n);
+  auto groups = [&](int shift) { return (int)(((bytes / (kGroup * 16) + 2) >> shift) + 1); };
+  while (a.parts_shift < most && bytes >> (a.parts_shift + 1) >= 16384) ++a.parts_shift;
+  const int64_t ctas = places << (pair + a.parts_shift);
+  // all at once: parts held. More: parts streamed, and what is decided left out.
+  const bool held = groups(a.parts_shift) <= kHeldGroups && ctas <= (int64_t)sms * Form<true>::kCtas;
+  a.held = groups(a.parts_shift);
+  int rc = WHEAD_OK;
+  if (ctas > (int64_t)sms * Form<false>::kCtas && a.gamma > 0) rc = whead_kv_impl::launch_after(verify_begin, dim3((unsigned)((places + 255) / 256)), 256, 0, stream, a);
+  else a.first = nullptr;
   if (rc != WHEAD_OK) return rc;
-  if (greedy) return whead_kv_impl::launch_after(verify_greedy, dim3((unsigned)a.n), 32, 0, stream, a);
+  if (greedy) rc = held ? launch_rows<true, true>(a, ctas, device, stream) : launch_rows<true, false>(a, ctas, device, stream);
+  else rc = held ? launch_rows<false, true>(a, ctas, device, stream) : launch_rows<false, false>(a, ctas, device, stream);
+  if (rc != WHEAD_OK) return rc;
+  if (greedy) return whead_kv_impl::launch_after(verify_greedy, dim3((unsigned)a.n), (a.gamma + 32) / 32 * 32, 0, stream, a);
   a.ctas_shift = 0;
-  while ((2 << a.ctas_shift) <= kMaxCluster && a.n << (a.ctas_shift + 1) <= (int64_t)sms * 3 && a.V >> (a.ctas_shift + 1) >= 4 * kDrawThreads) ++a.ctas_shift;
+  while ((2 << a.ctas_shift) <= kMaxCluster && (int64_t)a.n << (a.ctas_shift + 1) <= (int64_t)sms * 3 && a.V >> (a.ctas_shift + 1) >= 4 * kDrawThreads) ++a.ctas_shift;
   return launch_clusters(verify_draw, a.n, 1 << a.ctas_shift, kDrawThreads, 0, stream, granted, device, a);
 }
 
@@ -382,8 +481,8 @@ using namespace whead_verify_impl;
 
 extern "C" int64_t whead_verify_workspace_bytes(int64_t n, int32_t gamma) {
   if (n < 0 || gamma < 0) return WHEAD_ERR_INVALID_ARG;
-  if (gamma > WHEAD_MAX_DRAFTS || n > ((1 << 27) - 1) / (2 * gamma + 1)) return WHEAD_ERR_UNSUPPORTED;
-  return whead_kv_impl::align256(n * (2 * gamma + 1) * (int64_t)sizeof(float2));
+  if (gamma > WHEAD_MAX_DRAFTS || n > ((1 << 27) - 1) / (2 * gamma + 2)) return WHEAD_ERR_UNSUPPORTED;
+  return layout(n, gamma).total;
 }
 
 extern "C" int whead_verify(const whead_verify_args* x) {
@@ -404,6 +503,8 @@ extern "C" int whead_verify(const whead_verify_args* x) {
     (void)cudaGetLastError();
     return WHEAD_ERR_CUDA;
   }
+  const Layout l = layout(x->n, x->gamma);
+  char* w = static_cast<char*>(x->workspace);
   VerifyArgs a{};
   a.target = x->target;
   a.draft = with_draft ? x->draft : nullptr;
@@ -411,7 +512,9 @@ extern "C" int whead_verify(const whead_verify_args* x) {
   a.drafted = x->drafted;
   a.said = x->said;
   a.count = x->count;
-  a.stats = static_cast<float2*>(x->workspace);
+  a.parts = reinterpret_cast<float2*>(w);
+  a.first = reinterpret_cast<int32_t*>(w + l.first);
+  a.arrived = reinterpret_cast<int32_t*>(w + l.arrived);
   a.target_stride_n = x->target_stride_n;
   a.target_stride_t = x->target_stride_t;
   a.draft_stride_n = x->draft_stride_n;
@@ -421,7 +524,7 @@ extern "C" int whead_verify(const whead_verify_args* x) {
   a.target_dtype = x->target_dtype;
   a.draft_dtype = x->draft_dtype;
   a.step = x->step;
-  a.n = x->n;
+  a.n = (int)x->n;
   if (x->temperature > 0) {
     a.inverse = 1.0 / x->temperature;
     a.c = (float)(1.4426950408889634 / x->temperature);

@@ -289,17 +289,17 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
   Sums sums;
   if (ctas > 1) {
     if (warp == 0) {
-      sums = parts_joined(s.part, WARPS, a.c);
+      sums = parts_joined(s.part[min(lane, WARPS - 1)], WARPS, a.c);
       if (lane == 0) *in_first(&s.cluster[rank]) = sums;
     }
     __syncwarp();
     cluster_arrive();
     if (rank != 0) return;
     cluster_wait();
-    sums = parts_joined(s.cluster, ctas, a.c);
+    sums = parts_joined(s.cluster[min(lane, ctas - 1)], ctas, a.c);
   } else {
     if (TOP) __syncthreads();
-    sums = parts_joined(s.part, WARPS, a.c);
+    sums = parts_joined(s.part[min(lane, WARPS - 1)], WARPS, a.c);
   }
   const float top = sums.ref, log_s = log2f(sums.s), k = top * a.c;
   const bool none = sums.s == 0.0f, bad = isnan(sums.s);

@@ -50,12 +50,12 @@ class LogProbs(NamedTuple):
 
 
 _lib = None
-_CODES = None
+_torch = _CODES = _raw_stream = _device = _int32 = _float32 = None
 
 
 def load() -> ctypes.CDLL:
     """The library with these calls declared. Raises if it is not built."""
-    global _lib, _CODES
+    global _lib, _torch, _CODES, _raw_stream, _device, _int32, _float32
     if _lib is None:
         import torch
         L = _wh.load()
@@ -65,40 +65,39 @@ def load() -> ctypes.CDLL:
         L.whead_verify_workspace_bytes.restype = _i64
         L.whead_verify.argtypes = [_vp]
         L.whead_verify.restype = ctypes.c_int
+        _torch, _int32, _float32 = torch, torch.int32, torch.float32
         _CODES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a torch without CUDA has neither
+        _device = getattr(torch._C, "_cuda_getDevice", None)
         _lib = L
     return _lib
 
 
-def _logits(x, dims, what, device=None):
+def _logits(x, shape, strides, dims, index, what):
     """The code of a tensor of logits, checked."""
-    import torch
     code = _CODES.get(x.dtype)
     if code is None:
         raise TypeError(f"{what}: {x.dtype} is not supported")
-    if x.dim() not in dims or x.shape[-1] < 1 or x.stride(-1) != 1 and x.shape[-1] > 1:
+    if len(shape) not in dims or shape[-1] < 1 or strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{what}: {' or '.join(map(str, dims))} dimensions are wanted, the last one the vocabulary and contiguous")
-    if not x.is_cuda or (device is not None and x.get_device() != device):
+    if not x.is_cuda or x.get_device() != index:
         raise ValueError(f"{what}: a tensor on one CUDA device with the others is wanted")
-    if x.requires_grad and torch.is_grad_enabled():
+    if x.requires_grad and _torch.is_grad_enabled():
         raise ValueError(f"{what}: no gradients are passed on; call it under torch.no_grad() or on detached tensors")
     return code
 
 
-def _ints(x, shape, device, what):
-    import torch
-    if x.dtype is not torch.int32 or x.shape != shape or not x.is_contiguous() or x.get_device() != device:
+def _ints(x, shape, index, what):
+    if x.dtype is not _int32 or x.shape != shape or not x.is_contiguous() or x.get_device() != index:
         raise ValueError(f"{what}: a contiguous int32 tensor of shape {tuple(shape)} on the logits' device is wanted")
     return x.data_ptr()
 
 
 def _call(call, args, index):
-    import torch
-    args.stream = torch._C._cuda_getCurrentRawStream(index)
-    if torch._C._cuda_getDevice() == index:
+    if _device() == index:
         rc = call(ctypes.addressof(args))
     else:
-        with torch.cuda.device(index):
+        with _torch.cuda.device(index):
             rc = call(ctypes.addressof(args))
     if rc:
         raise _wh.WheadError(rc, call.__name__)
@@ -111,29 +110,33 @@ def logprobs(logits, tokens=None, *, top=0, temperature=1.0) -> LogProbs:
     top: how many of the best tokens to give (at most 32), equal logits in the tokens' order; -1 and -inf past the tokens that can be.
     Logits of -inf are tokens that cannot be. A row of nothing else has lse and log probabilities of -inf and entropy 0; a row with NaN or
     +inf gives NaN, and -1 for every alternative."""
-    import torch
-    L = load()
-    code = _logits(logits, (2, 3), "logits")
-    index, device = logits.get_device(), logits.device
-    shape, strides = logits.shape, logits.stride()
-    rows = shape[:-1]
-    n, t = (shape[0], 1) if len(shape) == 2 else (shape[0], shape[1])
-    top, temperature = int(top), float(temperature)
+    L = _lib or load()
+    index, shape, strides = logits.get_device(), logits.shape, logits.stride()
+    code = _logits(logits, shape, strides, (2, 3), index, "logits")
     if not 0 <= top <= MAX_TOP:
         raise ValueError(f"0 <= top <= {MAX_TOP} is wanted")
-    entropy = torch.empty(rows, dtype=torch.float32, device=device)
-    lse = torch.empty(rows, dtype=torch.float32, device=device)
-    logprob = top_tokens = top_logprobs = token_ptr = None
+    device, empty, f32 = logits.device, _torch.empty, _float32
+    if len(shape) == 2:
+        n, V = shape
+        t, stride_t, rows = 1, 0, (n,)
+    else:
+        n, t, V = shape
+        stride_t, rows = strides[1], (n, t)
+    # addresses first, tensors after: what is not asked for stays None
+    logprob = top_tokens = top_logprobs = a0 = a1 = a2 = a3 = None
     if tokens is not None:
-        token_ptr = _ints(tokens, rows, index, "tokens")
-        logprob = torch.empty(rows, dtype=torch.float32, device=device)
+        a0 = _ints(tokens, rows, index, "tokens")
+        logprob = empty(rows, dtype=f32, device=device)
+        a1 = logprob.data_ptr()
+    entropy = empty(rows, dtype=f32, device=device)
+    lse = empty(rows, dtype=f32, device=device)
     if top:
-        top_tokens = torch.empty((*rows, top), dtype=torch.int32, device=device)
-        top_logprobs = torch.empty((*rows, top), dtype=torch.float32, device=device)
-    a = LogprobsArgs(logits.data_ptr(), token_ptr, None if logprob is None else logprob.data_ptr(), entropy.data_ptr(), lse.data_ptr(),
-                     top_tokens.data_ptr() if top else None, top_logprobs.data_ptr() if top else None, strides[0],
-                     strides[1] if len(shape) == 3 else 0, n, t, shape[-1], temperature, code, top)
-    _call(L.whead_logprobs, a, index)
+        wide = (*rows, top)
+        top_tokens = empty(wide, dtype=_int32, device=device)
+        top_logprobs = empty(wide, dtype=f32, device=device)
+        a2, a3 = top_tokens.data_ptr(), top_logprobs.data_ptr()
+    _call(L.whead_logprobs, LogprobsArgs(logits.data_ptr(), a0, a1, entropy.data_ptr(), lse.data_ptr(), a2, a3, strides[0], stride_t, n, t, V,
+                                         temperature, code, top, _raw_stream(index)), index)
     return LogProbs(logprob, entropy, lse, top_tokens, top_logprobs)
 
 
@@ -148,34 +151,33 @@ def verify(target, tokens, draft=None, *, temperature=0.0, draft_temperature=Non
     token and the drafts. temperature 0: drafts stay while they are the target's best token. Above: every token said is distributed as the
     target's own; seed and step (the walk's t0) number the draws as they do the walk's, and may be the walk's.
     In a row of target with NaN, +inf or nothing but -inf no draft stays and the token after is -1."""
-    import torch
-    L = load()
-    code = _logits(target, (3,), "target")
-    index, device = target.get_device(), target.device
-    n, rows, V = target.shape
+    L = _lib or load()
+    index, shape, strides = target.get_device(), target.shape, target.stride()
+    code = _logits(target, shape, strides, (3,), index, "target")
+    n, rows, V = shape
     gamma = rows - 1
     if not 0 <= gamma <= MAX_DRAFTS:
         raise ValueError(f"target: (n, gamma + 1, V) with 0 <= gamma <= {MAX_DRAFTS} is wanted")
     token_ptr = _ints(tokens, (n, gamma), index, "tokens")
     drafted_ptr = None if drafted is None else _ints(drafted, (n,), index, "drafted")
-    temperature, step, seed = float(temperature), int(step), int(seed)
     draft_ptr, draft_code, d0, d1 = None, 0, 0, 0
     if draft is not None:
-        draft_code = _logits(draft, (3,), "draft", index)
+        draft_strides = draft.stride()
+        draft_code = _logits(draft, draft.shape, draft_strides, (3,), index, "draft")
         if draft.shape != (n, gamma, V):
             raise ValueError(f"draft: shape {(n, gamma, V)} is wanted")
-        draft_ptr, (d0, d1, _) = draft.data_ptr(), draft.stride()
+        draft_ptr, (d0, d1, _) = draft.data_ptr(), draft_strides
     if not 0 <= step < 2 ** 32:
         raise ValueError("0 <= step < 2^32 is wanted")
     need = L.whead_verify_workspace_bytes(n, gamma)
     if need < 0:
         raise _wh.WheadError(need, "whead_verify_workspace_bytes")
-    said = torch.empty((n, rows), dtype=torch.int32, device=device)
-    count = torch.empty(n, dtype=torch.int32, device=device)
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    s0, s1, _ = target.stride()
-    a = VerifyArgs(target.data_ptr(), draft_ptr, token_ptr, drafted_ptr, said.data_ptr(), count.data_ptr(), s0, s1, d0, d1, n, V, gamma, code,
-                   draft_code, step, temperature, temperature if draft_temperature is None else float(draft_temperature), seed & (2 ** 64 - 1),
-                   workspace.data_ptr(), need)
-    _call(L.whead_verify, a, index)
+    device, empty = target.device, _torch.empty
+    said = empty((n, rows), dtype=_int32, device=device)
+    count = empty((n,), dtype=_int32, device=device)
+    workspace = empty((need,), dtype=_torch.uint8, device=device)
+    _call(L.whead_verify, VerifyArgs(target.data_ptr(), draft_ptr, token_ptr, drafted_ptr, said.data_ptr(), count.data_ptr(), strides[0], strides[1],
+                                     d0, d1, n, V, gamma, code, draft_code, step, temperature,
+                                     temperature if draft_temperature is None else draft_temperature, seed & 0xFFFFFFFFFFFFFFFF,
+                                     workspace.data_ptr(), need, _raw_stream(index)), index)
     return said, count
