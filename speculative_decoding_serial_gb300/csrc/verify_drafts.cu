@@ -3,7 +3,7 @@
 // Two kernels. The first takes rows of logits: at temperature 0 their largest value's token, else their largest value and sum of
 // exponentials, a CTA a part of a row. The second, for each entry, joins the parts, finds the first draft that does not stay and draws the
 // token of that row: the largest of r_v / E_v with r = max(p - q, 0), E = -log U. Since E >= 1 - U, only a token with r_v / (1 - U)
-// above the best so far needs its logarithm; 1 - U is known exactly from the word.
+// above the CTA's best so far needs its logarithm; 1 - U is known exactly from the word.
 //
 // Rows after the first draft that does not stay are not needed. Where there are more rows than the device takes at once, CTAs come in the order of
 // the drafts' places, whoever finishes a place decides on its draft, and parts of later places that find theirs decided return
@@ -77,16 +77,18 @@ __device__ __forceinline__ int row_token(const VerifyArgs& a, int i, int t) {
   return bad ? -1 : token;
 }
 
+// p and q of one token in 64 bits.
+__device__ __noinline__ double probability64(float x, float2 stats, double inverse) { return exp(((double)x - stats.x) * inverse) / stats.y; }
+
 // Whether draft t stays, given that all before it do.
-__device__ __forceinline__ bool draft_stays(const VerifyArgs& a, int i, int t, int x, float2 ps, float2 qs) {
+__device__ __noinline__ bool draft_stays(const VerifyArgs& a, int i, int t, int x, float2 ps, float2 qs) {
   if ((unsigned)x >= (unsigned)a.V || !sound(ps) || !sound(qs)) return false;
   const float xp = load_one(a.target, i * a.target_stride_n + t * a.target_stride_t + x, a.target_dtype);
   const float xq = a.draft ? load_one(a.draft, i * a.draft_stride_n + t * a.draft_stride_t + x, a.draft_dtype) : 0.0f;
   const float u = uniform(philox(make_uint4(0u, a.step + t, (uint32_t)i, 2u), a.seed).x);
   const float p = ex2((xp - ps.x) * a.c) / ps.y, q = a.draft ? ex2((xq - qs.x) * a.draft_c) / qs.y : 1.0f;
   if (fabsf(u * q - p) > kNear * p && p >= 1e-30f) return u * q < p;
-  const double dp = exp(((double)xp - ps.x) * a.inverse) / ps.y, dq = a.draft ? exp(((double)xq - qs.x) * a.draft_inverse) / qs.y : 1.0;
-  return u * dq < dp;
+  return u * (a.draft ? probability64(xq, qs, a.draft_inverse) : 1.0) < probability64(xp, ps, a.inverse);
 }
 
 // Values for `first` and `arrived` before the rows.
@@ -267,26 +269,34 @@ __device__ __forceinline__ Best warp_best(Best b) {
 }
 
 struct DrawShared {
-  int stay, next;
+  int stay, next, known;
   float2 ps[WHEAD_MAX_DRAFTS + 1], qs[WHEAD_MAX_DRAFTS + 1];
   Best part[kDrawWarps];
   Best cluster[kMaxCluster];
 };
 
-// Four logits from `at` on, of which `live` are there; `wide`: they can be read as one.
-__device__ __forceinline__ void load_four_logits(const void* p, int64_t at, int dtype, bool wide, int live, float (&x)[4]) {
+// Four logits from `at` on, of which `live` are there, as they are; `wide`: they can be read as one. What is not there is -inf.
+__device__ __forceinline__ uint4 load_quad(const void* p, int64_t at, int dtype, bool wide, int live) {
   if (wide && live >= 4) {
-    if (dtype == WHEAD_F32) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at));
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + at));
-      const float2 lo = whead_kv_impl::unpack16(v.x, dtype), hi = whead_kv_impl::unpack16(v.y, dtype);
-      x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
-    }
+    if (dtype == WHEAD_F32) return __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at));
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + at));
+    return make_uint4(v.x, v.y, 0u, 0u);
+  }
+  uint32_t w[4];
+  if (dtype == WHEAD_F32) {
+    for (int k = 0; k < 4; ++k) w[k] = k < live ? __ldg(static_cast<const uint32_t*>(p) + at + k) : Type<WHEAD_F32>::kNone;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  const uint32_t none = (dtype == WHEAD_BF16 ? Type<WHEAD_BF16>::kNone : Type<WHEAD_F16>::kNone) & 0xFFFFu;
+  for (int k = 0; k < 4; ++k) w[k] = k < live ? __ldg(static_cast<const unsigned short*>(p) + at + k) : none;
+  return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, 0u, 0u);
+}
+__device__ __forceinline__ void quad_values(const uint4& v, int dtype, float (&x)[4]) {
+  if (dtype == WHEAD_F32) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
   } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = k < live ? load_one(p, at + k, dtype) : -INFINITY;
+    const float2 lo = whead_kv_impl::unpack16(v.x, dtype), hi = whead_kv_impl::unpack16(v.y, dtype);
+    x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
   }
 }
 
@@ -298,43 +308,71 @@ struct DrawRow {
   bool q, p_wide, q_wide;  // q: there is a row of the draft's to take off
 };
 
-// The best tokens of four at a time, from `from` on in steps; `whole`: of p itself, else of max(p - q, 0).
-__device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int i, int from, int step, bool whole) {
-  constexpr int kTurn = 3;  // loads under way
+// The best tokens of four at a time, from `from` on in steps; `whole`: of p itself, else of max(p - q, 0). Philox takes some half of the issue
+// slots; a token that the bound does not rule out (a few dozen of a CTA) takes a loop of its own, so that its logarithm and division are
+// there once and not four times in the loop over all.
+__device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int i, int from, int step, bool whole, DrawShared& s) {
   Best best{0.0f, 0.0f, -1, -1};
-  const float p_inv = 1.0f / d.ps.y, q_inv = 1.0f / d.qs.y;
+  const float p_off = -log2f(d.ps.y), q_off = -log2f(d.qs.y);
   const bool with_q = d.q && !whole;
-  const int quads = (a.V + 3) / 4;
-  for (int g0 = from; g0 < quads; g0 += kTurn * step) {
-    float x[kTurn][4], y[kTurn][4];
+  const int quads = (a.V + 3) / 4, taken = !whole && !a.draft ? d.drafted : -1;
+  float known = 0.0f;  // less than the CTA's best key by 2^-15, as far as this warp knows it
+  uint4 x[3], y[3];    // this turn's, and two turns' ahead
+  auto load = [&](int g, uint4& u, uint4& v) {
+    if (g < quads) {
+      u = load_quad(a.target, d.p_at + 4 * g, a.target_dtype, d.p_wide, a.V - 4 * g);
+      if (with_q) v = load_quad(a.draft, d.q_at + 4 * g, a.draft_dtype, d.q_wide, a.V - 4 * g);
+    }
+  };
+  load(from, x[0], y[0]);
+  load(from + step, x[1], y[1]);
+#pragma unroll 1
+  for (int g = from; __any_sync(~0u, g < quads); g += step) {
+    load(g + 2 * step, x[2], y[2]);
+    float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (g < quads) {
+      quad_values(x[0], a.target_dtype, r);
 #pragma unroll
-    for (int n = 0; n < kTurn; ++n) {
-      const int g = g0 + n * step;
-      if (g < quads) {
-        load_four_logits(a.target, d.p_at + 4 * g, a.target_dtype, d.p_wide, a.V - 4 * g, x[n]);
-        if (with_q) load_four_logits(a.draft, d.q_at + 4 * g, a.draft_dtype, d.q_wide, a.V - 4 * g, y[n]);
+      for (int k = 0; k < 4; ++k) r[k] = ex2(__fmaf_rn(r[k] - d.ps.x, a.c, p_off));
+      if (with_q) {
+        float q[4];
+        quad_values(y[0], a.draft_dtype, q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] -= ex2(__fmaf_rn(q[k] - d.qs.x, a.draft_c, q_off));
+      }
+      if (taken >> 2 == g) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((taken & 3) == k) r[k] = 0.0f;
       }
     }
+    const uint4 word = philox(make_uint4((uint32_t)g, a.step + d.stay, (uint32_t)i, 1u), a.seed);
+    const uint32_t w[4] = {word.x, word.y, word.z, word.w};
+    // r / E <= r / (1 - U) and 1 - U > 2 - 2^-23 - f, f = 1 + (w >> 9) 2^-23
+    unsigned may = 0;
 #pragma unroll
-    for (int n = 0; n < kTurn; ++n) {
-      const int g = g0 + n * step;
-      if (g >= quads) break;
-      float r[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        r[k] = ex2((x[n][k] - d.ps.x) * a.c) * p_inv;
-        if (with_q) r[k] -= ex2((y[n][k] - d.qs.x) * a.draft_c) * q_inv;
-        else if (!whole && !a.draft && 4 * g + k == d.drafted) r[k] = 0.0f;
-      }
-      if (!(fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3])) > 0.0f)) continue;
-      const uint4 word = philox(make_uint4((uint32_t)g, a.step + d.stay, (uint32_t)i, 1u), a.seed);
-      const uint32_t w[4] = {word.x, word.y, word.z, word.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float rest = (float)(0x800000u - (w[k] >> 9)) - 0.5f;  // (1 - U) 2^23, exactly
-        if (r[k] > 0.0f && r[k] * 8388736.0f > best.k1 * rest) add(best, r[k] / -logf(uniform(w[k])), 4 * g + k);
-      }
+    for (int k = 0; k < 4; ++k) {
+      const float rest = (2.0f - 0x1p-23f) - __uint_as_float(__funnelshift_r(w[k], 0x7Fu, 9));
+      may |= r[k] > known * rest ? 1u << k : 0u;
     }
+    if (__any_sync(~0u, may != 0)) {
+      while (may) {
+        const int k = __ffs(may) - 1;
+        may &= may - 1;
+        const float rk = k & 2 ? (k & 1 ? r[3] : r[2]) : (k & 1 ? r[1] : r[0]);
+        const uint32_t wk = k & 2 ? (k & 1 ? w[3] : w[2]) : (k & 1 ? w[1] : w[0]);
+        add(best, rk / -logf(uniform(wk)), 4 * g + k);
+      }
+      __syncwarp();
+      const float high = warp_max(best.k1);
+      if ((threadIdx.x & 31) == 0) atomicMax(&s.known, __float_as_int(high));  // positive floats are ordered as their bits
+      known = fmaxf(known, high * (1.0f - 0x1p-15f));
+    }
+    known = fmaxf(known, __int_as_float(*(volatile int*)&s.known) * (1.0f - 0x1p-15f));
+    x[0] = x[1];
+    x[1] = x[2];
+    y[0] = y[1];
+    y[1] = y[2];
   }
   return best;
 }
@@ -361,9 +399,13 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
   const int known = a.first ? min(a.first[i], have) : have;  // the rows up to here are done
   const int32_t* tokens = a.tokens + (int64_t)i * a.gamma;
   if (ctas > 1) cluster_arrive();
-  if (tid == 0) s.stay = known;
+  if (tid == 0) {
+    s.stay = known;
+    s.known = 0;
+  }
   __syncthreads();
-  for (int t = warp; t <= known; t += kDrawWarps) {
+  // which drafts stay: where rows have been left out it is known already
+  for (int t = a.first ? known + warp : warp; t <= known; t += kDrawWarps) {
     const int x = t < have ? tokens[t] : -1;
     const float2 ps = row_sums(a, i, t, 0), qs = t < have && a.draft ? row_sums(a, i, t, 1) : make_float2(0.0f, 1.0f);
     if (lane == 0) {
@@ -385,36 +427,39 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
   const int p_size = a.target_dtype == WHEAD_F32 ? 4 : 2, q_size = a.draft_dtype == WHEAD_F32 ? 4 : 2;
   d.p_wide = ((reinterpret_cast<uintptr_t>(a.target) + d.p_at * p_size) & (4 * p_size - 1)) == 0;
   d.q_wide = d.q && ((reinterpret_cast<uintptr_t>(a.draft) + d.q_at * q_size) & (4 * q_size - 1)) == 0;
-  bool whole = !rejected;
-  Best best{0.0f, 0.0f, -1, -1};
-  if (some) best = draw(a, d, i, rank * kDrawThreads + tid, ctas * kDrawThreads, whole);
-  best = cta_best(best, s);
-  if (ctas > 1) {
-    cluster_wait();  // all have started
-    if (tid == 0) *in_first(&s.cluster[rank]) = best;
-    __syncwarp();
-    cluster_arrive();
-    if (rank != 0) return;
-    cluster_wait();
-    if (warp == 0) best = warp_best(lane < ctas ? s.cluster[lane] : Best{0.0f, 0.0f, -1, -1});
-  }
-  if (tid == 0) s.next = best.v1;
-  __syncthreads();
-  if (some && !whole && s.next < 0) {  // rounding left nothing of p - q
-    whole = true;
-    best = cta_best(draw(a, d, i, tid, kDrawThreads, true), s);
+  bool whole = !rejected, alone = ctas == 1;
+  Best best;
+  while (true) {
+    best = Best{0.0f, 0.0f, -1, -1};
+    if (some) best = draw(a, d, i, alone ? tid : rank * kDrawThreads + tid, alone ? kDrawThreads : ctas * kDrawThreads, whole, s);
+    best = cta_best(best, s);
+    if (!alone) {
+      cluster_wait();  // all have started
+      if (tid == 0) *in_first(&s.cluster[rank]) = best;
+      __syncwarp();
+      cluster_arrive();
+      if (rank != 0) return;
+      cluster_wait();
+      if (warp == 0) best = warp_best(lane < ctas ? s.cluster[lane] : Best{0.0f, 0.0f, -1, -1});
+      alone = true;
+    }
     if (tid == 0) s.next = best.v1;
+    __syncthreads();
+    if (!some || whole || s.next >= 0) break;
+    whole = true;  // rounding left nothing of p - q: from p, by this CTA
   }
   if (tid == 0 && best.v2 >= 0 && best.k1 - best.k2 <= kNear * best.k1) {
-    auto key = [&](int v) {
-      double r = exp(((double)load_one(a.target, d.p_at + v, a.target_dtype) - d.ps.x) * a.inverse) / d.ps.y;
-      if (!whole && d.q) r -= exp(((double)load_one(a.draft, d.q_at + v, a.draft_dtype) - d.qs.x) * a.draft_inverse) / d.qs.y;
+    double key[2];
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      const int v = k ? best.v2 : best.v1;
+      double r = probability64(load_one(a.target, d.p_at + v, a.target_dtype), d.ps, a.inverse);
+      if (!whole && d.q) r -= probability64(load_one(a.draft, d.q_at + v, a.draft_dtype), d.qs, a.draft_inverse);
       const uint4 word = philox(make_uint4((uint32_t)v >> 2, a.step + d.stay, (uint32_t)i, 1u), a.seed);
       const uint32_t w = v & 2 ? (v & 1 ? word.w : word.z) : (v & 1 ? word.y : word.x);
-      return r / -log((double)uniform(w));
-    };
-    const double k1 = key(best.v1), k2 = key(best.v2);
-    if (k2 > k1 || (k2 == k1 && best.v2 < best.v1)) s.next = best.v2;
+      key[k] = r / -log((double)uniform(w));
+    }
+    if (key[1] > key[0] || (key[1] == key[0] && best.v2 < best.v1)) s.next = best.v2;
   }
   __syncthreads();
   write_said(a, i, d.stay, s.next, tid, kDrawThreads);
