@@ -6,8 +6,8 @@
 // above the CTA's best so far needs its logarithm; 1 - U is known exactly from the word.
 //
 // Rows after the first draft that does not stay are not needed. Where there are more rows than the device takes at once, CTAs come in the order of
-// the drafts' places, whoever finishes a place decides on its draft, and parts of later places that find theirs decided return
-// at once. Results do not depend on how many do: whoever decides joins the same parts in the same order.
+// the drafts' places, whoever finishes a place decides on its draft, and parts of later places that find
+// theirs decided are left out. Results do not depend on how many are: whoever decides joins the same parts in the same order.
 //
 // What is near a border is settled in fp64: a draft whose U q and p differ by less than 2^-16 of p, and the two best tokens where they do.
 #include "verify_common.cuh"
@@ -34,6 +34,7 @@ struct VerifyArgs {
   int32_t* said;
   int32_t* count;
   float2* parts;     // n x (gamma + 1) x (target, draft) x parts: (largest, sum); at temperature 0 (largest or NaN, token)
+  float* logit;      // n x (gamma + 1) x (target, draft): the draft's, NaN where it is no token
   int32_t* first;    // n: the first place whose draft is known not to stay; NULL: all rows are taken
   int32_t* arrived;  // n x (gamma + 1): parts of a place that are done
   int64_t target_stride_n, target_stride_t, draft_stride_n, draft_stride_t;
@@ -80,16 +81,15 @@ __device__ __forceinline__ int row_token(const VerifyArgs& a, int i, int t) {
 // p and q of one token in 64 bits.
 __device__ __noinline__ double probability64(float x, float2 stats, double inverse) { return exp(((double)x - stats.x) * inverse) / stats.y; }
 
-// Whether draft t stays, given that all before it do.
-__device__ __noinline__ bool draft_stays(const VerifyArgs& a, int i, int t, int x, float2 ps, float2 qs) {
-  if ((unsigned)x >= (unsigned)a.V || !sound(ps) || !sound(qs)) return false;
-  const float xp = load_one(a.target, i * a.target_stride_n + t * a.target_stride_t + x, a.target_dtype);
-  const float xq = a.draft ? load_one(a.draft, i * a.draft_stride_n + t * a.draft_stride_t + x, a.draft_dtype) : 0.0f;
+// Whether draft t, whose logits are xp and xq, stays, given that all before it do.
+__device__ __noinline__ bool draft_stays(const VerifyArgs& a, int i, int t, float xp, float xq, float2 ps, float2 qs) {
+  if (isnan(xp) || !sound(ps) || !sound(qs)) return false;
   const float u = uniform(philox(make_uint4(0u, a.step + t, (uint32_t)i, 2u), a.seed).x);
   const float p = ex2((xp - ps.x) * a.c) / ps.y, q = a.draft ? ex2((xq - qs.x) * a.draft_c) / qs.y : 1.0f;
   if (fabsf(u * q - p) > kNear * p && p >= 1e-30f) return u * q < p;
   return u * (a.draft ? probability64(xq, qs, a.draft_inverse) : 1.0) < probability64(xp, ps, a.inverse);
 }
+__device__ __forceinline__ float* logit_of(const VerifyArgs& a, int i, int t, int of_draft) { return a.logit + ((int64_t)i * (a.gamma + 1) + t) * 2 + of_draft; }
 
 // Values for `first` and `arrived` before the rows.
 __global__ void __launch_bounds__(256) verify_begin(const __grid_constant__ VerifyArgs a) {
@@ -124,7 +124,7 @@ struct RowShared {
   int last;
 };
 
-// One part of a row by a CTA; its first thread gets what `parts` holds.
+// One part of a row by a CTA; its first warp gets what `parts` holds.
 template <int DT, bool GREEDY, bool HELD>
 __device__ __forceinline__ float2 row_part(const VerifyArgs& a, const Row& row, int part, float c, uint4* held, RowShared& s) {
   constexpr int N = Type<DT>::kPer, WARPS = Form<HELD>::kWarps;
@@ -147,10 +147,9 @@ __device__ __forceinline__ float2 row_part(const VerifyArgs& a, const Row& row, 
     f = warp_first(f);
     if (lane == 0) s.first[warp] = f;
     __syncthreads();
-    if (warp != 0) return make_float2(0.0f, 0.0f);
     f = warp_first(s.first[lane & (WARPS - 1)]);
     int token = -1;
-    if (lane == 0 && !f.bad && f.top > -INFINITY) {
+    if (tid == 0 && !f.bad && f.top > -INFINITY) {
       float x[N];
       values_of<DT>(load_vector<DT>(row, f.at), x);
 #pragma unroll
@@ -167,7 +166,6 @@ __device__ __forceinline__ float2 row_part(const VerifyArgs& a, const Row& row, 
     Sums q = warp_joined(p, c);
     if (lane == 0) s.part[warp] = q;
     __syncthreads();
-    if (warp != 0) return make_float2(0.0f, 0.0f);
     q = parts_joined(s.part[min(lane, WARPS - 1)], WARPS, c);
     return make_float2(q.ref, q.s);
   }
@@ -184,13 +182,14 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) v
   const int part = blockIdx.x & ((1 << a.parts_shift) - 1), of_draft = rest & pair, t = (rest >> pair) / a.n, i = (rest >> pair) - t * a.n;
   const int have = drafts_of(a, i);
   if (t + of_draft > have) return;
+  const void* p = of_draft ? a.draft : a.target;
+  const int dtype = of_draft ? a.draft_dtype : a.target_dtype;
+  const float c = of_draft ? a.draft_c : a.c;
   if (a.first) {
     if (__syncthreads_or(tid == 0 && *(volatile const int32_t*)(a.first + i) < t)) return;
   }
-  const void* p = of_draft ? a.draft : a.target;
   const int64_t at = of_draft ? i * a.draft_stride_n + t * a.draft_stride_t : i * a.target_stride_n + t * a.target_stride_t;
-  const int dtype = of_draft ? a.draft_dtype : a.target_dtype;
-  const float c = of_draft ? a.draft_c : a.c;
+  const int x = t < have ? __ldg(a.tokens + (int64_t)i * a.gamma + t) : -1;
   float2 mine;
   if (dtype == WHEAD_BF16) mine = row_part<WHEAD_BF16, GREEDY, HELD>(a, row_at<WHEAD_BF16>(p, at, a.V), part, c, held, s);
   else if (dtype == WHEAD_F16) mine = row_part<WHEAD_F16, GREEDY, HELD>(a, row_at<WHEAD_F16>(p, at, a.V), part, c, held, s);
@@ -198,6 +197,7 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) v
   if (tid >= 32) return;
   if (tid == 0) {
     __stcg(parts_of(a, i, t, of_draft) + part, mine);
+    if (!GREEDY && part == 0) __stcg(logit_of(a, i, t, of_draft), (unsigned)x < (unsigned)a.V ? load_one(p, at + x, dtype) : NAN);
     s.last = 0;
     if (a.first && t < have) {
       unsigned done;
@@ -208,13 +208,12 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) v
   __syncwarp();
   if (!s.last) return;
   // the place is done: its draft is decided on
-  const int x = a.tokens[(int64_t)i * a.gamma + t];
   bool stays;
   if constexpr (GREEDY) {
     stays = x >= 0 && row_token(a, i, t) == x;
   } else {
     const float2 ps = row_sums(a, i, t, 0), qs = pair ? row_sums(a, i, t, 1) : make_float2(0.0f, 1.0f);
-    stays = draft_stays(a, i, t, x, ps, qs);
+    stays = draft_stays(a, i, t, __ldcg(logit_of(a, i, t, 0)), pair ? __ldcg(logit_of(a, i, t, 1)) : 0.0f, ps, qs);
   }
   if (tid == 0 && !stays) atomicMin(a.first + i, t);
 }
@@ -258,14 +257,16 @@ __device__ __forceinline__ void add(Best& b, float k, int v) {
     b.v2 = v;
   }
 }
+// Over a warp; every lane gets them. Keys are not negative, and such floats are ordered as their bits.
 __device__ __forceinline__ Best warp_best(Best b) {
-#pragma unroll 1
-  for (int o = 16; o; o >>= 1) {
-    const Best y{__shfl_xor_sync(~0u, b.k1, o), __shfl_xor_sync(~0u, b.k2, o), __shfl_xor_sync(~0u, b.v1, o), __shfl_xor_sync(~0u, b.v2, o)};
-    add(b, y.k1, y.v1);
-    add(b, y.k2, y.v2);
-  }
-  return b;
+  const unsigned high = __reduce_max_sync(~0u, b.v1 >= 0 ? __float_as_uint(b.k1) : 0u);
+  const int v = __reduce_min_sync(~0u, b.v1 >= 0 && __float_as_uint(b.k1) == high ? b.v1 : INT_MAX);
+  const bool won = b.v1 == v;
+  const float k2 = won ? b.k2 : b.k1;
+  const int v2 = won ? b.v2 : b.v1;
+  const unsigned next = __reduce_max_sync(~0u, v2 >= 0 ? __float_as_uint(k2) : 0u);
+  const int w = __reduce_min_sync(~0u, v2 >= 0 && __float_as_uint(k2) == next ? v2 : INT_MAX);
+  return Best{__uint_as_float(high), __uint_as_float(next), v == INT_MAX ? -1 : v, w == INT_MAX ? -1 : w};
 }
 
 struct DrawShared {
@@ -275,27 +276,38 @@ struct DrawShared {
   Best cluster[kMaxCluster];
 };
 
-// Four logits from `at` on, of which `live` are there, as they are; `wide`: they can be read as one. What is not there is -inf.
-__device__ __forceinline__ uint4 load_quad(const void* p, int64_t at, int dtype, bool wide, int live) {
-  if (wide && live >= 4) {
-    if (dtype == WHEAD_F32) return __ldg(reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at));
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + at));
-    return make_uint4(v.x, v.y, 0u, 0u);
+// Four logits from `at` on, as they are; `wide`: they can be read as one.
+template <int DT>
+using Quad = std::conditional_t<DT == WHEAD_F32, uint4, uint2>;
+template <int DT, bool WIDE>
+__device__ __forceinline__ Quad<DT> load_quad(const void* p, int64_t at) {
+  if constexpr (DT == WHEAD_F32) {
+    const uint32_t* x = static_cast<const uint32_t*>(p) + at;
+    if constexpr (WIDE) return __ldg(reinterpret_cast<const uint4*>(x));
+    else return make_uint4(__ldg(x), __ldg(x + 1), __ldg(x + 2), __ldg(x + 3));
+  } else {
+    const unsigned short* x = static_cast<const unsigned short*>(p) + at;
+    if constexpr (WIDE) return __ldg(reinterpret_cast<const uint2*>(x));
+    else return make_uint2(__ldg(x) | (uint32_t)__ldg(x + 1) << 16, __ldg(x + 2) | (uint32_t)__ldg(x + 3) << 16);
   }
-  uint32_t w[4];
-  if (dtype == WHEAD_F32) {
-    for (int k = 0; k < 4; ++k) w[k] = k < live ? __ldg(static_cast<const uint32_t*>(p) + at + k) : Type<WHEAD_F32>::kNone;
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  const uint32_t none = (dtype == WHEAD_BF16 ? Type<WHEAD_BF16>::kNone : Type<WHEAD_F16>::kNone) & 0xFFFFu;
-  for (int k = 0; k < 4; ++k) w[k] = k < live ? __ldg(static_cast<const unsigned short*>(p) + at + k) : none;
-  return make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, 0u, 0u);
 }
-__device__ __forceinline__ void quad_values(const uint4& v, int dtype, float (&x)[4]) {
-  if (dtype == WHEAD_F32) {
+// A row's last ones, fewer than four; -inf for the rest.
+template <int DT>
+__device__ __noinline__ Quad<DT> load_last(const void* p, int64_t at, int live) {
+  uint32_t w[4];
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (DT == WHEAD_F32) w[k] = k < live ? __ldg(static_cast<const uint32_t*>(p) + at + k) : Type<DT>::kNone;
+    else w[k] = k < live ? (uint32_t)__ldg(static_cast<const unsigned short*>(p) + at + k) : Type<DT>::kNone & 0xFFFFu;
+  }
+  if constexpr (DT == WHEAD_F32) return make_uint4(w[0], w[1], w[2], w[3]);
+  else return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+template <int DT>
+__device__ __forceinline__ void quad_values(const Quad<DT>& v, float (&x)[4]) {
+  if constexpr (DT == WHEAD_F32) {
     x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
   } else {
-    const float2 lo = whead_kv_impl::unpack16(v.x, dtype), hi = whead_kv_impl::unpack16(v.y, dtype);
+    const float2 lo = whead_kv_impl::unpack16(v.x, DT), hi = whead_kv_impl::unpack16(v.y, DT);
     x[0] = lo.x; x[1] = lo.y; x[2] = hi.x; x[3] = hi.y;
   }
 }
@@ -305,74 +317,92 @@ struct DrawRow {
   int64_t p_at, q_at;
   float2 ps, qs;
   int stay, drafted;       // the draft that does not stay, -1: none
-  bool q, p_wide, q_wide;  // q: there is a row of the draft's to take off
+  bool q, wide;            // there is a row of the draft's to take off; quads can be read as one
 };
 
-// The best tokens of four at a time, from `from` on in steps; `whole`: of p itself, else of max(p - q, 0). Philox takes some half of the issue
-// slots; a token that the bound does not rule out (a few dozen of a CTA) takes a loop of its own, so that its logarithm and division are
-// there once and not four times in the loop over all.
+// The best tokens of four at a time, from `from` on in steps; `whole`: of p itself, else of max(p - q, 0). Philox takes half of the issue
+// slots, the exponentials as long on their own unit. A token that the bound does not rule out (a few dozen of a CTA) takes a loop of its own,
+// so that its logarithm and division are there once and not eight times in the loop over all.
+template <int PT, int QT, bool WIDE>
 __device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int i, int from, int step, bool whole, DrawShared& s) {
+  constexpr int kTurn = 2;             // quads of a thread whose loads are under way at once
+  constexpr int DT = QT < 0 ? PT : QT; // of the draft's row, where there is one
   Best best{0.0f, 0.0f, -1, -1};
   const float p_off = -log2f(d.ps.y), q_off = -log2f(d.qs.y);
-  const bool with_q = d.q && !whole;
-  const int quads = (a.V + 3) / 4, taken = !whole && !a.draft ? d.drafted : -1;
+  const bool with_q = QT >= 0 && d.q && !whole;
+  const int quads = (a.V + 3) / 4, full = a.V / 4, taken = QT < 0 && !whole ? d.drafted : -1;
   float known = 0.0f;  // less than the CTA's best key by 2^-15, as far as this warp knows it
-  uint4 x[3], y[3];    // this turn's, and two turns' ahead
-  auto load = [&](int g, uint4& u, uint4& v) {
-    if (g < quads) {
-      u = load_quad(a.target, d.p_at + 4 * g, a.target_dtype, d.p_wide, a.V - 4 * g);
-      if (with_q) v = load_quad(a.draft, d.q_at + 4 * g, a.draft_dtype, d.q_wide, a.V - 4 * g);
-    }
-  };
-  load(from, x[0], y[0]);
-  load(from + step, x[1], y[1]);
 #pragma unroll 1
-  for (int g = from; __any_sync(~0u, g < quads); g += step) {
-    load(g + 2 * step, x[2], y[2]);
-    float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (g < quads) {
-      quad_values(x[0], a.target_dtype, r);
+  for (int g0 = from; __any_sync(~0u, g0 < quads); g0 += kTurn * step) {
+    Quad<PT> x[kTurn];
+    Quad<DT> y[kTurn];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) r[k] = ex2(__fmaf_rn(r[k] - d.ps.x, a.c, p_off));
+    for (int n = 0; n < kTurn; ++n) {
+      const int g = g0 + n * step;
+      if (g < full) {
+        x[n] = load_quad<PT, WIDE>(a.target, d.p_at + 4 * g);
+        if (with_q) y[n] = load_quad<DT, WIDE>(a.draft, d.q_at + 4 * g);
+      } else if (g < quads) {
+        x[n] = load_last<PT>(a.target, d.p_at + 4 * g, a.V - 4 * g);
+        if (with_q) y[n] = load_last<DT>(a.draft, d.q_at + 4 * g, a.V - 4 * g);
+      }
+    }
+    float r[4 * kTurn];
+    uint32_t w[4 * kTurn];
+#pragma unroll
+    for (int n = 0; n < kTurn; ++n) {
+      const int g = g0 + n * step;
+      const uint4 word = philox(make_uint4((uint32_t)g, a.step + d.stay, (uint32_t)i, 1u), a.seed);
+      w[4 * n] = word.x; w[4 * n + 1] = word.y; w[4 * n + 2] = word.z; w[4 * n + 3] = word.w;
+      float p[4];
+      quad_values<PT>(x[n], p);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) p[k] = ex2(__fmaf_rn(p[k] - d.ps.x, a.c, p_off));
       if (with_q) {
         float q[4];
-        quad_values(y[0], a.draft_dtype, q);
+        quad_values<DT>(y[n], q);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] -= ex2(__fmaf_rn(q[k] - d.qs.x, a.draft_c, q_off));
+        for (int k = 0; k < 4; ++k) p[k] -= ex2(__fmaf_rn(q[k] - d.qs.x, a.draft_c, q_off));
       }
-      if (taken >> 2 == g) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if ((taken & 3) == k) r[k] = 0.0f;
-      }
+      for (int k = 0; k < 4; ++k) r[4 * n + k] = g >= quads || (QT < 0 && taken == 4 * g + k) ? 0.0f : p[k];
     }
-    const uint4 word = philox(make_uint4((uint32_t)g, a.step + d.stay, (uint32_t)i, 1u), a.seed);
-    const uint32_t w[4] = {word.x, word.y, word.z, word.w};
+    if (known == 0.0f) {  // E < (1 - U) / U: a key that is reached, before any is known
+      float low = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4 * kTurn; ++e) {
+        const float u = uniform(w[e]);
+        low = fmaxf(low, r[e] * __fdividef(u, 1.0f - u));
+      }
+      known = warp_max(low) * (1.0f - 0x1p-14f);
+    }
     // r / E <= r / (1 - U) and 1 - U > 2 - 2^-23 - f, f = 1 + (w >> 9) 2^-23
     unsigned may = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float rest = (2.0f - 0x1p-23f) - __uint_as_float(__funnelshift_r(w[k], 0x7Fu, 9));
-      may |= r[k] > known * rest ? 1u << k : 0u;
+    for (int e = 0; e < 4 * kTurn; ++e) {
+      const float rest = (2.0f - 0x1p-23f) - __uint_as_float(__funnelshift_r(w[e], 0x7Fu, 9));
+      may |= r[e] > known * rest ? 1u << e : 0u;
     }
     if (__any_sync(~0u, may != 0)) {
       while (may) {
-        const int k = __ffs(may) - 1;
+        const int e = __ffs(may) - 1;
         may &= may - 1;
-        const float rk = k & 2 ? (k & 1 ? r[3] : r[2]) : (k & 1 ? r[1] : r[0]);
-        const uint32_t wk = k & 2 ? (k & 1 ? w[3] : w[2]) : (k & 1 ? w[1] : w[0]);
-        add(best, rk / -logf(uniform(wk)), 4 * g + k);
+        float re = 0.0f;
+        uint32_t we = 0;
+#pragma unroll
+        for (int n = 0; n < 4 * kTurn; ++n)
+          if (n == e) {
+            re = r[n];
+            we = w[n];
+          }
+        add(best, re / -logf(uniform(we)), 4 * (g0 + e / 4 * step) + e % 4);
       }
       __syncwarp();
       const float high = warp_max(best.k1);
-      if ((threadIdx.x & 31) == 0) atomicMax(&s.known, __float_as_int(high));  // positive floats are ordered as their bits
+      if ((threadIdx.x & 31) == 0) atomicMax(&s.known, __float_as_int(high));
       known = fmaxf(known, high * (1.0f - 0x1p-15f));
     }
     known = fmaxf(known, __int_as_float(*(volatile int*)&s.known) * (1.0f - 0x1p-15f));
-    x[0] = x[1];
-    x[1] = x[2];
-    y[0] = y[1];
-    y[1] = y[2];
   }
   return best;
 }
@@ -390,6 +420,8 @@ __device__ __forceinline__ Best cta_best(Best b, DrawShared& s) {
   return b;
 }
 
+// PT, QT: types of the target's and the draft's logits, QT -1: drafts without logits.
+template <int PT, int QT>
 __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_constant__ VerifyArgs a) {
   after_previous();
   __shared__ DrawShared s;
@@ -406,12 +438,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
   __syncthreads();
   // which drafts stay: where rows have been left out it is known already
   for (int t = a.first ? known + warp : warp; t <= known; t += kDrawWarps) {
-    const int x = t < have ? tokens[t] : -1;
+    const float xp = __ldcg(logit_of(a, i, t, 0)), xq = a.draft ? __ldcg(logit_of(a, i, t, 1)) : 0.0f;
     const float2 ps = row_sums(a, i, t, 0), qs = t < have && a.draft ? row_sums(a, i, t, 1) : make_float2(0.0f, 1.0f);
     if (lane == 0) {
       s.ps[t] = ps;
       s.qs[t] = qs;
-      if (t < known && !draft_stays(a, i, t, x, ps, qs)) atomicMin(&s.stay, t);
+      if (t < known && !draft_stays(a, i, t, xp, xq, ps, qs)) atomicMin(&s.stay, t);
     }
   }
   __syncthreads();
@@ -424,14 +456,14 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
   d.q = rejected && a.draft && sound(d.qs);
   d.p_at = i * a.target_stride_n + d.stay * a.target_stride_t;
   d.q_at = i * a.draft_stride_n + d.stay * a.draft_stride_t;
-  const int p_size = a.target_dtype == WHEAD_F32 ? 4 : 2, q_size = a.draft_dtype == WHEAD_F32 ? 4 : 2;
-  d.p_wide = ((reinterpret_cast<uintptr_t>(a.target) + d.p_at * p_size) & (4 * p_size - 1)) == 0;
-  d.q_wide = d.q && ((reinterpret_cast<uintptr_t>(a.draft) + d.q_at * q_size) & (4 * q_size - 1)) == 0;
+  auto wide = [](const void* p, int64_t at, int size) { return ((reinterpret_cast<uintptr_t>(p) + at * size) & (4 * size - 1)) == 0; };
+  d.wide = wide(a.target, d.p_at, Type<PT>::kSize) && (QT < 0 || !d.q || wide(a.draft, d.q_at, QT == WHEAD_F32 ? 4 : 2));
   bool whole = !rejected, alone = ctas == 1;
   Best best;
   while (true) {
     best = Best{0.0f, 0.0f, -1, -1};
-    if (some) best = draw(a, d, i, alone ? tid : rank * kDrawThreads + tid, alone ? kDrawThreads : ctas * kDrawThreads, whole, s);
+    const int from = alone ? tid : rank * kDrawThreads + tid, step = alone ? kDrawThreads : ctas * kDrawThreads;
+    if (some) best = d.wide ? draw<PT, QT, true>(a, d, i, from, step, whole, s) : draw<PT, QT, false>(a, d, i, from, step, whole, s);
     best = cta_best(best, s);
     if (!alone) {
       cluster_wait();  // all have started
@@ -453,8 +485,8 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       const int v = k ? best.v2 : best.v1;
-      double r = probability64(load_one(a.target, d.p_at + v, a.target_dtype), d.ps, a.inverse);
-      if (!whole && d.q) r -= probability64(load_one(a.draft, d.q_at + v, a.draft_dtype), d.qs, a.draft_inverse);
+      double r = probability64(load_one(a.target, d.p_at + v, PT), d.ps, a.inverse);
+      if (QT >= 0 && !whole && d.q) r -= probability64(load_one(a.draft, d.q_at + v, QT), d.qs, a.draft_inverse);
       const uint4 word = philox(make_uint4((uint32_t)v >> 2, a.step + d.stay, (uint32_t)i, 1u), a.seed);
       const uint32_t w = v & 2 ? (v & 1 ? word.w : word.z) : (v & 1 ? word.y : word.x);
       key[k] = r / -log((double)uniform(w));
@@ -480,34 +512,57 @@ int most_parts_shift(int64_t n) {
 static_assert(kMaxParts == 1 << 4, "");
 
 struct Layout {
-  int64_t first, arrived, total;
+  int64_t logit, first, arrived, total;
 };
 Layout layout(int64_t n, int gamma) {
   const int64_t places = n * (gamma + 1);
   Layout l;
-  l.first = whead_kv_impl::align256((places * 2 << most_parts_shift(n)) * (int64_t)sizeof(float2));
+  l.logit = whead_kv_impl::align256((places * 2 << most_parts_shift(n)) * (int64_t)sizeof(float2));
+  l.first = l.logit + whead_kv_impl::align256(places * 2 * 4);
   l.arrived = l.first + whead_kv_impl::align256(n * 4);
   l.total = l.arrived + whead_kv_impl::align256(places * 4);
   return l;
 }
 
-int launch(const VerifyArgs& from, int device, int sms, cudaStream_t stream) {
+template <int PT, int QT>
+int launch_draw(const VerifyArgs& a, int device, cudaStream_t stream) {
   static std::atomic<bool> granted[kMaxDevices];
+  return launch_clusters(verify_draw<PT, QT>, a.n, 1 << a.ctas_shift, kDrawThreads, 0, stream, granted, device, a);
+}
+template <int PT>
+int launch_draw(const VerifyArgs& a, int device, cudaStream_t stream) {
+  if (!a.draft) return launch_draw<PT, -1>(a, device, stream);
+  switch (a.draft_dtype) {
+    case WHEAD_BF16: return launch_draw<PT, WHEAD_BF16>(a, device, stream);
+    case WHEAD_F16: return launch_draw<PT, WHEAD_F16>(a, device, stream);
+    default: return launch_draw<PT, WHEAD_F32>(a, device, stream);
+  }
+}
+
+int launch(const VerifyArgs& from, int device, int sms, cudaStream_t stream) {
   VerifyArgs a = from;
   const bool greedy = a.inverse == 0.0;
   const int pair = a.draft ? 1 : 0;
   const int64_t places = (int64_t)a.n * (a.gamma + 1), bytes = (int64_t)a.V * std::max(dtype_size(a.target_dtype), pair ? dtype_size(a.draft_dtype) : 0);
   // parts of 16 KB or more, as many as there is room for (by the entries)
-  const int most = most_parts_shift(a.n);
   auto groups = [&](int shift) { return (int)(((bytes / (kGroup * 16) + 2) >> shift) + 1); };
-  while (a.parts_shift < most && bytes >> (a.parts_shift + 1) >= 16384) ++a.parts_shift;
-  const int64_t ctas = places << (pair + a.parts_shift);
-  // all at once: parts held. More: parts streamed, and what is decided left out.
-  const bool held = groups(a.parts_shift) <= kHeldGroups && ctas <= (int64_t)sms * Form<true>::kCtas;
+  auto fits = [&](int shift) { return groups(shift) <= kHeldGroups && places << (pair + shift) <= (int64_t)sms * Form<true>::kCtas; };
+  int shift = 0;
+  while (shift < most_parts_shift(a.n) && bytes >> (shift + 1) >= 16384) ++shift;
+  // parts held where all are there at once so, if need be in fewer parts
+  int less = shift;
+  while (less > 0 && !fits(less)) --less;
+  const bool held = fits(less);
+  a.parts_shift = held ? less : shift;
   a.held = groups(a.parts_shift);
+  const int64_t ctas = places << (pair + a.parts_shift);
+  // else parts streamed; where they are more than the device takes at once, what is decided is left out
   int rc = WHEAD_OK;
-  if (ctas > (int64_t)sms * Form<false>::kCtas && a.gamma > 0) rc = whead_kv_impl::launch_after(verify_begin, dim3((unsigned)((places + 255) / 256)), 256, 0, stream, a);
-  else a.first = nullptr;
+  if (ctas > (int64_t)sms * Form<false>::kCtas && a.gamma > 0) {
+    rc = whead_kv_impl::launch_after(verify_begin, dim3((unsigned)((places + 255) / 256)), 256, 0, stream, a);
+  } else {
+    a.first = nullptr;
+  }
   if (rc != WHEAD_OK) return rc;
   if (greedy) rc = held ? launch_rows<true, true>(a, ctas, device, stream) : launch_rows<true, false>(a, ctas, device, stream);
   else rc = held ? launch_rows<false, true>(a, ctas, device, stream) : launch_rows<false, false>(a, ctas, device, stream);
@@ -515,7 +570,11 @@ int launch(const VerifyArgs& from, int device, int sms, cudaStream_t stream) {
   if (greedy) return whead_kv_impl::launch_after(verify_greedy, dim3((unsigned)a.n), (a.gamma + 32) / 32 * 32, 0, stream, a);
   a.ctas_shift = 0;
   while ((2 << a.ctas_shift) <= kMaxCluster && (int64_t)a.n << (a.ctas_shift + 1) <= (int64_t)sms * 3 && a.V >> (a.ctas_shift + 1) >= 4 * kDrawThreads) ++a.ctas_shift;
-  return launch_clusters(verify_draw, a.n, 1 << a.ctas_shift, kDrawThreads, 0, stream, granted, device, a);
+  switch (a.target_dtype) {
+    case WHEAD_BF16: return launch_draw<WHEAD_BF16>(a, device, stream);
+    case WHEAD_F16: return launch_draw<WHEAD_F16>(a, device, stream);
+    default: return launch_draw<WHEAD_F32>(a, device, stream);
+  }
 }
 
 }  // namespace
@@ -558,6 +617,7 @@ extern "C" int whead_verify(const whead_verify_args* x) {
   a.said = x->said;
   a.count = x->count;
   a.parts = reinterpret_cast<float2*>(w);
+  a.logit = reinterpret_cast<float*>(w + l.logit);
   a.first = reinterpret_cast<int32_t*>(w + l.first);
   a.arrived = reinterpret_cast<int32_t*>(w + l.arrived);
   a.target_stride_n = x->target_stride_n;
