@@ -291,6 +291,12 @@ __device__ __forceinline__ Quad<DT> load_quad(const void* p, int64_t at) {
     else return make_uint2(__ldg(x) | (uint32_t)__ldg(x + 1) << 16, __ldg(x + 2) | (uint32_t)__ldg(x + 3) << 16);
   }
 }
+template <int DT>
+__device__ __forceinline__ Quad<DT> no_quad() {
+  constexpr uint32_t x = Type<DT>::kNone;
+  if constexpr (DT == WHEAD_F32) return make_uint4(x, x, x, x);
+  else return make_uint2(x, x);
+}
 // A row's last ones, fewer than four; -inf for the rest.
 template <int DT>
 __device__ __noinline__ Quad<DT> load_last(const void* p, int64_t at, int live) {
@@ -345,6 +351,9 @@ __device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int 
       } else if (g < quads) {
         x[n] = load_last<PT>(a.target, d.p_at + 4 * g, a.V - 4 * g);
         if (with_q) y[n] = load_last<DT>(a.draft, d.q_at + 4 * g, a.V - 4 * g);
+      } else {
+        x[n] = no_quad<PT>();
+        y[n] = no_quad<DT>();
       }
     }
     float r[4 * kTurn];
@@ -365,7 +374,7 @@ __device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int 
         for (int k = 0; k < 4; ++k) p[k] -= ex2(__fmaf_rn(q[k] - d.qs.x, a.draft_c, q_off));
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) r[4 * n + k] = g >= quads || (QT < 0 && taken == 4 * g + k) ? 0.0f : p[k];
+      for (int k = 0; k < 4; ++k) r[4 * n + k] = QT < 0 && taken == 4 * g + k ? 0.0f : p[k];
     }
     if (known == 0.0f) {  // E < (1 - U) / U: a key that is reached, before any is known
       float low = 0.0f;
@@ -377,13 +386,14 @@ __device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int 
       known = warp_max(low) * (1.0f - 0x1p-14f);
     }
     // r / E <= r / (1 - U) and 1 - U > 2 - 2^-23 - f, f = 1 + (w >> 9) 2^-23
-    unsigned may = 0;
+    auto over = [&](int e) { return __fmaf_rn(known, __uint_as_float(__funnelshift_r(w[e], 0x7Fu, 9)) - (2.0f - 0x1p-23f), r[e]); };
+    float most = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4 * kTurn; ++e) {
-      const float rest = (2.0f - 0x1p-23f) - __uint_as_float(__funnelshift_r(w[e], 0x7Fu, 9));
-      may |= r[e] > known * rest ? 1u << e : 0u;
-    }
-    if (__any_sync(~0u, may != 0)) {
+    for (int e = 0; e < 4 * kTurn; ++e) most = fmaxf(most, over(e));
+    if (__any_sync(~0u, most > 0.0f)) {
+      unsigned may = 0;
+#pragma unroll
+      for (int e = 0; e < 4 * kTurn; ++e) may |= over(e) > 0.0f ? 1u << e : 0u;
       while (may) {
         const int e = __ffs(may) - 1;
         may &= may - 1;
