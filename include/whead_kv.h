@@ -102,12 +102,13 @@ typedef struct {
   int32_t window;           /* 0, or the number of latest keys that a token sees (needs causal) */
   int32_t tree_words;       /* 64-bit words of a token's mask: 64 * tree_words >= max_q */
   float scale;              /* of the scores q . k */
+  int32_t sinks;            /* with a window: the slot's first keys that stay visible behind it */
 } whead_kv_attend_args;
 
 /*
  * Attention of each entry's query tokens over its slot's keys and values. With T query tokens and length L, query t
  * stands at position p = L - T + t, so that append comes before attend. It sees the keys j < L, and of those, with
- * causal, j <= p; with a window, j > p - window; with a tree, for j >= L - T, those whose bit j - (L - T) is set in its
+ * causal, j <= p; with a window, j > p - window or j < sinks; with a tree, for j >= L - T, those whose bit j - (L - T) is set in its
  * mask. A query that sees none gives zeros and lse -inf. Scores, which may be of any finite size, maxima, exponentials and sums
  * are in fp32; the exponentials are rounded to f16 (2^-11 at most) where they meet the values.
  * Device errors: WHEAD_ERR_INVALID_ARG for an entry whose offsets are out of order or past total, or that has more than max_q

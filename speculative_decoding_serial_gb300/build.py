@@ -13,10 +13,10 @@ LIB = os.path.join(BUILD, "libwhead.so")
 # copied a step ahead), the 4-bit KV cache's calls, the verification of drafts; compiled in parallel
 SOURCES = [os.path.join(CSRC, n) for n in ("whead_api.cu", "walk_resident.cu", "walk_resident_rec.cu",
                                            "walk_async.cu", "walk_async_rec.cu",
-                                           "kv_cache.cu", "kv_attend.cu", "kv_attend_tiles.cu",
+                                           "kv_cache.cu", "kv_attend.cu", "kv_attend_sinks.cu", "kv_attend_tiles.cu", "kv_attend_tiles_sinks.cu",
                                            "verify_logprobs.cu", "verify_drafts.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, n) for n in ("walk_kernel.cuh", "walk_launch.cuh", "walk_launch.h",
-                                                      "kv_common.cuh", "kv_schedule.cuh", "verify_common.cuh")] + [
+                                                      "kv_common.cuh", "kv_schedule.cuh", "kv_attend_rows.cuh", "kv_attend_tiles.cuh", "verify_common.cuh")] + [
     os.path.join(ROOT, "include", n) for n in ("whead.h", "whead_kv.h", "whead_verify.h")]
 # measurement-only library used by the benchmark for the roofline's on-chip figures
 PROBE_LIB = os.path.join(BUILD, "libwhead_probe.so")

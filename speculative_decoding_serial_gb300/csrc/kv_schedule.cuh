@@ -2,7 +2,8 @@
 //
 // The work is a list of items, one for each entry, tile of query rows and KV head. A row is a query token and one of the
 // query heads of a KV head (row = token * group + head in the group), so that all rows of a tile read the same keys. An
-// item is a run of units of UNIT keys, from the first that one of its rows sees to the last. All units, laid end to end,
+// item is a run of units of UNIT keys, from the first that one of its rows sees to the last, but for those between the first keys that stay
+// visible and a window. All units, laid end to end,
 // are cut into as many equal ranges as there are CTAs: ragged lengths need no balancing, and a long sequence alone fills
 // the device. Each item counts kLead units more than it has, ahead of its own: a CTA that goes on to another item spends some 9,000
 // cycles on the joins, the query rows and the first copies, a unit 2,800 to 3,400 (16 sequences of 300 to 8,200 keys: with equal
@@ -33,9 +34,11 @@ struct AttendArgs {
   int planned;  // the CTAs' starts are in the workspace
   int apart;    // a kernel of its own joins the parts (few rows; always so for many)
   int small;    // all units are less than 2^31
+  int sinks;    // first keys that a window leaves visible, 0 without one (with SINKS, below)
+  int early;    // their units
 };
 
-// The rows of a tile for entries of at most `rows` rows a KV head: up to 32 for the kernel of few rows (kv_attend.cu), above for that of many.
+// The rows of a tile for entries of at most `rows` rows a KV head: up to 32 for the kernel of few rows (kv_attend_rows.cuh), above for that of many.
 // Up to 32 rows the keys' bytes and their unpacking are the work, and the rows ride along in one pass; above, every 32 rows would
 // unpack the keys again, and the tiles' products cost the same for 36 rows as for 128. 64 sequences on 8,192 keys, 8 KV heads, by rows
 // and tiles: 32 rows 268 and 399 us, 36 rows 510 and 403; 16 on 4,096: 44 and 61, 80 and 54. Fewer rows have kernels of fewer registers: 4
@@ -48,15 +51,22 @@ inline int tile_rows(int head_dim, int64_t rows) {
 // Most items of a launch: whoever looks through them steps by up to 1024 beyond the last, in ints.
 constexpr int64_t kMaxItems = INT32_MAX - 4096;
 
-// Attention of more than a few rows a KV head (kv_attend_tiles.cu); head_dim 64 or 128.
+// Attention of few rows a KV head, in tiles of 8, 16 or 32 (kv_attend_rows.cuh), and of more (kv_attend_tiles.cuh; head_dim 64 or 128).
+template <bool SINKS>
+int launch_few(const struct HostCache& h, const AttendArgs& a, int max_q, int tile);
+template <bool SINKS>
 int launch_tiles(const struct HostCache& h, const AttendArgs& a, int max_q);
 
 // One (entry, row tile): its rows and the units that they see.
 struct Tile {
   int slot, len, tokens, first;  // first: row of q of the entry's first token
   int row0, rows;                // the tile's first row, and its rows
-  int unit0, units;              // units of one KV head
+  int unit0, units;              // units of one KV head that are seen, and those that are left out before them (with SINKS: after the first keys')
 };
+// A tile's unit as a unit of the slot. SINKS: the call has first keys that stay visible. Its kernels are apart: one for both cost the others 2 to 4 %
+// (32 sequences on 2,000 to 32,768 keys 120.6 us and 122.7, 8 x 17 tokens 31.3 and 32.7, prompts with a window 146 and 149).
+template <bool SINKS>
+__device__ __forceinline__ int unit_at(const AttendArgs& a, const Tile& t, int u) { return (!SINKS || u >= a.early ? t.unit0 : 0) + u; }
 
 // The token of a row: division by the group, by multiplication with its reciprocal rounded up to 33 bits (Granlund and Montgomery, "Division
 // by invariant integers using multiplication", 1994, figure 4.1). A division takes some 150 cycles of latency, and there are several
@@ -77,7 +87,7 @@ inline void set_group(AttendArgs* a, int group) {
 // as an int holds, so that their difference is formed only where it is not.
 __device__ __forceinline__ int window_begin(const AttendArgs& a, int pos) { return pos >= a.window ? pos - a.window + 1 : 0; }
 
-template <int UNIT>
+template <int UNIT, bool SINKS>
 __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, int item, int tile_rows) {
   Tile t;
   const int i = a.row_tiles == 1 ? item : item / a.row_tiles, m = item - i * a.row_tiles;
@@ -105,6 +115,7 @@ __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, i
   if (a.causal) hi = min(max(t.len - t.tokens + t1 + 1, 0), t.len);
   if (a.window) lo = window_begin(a, t.len - t.tokens + t0);
   t.unit0 = lo / UNIT;
+  if (SINKS) t.unit0 = max(t.unit0 - a.early, 0);
   t.units = max((hi + UNIT - 1) / UNIT - t.unit0, 1);  // at least one: somebody has to write the rows
   return t;
 }
@@ -112,12 +123,13 @@ __device__ __forceinline__ Tile make_tile(const Cache& c, const AttendArgs& a, i
 // What a tile counts for in the division of the work: all KV heads' units, and their leads.
 __device__ __forceinline__ long long tile_cost(const Cache& c, const Tile& t) { return t.units ? (long long)(t.units + kLead) * c.kv_heads : 0; }
 
-// The keys that a row sees: lo <= j < hi, and the bits of its mask for j >= draft.
+// The keys that a row sees: lo <= j < hi (with SINKS, j < sinks too), and the bits of its mask for j >= draft.
 struct RowView {
   int lo, hi, draft;
   const unsigned long long* bits;
 };
 
+template <bool SINKS>
 __device__ __forceinline__ RowView row_view(const AttendArgs& a, const Tile& t, int row) {
   RowView v{0, 0, 0x7FFFFFFF, nullptr};
   if (row >= t.row0 + t.rows) return v;
@@ -132,8 +144,9 @@ __device__ __forceinline__ RowView row_view(const AttendArgs& a, const Tile& t, 
   return v;
 }
 
-__device__ __forceinline__ bool sees(const RowView& v, int j) {
-  if (j < v.lo || j >= v.hi) return false;
+template <bool SINKS>
+__device__ __forceinline__ bool sees(const AttendArgs& a, const RowView& v, int j) {
+  if ((j < v.lo && (!SINKS || j >= a.sinks)) || j >= v.hi) return false;
   if (j < v.draft) return true;
   const int u = j - v.draft;
   return (v.bits[u >> 6] >> (u & 63)) & 1;
@@ -204,7 +217,7 @@ struct SchedShared {
 };
 
 // This CTA's start, from the lengths themselves (few items).
-template <int THREADS, int UNIT>
+template <int THREADS, int UNIT, bool SINKS>
 __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a, int tile_rows, SchedShared& s) {
   const int items = a.n * a.row_tiles;
   Start r;
@@ -212,7 +225,7 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
     // every warp finds the start for itself, a lane an item: no barrier before the CTA's first loads, and 32-bit sums
     const int lane = threadIdx.x & 31;
     Tile tile{};
-    if (lane < items) tile = make_tile<UNIT>(c, a, lane, tile_rows);
+    if (lane < items) tile = make_tile<UNIT, SINKS>(c, a, lane, tile_rows);
     const int mine = (int)tile_cost(c, tile);
     int sum = mine;
 #pragma unroll
@@ -242,7 +255,7 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
   Tile tile{};
   for (int base = 0; base < items; base += THREADS) {
     const int it = base + threadIdx.x;
-    if (it < items) tile = make_tile<UNIT>(c, a, it, tile_rows);
+    if (it < items) tile = make_tile<UNIT, SINKS>(c, a, it, tile_rows);
     mine = it < items ? tile_cost(c, tile) : 0;
     long long all;
     before = r.total + scan64<THREADS>(mine, s.warps, all);
@@ -265,7 +278,7 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
     long long sum = 0;
     for (int base = 0; base < items && sum <= x; base += THREADS) {
       const int it = base + threadIdx.x;
-      mine = it < items ? tile_cost(c, make_tile<UNIT>(c, a, it, tile_rows)) : 0;
+      mine = it < items ? tile_cost(c, make_tile<UNIT, SINKS>(c, a, it, tile_rows)) : 0;
       long long all;
       before = sum + scan64<THREADS>(mine, s.warps, all);
       if (mine > 0 && before <= x && x < before + mine) {
@@ -282,7 +295,7 @@ __device__ __forceinline__ Start find_start(const Cache& c, const AttendArgs& a,
 }
 
 // The same for all CTAs of a launch, by one CTA, into the workspace (many items).
-template <int UNIT>
+template <int UNIT, bool SINKS>
 static __global__ void __launch_bounds__(1024, 1) attend_plan(const __grid_constant__ Cache c, const __grid_constant__ AttendArgs a, int tile_rows, int ctas) {
   after_previous();
   __shared__ long long warps[32];
@@ -291,7 +304,7 @@ static __global__ void __launch_bounds__(1024, 1) attend_plan(const __grid_const
   for (int base = 0; base < items; base += 1024) {
     const int it = base + threadIdx.x;
     long long all;
-    scan64<1024>(it < items ? tile_cost(c, make_tile<UNIT>(c, a, it, tile_rows)) : 0, warps, all);
+    scan64<1024>(it < items ? tile_cost(c, make_tile<UNIT, SINKS>(c, a, it, tile_rows)) : 0, warps, all);
     total += all;
   }
   Start r;
@@ -300,7 +313,7 @@ static __global__ void __launch_bounds__(1024, 1) attend_plan(const __grid_const
   long long sum = 0;
   for (int base = 0; base < items; base += 1024) {
     const int it = base + threadIdx.x;
-    const long long mine = it < items ? tile_cost(c, make_tile<UNIT>(c, a, it, tile_rows)) : 0;
+    const long long mine = it < items ? tile_cost(c, make_tile<UNIT, SINKS>(c, a, it, tile_rows)) : 0;
     long long all;
     const long long before = sum + scan64<1024>(mine, warps, all);
     sum += all;
@@ -320,9 +333,9 @@ static __global__ void __launch_bounds__(1024, 1) attend_plan(const __grid_const
   }
 }
 
-template <int THREADS, int UNIT>
+template <int THREADS, int UNIT, bool SINKS>
 __device__ __forceinline__ Start get_start(const Cache& c, const AttendArgs& a, int tile_rows, SchedShared& s) {
-  if (!a.planned) return find_start<THREADS, UNIT>(c, a, tile_rows, s);
+  if (!a.planned) return find_start<THREADS, UNIT, SINKS>(c, a, tile_rows, s);
   if (threadIdx.x == 0) s.has_tile = 0;
   __syncthreads();
   Start r;
@@ -347,14 +360,14 @@ __device__ __forceinline__ void put_record(const Cache& c, int item, int h, int 
 // Joins the parts of the items that are cut: block (k, z) the z-th `slice` rows of the item that begins in CTA k's range. Bound by
 // latency, so four parts' loads are under way at once. A kernel of its own spreads this over the device: by the last CTA of each
 // item it took 20 us of 84 (8 sequences, 68 rows, 5 parts), and 55 of 71 for one sequence (32 rows, 32 parts).
-template <int D, int ROWS, int UNIT>
+template <int D, int ROWS, int UNIT, bool SINKS>
 __global__ void __launch_bounds__(128) join_parts(const __grid_constant__ Cache c, const __grid_constant__ AttendArgs a, int slice) {
   after_previous();
   const int4 record = __ldcg(reinterpret_cast<const int4*>(c.records) + blockIdx.x);
   const int parts = record.z;
   if (parts == 0) return;
   constexpr int kPart = ROWS * (D + 2), kLanes = D / 4, kAt = 128 / kLanes;
-  const Tile tile = make_tile<UNIT>(c, a, record.x, ROWS);
+  const Tile tile = make_tile<UNIT, SINKS>(c, a, record.x, ROWS);
   const float gv = c.v_scale[record.y];
   auto part_at = [&](int k) { return c.partial + (int64_t)(k == 0 ? record.w : 2 * ((int)blockIdx.x + k)) * kPart; };
   const int col = threadIdx.x % kLanes * 4;
@@ -404,11 +417,11 @@ __global__ void __launch_bounds__(128) join_parts(const __grid_constant__ Cache 
 // A block takes as many rows as its threads hold, and no second pass (one sequence of 4,096 keys, 256 rows: 35 us, with 16 rows a block
 // 45). Where entries have several tiles there are blocks enough, most with nothing to join, and fewer are better (2 x 2048 tokens 299
 // us, with 4 rows a block 300; one of 2048 on 512 keys 29 and 32).
-template <int D, int ROWS, int UNIT>
+template <int D, int ROWS, int UNIT, bool SINKS>
 int launch_join(const HostCache& h, const AttendArgs& a, int ctas, int max_q) {
   const int64_t most = (int64_t)max_q * a.group, rows = most < ROWS ? most : ROWS;
   const int slice = most > 256 ? 16 : 512 / D;
-  return launch_after(join_parts<D, ROWS, UNIT>, dim3((unsigned)ctas, (unsigned)((rows + slice - 1) / slice)), 128, 0, h.stream, h.c, a, slice);
+  return launch_after(join_parts<D, ROWS, UNIT, SINKS>, dim3((unsigned)ctas, (unsigned)((rows + slice - 1) / slice)), 128, 0, h.stream, h.c, a, slice);
 }
 
 }  // namespace whead_kv_impl

@@ -39,7 +39,7 @@ class KvParams(ctypes.Structure):
 class KvAttendArgs(ctypes.Structure):
     _fields_ = [("q", _vp), ("out", _vp), ("lse", _vp), ("indptr", _vp), ("slots", _vp), ("tree", _vp), ("total", _i64),
                 ("q_token_stride", _i64), ("q_head_stride", _i64), ("n", _i32), ("heads", _i32), ("max_q", _i32),
-                ("dtype", _i32), ("causal", _i32), ("window", _i32), ("tree_words", _i32), ("scale", ctypes.c_float)]
+                ("dtype", _i32), ("causal", _i32), ("window", _i32), ("tree_words", _i32), ("scale", ctypes.c_float), ("sinks", _i32)]
 
 
 _lib = None
@@ -222,13 +222,13 @@ class KvCache:
         self._call(self._lib.whead_kv_read, self._ints(start, (n,), "start"), sl, n, count, code, k.data_ptr(), v.data_ptr())
         return k, v
 
-    def attend(self, q, indptr=None, slots=None, *, scale=None, causal=True, window=0, tree=None, max_q=None, out=None,
+    def attend(self, q, indptr=None, slots=None, *, scale=None, causal=True, window=0, sinks=0, tree=None, max_q=None, out=None,
                lse=None):
         """Attention of q (total, heads, head_dim), bfloat16 or float16, over the slots' keys and values: (out, lse).
 
         Entry i's query tokens are rows indptr[i] .. indptr[i + 1] - 1 (None: an equal share each); they are its slot's
         last tokens, so append them first. A token sees its slot's keys, with causal those up to itself, with a window the
-        latest `window` of these. tree (int64, (total,) or (total, words)): for each token, the bits of the entry's own
+        latest `window` of these and of the slot's first `sinks` (streams that a model has to see the beginning of). tree (int64, (total,) or (total, words)): for each token, the bits of the entry's own
         tokens that it sees, besides everything before them. scale defaults to head_dim ** -0.5. With indptr, max_q says
         how many query tokens an entry has at most (default: total, or as many as tree has bits for); one that has more is
         reported by status() and its rows are not written. A token that sees nothing gets zeros and -inf. out (as q,
@@ -259,10 +259,10 @@ class KvCache:
             words, bits = 1 if tree.dim() == 1 else tree.shape[1], tree.data_ptr()
         if max_q is None:
             max_q = total // max(n, 1) if indptr is None else min(total, 64 * words) if words else total
-        if not (INT_MIN <= window <= INT_MAX and INT_MIN <= max_q <= INT_MAX):  # ctypes would wrap them; the library refuses what is negative
-            raise ValueError("0 <= window, max_q < 2^31 is wanted")
+        if not (INT_MIN <= window <= INT_MAX and INT_MIN <= max_q <= INT_MAX and INT_MIN <= sinks <= INT_MAX):
+            raise ValueError("0 <= window, max_q, sinks < 2^31 is wanted")  # ctypes would wrap them; the library refuses what is negative
         a = KvAttendArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr(), ip, sl, bits, total, strides[0], strides[1], n, heads, max_q, code,
-                         bool(causal), window, words, self._scale if scale is None else scale)
+                         bool(causal), window, words, self._scale if scale is None else scale, sinks)
         self._call(self._lib.whead_kv_attend, ctypes.addressof(a))
         return out, lse
 

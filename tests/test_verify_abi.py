@@ -53,6 +53,17 @@ def test_logprobs_refuses(L, kw, code):
     assert keep is not None
 
 
+def test_first_tokens_below_zero_are_refused(L):
+    """sinks of the cache's attention (whead_kv.h)."""
+    from speculative_decoding_serial_gb300 import kv
+    K = kv.load()
+    p = kv.KvParams(page_size=64, kv_heads=8, head_dim=128, max_seqs=4, max_pages=16, num_pages=64, pool=FAKE, lens=FAKE, refs=FAKE, tables=FAKE,
+                    k_scale=FAKE, v_scale=FAKE, workspace=FAKE, workspace_bytes=1 << 40)
+    a = kv.KvAttendArgs(q=FAKE, out=FAKE, lse=FAKE, total=8, q_token_stride=4096, q_head_stride=128, n=2, heads=32, max_q=4, causal=1, window=9, scale=0.1,
+                        sinks=-1)
+    assert K.whead_kv_attend(ctypes.addressof(p), ctypes.addressof(a)) == wh.ERR_INVALID_ARG
+
+
 def test_no_rows_are_no_work(L):
     assert L.whead_logprobs(None) == wh.ERR_INVALID_ARG
     assert L.whead_verify(None) == wh.ERR_INVALID_ARG
