@@ -20,7 +20,10 @@ namespace whead_verify_impl {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kMaxRuns = 4224;  // largest values kept by a CTA: of groups, or of runs of 2^shift groups in rows of more (2^24 logits: shift 4)
+static_assert(64 % kMaxCluster == 0, "");
 constexpr int kListed = 128, kVectors = 96, kCandidates = kVectors * 8, kSubs = 64;
 
 struct LogprobArgs {
@@ -45,10 +48,12 @@ struct TopShared {
   int found, listed, vectors;                                       // candidates, groups and vectors that reach the bound
   int list[kListed];
   alignas(16) uint32_t sub[kSubs];                                  // largest values of the CTA's parts
+  alignas(16) uint32_t all[kSubs];                                  // of the row's
+  int pushed;                                                       // numbers in `best`, in the cluster's first CTA
   uint4 vector[kVectors];
   int vector_at[kVectors];
   alignas(16) unsigned long long candidate[kCandidates];            // key, then the complement of the token
-  alignas(16) unsigned long long best[kMaxCluster * WHEAD_MAX_TOP]; // each CTA's, in order; 0: none
+  alignas(16) unsigned long long best[kMaxCluster * WHEAD_MAX_TOP]; // the cluster's CTAs' best, in no order (one CTA: in order); 0: none
   // the way for rows where too many values reach the bound
   int picked;                                                       // what pick() found: how many keys, their indexes
   int order[WHEAD_MAX_TOP];
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
   const int n_runs = g1 > g0 ? ((g1 - 1) >> a.shift) - (g0 >> a.shift) + 1 : 0;
   if constexpr (TOP) {
     if (tid == 0) {
-      top_shared.found = top_shared.listed = top_shared.vectors = 0;
+      top_shared.found = top_shared.listed = top_shared.vectors = top_shared.pushed = 0;
       top_shared.bound = ~0u;
     }
     if (tid < kMaxCluster * WHEAD_MAX_TOP) top_shared.best[tid] = 0;
@@ -229,13 +234,30 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
   if constexpr (TOP) {
     TopShared& ts = top_shared;
     // The CTA's values are in kSubs parts. The `top`-th of their largest values is one that `top` values reach, and on rows
-    // without an order few more do. It is the lowest that fewer than `top` are greater than.
+    // without an order few more do. It is the lowest that fewer than `top` are greater than. For a long list a cluster's CTAs find one
+    // bound for the row, by kSubs parts of it, which lets that many fewer values through (64 x 248064 top 20: 16.5 us, by bounds of
+    // their own 19.7); for a short list the trade takes longer than it saves (1 x 151936 top 5: 6.3 us, by bounds of their own 5.4).
+    const uint32_t* sub = ts.sub;
+    if (ctas > 1) cluster_wait();  // all have started
+    if (ctas > 1 && a.top > 8) {
+      const int each = kSubs >> a.ctas_shift;  // of this CTA's: every `ctas` parts are one
+      if (tid < kSubs) {
+        const int k = tid & (each - 1), to = tid >> (6 - a.ctas_shift);
+        uint32_t high = 0;
+        for (int e = 0; e < ctas; ++e) high = max(high, ts.sub[k * ctas + e]);
+        *cg::this_cluster().map_shared_rank(&ts.all[rank * each + k], to) = high;
+      }
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+      sub = ts.all;
+    }
     if (tid < kSubs) {
-      const uint32_t mine = ts.sub[tid];
+      const uint32_t mine = sub[tid];
       int before = 0;
 #pragma unroll
       for (int k = 0; k < kSubs; k += 4) {
-        const uint4 y = *reinterpret_cast<const uint4*>(ts.sub + k);
+        const uint4 y = *reinterpret_cast<const uint4*>(sub + k);
         before += (y.x > mine) + (y.y > mine) + (y.z > mine) + (y.w > mine);
       }
       const uint32_t low = __reduce_min_sync(~0u, before < a.top ? mine : ~0u);
@@ -272,14 +294,15 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
       if (x >= least) ts.candidate[atomicAdd(&ts.found, 1)] = (unsigned long long)key_of<DT>(x) << 32 | (uint32_t)~(uint32_t)(ts.vector_at[e / N] * N + e % N - row.off);
     }
     __syncthreads();
-    if (ctas > 1) cluster_wait();  // all have started
     // ranked by counting those that come before
-    unsigned long long* best = ctas > 1 ? in_first(ts.best) + rank * a.top : ts.best;
     const int found = ts.found;
     for (int e = tid; e < found; e += THREADS) {
       const unsigned long long mine = ts.candidate[e];
       const int before = greater(ts.candidate, found, mine);
-      if (before < a.top) best[before] = mine;
+      if (before < a.top) {
+        if (ctas > 1) in_first(ts.best)[atomicAdd(in_first(&ts.pushed), 1)] = mine;
+        else ts.best[before] = mine;
+      }
     }
   } else if (ctas > 1) {
     cluster_wait();
@@ -318,7 +341,7 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
   }
   if constexpr (TOP) {
     TopShared& ts = top_shared;
-    const int n = ctas * a.top;  // at most a place a thread
+    const int n = ctas > 1 ? ts.pushed : a.top;  // at most a place a thread
     const unsigned long long mine = tid < n && !bad ? ts.best[tid] : 0ull;
     int before = tid;
     if (ctas > 1 && mine != 0) before = greater(ts.best, n, mine);
