@@ -79,7 +79,8 @@ typedef struct {
  * rounding leaves nothing of that), in the row after the last draft from p; so that every token is one of the target's distribution.
  * It is the token of the largest p_v / E_v, E_v = -log U_v, equal ones: the lowest.
  * U = ((w >> 9) + 0.5) 2^-23 from words of Philox4x32-10 with key `seed` and counters (v / 4, step + t, i, 1), word v % 4, for the token
- * after entry i's drafts in row t, and (0, step + t, i, 2), word 0, for draft t: apart from the walk's own, whose last word is 0.
+ * after entry i's drafts in row t, and (0, step + t, i, 2), word 0, for draft t (sums modulo 2^32): apart from the walk's own, whose last
+ * word is 0.
  * A draft that is no token of 0..V-1 does not stay, nor one whose row of `draft` has no distribution (the next token is then drawn
  * from p). In a row of `target` without a distribution no draft stays and the token after is -1.
  */

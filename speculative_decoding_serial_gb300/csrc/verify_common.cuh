@@ -201,6 +201,11 @@ __device__ __forceinline__ float shift_of(float from, float to, float c) {
   const float k0 = from * c, k1 = to * c;
   return max_nan(plain(k0) && plain(k1) ? k0 - k1 : (from - to) * c, -1e4f);
 }
+// What a reference's k was rounded by: s is the sum of 2^((x - ref) c) times 2^off, off some 2^-24 of k.
+__device__ __forceinline__ float offset_of(float ref, float c) {
+  const float k = ref * c;
+  return plain(k) ? __fmaf_rn(ref, c, -k) : 0.0f;
+}
 // The same sums for another reference. A part without a value has s = a = 0 and any reference.
 __device__ __forceinline__ Sums moved(const Sums& p, float ref, float c) {
   if (p.s == 0.0f) return Sums{ref, 0.0f, 0.0f};

@@ -10,6 +10,10 @@
 // theirs decided are left out. Results do not depend on how many are: whoever decides joins the same parts in the same order.
 //
 // What is near a border is settled in fp64: a draft whose U q and p differ by less than 2^-16 of p, and the two best tokens where they do.
+//
+// 64 entries of 16 drafts, 151,936 logits, bf16 and f32 for the drafts', a draft in five refused: rows 72 us (418 MB at 5.8 TB/s, of which 284 MB are
+// needed: places that began before the one ahead was decided), drawing 27 us (176 issue slots for four tokens of a warp, Philox 86 of them; 256 CTAs on
+// 304 places). 8 entries, greedy, f32: all rows, 14 us, 5.9 TB/s. One entry, bf16: rows 5 us, drawing 8, ten times four tokens a thread.
 #include "verify_common.cuh"
 
 #include <algorithm>
@@ -51,12 +55,14 @@ __device__ __forceinline__ float2* parts_of(const VerifyArgs& a, int i, int t, i
 }
 __device__ __forceinline__ float uniform(uint32_t w) { return ((float)(w >> 9) + 0.5f) * 0x1p-23f; }
 
-// A row's largest value and sum, by a warp, from its parts; every lane gets them.
+// A row's largest value m and sum of 2^((x - m) c), by a warp, from its parts; every lane gets them.
 __device__ __forceinline__ float2 row_sums(const VerifyArgs& a, int i, int t, int of_draft) {
   const int lane = threadIdx.x & 31, n = 1 << a.parts_shift;
   const float2 x = __ldcg(parts_of(a, i, t, of_draft) + min(lane, n - 1));
-  const Sums s = parts_joined(Sums{x.x, x.y, 0.0f}, n, of_draft ? a.draft_c : a.c);
-  return make_float2(s.ref, s.s);
+  const float c = of_draft ? a.draft_c : a.c;
+  const Sums s = parts_joined(Sums{x.x, x.y, 0.0f}, n, c);
+  const float off = offset_of(s.ref, c);  // mostly so small that 1 - off ln 2 is nearer to 2^-off than the exponential's own rounding
+  return make_float2(s.ref, fabsf(off) < 0x1p-12f ? __fmaf_rn(s.s, -off * kLn2, s.s) : s.s * ex2(-off));
 }
 // Whether a row has a distribution.
 __device__ __forceinline__ bool sound(float2 x) { return x.y > 0.0f && x.y < INFINITY; }

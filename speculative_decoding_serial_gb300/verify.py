@@ -167,6 +167,7 @@ def verify(target, tokens, draft=None, *, temperature=0.0, draft_temperature=Non
         if draft.shape != (n, gamma, V):
             raise ValueError(f"draft: shape {(n, gamma, V)} is wanted")
         draft_ptr, (d0, d1, _) = draft.data_ptr(), draft_strides
+    step, seed = int(step), int(seed)  # whole numbers of any type
     if not 0 <= step < 2 ** 32:
         raise ValueError("0 <= step < 2^32 is wanted")
     need = L.whead_verify_workspace_bytes(n, gamma)

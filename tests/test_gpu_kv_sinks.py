@@ -139,6 +139,19 @@ def test_attend_ragged_trees_with_first_tokens(torch, kv, d, group):
         check(torch, c, kvs, q, counts, out, lse, window, sinks, tree.view(np.int64), rows=[0, 3, 4, 20, 63])
 
 
+@pytest.mark.parametrize("t,d,n", [(1, 64, 700), (9, 64, 700), (17, 64, 900), (1, 256, 700)])
+def test_attend_many_entries_with_first_tokens(torch, kv, t, d, n):
+    """So many entries that their division is planned ahead; a few looked at."""
+    g = np.random.RandomState(n + t)
+    lens = g.randint(t, 300, n).tolist()
+    c, kvs = fill(torch, kv, lens, 1, d, 16, seed=3)
+    q = randn(torch, (n * t, 4, d), torch.bfloat16, 4)
+    out, lse = c.attend(q, window=37, sinks=20)
+    assert c.status() == 0
+    for i in list(range(0, n, 97)) + [n - 1]:
+        check(torch, c, [kvs[i]], q[i * t:(i + 1) * t], [t], out[i * t:(i + 1) * t], lse[i * t:(i + 1) * t], 37, 20, rows=[0, t - 1])
+
+
 def test_first_tokens_in_shared_pages_and_other_slots(torch, kv):
     """A prompt's pages shared by forks, entries in another order, strides, and what lies past a slot's end."""
     h, d, t = 2, 128, 3

@@ -383,6 +383,62 @@ def test_tokens_said_are_distributed_as_the_target_says(torch, V):
     assert abs((count > 1).float().mean().item() - stay) <= 5 * math.sqrt(0.25 / n)
 
 
+def test_verify_of_logits_far_from_zero(torch, V):
+    """4,000,000 entries of four tokens whose logits lie around 1,000: a reference rounded to fp32 is off by up to 6e-5 there (in log2 units), which the
+    sums must not take over into p and q. Decisions nearer than 2^-19 may go either way: p and q are off by some 2^-21 each (the sum's
+    exponentials 2^-22, its additions, the factor log2(e) rounded times differences below 16)."""
+    n, temperature = 4000000, 1.0
+    g = torch.Generator(device="cuda").manual_seed(4)
+    at = torch.rand((n, 1, 1), generator=g, device="cuda") * 400 + 800
+    x = at + torch.randn((n, 2, 4), generator=g, device="cuda") * 2
+    y = at + 50 + torch.randn((n, 1, 4), generator=g, device="cuda") * 2
+    tokens = torch.randint(0, 4, (n, 1), generator=g, device="cuda", dtype=torch.int32)
+    said, count = V.verify(x, tokens, y, temperature=temperature, seed=99)
+    i = tokens.long()
+    p, q = (torch.softmax(z[:, 0].double() / temperature, -1).gather(1, i)[:, 0].cpu().numpy() for z in (x, y))
+    u = R.uniform(R.philox(99, 0, 0, np.arange(n), 2)[0])
+    stays, sure = u * q < p, np.abs(u * q - p) > 2.0 ** -19 * p
+    got = (count > 1).cpu().numpy()
+    assert (got == stays)[sure].all(), int((got != stays)[sure].sum())
+    assert sure.mean() > 0.9999 and torch.equal(said[:, 0][count > 1], tokens[:, 0][count > 1])
+
+
+def test_seeds_and_steps_of_any_integer_type(torch, V):
+    x, y, tokens = case(torch, 2, 3, 100, torch.float32, torch.float32)
+    want = V.verify(x, tokens, y, temperature=1.0, seed=2 ** 63 + 5, step=7)
+    got = V.verify(x, tokens, y, temperature=1.0, seed=np.uint64(2 ** 63 + 5), step=np.int64(7))
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    a, b = V.verify(x, tokens, y, temperature=1.0, seed=-1), V.verify(x, tokens, y, temperature=1.0, seed=2 ** 64 - 1)
+    assert torch.equal(a[0], b[0])
+
+
+def test_first_calls_of_a_process_inside_a_capture(torch):
+    """Nothing of a call needs to have run before it is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch
+from speculative_decoding_serial_gb300 import verify as V
+x = torch.randn((3, 5, 4001), device="cuda").bfloat16()
+y, t = x[:, :4].float(), x[:, :4].argmax(-1).to(torch.int32)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    a = V.logprobs(x, top=5)
+    b = V.verify(x, t, y, temperature=1.0, seed=3)
+    c = V.verify(x, t)
+g.replay()
+torch.cuda.synchronize()
+for got, want in ((a, V.logprobs(x, top=5)), (b, V.verify(x, t, y, temperature=1.0, seed=3)), (c, V.verify(x, t))):
+    assert all(p is q or torch.equal(p, q) for p, q in zip(got, want))
+print("same")
+"""
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and "same" in run.stdout, run.stderr
+
+
 def test_verify_twice_on_another_stream_and_replayed(torch, V):
     x, y, tokens = case(torch, 7, 5, 9001, torch.bfloat16, torch.bfloat16)
     want, again = (V.verify(x, tokens, y, temperature=1.0, seed=1) for _ in range(2))
