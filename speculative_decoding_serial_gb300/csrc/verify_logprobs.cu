@@ -10,8 +10,8 @@
 // exactly (pick_candidates; one row 7 -> 21 us, 2,048 rows 122 -> 168 with 20 alternatives of sorted logits). None of this is part of the
 // pass, whose work does not depend on the order of the logits.
 //
-// 4,096 rows of 151,936 bf16 logits: 183 us, the rate of a copy, without alternatives; 206 with the best one (6.0 TB/s; 69 % of the issue slots in use),
-// 223 with 20: while a CTA picks it does not stream. 6 CTAs an SM of 40 registers: with 5 243 us, with 8, which spill, 302. One row: 5.8 us with 5
+// 4,096 rows of 151,936 bf16 logits: 182 us, the rate of a copy, without alternatives; 201 with the best one (6.2 TB/s; 69 % of the issue slots in use),
+// 221 with 20: while a CTA picks it does not stream. 6 CTAs an SM of 40 registers: with 5 18 us more, with 8, which spill, 76. One row: 5.8 us with 5
 // alternatives, 3.7 without: launch, copies, join, bound, ranking and the cluster's trade, a microsecond or less each.
 #include "verify_common.cuh"
 
@@ -29,6 +29,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kMaxRuns = 4224;  // largest values kept by a CTA: of groups, or of runs of 2^shift groups in rows of more (2^24 logits: shift 4)
 static_assert(64 % kMaxCluster == 0, "");
+constexpr int kFetchAhead = 16 * 1024;
 constexpr int kListed = 128, kVectors = 96, kCandidates = kVectors * 8, kSubs = 64;
 
 struct LogprobArgs {
@@ -41,6 +42,7 @@ struct LogprobArgs {
   float* top_logprobs;
   int64_t stride_n, stride_t;
   int t, V, top, ctas_shift, shift, runs, held;  // runs: room for largest values; held: for groups
+  int ahead;                                     // CTAs that the device holds, where a row is one and there are more; else 0
   float c, inverse, inverse_low;                 // log2(e) / T, 1 / T, and what that was rounded by
 };
 
@@ -223,6 +225,18 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
   };
   if (HELD) over_held(g0, g1, held, step);
   else over_groups<DT>(row, g0, g1, step);
+  // While this CTA joins and picks it reads nothing; the beginning of the row that comes in its place is fetched as far as L2 meanwhile (4,096
+  // rows, top 1: 206 us without, 201 with 16 KB, 202 with 32, 206 with 64).
+  if (!HELD && tid == 0 && a.ahead) {
+    const unsigned next = blockIdx.x + a.ahead;
+    if (next < gridDim.x) {
+      const int ni = a.t == 1 ? next : next / a.t;
+      const Row row = row_at<DT>(a.logits, ni * a.stride_n + ((int)next - ni * a.t) * a.stride_t, a.V);
+      const char* from = row.base + (row.off ? 16 : 0);
+      const int bytes = min(kFetchAhead, (a.V * Type<DT>::kSize - 16) & ~15);
+      if (bytes > 0) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(bytes) : "memory");
+    }
+  }
   {
     const Sums w = warp_joined(p, a.c);
     if (lane == 0) s.part[warp] = w;
@@ -414,6 +428,8 @@ extern "C" int whead_logprobs(const whead_logprobs_args* x) {
   const Division d = divide(rows, x->V * dtype_size(x->dtype), sms);
   a.ctas_shift = d.shift;
   a.held = d.groups;
+  const int64_t room = (int64_t)sms * Form<false>::kCtas;
+  a.ahead = !d.held && d.shift == 0 && rows > room ? (int)room : 0;
   while (((d.groups >> a.shift) + 2) > kMaxRuns) ++a.shift;
   a.runs = (d.groups >> a.shift) + 2;
   cudaStream_t stream = static_cast<cudaStream_t>(x->stream);
