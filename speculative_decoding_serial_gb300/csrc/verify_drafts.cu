@@ -131,8 +131,8 @@ struct RowShared {
 };
 
 // One part of a row by a CTA; its first warp gets what `parts` holds.
-template <int DT, bool GREEDY, bool HELD>
-__device__ __forceinline__ float2 row_part(const VerifyArgs& a, const Row& row, int part, float c, uint4* held, RowShared& s) {
+template <int DT, bool GREEDY, bool HELD, typename F>
+__device__ __forceinline__ float2 row_part(const VerifyArgs& a, const Row& row, int part, float c, uint4* held, RowShared& s, F after_pass) {
   constexpr int N = Type<DT>::kPer, WARPS = Form<HELD>::kWarps;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int groups = row_groups<DT>(row), g0 = run_begin(groups, a.parts_shift, part), g1 = run_begin(groups, a.parts_shift, part + 1);
@@ -171,6 +171,7 @@ __device__ __forceinline__ float2 row_part(const VerifyArgs& a, const Row& row, 
     else over_groups<DT>(row, g0, g1, step);
     Sums q = warp_joined(p, c);
     if (lane == 0) s.part[warp] = q;
+    after_pass();
     __syncthreads();
     q = parts_joined(s.part[min(lane, WARPS - 1)], WARPS, c);
     return make_float2(q.ref, q.s);
@@ -196,14 +197,17 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) v
   }
   const int64_t at = of_draft ? i * a.draft_stride_n + t * a.draft_stride_t : i * a.target_stride_n + t * a.target_stride_t;
   const int x = t < have ? __ldg(a.tokens + (int64_t)i * a.gamma + t) : -1;
+  // the draft's logit, by a thread of the second warp: what the first arrives with comes after a barrier
+  auto logit = [&] {
+    if (part == 0 && tid == 32) __stcg(logit_of(a, i, t, of_draft), (unsigned)x < (unsigned)a.V ? load_one(p, at + x, dtype) : NAN);
+  };
   float2 mine;
-  if (dtype == WHEAD_BF16) mine = row_part<WHEAD_BF16, GREEDY, HELD>(a, row_at<WHEAD_BF16>(p, at, a.V), part, c, held, s);
-  else if (dtype == WHEAD_F16) mine = row_part<WHEAD_F16, GREEDY, HELD>(a, row_at<WHEAD_F16>(p, at, a.V), part, c, held, s);
-  else mine = row_part<WHEAD_F32, GREEDY, HELD>(a, row_at<WHEAD_F32>(p, at, a.V), part, c, held, s);
+  if (dtype == WHEAD_BF16) mine = row_part<WHEAD_BF16, GREEDY, HELD>(a, row_at<WHEAD_BF16>(p, at, a.V), part, c, held, s, logit);
+  else if (dtype == WHEAD_F16) mine = row_part<WHEAD_F16, GREEDY, HELD>(a, row_at<WHEAD_F16>(p, at, a.V), part, c, held, s, logit);
+  else mine = row_part<WHEAD_F32, GREEDY, HELD>(a, row_at<WHEAD_F32>(p, at, a.V), part, c, held, s, logit);
   if (tid >= 32) return;
   if (tid == 0) {
     __stcg(parts_of(a, i, t, of_draft) + part, mine);
-    if (!GREEDY && part == 0) __stcg(logit_of(a, i, t, of_draft), (unsigned)x < (unsigned)a.V ? load_one(p, at + x, dtype) : NAN);
     s.last = 0;
     if (a.first && t < have) {
       unsigned done;
