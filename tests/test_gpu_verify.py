@@ -293,6 +293,34 @@ def test_verify_large_vocabulary(torch, V, n):
     check_verify(torch, V, x, tokens, None, 0.9, seed=17)
 
 
+@pytest.mark.parametrize("target,draft", [("bf16", "f32"), ("f16", ""), ("f32", "f32")])
+def test_verify_many_entries_some_refused_early(torch, V, target, draft):
+    """So many that places behind a refused draft are left out; ragged; entries looked at here and there, and twice the same."""
+    n, gamma, vocab = 300, 6, 20011
+    x, y, tokens = case(torch, n, gamma, vocab, getattr(torch, KINDS[target]), getattr(torch, KINDS[draft]) if draft else None, spread=0.4)
+    best = x[:, :gamma].float().argmax(-1).to(torch.int32)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    drafted = torch.randint(0, gamma + 1, (n,), generator=g, device="cuda", dtype=torch.int32)
+    for temperature, said_tokens in ((0.0, torch.where(torch.rand((n, gamma), generator=g, device="cuda") < 0.8, best, tokens)), (1.0, tokens)):
+        for have in (None, drafted):
+            a, b = (V.verify(x, said_tokens, y, temperature=temperature, seed=6, step=1, drafted=have) for _ in range(2))
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            for i in range(0, n, 23):
+                h = gamma if have is None else int(have[i])
+                want, c, margin = R.verify(x[i].double().cpu().numpy(), said_tokens[i].cpu().numpy(), y[i].double().cpu().numpy() if draft else None,
+                                           temperature, temperature, 6, 1, i, h)
+                assert margin < NEAR or (a[0][i].tolist() == want.tolist() and int(a[1][i]) == c), (i, a[0][i].tolist(), want.tolist())
+            assert 1 < a[1].float().mean().item() < gamma
+
+
+@pytest.mark.parametrize("n,vocab", [(1, 7), (3, 5003), (2, 151936), (400, 900)])
+def test_verify_where_nothing_is_left_of_the_difference(torch, V, n, vocab):
+    """Drafts that are no tokens, of the target's own distribution: the token after is drawn from that."""
+    x, _, tokens = case(torch, n, 2, vocab, torch.float32, torch.float32)
+    tokens = torch.full_like(tokens, -1)
+    check_verify(torch, V, x, tokens, x[:, :2], 1.0, seed=21)
+
+
 def test_verify_ragged(torch, V):
     x, y, tokens = case(torch, 12, 6, 3001, torch.bfloat16, torch.bfloat16, spread=0.1)
     drafted = torch.tensor([0, 1, 2, 3, 4, 5, 6, 7, 100, -1, -2 ** 31, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
