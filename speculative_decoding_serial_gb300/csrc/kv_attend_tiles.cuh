@@ -50,7 +50,7 @@ struct Shape {
   static constexpr int kGroup = 18 * D;
   static constexpr int kQ = 128 * D * 2, kK = kBlock * D * 2, kV = D * kBlock * 2;
   static constexpr int kOffWalk = 640;                   // the warps' places
-  static constexpr int kOffQ = 3072, kOffK = kOffQ + TILES * kQ, kOffV = kOffK + kBufs * kK;
+  static constexpr int kOffQ = 3 * 1024, kOffK = kOffQ + TILES * kQ, kOffV = kOffK + kBufs * kK;
   static constexpr int kBytes = kOffV + kBufs * kV + 1024;  // + alignment
   static constexpr int kCols = 512;                         // of tensor memory: two S, then O of each tile
 };
@@ -253,7 +253,7 @@ __device__ __forceinline__ bool next_segment(const Cache& c, const AttendArgs& a
   return true;
 }
 
-static_assert(sizeof(Head) <= 640 && 640 + 20 * sizeof(Walk) <= 3072, "");
+static_assert(sizeof(Head) <= 640 && 640 + 20 * sizeof(Walk) <= 3 * 1024, "");
 
 // A whole warp's wait. One that has run out is reported once; the warp then goes on without waiting, on whatever is there, to its end.
 __device__ __forceinline__ void await(const Cache& c, uint32_t bar, uint32_t parity, bool& dead) {
