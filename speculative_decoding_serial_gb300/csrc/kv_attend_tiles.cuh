@@ -185,15 +185,11 @@ __device__ __forceinline__ float row_exp(uint32_t st, const uint32_t (&seen)[2],
   return fmaxf(t0, t1);
 }
 
-// The keys key .. key + 31 that a row sees, as bits.
+// The keys key .. key + 31 that a row sees, as bits: without branches, in which the lanes would part (prompts with a window 139 -> 137 us).
 template <bool SINKS>
 __device__ __forceinline__ uint32_t sees32(const AttendArgs& a, const RowView& v, int key) {
-  uint32_t m = ~0u;
-  if (key + 32 > v.hi) m = v.hi <= key ? 0u : (1u << (v.hi - key)) - 1u;
-  if (key < v.lo) {
-    const uint32_t late = v.lo - key >= 32 ? 0u : ~0u << (v.lo - key), early = !SINKS || a.sinks <= key ? 0u : a.sinks - key >= 32 ? ~0u : (1u << (a.sinks - key)) - 1u;
-    m &= late | early;
-  }
+  auto first = [](int n) { return ~__funnelshift_lc(0u, ~0u, max(n, 0)); };  // n bits, at most 32
+  uint32_t m = first(v.hi - key) & (SINKS ? ~first(v.lo - key) | first(a.sinks - key) : ~first(v.lo - key));
   if (v.bits != nullptr && key + 32 > v.draft && m) {
     const int u = key - v.draft;  // the first key's bit
     uint32_t b;
@@ -218,14 +214,17 @@ struct Walk {
   Segment sg;
 };
 
-// The next segment, by a whole warp; false at the end.
+// The next segment, by a whole warp; false at the end. An item's heads follow one another: its tile, whose lengths come from memory, is found once (prompts
+// with a window 145.5 -> 142.8 us, without 305.4 -> 303.7).
 template <int ROWS, bool SINKS>
 __device__ __forceinline__ bool next_segment(const Cache& c, const AttendArgs& a, Walk& w, const SchedShared& sched) {
   const long long cur = w.cur, end = w.end;
   if (cur >= end) return false;
   int item = w.next_item;
   Segment s;
-  if (item == sched.item && sched.has_tile) {
+  if (item == w.sg.item && w.sg.tile.units > 0) {
+    s.tile = w.sg.tile;
+  } else if (item == sched.item && sched.has_tile) {
     s.tile = sched.tile;
   } else {
     while (true) {
@@ -321,7 +320,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
     walk.cur = range_begin(start, blockIdx.x);
     walk.end = range_begin(start, blockIdx.x + 1);
     walk.item_at = start.at;
-    walk.sg.u0 = walk.sg.u1 = 0;
+    walk.sg.u0 = walk.sg.u1 = walk.sg.item = 0;
     walk.sg.tile.units = 0;
     walk.next_item = start.item;
   }
@@ -394,7 +393,9 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
     mbar_wait(drain, 0);
     __syncwarp();
   } else if (warp >= S::kSoft) {
-    // ---- codes to f16 tiles: group w of each block
+    // ---- codes to f16 tiles: group w of each block. With two tiles 64 channels at a time: all roles' code together is more than the SM keeps of
+    // it, and an instruction that is not there was the next reason for a warp to wait after memory and barriers (prompts with a window 142.7 -> 139.4 us,
+    // without 303.9 and 304.5; one tile, 8 x 17 tokens, 31.3 by halves, 30.9 at once).
     const int w = warp - S::kSoft, g = lane >> 2, t = lane & 3;
     const int64_t page_bytes = (int64_t)c.kv_heads * (c.page_size >> 4) * S::kGroup;
     int n = 0;
@@ -452,16 +453,20 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
         if (n >= S::kBufs) await(c, smem_u32(&s.k_free[buf]), used, dead);
         if (key0 < len) {
           uint8_t* to = smem + S::kOffK + buf * S::kK + w * 2048 + g * 128 + (t & 1) * 8;
+#pragma unroll (TILES == 1 ? D / 64 : 1)
+          for (int j = 0; j < D / 64; ++j) {
+            const uint4 kw = j ? rk.code[D / 64 - 1] : rk.code[0];
+            const uint2 ks = j ? rk.scale[D / 64 - 1] : rk.scale[0];
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const uint4 kw = rk.code[b / 4];
-            uint32_t x[4], s0, s1;
-            e2m1x8_to_half2(b % 4 == 0 ? kw.x : b % 4 == 1 ? kw.y : b % 4 == 2 ? kw.z : kw.w, x);
-            e4m3x4_to_half2(b % 4 < 2 ? rk.scale[b / 4].x : rk.scale[b / 4].y, s0, s1);
-            const uint32_t sc = b & 1 ? s1 : s0;
-            uint8_t* at = to + b / 4 * (kBlock * 128) + ((((t >> 1) * 4 + b % 4) ^ g) << 4);
-            *reinterpret_cast<uint2*>(at) = make_uint2(hmul2_low(x[0], sc), hmul2_low(x[2], sc));
-            *reinterpret_cast<uint2*>(at + 1024) = make_uint2(hmul2_high(x[1], sc), hmul2_high(x[3], sc));
+            for (int b = 0; b < 4; ++b) {
+              uint32_t x[4], s0, s1;
+              e2m1x8_to_half2(b == 0 ? kw.x : b == 1 ? kw.y : b == 2 ? kw.z : kw.w, x);
+              e4m3x4_to_half2(b < 2 ? ks.x : ks.y, s0, s1);
+              const uint32_t sc = b & 1 ? s1 : s0;
+              uint8_t* at = to + j * (kBlock * 128) + ((((t >> 1) * 4 + b) ^ g) << 4);
+              *reinterpret_cast<uint2*>(at) = make_uint2(hmul2_low(x[0], sc), hmul2_low(x[2], sc));
+              *reinterpret_cast<uint2*>(at + 1024) = make_uint2(hmul2_high(x[1], sc), hmul2_high(x[3], sc));
+            }
           }
         }
         fence_async();
@@ -480,17 +485,20 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
         }
         uint8_t* to = smem + S::kOffV + buf * S::kV + w / 4 * (D * 128) + g * 128 + t * 4;
         const int c0 = ((w % 4 * 2) ^ g) << 4, c1 = ((w % 4 * 2 + 1) ^ g) << 4;
+#pragma unroll (TILES == 1 ? D / 64 : 1)
+        for (int j = 0; j < D / 64; ++j) {
+          const uint4 vw = j ? rv.code[D / 64 - 1] : rv.code[0], vs = j ? rv.scale[D / 64 - 1] : rv.scale[0];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint4 vw = rv.code[b / 4], vs = rv.scale[b / 4];
-          uint32_t x[4], s0, s1;
-          e2m1x8_to_half2(b % 4 == 0 ? vw.x : b % 4 == 1 ? vw.y : b % 4 == 2 ? vw.z : vw.w, x);
-          e4m3x4_to_half2((b % 4 == 0 ? vs.x : b % 4 == 1 ? vs.y : b % 4 == 2 ? vs.z : vs.w) & live, s0, s1);
-          uint8_t* at = to + b * 2048;
-          *reinterpret_cast<uint32_t*>(at + c0) = hmul2(x[0], s0);
-          *reinterpret_cast<uint32_t*>(at + 1024 + c0) = hmul2(x[1], s0);
-          *reinterpret_cast<uint32_t*>(at + c1) = hmul2(x[2], s1);
-          *reinterpret_cast<uint32_t*>(at + 1024 + c1) = hmul2(x[3], s1);
+          for (int b = 0; b < 4; ++b) {
+            uint32_t x[4], s0, s1;
+            e2m1x8_to_half2(b == 0 ? vw.x : b == 1 ? vw.y : b == 2 ? vw.z : vw.w, x);
+            e4m3x4_to_half2((b == 0 ? vs.x : b == 1 ? vs.y : b == 2 ? vs.z : vs.w) & live, s0, s1);
+            uint8_t* at = to + (j * 4 + b) * 2048;
+            *reinterpret_cast<uint32_t*>(at + c0) = hmul2(x[0], s0);
+            *reinterpret_cast<uint32_t*>(at + 1024 + c0) = hmul2(x[1], s0);
+            *reinterpret_cast<uint32_t*>(at + c1) = hmul2(x[2], s1);
+            *reinterpret_cast<uint32_t*>(at + 1024 + c1) = hmul2(x[3], s1);
+          }
         }
         fence_async();
         __syncwarp();
