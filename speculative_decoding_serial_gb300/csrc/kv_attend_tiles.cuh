@@ -586,6 +586,7 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       bool fresh = true;  // some row of the warp has no reference yet
       float ref = kNoKey;  // in units of the products; m = ref f
       const float bias = __fdividef(kBias, f);
+      const float gv = c.v_scale[sg.h];  // for the end, where its way from memory would be waited for
       float2 l = make_float2(0.f, 0.f);
       for (int u = sg.u0; u < sg.u1; ++u, ++n) {
         const int key0 = unit_at<SINKS>(a, tile, u) * kBlock;
@@ -675,7 +676,6 @@ __global__ void __launch_bounds__((Shape<D, TILES>::kThreads), 1) attend_tiles(c
       const float ll = (l.x + l.y) * back;
       constexpr int kPart = S::kRows * (D + 2);
       const int64_t out_row = (int64_t)(tile.first + tok) * a.heads + head;
-      const float gv = c.v_scale[sg.h];
       float* part = c.partial + (int64_t)part_slot(start, sg, blockIdx.x) * kPart;
       const float scale = whole ? (ll != 0.0f ? gv / ll : 0.0f) : back;
 #pragma unroll 1
