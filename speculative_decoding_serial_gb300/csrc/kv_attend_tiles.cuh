@@ -12,8 +12,8 @@
 // What holds it back. Prompts: no unit is full (53 % of the issue slots, 46 % of the tensor pipe, 41 % of the ALU, 23 % of the
 // exponentials); the roles wait for one another, the longest of them the softmax, one thread a row. At 128 keys a row and block its 128
 // exponentials, as many differences, products, maxima, additions and half as many packings are some 650 issue slots of a warp; eight
-// such warps and the eight that unpack share four schedulers. 2 x 2048 tokens on 4,100 and 6,200 keys, 32 query heads on 8: 303 us,
-// 1.01 PFLOP/s, 53 % of the measured rate of large matrix products; 64 channels 227 us. Two threads a row (half the chain, but a
+// such warps and the eight that unpack share four schedulers. 2 x 2048 tokens on 4,100 and 6,200 keys, 32 query heads on 8: 297 us,
+// 1.03 PFLOP/s, 54 % of the measured rate of large matrix products; 64 channels 225 us; a window of 1,024 133 us, with 100 first tokens 136. Two threads a row (half the chain, but a
 // trade of maxima and sums through shared memory for every block) and blocks of 64 keys (twice the barriers) were slower. For a few
 // tokens a sequence (8 x 17, 31 MB: 30 us) what a CTA does once (tensor memory, query rows, the first blocks, its part for the joining)
 // and the chain through one block: copy, unpack, QK, softmax, PV.
