@@ -386,7 +386,9 @@ __device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int 
 #pragma unroll
       for (int k = 0; k < 4; ++k) r[4 * n + k] = QT < 0 && taken == 4 * g + k ? 0.0f : p[k];
     }
-    if (known == 0.0f) {  // E < (1 - U) / U: a key that is reached, before any is known
+    // E < (1 - U) / U: a key that is reached, before any is known. By a vote: every lane has read s.known for itself while others raise it, and
+    // warp_max needs all lanes to come.
+    if (__all_sync(~0u, known == 0.0f)) {
       float low = 0.0f;
 #pragma unroll
       for (int e = 0; e < 4 * kTurn; ++e) {
