@@ -196,15 +196,16 @@ struct Sums {
   float ref, s, a;
 };
 __device__ __forceinline__ bool plain(float k) { return fabsf(k) < 0x1p23f; }
-// What d becomes less by when the reference goes from one value to another (at most 10,000: 2^-10000 is 0, and times 0 too).
-__device__ __forceinline__ float shift_of(float from, float to, float c) {
-  const float k0 = from * c, k1 = to * c;
-  return max_nan(plain(k0) && plain(k1) ? k0 - k1 : (from - to) * c, -1e4f);
-}
-// What a reference's k was rounded by: s is the sum of 2^((x - ref) c) times 2^off, off some 2^-24 of k.
+// What a reference's k was rounded by: s is the sum of 2^((x - ref) c) times 2^off, off some 2^-24 of k, up to a quarter where k is near 2^23.
 __device__ __forceinline__ float offset_of(float ref, float c) {
-  const float k = ref * c;
+  const float k = __fmul_rn(ref, c);
   return plain(k) ? __fmaf_rn(ref, c, -k) : 0.0f;
+}
+// What d becomes less by when the reference goes from one value to another (at most 10,000: 2^-10000 is 0, and times 0 too). Where one of them has a
+// k and the other none, the sums go from one way of referring to the other.
+__device__ __forceinline__ float shift_of(float from, float to, float c) {
+  const float k0 = __fmul_rn(from, c), k1 = __fmul_rn(to, c);  // as they are: not within a multiply-add
+  return max_nan(plain(k0) && plain(k1) ? k0 - k1 : (from - to) * c + (offset_of(to, c) - offset_of(from, c)), -1e4f);
 }
 // The same sums for another reference. A part without a value has s = a = 0 and any reference.
 __device__ __forceinline__ Sums moved(const Sums& p, float ref, float c) {

@@ -343,17 +343,16 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
     if (TOP) __syncthreads();
     sums = parts_joined(s.part[min(lane, WARPS - 1)], WARPS, a.c);
   }
-  const float top = sums.ref, log_s = log2f(sums.s), k = top * a.c;
+  const float top = sums.ref, log_s = log2f(sums.s), k = top * a.c, off = offset_of(top, a.c);
   const bool none = sums.s == 0.0f, bad = isnan(sums.s);
   auto log_p = [&](float x) {
     if (bad) return sums.s;
     if (none || x == -INFINITY) return -INFINITY;
     // a token at the type's lowest value keeps its finite log probability
-    return plain(k) && plain(x * a.c) ? (__fmaf_rn(x, a.c, -k) - log_s) * kLn2 : (x - top) * a.inverse - log_s * kLn2;
+    return plain(k) && plain(x * a.c) ? (__fmaf_rn(x, a.c, -k) - log_s) * kLn2 : (x - top) * a.inverse - (log_s - off) * kLn2;
   };
   if (tid == THREADS - 32) {  // not the warps that write alternatives
-    // m / T itself, and what k was rounded by
-    const float off = offset_of(top, a.c);
+    // m / T itself, and what k was rounded by (0 where it is not formed)
     if (a.lse) a.lse[r] = bad ? sums.s : none ? -INFINITY : plain(k) ? __fmaf_rn(top, a.inverse, __fmaf_rn(top, a.inverse_low, (log_s - off) * kLn2)) : top * a.inverse + log_s * kLn2;
     if (a.entropy) a.entropy[r] = bad ? sums.s : none ? 0.0f : fmaxf((log_s - __fdividef(sums.a, sums.s)) * kLn2, 0.0f);
     if (a.logprob) a.logprob[r] = log_p(x_token);
