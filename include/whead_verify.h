@@ -77,7 +77,8 @@ typedef struct {
  * Above 0, with p the target's distribution and q the drafts' (without `draft`: all on the draft): draft t stays if all before it do and
  * U_t q(x_t) < p(x_t). In the first row whose draft does not stay the token after it is drawn from max(p - q, 0) (from p, where
  * rounding leaves nothing of that), in the row after the last draft from p; so that every token is one of the target's distribution.
- * It is the token of the largest p_v / E_v, E_v = -log U_v, equal ones: the lowest.
+ * It is the token of the largest p_v / E_v, E_v = -log U_v, equal ones: the lowest. p and q are exact but for fp32's sums and exponentials, some
+ * 2^-20: what is decided by less than that (of p, not of p - q) may go either way, the same way whenever the same call is made.
  * U = ((w >> 9) + 0.5) 2^-23 from words of Philox4x32-10 with key `seed` and counters (v / 4, step + t, i, 1), word v % 4, for the token
  * after entry i's drafts in row t, and (0, step + t, i, 2), word 0, for draft t (sums modulo 2^32): apart from the walk's own, whose last
  * word is 0.

@@ -9,7 +9,9 @@
 // the drafts' places, whoever finishes a place decides on its draft, and parts of later places that find
 // theirs decided are left out. Results do not depend on how many are: whoever decides joins the same parts in the same order.
 //
-// What is near a border is settled in fp64: a draft whose U q and p differ by less than 2^-16 of p, and the two best tokens where they do.
+// What is near a border is settled in fp64: a draft whose U q and p differ by less than 2^-16 of p, and the two best tokens where their keys
+// do. p and q are off by some 2^-20 in fp32, and p - q by p / (p - q) times that, so that keys of p - q are settled from 2^-9 on: drafts' rows as near
+// to the target's as p - q = p / 1000. The sums of p and q stay those of fp32, and three keys so near to one another are not told apart.
 //
 // 64 entries of 16 drafts, 151,936 logits, bf16 and f32 for the drafts', a draft in five refused: rows 72 us (418 MB at 5.8 TB/s, of which 284 MB are
 // needed: places that began before the one ahead was decided), drawing 27 us (176 issue slots for four tokens of a warp, Philox 86 of them; 256 CTAs on
@@ -26,7 +28,8 @@ namespace whead_verify_impl {
 
 namespace {
 
-constexpr float kNear = 0x1p-16f;
+constexpr float kNear = 0x1p-16f;            // relative: what is settled in fp64
+constexpr float kNearOfDifference = 0x1p-9f; // the same for keys of p - q; one draw in 512 or fewer is that near
 constexpr int kDrawThreads = 512, kDrawWarps = kDrawThreads / 32;
 constexpr int kMaxParts = 16;  // of a row
 
@@ -347,7 +350,8 @@ __device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int 
   const float p_off = -log2f(d.ps.y), q_off = -log2f(d.qs.y);
   const bool with_q = QT >= 0 && d.q && !whole;
   const int quads = (a.V + 3) / 4, full = a.V / 4, taken = QT < 0 && !whole ? d.drafted : -1;
-  float known = 0.0f;  // less than the CTA's best key by 2^-15, as far as this warp knows it
+  constexpr float kBelow = 1.0f - 2.0f * kNearOfDifference;  // so that the keys that are settled with the best are not ruled out
+  float known = 0.0f;  // kBelow times the CTA's best key, as far as this warp knows it
 #pragma unroll 1
   for (int g0 = from; __any_sync(~0u, g0 < quads); g0 += kTurn * step) {
     Quad<PT> x[kTurn];
@@ -395,7 +399,7 @@ __device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int 
         const float u = uniform(w[e]);
         low = fmaxf(low, r[e] * __fdividef(u, 1.0f - u));
       }
-      known = warp_max(low) * (1.0f - 0x1p-14f);
+      known = warp_max(low) * kBelow;
     }
     // r / E <= r / (1 - U) and 1 - U > 2 - 2^-23 - f, f = 1 + (w >> 9) 2^-23
     auto over = [&](int e) { return __fmaf_rn(known, __uint_as_float(__funnelshift_r(w[e], 0x7Fu, 9)) - (2.0f - 0x1p-23f), r[e]); };
@@ -422,9 +426,9 @@ __device__ __forceinline__ Best draw(const VerifyArgs& a, const DrawRow& d, int 
       __syncwarp();
       const float high = warp_max(best.k1);
       if ((threadIdx.x & 31) == 0) atomicMax(&s.known, __float_as_int(high));
-      known = fmaxf(known, high * (1.0f - 0x1p-15f));
+      known = fmaxf(known, high * kBelow);
     }
-    known = fmaxf(known, __int_as_float(*(volatile int*)&s.known) * (1.0f - 0x1p-15f));
+    known = fmaxf(known, __int_as_float(*(volatile int*)&s.known) * kBelow);
   }
   return best;
 }
@@ -502,13 +506,14 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw(const __grid_cons
     if (!some || whole || s.next >= 0) break;
     whole = true;  // rounding left nothing of p - q: from p, by this CTA
   }
-  if (tid == 0 && best.v2 >= 0 && best.k1 - best.k2 <= kNear * best.k1) {
+  const bool difference = QT >= 0 && !whole && d.q;
+  if (tid == 0 && best.v2 >= 0 && best.k1 - best.k2 <= (difference ? kNearOfDifference : kNear) * best.k1) {
     double key[2];
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
       const int v = k ? best.v2 : best.v1;
       double r = probability64(load_one(a.target, d.p_at + v, PT), d.ps, a.inverse);
-      if (QT >= 0 && !whole && d.q) r -= probability64(load_one(a.draft, d.q_at + v, QT), d.qs, a.draft_inverse);
+      if (difference) r -= probability64(load_one(a.draft, d.q_at + v, QT), d.qs, a.draft_inverse);
       const uint4 word = philox(make_uint4((uint32_t)v >> 2, a.step + d.stay, (uint32_t)i, 1u), a.seed);
       const uint32_t w = v & 2 ? (v & 1 ? word.w : word.z) : (v & 1 ? word.y : word.x);
       key[k] = r / -log((double)uniform(w));

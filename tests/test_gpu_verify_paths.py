@@ -75,3 +75,26 @@ def test_verify_where_references_pass_the_border(torch, V, sign, n, vocab):  # n
     y = steps_around(torch, (n, 2, vocab), 1e-6, sign, -5, 1, vocab + 2)
     tokens = y.argmax(-1).to(torch.int32)
     check_verify(torch, V, x, tokens, y, 1e-6, seed=31)
+
+
+# ---------------------------------------------------------------------------------------------------- drawing from small differences
+
+def test_draws_where_the_drafts_are_near_the_target(torch, V):  # noqa: F811
+    """2,000,000 entries draw from max(p - q, 0) where that is p / 129: p and q, off by some 2^-20 in fp32, leave it off by 10^-4, in opposite directions
+    for the tokens of this row. The sums are of one exponential of 0 and of some 2^-18, so that their rounding, below 2^-20, counts for all
+    tokens alike (p / (p - q) differs by 2^-19 from token to token): keys that differ by more than 2^-24 are to be told apart."""
+    n, seed = 2000000, 99
+    g = np.random.RandomState(1263)
+    x = np.concatenate([[0], -12.5 - g.rand(7) / 32]).astype(np.float32)
+    y = (x - np.float32(2.0 ** -7)).astype(np.float32)
+    y[0] = 0
+    p, q = R.distribution(x, 1.0), R.distribution(y, 1.0)
+    u = R.uniform(np.stack([np.stack(R.philox(seed, k, 0, np.arange(n), 1), 1) for k in range(2)], 1).reshape(n, 8))
+    key = np.maximum(p - q, 0) / -np.log(u)
+    want, ordered = key.argmax(1), np.sort(key, 1)
+    sure = ordered[:, -1] - ordered[:, -2] > 2.0 ** -24 * ordered[:, -1]
+    target, draft = (torch.from_numpy(z).cuda().expand(n, k, 8) for z, k in ((x, 2), (y, 1)))
+    said, count = V.verify(target, torch.full((n, 1), -1, dtype=torch.int32, device="cuda"), draft, temperature=1.0, seed=seed)
+    assert (count == 1).all()
+    got = said[:, 0].cpu().numpy()
+    assert sure.mean() > 0.99999 and int((got != want)[sure].sum()) == 0
