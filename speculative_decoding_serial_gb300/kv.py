@@ -8,7 +8,7 @@ A serial draft head returns gamma tokens a walk; this cache holds the target's k
     cache.compact(start, keep, count)       # what was accepted stays
     cache.fork(parents)                     # candidates take over one another's sequences
 
-No gradients pass through the cache: inputs that ask for them are refused outside torch.no_grad().
+No gradients pass through the cache: inputs that ask for them are refused outside torch.no_grad(), inputs with forward-mode tangents everywhere.
 Calls go to the current torch stream. They share the cache's workspace: calls on other streams have to be ordered
 after them by events. There is no fallback: without the built library, loading raises.
 """
@@ -177,9 +177,10 @@ class KvCache:
             raise ValueError(f"{what}: a contiguous int32 tensor of shape {shape} on {self.device} is wanted")
         return x.data_ptr()
 
-    def _no_grad(self, what):
-        if self._torch.is_grad_enabled():
-            raise ValueError(f"{what}: the cache passes no gradients on; call it under torch.no_grad() or on detached tensors")
+    @staticmethod
+    def _no_grad(what, *tensors):
+        if _wh.asks_for_gradients(*tensors):
+            raise ValueError(f"{what}: the cache passes no gradients on; call it on detached tensors or, where none has a forward-mode tangent, under torch.no_grad()")
 
     def _entries(self, indptr, slots):
         """How many entries a call has, and the pointers of its offsets and slots."""
@@ -200,8 +201,7 @@ class KvCache:
         ks, vs = k.stride(), v.stride()
         if ks[2] != 1 or vs[2] != 1:
             raise ValueError("k and v: channels have to be contiguous")
-        if k.requires_grad or v.requires_grad:
-            self._no_grad("k and v")
+        self._no_grad("k and v", k, v)
         self._call(self._lib.whead_kv_append, k.data_ptr(), v.data_ptr(), _code(k.dtype, "k and v"), ks[0], ks[1], vs[0], vs[1], ip, sl,
                    n, shape[0])
 
@@ -238,8 +238,7 @@ class KvCache:
         shape, strides = q.shape, q.stride()
         if len(shape) != 3 or shape[2] != self.head_dim or strides[2] != 1 or q.get_device() != self._index:
             raise ValueError(f"q: shape (total, heads, {self.head_dim}) with contiguous channels on the cache's device is wanted")
-        if q.requires_grad:
-            self._no_grad("q")
+        self._no_grad("q", q)
         total, heads = shape[0], shape[1]
         dtype = q.dtype
         code = _code(dtype, "attend", f32=False)

@@ -6,8 +6,8 @@ A walk drafts gamma tokens, the target gives logits after the last token and aft
     cache.compact(start, keep, count)                                              # (kv.py) the others leave the cache
     r = logprobs(logits, said, top=5)                                              # log probabilities, entropy, alternatives
 
-No gradients pass through them: inputs that ask for gradients are refused outside torch.no_grad(). Calls go to the current torch
-stream. There is no fallback: without the built library, loading raises.
+No gradients pass through them: inputs that ask for gradients are refused outside torch.no_grad(), inputs with forward-mode tangents everywhere.
+Calls go to the current torch stream. There is no fallback: without the built library, loading raises.
 """
 from __future__ import annotations
 
@@ -78,12 +78,12 @@ def _logits(x, shape, strides, dims, index, what):
     code = _CODES.get(x.dtype)
     if code is None:
         raise TypeError(f"{what}: {x.dtype} is not supported")
+    if _wh.asks_for_gradients(x):
+        raise ValueError(f"{what}: no gradients are passed on; call it on detached tensors or, where none has a forward-mode tangent, under torch.no_grad()")
     if len(shape) not in dims or shape[-1] < 1 or strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{what}: {' or '.join(map(str, dims))} dimensions are wanted, the last one the vocabulary and contiguous")
     if not x.is_cuda or x.get_device() != index:
         raise ValueError(f"{what}: a tensor on one CUDA device with the others is wanted")
-    if x.requires_grad and _torch.is_grad_enabled():
-        raise ValueError(f"{what}: no gradients are passed on; call it under torch.no_grad() or on detached tensors")
     return code
 
 

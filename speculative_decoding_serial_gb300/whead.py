@@ -129,6 +129,24 @@ def strerror(code: int) -> str:
     return load().whead_strerror(int(code)).decode()
 
 
+_forward_ad = None
+
+
+def asks_for_gradients(*tensors) -> bool:
+    """Whether a call on these tensors would be asked for gradients: backward, outside torch.no_grad(), or forward, by a tangent that
+    one of them carries (which no_grad() does not hold back)."""
+    global _forward_ad
+    if _forward_ad is None:
+        from torch.autograd import forward_ad as _forward_ad
+    if _forward_ad._current_level >= 0 and any(_forward_ad.unpack_dual(x).tangent is not None for x in tensors):
+        return True
+    for x in tensors:
+        if x.requires_grad:
+            import torch
+            return torch.is_grad_enabled()
+    return False
+
+
 def _check(code: int, what: str):
     if code != OK:
         raise WheadError(code, what)

@@ -98,3 +98,21 @@ def test_draws_where_the_drafts_are_near_the_target(torch, V):  # noqa: F811
     assert (count == 1).all()
     got = said[:, 0].cpu().numpy()
     assert sure.mean() > 0.99999 and int((got != want)[sure].sum()) == 0
+
+
+# ---------------------------------------------------------------------------------------------------- gradients that go forward
+
+def test_forward_mode_tangents_are_refused(torch, V):  # noqa: F811
+    from torch.autograd import forward_ad
+    x, y, tokens = case(torch, 2, 3, 100, torch.float32, torch.float32)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        for call in (lambda: V.logprobs(dual), lambda: V.verify(dual, tokens, y, temperature=1.0),
+                     lambda: V.verify(x, tokens, forward_ad.make_dual(y, torch.ones_like(y)), temperature=1.0)):
+            with pytest.raises(ValueError, match="gradients"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="gradients"):  # which keeps no tangent back
+                call()
+        V.logprobs(x)
+        V.logprobs(forward_ad.unpack_dual(dual).primal)
+    V.logprobs(x)
