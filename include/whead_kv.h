@@ -102,7 +102,8 @@ typedef struct {
   int32_t window;           /* 0, or the number of latest keys that a token sees (needs causal) */
   int32_t tree_words;       /* 64-bit words of a token's mask: 64 * tree_words >= max_q */
   float scale;              /* of the scores q . k */
-  int32_t sinks;            /* with a window: the slot's first keys that stay visible behind it */
+  int32_t sinks;            /* with a window: the slot's first keys that stay visible behind it; without one it is not looked at. (Added at the
+                               end: callers built against a header without it are to be rebuilt if they use windows.) */
 } whead_kv_attend_args;
 
 /*

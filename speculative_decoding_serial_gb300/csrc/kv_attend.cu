@@ -13,7 +13,7 @@ extern "C" int whead_kv_attend(const whead_kv* kv, const whead_kv_attend_args* x
   if (x->n < 0 || x->n > kv->max_seqs || x->total < 0 || x->total >= INT_MAX || x->max_q < 0 || x->heads < 1) return WHEAD_ERR_INVALID_ARG;
   if (kv->kv_heads < 1 || x->heads % kv->kv_heads) return WHEAD_ERR_INVALID_ARG;
   if (x->dtype != WHEAD_KV_BF16 && x->dtype != WHEAD_KV_F16) return WHEAD_ERR_UNSUPPORTED;
-  if (x->window < 0 || x->sinks < 0 || ((x->window || x->tree) && !x->causal) || !std::isfinite(x->scale)) return WHEAD_ERR_INVALID_ARG;
+  if (x->window < 0 || (x->window > 0 && x->sinks < 0) || ((x->window || x->tree) && !x->causal) || !std::isfinite(x->scale)) return WHEAD_ERR_INVALID_ARG;
   if (x->tree && (x->tree_words < 1 || (int64_t)x->tree_words * 64 < x->max_q || !aligned(x->tree, 8))) return WHEAD_ERR_INVALID_ARG;
   HostCache h;
   if (x->n == 0 || x->total == 0) return x->total > 0 ? WHEAD_ERR_INVALID_ARG : host_cache(kv, &h);

@@ -258,8 +258,9 @@ class KvCache:
             words, bits = 1 if tree.dim() == 1 else tree.shape[1], tree.data_ptr()
         if max_q is None:
             max_q = total // max(n, 1) if indptr is None else min(total, 64 * words) if words else total
-        if not (INT_MIN <= window <= INT_MAX and INT_MIN <= max_q <= INT_MAX and INT_MIN <= sinks <= INT_MAX):
-            raise ValueError("0 <= window, max_q, sinks < 2^31 is wanted")  # ctypes would wrap them; the library refuses what is negative
+        if not (INT_MIN <= window <= INT_MAX and INT_MIN <= max_q <= INT_MAX and INT_MIN <= sinks <= INT_MAX) or (sinks < 0 and not window):
+            # ctypes would wrap them; the library refuses what is negative, but looks at sinks with a window alone
+            raise ValueError("0 <= window, max_q, sinks < 2^31 is wanted")
         a = KvAttendArgs(q.data_ptr(), out.data_ptr(), lse.data_ptr(), ip, sl, bits, total, strides[0], strides[1], n, heads, max_q, code,
                          bool(causal), window, words, self._scale if scale is None else scale, sinks)
         self._call(self._lib.whead_kv_attend, ctypes.addressof(a))

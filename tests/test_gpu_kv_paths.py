@@ -22,3 +22,13 @@ def test_forward_mode_tangents_are_refused(torch, kv):  # noqa: F811
         c.append(k, v)
     c.attend(q)
     assert c.lens.item() == 1 and c.status() == 0
+
+
+def test_first_tokens_below_zero_are_refused_without_a_window(torch, kv):  # noqa: F811
+    """The library looks at them only with a window; the binding always does."""
+    c = make(kv, torch, 1, 64, 1, 64, 16)
+    k, v, q = (randn(torch, (1, 1, 64), torch.bfloat16, i) for i in range(3))
+    c.append(k, v)
+    with pytest.raises(ValueError):
+        c.attend(q, sinks=-1)
+    assert c.status() == 0
