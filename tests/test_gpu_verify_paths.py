@@ -100,6 +100,87 @@ def test_draws_where_the_drafts_are_near_the_target(torch, V):  # noqa: F811
     assert sure.mean() > 0.99999 and int((got != want)[sure].sum()) == 0
 
 
+# ---------------------------------------------------------------------------------------------------- forms of the kernels
+
+@pytest.mark.parametrize("kind,rows,vocab", [
+    ("bfloat16", 64, 248064), ("float16", 100, 151936), ("float32", 100, 70001),   # 8 CTAs a row, streamed
+    ("bfloat16", 150, 151936), ("float32", 200, 40003),                            # 4
+    ("float16", 300, 100003), ("bfloat16", 450, 40001), ("float32", 310, 20001),   # 2
+    ("bfloat16", 1000, 40000), ("float32", 470, 40000)])                           # 1
+@pytest.mark.parametrize("top", [0, 5, 20])
+def test_logprobs_of_many_rows(torch, V, kind, rows, vocab, top):  # noqa: F811
+    """Rows streamed by clusters of every size, against the model itself; equal and sorted rows among them, which go the exact way."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = (torch.randn((rows, vocab), generator=g, device="cuda") * 3).to(getattr(torch, kind))
+    x[1] = 1.5
+    x[2] = x[2].sort()[0]
+    x[3, 100:] = torch.finfo(x.dtype).min
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    tokens[3] = 50
+    r = V.logprobs(x, tokens, top=top, temperature=0.9)
+    check_rows(r, x, tokens, top, 0.9, [0, 1, 2, 3, rows // 2, rows - 1])
+
+
+@pytest.mark.parametrize("kind", ["bfloat16", "float16", "float32"])
+def test_logprobs_of_rows_with_more_groups_than_a_cta_keeps(torch, V, kind):  # noqa: F811
+    """500 times one row of 2^24 - 1 logits, a CTA each: it keeps the largest values of runs of 16 groups (f32) or 8. A few tokens stand out; then all are
+    equal; then they are in order, with many equal ones."""
+    dtype, vocab, rows, top = getattr(torch, kind), 2 ** 24 - 1, 500, 32
+    g = torch.Generator(device="cuda").manual_seed(8)
+    few = torch.full((vocab,), -4.0, device="cuda")
+    at = torch.randperm(vocab, generator=g, device="cuda")[:60]
+    at[:6] = torch.tensor([0, 1, vocab - 1, vocab - 2, vocab // 2, vocab // 2 + 1], device="cuda")
+    few[at] = torch.randint(0, 9, (60,), generator=g, device="cuda").float()
+    order = torch.arange(vocab, device="cuda") // 8192 / 64.0
+    for x in (few, torch.full_like(few, 0.25), order, order.flip(0)):
+        x = x.to(dtype)
+        best, high = [], x.unique(sorted=True).flip(0)
+        for value in high:  # equal ones: the lower tokens first
+            best += (x == value).nonzero()[:top, 0].tolist()
+            if len(best) >= top:
+                break
+        best = best[:top]
+        r = V.logprobs(x.expand(rows, -1), top=top)
+        z = x.double()
+        lse = torch.logsumexp(z, 0).item()
+        S = 6 * 2.0 ** -22 + U * (vocab / 512 + 20) + 3 * U * (torch.softmax(z, 0) * (z.max() - z)).sum().item()
+        for i in (0, 1, rows - 1):
+            assert r.top_tokens[i].tolist() == best
+            assert abs(r.lse[i].item() - lse) <= S + 4 * U * abs(lse)
+            want = z[best].cpu().numpy() - lse
+            assert (np.abs(r.top_logprobs[i].cpu().numpy() - want) <= S + 4 * U * np.abs(want)).all()
+        assert torch.equal(r.top_tokens, r.top_tokens[:1].expand(rows, -1))
+
+
+@pytest.mark.parametrize("n,gamma,vocab,kind", [(500, 4, 5003, "bf16"), (470, 8, 2000, "f32"), (30, 5, 151936, "bf16"), (60, 16, 151936, "f16"), (120, 3, 70001, "f32")])
+def test_rows_behind_a_refused_draft_left_out(torch, V, n, gamma, vocab, kind):  # noqa: F811
+    """Greedy, and sampled drafts without logits: so many entries that what is decided in time is left out, by rows of one part and of several; ragged."""
+    x, _, tokens = case(torch, n, gamma, vocab, getattr(torch, KINDS[kind]), None)
+    best = x[:, :gamma].float().argmax(-1).to(torch.int32)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    some = torch.where(torch.rand((n, gamma), generator=g, device="cuda") < 0.7, best, tokens)
+    drafted = torch.randint(0, gamma + 1, (n,), generator=g, device="cuda", dtype=torch.int32)
+    few = list(range(0, n, -(-n // 12))) + [n - 1]
+    host = {i: x[i].double().cpu().numpy() for i in few}
+    for temperature in (0.0, 0.8):
+        for have in (None, drafted):
+            a, b = (V.verify(x, some, temperature=temperature, seed=6, step=1, drafted=have) for _ in range(2))
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+            for i in few:
+                want, c, margin = R.verify(host[i], some[i].cpu().numpy(), None, temperature, temperature, 6, 1, i, gamma if have is None else int(have[i]))
+                assert margin < NEAR or (a[0][i].tolist() == want.tolist() and int(a[1][i]) == c), (i, a[0][i].tolist(), want.tolist())
+            if have is None and temperature == 0:
+                assert 1 < a[1].float().mean().item() < gamma + 1
+    # greedy, every entry: against torch
+    said, count = V.verify(x, some, drafted=drafted)
+    full = x.float()
+    token = torch.stack([(full[:, t] == full[:, t].amax(-1, keepdim=True)).int().argmax(-1) for t in range(gamma + 1)], 1).to(torch.int32)
+    stay = ((token[:, :gamma] == some) & (torch.arange(gamma, device="cuda") < drafted[:, None])).int().cumprod(1).sum(1)
+    at = torch.arange(gamma + 1, device="cuda")[None]
+    assert torch.equal(count.long(), stay + 1)
+    assert torch.equal(said, torch.where(at <= stay[:, None], token, torch.full_like(token, -1)))
+
+
 # ---------------------------------------------------------------------------------------------------- gradients that go forward
 
 def test_forward_mode_tangents_are_refused(torch, V):  # noqa: F811
