@@ -62,7 +62,7 @@ typedef struct {
   int64_t V;               /* 1 <= V < 2^24 */
   int32_t gamma;           /* 0..WHEAD_MAX_DRAFTS */
   int32_t target_dtype, draft_dtype;
-  uint32_t step;           /* absolute index of the first draft's position */
+  uint32_t step;           /* the call's draws have the numbers step .. step + gamma, for all its entries: they only have to be fresh for `seed` */
   double temperature;      /* of the target: 0, or > 0 */
   double draft_temperature;/* > 0: of the drafts' logits */
   uint64_t seed;

@@ -149,7 +149,8 @@ def verify(target, tokens, draft=None, *, temperature=0.0, draft_temperature=Non
     int32: how many of its drafts an entry has (None: gamma).
     said[i, :count[i]] are the drafts that stay and the token after them, -1 the rest; count[i] is what KvCache.compact keeps of the last
     token and the drafts. temperature 0: drafts stay while they are the target's best token. Above: every token said is distributed as the
-    target's own; seed and step (the walk's t0) number the draws as they do the walk's, and may be the walk's.
+    target's own; seed and step number the draws, step .. step + gamma for all entries of a call, however far each has come: these only have to be
+    fresh, and may be the walk's seed and t0.
     In a row of target with NaN, +inf or nothing but -inf no draft stays and the token after is -1."""
     L = _lib or load()
     index, shape, strides = target.get_device(), target.shape, target.stride()
