@@ -9,13 +9,13 @@
 // issued by halves of 64 keys, each as soon as the product with P has read that half, and the softmax starts on the first (this and the two issuing
 // warps: 2 prompts of 2,048 tokens 344 -> 300 us).
 //
-// What holds it back. Prompts: no unit is full (53 % of the issue slots, 46 % of the tensor pipe, 41 % of the ALU, 23 % of the
+// What holds it back. Prompts: no unit is full (55 % of the issue slots, 44 % of the tensor pipe, 44 % of the ALU, 22 % of the
 // exponentials); the roles wait for one another, the longest of them the softmax, one thread a row. At 128 keys a row and block its 128
 // exponentials, as many differences, products, maxima, additions and half as many packings are some 650 issue slots of a warp; eight
-// such warps and the eight that unpack share four schedulers. 2 x 2048 tokens on 4,100 and 6,200 keys, 32 query heads on 8: 297 us,
-// 1.03 PFLOP/s, 54 % of the measured rate of large matrix products; 64 channels 225 us; a window of 1,024 133 us, with 100 first tokens 136. Two threads a row (half the chain, but a
-// trade of maxima and sums through shared memory for every block) and blocks of 64 keys (twice the barriers) were slower. For a few
-// tokens a sequence (8 x 17, 31 MB: 30 us) what a CTA does once (tensor memory, query rows, the first blocks, its part for the joining)
+// such warps and the eight that unpack share four schedulers. 2 x 2048 tokens on 5,001 and 6,200 keys, 32 query heads on 8:
+// 297 us, 1.03 PFLOP/s, 54 % of the measured rate of large matrix products; 64 channels 225 us; on 4,835 and 6,200 keys a window of 1,024 128 us, with
+// 100 first tokens 136. Two threads a row (half the chain, but a trade of maxima and sums through shared memory for every block) and blocks of 64
+// keys (twice the barriers) were slower. For a few tokens a sequence (8 x 17, 31 MB: 30 us) what a CTA does once (tensor memory, query rows, the first blocks, its part for the joining)
 // and the chain through one block: copy, unpack, QK, softmax, PV.
 //
 // Shared memory holds operands in rows of 128 bytes (64 f16), 8 rows to an atom of 1024 bytes, 16-byte chunks swizzled by the row.

@@ -254,8 +254,9 @@ __global__ void __launch_bounds__((Form<HELD>::kThreads), (Form<HELD>::kCtas)) l
     TopShared& ts = top_shared;
     // The CTA's values are in kSubs parts. The `top`-th of their largest values is one that `top` values reach, and on rows
     // without an order few more do. It is the lowest that fewer than `top` are greater than. For a long list a cluster's CTAs find one
-    // bound for the row, by kSubs parts of it, which lets that many fewer values through (64 x 248064 top 20: 16.5 us, by bounds of
-    // their own 19.7); for a short list the trade takes longer than it saves (1 x 151936 top 5: 6.3 us, by bounds of their own 5.8).
+    // bound for the row, by kSubs parts of it, which lets that many fewer values through; for a short list the trade takes longer than it
+    // saves. One bound and bounds of their own, us, by the list's length: 1 x 151936 top 5 6.5, 6.1; top 8 6.5, 6.2; top 12 6.6, 6.5; top 20 6.6,
+    // 7.2; top 32 6.9, 8.1. 17 x 151936: 7.9, 7.7; 7.9, 8.0; 7.9, 8.3; 8.0, 9.2; 8.3, 10.9. 64 x 248064: 16.1, 16.1; 16.2, 16.7; 16.4, 17.5; 16.6, 19.7; 17.2, 24.7.
     const uint32_t* sub = ts.sub;
     if (ctas > 1) cluster_wait();  // all have started
     if (ctas > 1 && a.top > 8) {
